@@ -82,6 +82,7 @@ enum {
 enum { SPEC_KV_NHD = 0, SPEC_KV_HND = 1 };  /* paged KV cache layouts */
 enum { SPEC_CACHE_SAME = 0, SPEC_CACHE_FP8_E4M3 = 1, SPEC_CACHE_FP8_E5M2 = 2 };
 enum { SPEC_SCALE_TENSOR = 0, SPEC_SCALE_PER_TOKEN = 1 };   /* fp8 KV scale forms */
+enum { SPEC_ROPE_HALVES = 0, SPEC_ROPE_PAIRS = 1 };         /* which elements rotate together */
 
 /* Row-statistics flag bits (spec_row_stats row_flags). */
 enum { SPEC_ROW_NAN = 1, SPEC_ROW_POSINF = 2, SPEC_ROW_ALL_NEGINF = 4 };
@@ -97,13 +98,17 @@ enum {
     SPEC_K_LAZY_SAMPLE = 6,
     SPEC_K_KV_COMMIT = 7,
     SPEC_K_BUDGET = 8,          /* adaptive node-budget update */
-    SPEC_K_COUNT = 9
+    SPEC_K_QK_ROPE = 9,         /* head norm and rotation of queries and keys */
+    SPEC_K_KV_COMMIT_FP4 = 10,  /* K/V rows into the 4-bit cache */
+    SPEC_K_KV_LOAD_FP4 = 11,    /* 4-bit cache back to rows */
+    SPEC_K_TREE_ATTN = 12,      /* tree attention over the 4-bit cache */
+    SPEC_K_COUNT = 13
 };
 
 /*
  * Create a handle for `device` able to serve calls with B <= max_B, N <= max_N (<= 64) and
  * V <= max_V (<= 2^21). Allocates a device workspace of 232 * max_B * max_N + 4 * max_B
- * bytes with cudaMalloc (released by spec_verify_destroy). Returns SPEC_ERR_ARG for out-of-range limits,
+ * + 16384 bytes with cudaMalloc (released by spec_verify_destroy). Returns SPEC_ERR_ARG for out-of-range limits,
  * SPEC_ERR_CUDA if the device cannot be used, SPEC_ERR_WORKSPACE if allocation fails.
  */
 int spec_verify_init(spec_handle *h, int max_B, int max_N, int64_t max_V, int device);
@@ -216,6 +221,124 @@ int spec_kv_commit(spec_handle h, const void *src_k, const void *src_v, int src_
                    int64_t num_blocks, const int32_t *block_table, int max_blocks,
                    const int32_t *seq_pos, const float *k_scale, const float *v_scale,
                    int scale_per_token, int32_t *commit_status, void *stream);
+
+/*
+ * The tree step of the target model around a verification, over a KV cache held in 4 bits:
+ * spec_qk_norm_rope turns the projections of the tree's nodes into queries and keys at their
+ * tree positions, spec_tree_attention_fp4 is the attention of the one forward over all nodes
+ * (the mask of spec_build_tree_mask, EmbodiInfer PR #11 commit 4b728e2), spec_kv_commit_fp4
+ * keeps the accepted nodes' K/V, and spec_kv_load_fp4 reads a cache back.
+ *
+ * Row arguments of these four calls ([B, N, H, D] of `dtype`) may be columns of a wider
+ * matrix: each comes with the number of elements from one token (b, n) to the next, at least
+ * H * D; the heads of a token and the elements of a head are contiguous.
+ *
+ * The 4-bit paged cache (host struct, copied at the call; the pointers are device memory):
+ *   k, v         e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign in bit 3), two per byte, the
+ *                even element in the low nibble: SPEC_KV_NHD [num_blocks, block_size, H, D/2] or
+ *                SPEC_KV_HND [num_blocks, H, block_size, D/2]; 16-byte aligned;
+ *   k_sf, v_sf   e4m3 block scales, one per 16 consecutive elements of a head: the same order
+ *                of tokens and heads with D/16 bytes each; 16-byte aligned;
+ *   k_scale, v_scale   device float32, one value per cache (NULL = 1), positive and between
+ *                2^-100 and 2^100;
+ *   block_table  int32 [B, max_blocks]: cache block of each block_size tokens of request b.
+ * An element's value is code * block scale * tensor scale. D is a multiple of 16, at most 512;
+ * a cache has fewer than 2^32 rows (num_blocks * block_size * H).
+ * Storing x, with r = RN(1 / tensor scale) and all products rounded to float32:
+ *   block scale s = e4m3(max|x| * RN(r * RN(1/6))), nearest even, at most 448;
+ *   code = e2m1(x * RN(RN(1/s) * r)), nearest even, at most 6 in magnitude; all codes are 0
+ *   where s is 0. The sign of a code 0 is not specified. A block that holds a NaN gets the
+ *   block scale NaN.
+ */
+typedef struct {
+    void *k, *v, *k_sf, *v_sf;
+    const float *k_scale, *v_scale;
+    int64_t num_blocks;
+    int32_t layout, block_size, H, D;
+    const int32_t *block_table;
+    int32_t max_blocks;
+} spec_fp4_cache;
+
+/*
+ * Norm of every query and key head and the rotation by the node's position, in one pass.
+ *   q [B, N, Hq, D], k [B, N, Hkv, D] of dtype (SPEC_F32 / SPEC_BF16 / SPEC_F16);
+ *   q_weight, k_weight   [D] of dtype, or both NULL for no norm:
+ *                y = x / sqrt(mean(x^2) + eps) * weight;
+ *   inv_freq     float32 [rot / 2]: angle of pair i = position * inv_freq[i], position =
+ *                seq_pos[b] + depth[b][n]. The angle's turn is formed in 64-bit fixed point, so
+ *                it is exact to 2^-32 of a turn at any 32-bit position;
+ *   rot          rotated elements of a head, even, 0 <= rot <= D; the others are only
+ *                normalised. Pair i is elements (i, i + rot/2) for SPEC_ROPE_HALVES, (2i, 2i+1)
+ *                for SPEC_ROPE_PAIRS; (a, c) becomes (a cos - c sin, c cos + a sin);
+ *   seq_pos      int32 [B]: position of node 0;
+ *   depth        int32 [B, N] (spec_build_tree_mask), or NULL for n itself (a chain, a prompt);
+ *   q_out, k_out rows of dtype; may be q and k themselves with the same strides.
+ * All arithmetic is float32, rounded once at the end. N is not limited by the handle here;
+ * 1 <= D <= 1024.
+ */
+int spec_qk_norm_rope(spec_handle h, const void *q, int64_t q_stride, const void *k,
+                      int64_t k_stride, int dtype, int B, int N, int Hq, int Hkv, int D,
+                      const void *q_weight, const void *k_weight, float eps,
+                      const float *inv_freq, int rot, int style, const int32_t *seq_pos,
+                      const int32_t *depth, void *q_out, int64_t q_out_stride, void *k_out,
+                      int64_t k_out_stride, void *stream);
+
+/*
+ * K/V rows into the 4-bit cache. src_k, src_v [B, N, H, D] of src_dtype with H and D the
+ * cache's. With kv_commit and accept_len (outputs of a verify call) slot j of request b
+ * (j = 0..accept_len[b]) takes node kv_commit[b][j], as in spec_kv_commit, and N is limited by
+ * the handle. With kv_commit NULL slot j takes row j (a prompt): j = 0..accept_len[b], or all N
+ * rows if accept_len is NULL too; an accept_len of -1 writes nothing, and N is not limited.
+ * Slot j is written at position seq_pos[b] + j. commit_status int32 [B] (may be NULL):
+ * SPEC_REQ_BAD_SLOT if a slot's position, block or node is outside its range (that slot is
+ * skipped), else 0.
+ */
+int spec_kv_commit_fp4(spec_handle h, const void *src_k, int64_t k_stride, const void *src_v,
+                       int64_t v_stride, int src_dtype, int B, int N,
+                       const spec_fp4_cache *cache, const int32_t *kv_commit,
+                       const int32_t *accept_len, const int32_t *seq_pos,
+                       int32_t *commit_status, void *stream);
+
+/*
+ * Positions start[b] .. start[b] + count[b] - 1 of the 4-bit cache as rows out_k, out_v
+ * [B, max_len, H, D] of out_dtype (contiguous): value rounded once from float32. Row i of
+ * request b is position start[b] + i; rows at and after count[b] and rows whose position or
+ * block is outside the table or the cache are zero. status int32 [B] (may be NULL):
+ * SPEC_REQ_BAD_SLOT if such a row is below count[b], or count[b] is outside [0, max_len].
+ */
+int spec_kv_load_fp4(spec_handle h, const spec_fp4_cache *cache, int B, const int32_t *start,
+                     const int32_t *count, int64_t max_len, void *out_k, void *out_v,
+                     int out_dtype, int32_t *status, void *stream);
+
+/*
+ * Attention of a tree's nodes over the 4-bit cache and the tree itself: for node n and query
+ * head h (its K/V head is h / (Hq / H)),
+ *   keys  = positions 0 .. ctx_len[b] - 1 of the cache, and the nodes j whose bit is set in
+ *           anc_mask[b][n] (bits at and above N are ignored);
+ *   out   = sum_j softmax_j(scale * q.k_j) v_j,   lse = log sum_j exp(scale * q.k_j).
+ * A node without any key gets out 0 and lse -inf. What a node does not see never influences
+ * its result, NaN and infinities included.
+ *   q [B, N, Hq, D], k, v [B, N, H, D] of dtype (SPEC_BF16 / SPEC_F16), H and D the cache's;
+ *   Hq a multiple of H; D 64, 128 or 256 (others: SPEC_ERR_UNSUPPORTED); scale finite, > 0;
+ *   ctx_len int32 [B]; anc_mask uint64 [B, N] (spec_build_tree_mask);
+ *   out [B, N, Hq, D] of dtype, lse float32 [B, N, Hq] (may be NULL), both contiguous;
+ *   status int32 [B] (may be NULL): SPEC_REQ_BAD_SLOT if ctx_len[b] is outside
+ *   [0, max_blocks * block_size] (it is clamped) or a block of the context is outside the cache
+ *   (its positions are not attended), else 0;
+ *   workspace: device memory of the size that spec_tree_attention_workspace gives for these
+ *   sizes, 256-byte aligned; its contents need not be kept or cleared between calls, and calls
+ *   that share it or the handle are serialised by the caller.
+ * Scores and softmax statistics are float32; probabilities are rounded to 16 bits with the
+ * largest of a row scaled near 1, for the product with V, which is exact in 16 bits.
+ */
+int spec_tree_attention_workspace(spec_handle h, int B, int N, int Hq, int H, int D,
+                                  int64_t *bytes);
+int spec_tree_attention_fp4(spec_handle h, const void *q, int64_t q_stride, const void *k,
+                            int64_t k_stride, const void *v, int64_t v_stride, int dtype, int B,
+                            int N, int Hq, const spec_fp4_cache *cache, const int32_t *ctx_len,
+                            const uint64_t *anc_mask, float scale, void *out, float *lse,
+                            int32_t *status, void *workspace, int64_t workspace_bytes,
+                            void *stream);
 
 /*
  * The vocabulary-streaming row statistics on their own (the first stage of both verify

@@ -24,7 +24,8 @@ SPEC_REQ_OK, SPEC_REQ_BAD_PARENT, SPEC_REQ_BAD_TOKEN, SPEC_REQ_BAD_ROW, SPEC_REQ
     0, 1, 2, 3, 4
 SPEC_ROW_NAN, SPEC_ROW_POSINF, SPEC_ROW_ALL_NEGINF = 1, 2, 4
 KERNEL_CLASSES = ("tree_mask", "row_stats", "draft_stats", "walk_greedy", "walk_sample",
-                  "lazy_greedy", "lazy_sample", "kv_commit", "budget")
+                  "lazy_greedy", "lazy_sample", "kv_commit", "budget", "qk_rope",
+                  "kv_commit_fp4", "kv_load_fp4", "tree_attn")
 SPEC_F16 = 2
 SPEC_REQ_BAD_SLOT = 5
 SPEC_REQ_BAD_BUDGET = 6
@@ -33,7 +34,17 @@ DBG_INDEX, DBG_ARRIVAL, DBG_WALK = 1, 2, 4
 SPEC_KV_NHD, SPEC_KV_HND = 0, 1
 SPEC_CACHE_SAME, SPEC_CACHE_FP8_E4M3, SPEC_CACHE_FP8_E5M2 = 0, 1, 2
 SPEC_SCALE_TENSOR, SPEC_SCALE_PER_TOKEN = 0, 1
+SPEC_ROPE_HALVES, SPEC_ROPE_PAIRS = 0, 1
 
+
+class Fp4CacheStruct(ctypes.Structure):
+    """spec_fp4_cache: the 4-bit paged cache as the library takes it (see Fp4Cache)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_sf", ctypes.c_void_p),
+                ("v_sf", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int64),
+                ("layout", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("block_table", ctypes.c_void_p), ("max_blocks", ctypes.c_int32)]
 
 
 class BudgetParams(ctypes.Structure):
@@ -100,6 +111,15 @@ def _open(path: str) -> ctypes.CDLL:
     lib.spec_set_node_budget.argtypes = [P, P]
     lib.spec_budget_update.argtypes = [P, ctypes.POINTER(BudgetParams), P, P, P, i32,
                                        i32, P, P, P]
+    C = ctypes.POINTER(Fp4CacheStruct)
+    lib.spec_qk_norm_rope.argtypes = [P, P, i64, P, i64, i32, i32, i32, i32, i32, i32, P, P, f32,
+                                      P, i32, i32, P, P, P, i64, P, i64, P]
+    lib.spec_kv_commit_fp4.argtypes = [P, P, i64, P, i64, i32, i32, i32, C, P, P, P, P, P]
+    lib.spec_kv_load_fp4.argtypes = [P, C, i32, P, P, i64, P, P, i32, P, P]
+    lib.spec_tree_attention_workspace.argtypes = [P, i32, i32, i32, i32, i32,
+                                                  ctypes.POINTER(i64)]
+    lib.spec_tree_attention_fp4.argtypes = [P, P, i64, P, i64, P, i64, i32, i32, i32, i32, C, P,
+                                            P, f32, P, P, P, P, i64, P]
     lib.spec_profile_begin.argtypes = [P]
     lib.spec_profile_end.argtypes = [P, P, P]
     lib.spec_error_string.argtypes = [i32]
@@ -338,6 +358,198 @@ def spec_kv_commit(h: Handle, src_k, src_v, kv_commit, accept_len, cache_k, cach
         _stream(stream, src_k.device)), "spec_kv_commit")
 
 
+# ---- the tree step over a 4-bit cache ----------------------------------------------------------
+
+class Fp4Cache:
+    """A 4-bit paged K/V cache (spec_fp4_cache): uint8 codes k, v [num_blocks, block_size, H,
+    D/2] (SPEC_KV_NHD) or [num_blocks, H, block_size, D/2] (SPEC_KV_HND), uint8 e4m3 block
+    scales k_sf, v_sf of the same shape but D/16, and float32 tensor scales of one element
+    (None = 1). Holds the tensors; block tables come with each call."""
+
+    def __init__(self, k, v, k_sf, v_sf, layout: int = SPEC_KV_NHD, k_scale=None, v_scale=None):
+        if layout not in (SPEC_KV_NHD, SPEC_KV_HND):
+            raise ValueError("layout must be SPEC_KV_NHD or SPEC_KV_HND")
+        if k.dim() != 4 or any(t.dtype != torch.uint8 for t in (k, v, k_sf, v_sf)):
+            raise TypeError("k, v, k_sf and v_sf must be 4-dimensional uint8 tensors")
+        if k.shape != v.shape or k_sf.shape != v_sf.shape or \
+                k.shape[:3] != k_sf.shape[:3] or k.shape[3] != 8 * k_sf.shape[3]:
+            raise ValueError("k, v: [..., D/2], k_sf, v_sf: [..., D/16] of one shape")
+        for s in (k_scale, v_scale):
+            if s is not None and (s.dtype != torch.float32 or s.numel() != 1):
+                raise TypeError("tensor scales must be float32 of one element")
+        self.k, self.v, self.k_sf, self.v_sf = k, v, k_sf, v_sf
+        self.k_scale, self.v_scale, self.layout = k_scale, v_scale, int(layout)
+        nhd = layout == SPEC_KV_NHD
+        self.num_blocks, self.D = k.shape[0], 2 * k.shape[3]
+        self.block_size, self.H = (k.shape[1], k.shape[2]) if nhd else (k.shape[2], k.shape[1])
+
+    @classmethod
+    def empty(cls, num_blocks: int, block_size: int, H: int, D: int, device,
+              layout: int = SPEC_KV_NHD, k_scale=None, v_scale=None) -> "Fp4Cache":
+        """A cache of zeros."""
+        if D % 16 != 0:
+            raise ValueError("D must be a multiple of 16")
+        shape = (num_blocks, block_size, H) if layout == SPEC_KV_NHD else \
+            (num_blocks, H, block_size)
+        one = [torch.zeros(shape + (n,), dtype=torch.uint8, device=device)
+               for n in (D // 2, D // 2, D // 16, D // 16)]
+        return cls(*one, layout, k_scale, v_scale)
+
+    def tensors(self):
+        return (self.k, self.v, self.k_sf, self.v_sf, self.k_scale, self.v_scale)
+
+    def struct(self, block_table) -> Fp4CacheStruct:
+        """The library's view of the cache with the block table int32 [B, max_blocks]."""
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [B, max_blocks]")
+        return Fp4CacheStruct(
+            *(_ptr(t) for t in self.tensors()), self.num_blocks, self.layout, self.block_size,
+            self.H, self.D, _ptr(_i32(block_table, "block_table")), block_table.shape[1])
+
+
+def _rows(t, name):
+    """(address, token stride) of rows [B, N, H, D], contiguous or columns of a wider matrix."""
+    if not t.is_cuda:
+        raise ValueError("tensors passed to the library must be CUDA tensors")
+    B, N, H, D = t.shape
+    sb, sn, sh, sd = t.stride()
+    token = sn if N > 1 else (sb if B > 1 else H * D)
+    if (D > 1 and sd != 1) or (H > 1 and sh != D) or (B > 1 and N > 1 and sb != N * sn) or \
+            token < H * D:
+        raise ValueError(f"{name}: heads and elements must be contiguous, and tokens evenly "
+                         "spaced")
+    return ctypes.c_void_p(t.data_ptr()), token
+
+
+def _shape(t, want, name):
+    if t is not None and tuple(t.shape) != tuple(want):
+        raise ValueError(f"{name} must be {list(want)}, got {list(t.shape)}")
+    return t
+
+
+def _same_dtype(tensors, dtype, where):
+    if any(t is not None and t.dtype != dtype for t in tensors):
+        raise TypeError(f"{where}: row tensors must share one dtype")
+
+
+def spec_qk_norm_rope(h: Handle, q, k, inv_freq, seq_pos, depth, q_out, k_out, q_weight=None,
+                      k_weight=None, eps: float = 1e-6, style: int = SPEC_ROPE_HALVES,
+                      stream=None):
+    """Norm of every query and key head and the rotation by seq_pos[b] + depth[b][n], in one
+    pass. q [B, N, Hq, D], k [B, N, Hkv, D]; inv_freq float32 [rot/2] (None: no rotation);
+    depth int32 [B, N] or None (n itself); weights [D] or None (no norm). q_out, k_out may be
+    q and k."""
+    where = "spec_qk_norm_rope"
+    B, N, Hq, D = q.shape
+    Hkv = k.shape[2]
+    _shape(k, (B, N, Hkv, D), "k")
+    _shape(q_out, q.shape, "q_out")
+    _shape(k_out, k.shape, "k_out")
+    _same_device((q, k, inv_freq, seq_pos, depth, q_out, k_out, q_weight, k_weight), _hdev(h),
+                 where)
+    _same_dtype((k, q_out, k_out, q_weight, k_weight), q.dtype, where)
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        _shape(w, (D,), name)
+    if inv_freq is not None and inv_freq.dtype != torch.float32:
+        raise TypeError("inv_freq must be float32")
+    _shape(_i32(seq_pos, "seq_pos"), (B,), "seq_pos")
+    if depth is not None:
+        _shape(_i32(depth, "depth"), (B, N), "depth")
+    (qp, qs), (kp, ks), (qo, qos), (ko, kos) = (
+        _rows(t, n) for t, n in ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out")))
+    _check(load().spec_qk_norm_rope(
+        h.ptr, qp, qs, kp, ks, _kv_dtype(q), B, N, Hq, Hkv, D, _ptr(q_weight), _ptr(k_weight),
+        float(eps), _ptr(inv_freq), 0 if inv_freq is None else 2 * inv_freq.numel(), int(style),
+        _ptr(seq_pos), _ptr(depth), qo, qos, ko, kos, _stream(stream, q.device)), where)
+
+
+def spec_kv_commit_fp4(h: Handle, src_k, src_v, cache: Fp4Cache, block_table, seq_pos,
+                       kv_commit=None, accept_len=None, commit_status=None, stream=None):
+    """K/V rows [B, N, H, D] into the 4-bit cache: the root and the accepted nodes of a verify
+    call (kv_commit, accept_len), or rows 0..accept_len[b] in order (kv_commit None; all N
+    without accept_len), at positions seq_pos[b] + j."""
+    where = "spec_kv_commit_fp4"
+    B, N, H, D = src_k.shape
+    _shape(src_k, (B, N, cache.H, cache.D), "src_k")
+    _shape(src_v, src_k.shape, "src_v")
+    _same_device((src_k, src_v, block_table, seq_pos, kv_commit, accept_len, commit_status,
+                  *cache.tensors()), _hdev(h), where)
+    _same_dtype((src_v,), src_k.dtype, where)
+    _shape(block_table, (B, block_table.shape[-1]), "block_table")
+    for t, want, name in ((seq_pos, (B,), "seq_pos"), (kv_commit, (B, N), "kv_commit"),
+                          (accept_len, (B,), "accept_len"),
+                          (commit_status, (B,), "commit_status")):
+        if t is not None:
+            _shape(_i32(t, name), want, name)
+    (kp, ks), (vp, vs) = _rows(src_k, "src_k"), _rows(src_v, "src_v")
+    _check(load().spec_kv_commit_fp4(
+        h.ptr, kp, ks, vp, vs, _kv_dtype(src_k), B, N, ctypes.byref(cache.struct(block_table)),
+        _ptr(kv_commit), _ptr(accept_len), _ptr(seq_pos), _ptr(commit_status),
+        _stream(stream, src_k.device)), where)
+
+
+def spec_kv_load_fp4(h: Handle, cache: Fp4Cache, block_table, start, count, out_k, out_v,
+                     status=None, stream=None):
+    """Positions start[b] .. start[b] + count[b] - 1 of the 4-bit cache into out_k, out_v
+    [B, max_len, H, D]; rows at and after count[b] become zero."""
+    where = "spec_kv_load_fp4"
+    B, max_len = out_k.shape[0], out_k.shape[1]
+    _shape(out_k, (B, max_len, cache.H, cache.D), "out_k")
+    _shape(out_v, out_k.shape, "out_v")
+    _same_device((out_k, out_v, block_table, start, count, status, *cache.tensors()), _hdev(h),
+                 where)
+    _same_dtype((out_v,), out_k.dtype, where)
+    _shape(block_table, (B, block_table.shape[-1]), "block_table")
+    for t, name in ((start, "start"), (count, "count"), (status, "status")):
+        if t is not None:
+            _shape(_i32(t, name), (B,), name)
+    _check(load().spec_kv_load_fp4(
+        h.ptr, ctypes.byref(cache.struct(block_table)), B, _ptr(start), _ptr(count), max_len,
+        _ptr(out_k), _ptr(out_v), _kv_dtype(out_k), _ptr(status),
+        _stream(stream, out_k.device)), where)
+
+
+def spec_tree_attention_workspace(h: Handle, B: int, N: int, Hq: int, H: int, D: int) -> int:
+    """Bytes of workspace that spec_tree_attention_fp4 needs for these sizes."""
+    n = ctypes.c_int64()
+    _check(load().spec_tree_attention_workspace(h.ptr, int(B), int(N), int(Hq), int(H), int(D),
+                                                ctypes.byref(n)),
+           "spec_tree_attention_workspace")
+    return n.value
+
+
+def spec_tree_attention_fp4(h: Handle, q, k, v, cache: Fp4Cache, block_table, ctx_len, anc_mask,
+                            scale: float, out, workspace, lse=None, status=None, stream=None):
+    """Attention of the tree's nodes q [B, N, Hq, D] over positions 0..ctx_len[b]-1 of the
+    4-bit cache and over the nodes k, v [B, N, H, D] that anc_mask (int64 [B, N] bit patterns,
+    build_tree_mask) lets each see."""
+    where = "spec_tree_attention_fp4"
+    B, N, Hq, D = q.shape
+    _shape(q, (B, N, Hq, cache.D), "q")
+    _shape(k, (B, N, cache.H, D), "k")
+    _shape(v, k.shape, "v")
+    _shape(out, q.shape, "out")
+    _same_device((q, k, v, block_table, ctx_len, anc_mask, out, workspace, lse, status,
+                  *cache.tensors()), _hdev(h), where)
+    _same_dtype((k, v, out), q.dtype, where)
+    _shape(block_table, (B, block_table.shape[-1]), "block_table")
+    _shape(_i32(ctx_len, "ctx_len"), (B,), "ctx_len")
+    if anc_mask.dtype not in (torch.int64, getattr(torch, "uint64", torch.int64)):
+        raise TypeError("anc_mask must be a 64-bit integer tensor")
+    _shape(anc_mask, (B, N), "anc_mask")
+    if lse is not None and lse.dtype != torch.float32:
+        raise TypeError("lse must be float32")
+    _shape(lse, (B, N, Hq), "lse")
+    if status is not None:
+        _shape(_i32(status, "status"), (B,), "status")
+    (qp, qs), (kp, ks), (vp, vs) = (_rows(t, n) for t, n in ((q, "q"), (k, "k"), (v, "v")))
+    _check(load().spec_tree_attention_fp4(
+        h.ptr, qp, qs, kp, ks, vp, vs, _kv_dtype(q), B, N, Hq,
+        ctypes.byref(cache.struct(block_table)), _ptr(ctx_len), _ptr(anc_mask), float(scale),
+        _ptr(out), _ptr(lse), _ptr(status), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream, q.device)), where)
+
+
 def spec_set_node_budget(h: Handle, n_active):
     """Later verify calls on ``h`` verify request b as its first n_active[b] nodes (device
     int32 [>= B], read when the kernels run); None verifies every node."""
@@ -443,6 +655,41 @@ def build_tree_mask(h: Handle, parent, stream=None) -> dict:
                status=torch.empty(B, dtype=torch.int32, device=dev))
     spec_build_tree_mask(h, parent, out["anc_mask"], out["depth"], out["status"], stream)
     return out
+
+
+def qk_norm_rope(h: Handle, q, k, inv_freq, seq_pos, depth=None, q_weight=None, k_weight=None,
+                 eps: float = 1e-6, style: int = SPEC_ROPE_HALVES, stream=None):
+    """-> new contiguous (q, k), normalised and rotated (see spec_qk_norm_rope)."""
+    qo, ko = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+    spec_qk_norm_rope(h, q, k, inv_freq, seq_pos, depth, qo, ko, q_weight, k_weight, eps, style,
+                      stream)
+    return qo, ko
+
+
+def kv_load_fp4(h: Handle, cache: Fp4Cache, block_table, start, count, max_len: int,
+                dtype=torch.bfloat16, stream=None):
+    """-> (k, v) rows [B, max_len, H, D] of ``dtype`` (see spec_kv_load_fp4)."""
+    shape = (block_table.shape[0], int(max_len), cache.H, cache.D)
+    k, v = (torch.empty(shape, dtype=dtype, device=cache.k.device) for _ in range(2))
+    spec_kv_load_fp4(h, cache, block_table, start, count, k, v, stream=stream)
+    return k, v
+
+
+def tree_attention_fp4(h: Handle, q, k, v, cache: Fp4Cache, block_table, ctx_len, anc_mask,
+                       scale: float, workspace=None, stream=None):
+    """-> (out [B, N, Hq, D], lse float32 [B, N, Hq]) (see spec_tree_attention_fp4). Without a
+    workspace one is taken from torch's allocator for the call."""
+    B, N, Hq, D = q.shape
+    if workspace is None:
+        size = spec_tree_attention_workspace(h, B, N, Hq, cache.H, D)
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
+    spec_tree_attention_fp4(h, q, k, v, cache, block_table, ctx_len, anc_mask, scale, out,
+                            workspace, lse, stream=stream)
+    return out, lse
 
 
 # ---- greedy verification without device allocation --------------------------------------------

@@ -50,6 +50,7 @@ struct spec_ctx {
     RowPart *piece = nullptr;             // small batches: per-piece row statistics
     int32_t *count = nullptr;             // ... and per-row arrivals (zero between calls)
     int32_t *dbg = nullptr;               // debug builds: violation bits per request [max_B]
+    int32_t *arrive = nullptr;            // tree attention: arrivals of split items (zero between)
     int inject_row = -1, inject_value = 0;   // debug builds: one armed counter injection
     int slots = 0;                        // CTAs of the split row-statistics kernel in a wave
     int sms = 0;                          // streaming multiprocessors of the device
@@ -275,7 +276,7 @@ int spec_verify_init(spec_handle *out, int max_B, int max_N, int64_t max_V, int 
     const size_t rows = (size_t)max_B * max_N;
     const size_t bytes =
         rows * (9 * 4 + kRowChunks * sizeof(float2) + kRowChunks * sizeof(RowPart) + 4) +
-        sizeof(int32_t) * (size_t)max_B;
+        sizeof(int32_t) * (size_t)max_B + sizeof(int32_t) * kAttnMaxCtas;
     if (cudaMalloc(&h->ws, bytes) != cudaSuccess) {
         cudaGetLastError();
         delete h;
@@ -300,10 +301,12 @@ int spec_verify_init(spec_handle *out, int max_B, int max_N, int64_t max_V, int 
     h->dflags = reinterpret_cast<int32_t *>(take(rows * 4));
     h->count = reinterpret_cast<int32_t *>(take(rows * 4));
     h->dbg = reinterpret_cast<int32_t *>(take(sizeof(int32_t) * (size_t)max_B));
+    h->arrive = reinterpret_cast<int32_t *>(take(sizeof(int32_t) * kAttnMaxCtas));
     int sms = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
         cudaMemset(h->count, 0, rows * 4) != cudaSuccess ||
-        cudaMemset(h->dbg, 0, sizeof(int32_t) * (size_t)max_B) != cudaSuccess) {
+        cudaMemset(h->dbg, 0, sizeof(int32_t) * (size_t)max_B) != cudaSuccess ||
+        cudaMemset(h->arrive, 0, sizeof(int32_t) * kAttnMaxCtas) != cudaSuccess) {
         cudaGetLastError();
         cudaFree(h->ws);
         delete h;
@@ -663,6 +666,251 @@ int spec_kv_commit(spec_handle h, const void *src_k, const void *src_v, int src_
         return SPEC_ERR_CUDA;
 #endif
     return timed(h, SPEC_K_KV_COMMIT, st, [&] { return launch_kv_commit(kp, vec, st); });
+}
+
+// ---- the tree step over a 4-bit cache --------------------------------------------------------
+
+namespace {
+
+bool float_type(int dtype) {
+    return dtype == SPEC_F32 || dtype == SPEC_BF16 || dtype == SPEC_F16;
+}
+
+// Rows of H heads x D elements, `stride` elements from token to token.
+bool rows_ok(const void *p, int64_t stride, int H, int D, int dtype) {
+    return p && aligned(p, dtype == SPEC_F32 ? 4 : 2) && stride >= (int64_t)H * D &&
+           stride <= (int64_t(1) << 32);
+}
+
+bool null_or_aligned(const void *p, size_t a) { return !p || aligned(p, a); }
+
+// The parts of a 4-bit cache that the host can check; a batch of none needs no block table.
+int check_cache(const spec_fp4_cache *c, int B) {
+    if (!c) return SPEC_ERR_ARG;
+    if (c->H < 1 || c->D < 16 || c->D % 16 != 0 || c->D > 512) return SPEC_ERR_ARG;
+    if (c->layout != SPEC_KV_NHD && c->layout != SPEC_KV_HND) return SPEC_ERR_ARG;
+    if (c->block_size < 1 || c->num_blocks < 1 || c->max_blocks < 1) return SPEC_ERR_ARG;
+    if (c->num_blocks > INT32_MAX || (int64_t)c->block_size * c->H > INT32_MAX ||
+        c->num_blocks > int64_t(UINT32_MAX) / ((int64_t)c->block_size * c->H) ||
+        (int64_t)c->max_blocks * c->block_size > INT32_MAX)
+        return SPEC_ERR_ARG;
+    if (!c->k || !c->v || !c->k_sf || !c->v_sf || (B > 0 && !c->block_table))
+        return SPEC_ERR_ARG;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_sf, 16) ||
+        !aligned(c->v_sf, 16) || !null_or_aligned(c->block_table, 4) ||
+        !null_or_aligned(c->k_scale, 4) || !null_or_aligned(c->v_scale, 4))
+        return SPEC_ERR_ARG;
+    return SPEC_OK;
+}
+
+}  // namespace
+
+int spec_qk_norm_rope(spec_handle h, const void *q, int64_t q_stride, const void *k,
+                      int64_t k_stride, int dtype, int B, int N, int Hq, int Hkv, int D,
+                      const void *q_weight, const void *k_weight, float eps,
+                      const float *inv_freq, int rot, int style, const int32_t *seq_pos,
+                      const int32_t *depth, void *q_out, int64_t q_out_stride, void *k_out,
+                      int64_t k_out_stride, void *stream) {
+    SPEC_RANGE("spec_qk_norm_rope");
+    if (!h) return SPEC_ERR_ARG;
+    if (B < 0 || B > h->max_B || N < 1 || (int64_t)B * N > INT32_MAX) return SPEC_ERR_ARG;
+    if (!float_type(dtype) || Hq < 1 || Hkv < 1 || D < 1 || D > 1024 || Hq > (1 << 20) ||
+        Hkv > (1 << 20))
+        return SPEC_ERR_ARG;
+    if (rot < 0 || rot > D || rot % 2 != 0) return SPEC_ERR_ARG;
+    if (style != SPEC_ROPE_HALVES && style != SPEC_ROPE_PAIRS) return SPEC_ERR_ARG;
+    if (!std::isfinite(eps) || eps < 0.f) return SPEC_ERR_ARG;
+    if ((q_weight == nullptr) != (k_weight == nullptr)) return SPEC_ERR_ARG;
+    if (B == 0) return SPEC_OK;
+    if (!rows_ok(q, q_stride, Hq, D, dtype) || !rows_ok(k, k_stride, Hkv, D, dtype) ||
+        !rows_ok(q_out, q_out_stride, Hq, D, dtype) ||
+        !rows_ok(k_out, k_out_stride, Hkv, D, dtype))
+        return SPEC_ERR_ARG;
+    if ((q_out == q && q_out_stride != q_stride) || (k_out == k && k_out_stride != k_stride))
+        return SPEC_ERR_ARG;
+    const size_t e = dtype == SPEC_F32 ? 4 : 2;
+    if (!null_or_aligned(q_weight, e) || !null_or_aligned(k_weight, e)) return SPEC_ERR_ARG;
+    if ((rot > 0 && !inv_freq) || !null_or_aligned(inv_freq, 4) || !seq_pos ||
+        !aligned(seq_pos, 4) || !null_or_aligned(depth, 4))
+        return SPEC_ERR_ARG;
+    DeviceScope ds(h->device);
+    if (!ds.ok()) return SPEC_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    QkRopeParams p;
+    p.x[0] = q;
+    p.x[1] = k;
+    p.stride[0] = q_stride;
+    p.stride[1] = k_stride;
+    p.y[0] = q_out;
+    p.y[1] = k_out;
+    p.ystride[0] = q_out_stride;
+    p.ystride[1] = k_out_stride;
+    p.w[0] = q_weight;
+    p.w[1] = k_weight;
+    p.H[0] = Hq;
+    p.H[1] = Hkv;
+    p.dtype = dtype;
+    p.tokens = (int64_t)B * N;
+    p.N = N;
+    p.D = D;
+    p.rot = rot;
+    p.pairs = style == SPEC_ROPE_PAIRS;
+    p.eps = eps;
+    p.inv_freq = inv_freq;
+    p.seq_pos = seq_pos;
+    p.depth = depth;
+    p.sms = h->sms;
+    return timed(h, SPEC_K_QK_ROPE, st, [&] { return launch_qk_rope(p, st); });
+}
+
+int spec_kv_commit_fp4(spec_handle h, const void *src_k, int64_t k_stride, const void *src_v,
+                       int64_t v_stride, int src_dtype, int B, int N,
+                       const spec_fp4_cache *cache, const int32_t *kv_commit,
+                       const int32_t *accept_len, const int32_t *seq_pos,
+                       int32_t *commit_status, void *stream) {
+    SPEC_RANGE("spec_kv_commit_fp4");
+    if (!h) return SPEC_ERR_ARG;
+    const int rc = check_cache(cache, B);
+    if (rc != SPEC_OK) return rc;
+    if (B < 0 || B > h->max_B || N < 1 || (int64_t)B * N > INT32_MAX) return SPEC_ERR_ARG;
+    if (kv_commit && (N > h->max_N || N > kMaxN || !accept_len)) return SPEC_ERR_ARG;
+    if (!float_type(src_dtype)) return SPEC_ERR_ARG;
+    if (B == 0) return SPEC_OK;
+    if (!rows_ok(src_k, k_stride, cache->H, cache->D, src_dtype) ||
+        !rows_ok(src_v, v_stride, cache->H, cache->D, src_dtype) || !seq_pos)
+        return SPEC_ERR_ARG;
+    if (!null_or_aligned(kv_commit, 4) || !null_or_aligned(accept_len, 4) ||
+        !aligned(seq_pos, 4) || !null_or_aligned(commit_status, 4))
+        return SPEC_ERR_ARG;
+    DeviceScope ds(h->device);
+    if (!ds.ok()) return SPEC_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    KvFp4Params p = {};
+    p.cache = *cache;
+    p.src[0] = src_k;
+    p.src[1] = src_v;
+    p.stride[0] = k_stride;
+    p.stride[1] = v_stride;
+    p.dtype = src_dtype;
+    p.B = B;
+    p.N = N;
+    p.kv_commit = kv_commit;
+    p.last = accept_len;
+    p.pos = seq_pos;
+    p.status = commit_status;
+    p.sms = h->sms;
+    return timed(h, SPEC_K_KV_COMMIT_FP4, st, [&] { return launch_kv_commit_fp4(p, st); });
+}
+
+int spec_kv_load_fp4(spec_handle h, const spec_fp4_cache *cache, int B, const int32_t *start,
+                     const int32_t *count, int64_t max_len, void *out_k, void *out_v,
+                     int out_dtype, int32_t *status, void *stream) {
+    SPEC_RANGE("spec_kv_load_fp4");
+    if (!h) return SPEC_ERR_ARG;
+    const int rc = check_cache(cache, B);
+    if (rc != SPEC_OK) return rc;
+    if (B < 0 || B > h->max_B || max_len < 0 || max_len > INT32_MAX) return SPEC_ERR_ARG;
+    if (!float_type(out_dtype)) return SPEC_ERR_ARG;
+    if (B == 0) return SPEC_OK;
+    const size_t e = out_dtype == SPEC_F32 ? 4 : 2;
+    if (!start || !count || !aligned(start, 4) || !aligned(count, 4) ||
+        !null_or_aligned(status, 4))
+        return SPEC_ERR_ARG;
+    if (max_len > 0 && (!out_k || !out_v || !aligned(out_k, e) || !aligned(out_v, e)))
+        return SPEC_ERR_ARG;
+    DeviceScope ds(h->device);
+    if (!ds.ok()) return SPEC_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    KvFp4Params p = {};
+    p.cache = *cache;
+    p.out[0] = out_k;
+    p.out[1] = out_v;
+    p.dtype = out_dtype;
+    p.B = B;
+    p.max_len = max_len;
+    p.last = count;
+    p.pos = start;
+    p.status = status;
+    p.sms = h->sms;
+    return timed(h, SPEC_K_KV_LOAD_FP4, st, [&] { return launch_kv_load_fp4(p, st); });
+}
+
+namespace {
+
+// Sizes of a tree attention call.
+int check_attention(spec_handle h, int B, int N, int Hq, int H, int D) {
+    if (!h) return SPEC_ERR_ARG;
+    if (B < 0 || B > h->max_B || N < 1 || N > h->max_N || N > kMaxN) return SPEC_ERR_ARG;
+    if (H < 1 || Hq < H || Hq % H != 0 || Hq > (1 << 16)) return SPEC_ERR_ARG;
+    return D == 64 || D == 128 || D == 256 ? SPEC_OK : SPEC_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+int spec_tree_attention_workspace(spec_handle h, int B, int N, int Hq, int H, int D,
+                                  int64_t *bytes) {
+    SPEC_RANGE("spec_tree_attention_workspace");
+    const int rc = check_attention(h, B, N, Hq, H, D);
+    if (rc != SPEC_OK) return rc;
+    if (!bytes) return SPEC_ERR_ARG;
+    *bytes = tree_attn_workspace(B, N, Hq / H, H, D, h->sms);
+    return SPEC_OK;
+}
+
+int spec_tree_attention_fp4(spec_handle h, const void *q, int64_t q_stride, const void *k,
+                            int64_t k_stride, const void *v, int64_t v_stride, int dtype, int B,
+                            int N, int Hq, const spec_fp4_cache *cache, const int32_t *ctx_len,
+                            const uint64_t *anc_mask, float scale, void *out, float *lse,
+                            int32_t *status, void *workspace, int64_t workspace_bytes,
+                            void *stream) {
+    SPEC_RANGE("spec_tree_attention_fp4");
+    if (!h) return SPEC_ERR_ARG;
+    int rc = check_cache(cache, B);
+    if (rc != SPEC_OK) return rc;
+    rc = check_attention(h, B, N, Hq, cache->H, cache->D);
+    if (rc != SPEC_OK) return rc;
+    if (dtype != SPEC_BF16 && dtype != SPEC_F16) return SPEC_ERR_ARG;
+    if (!std::isfinite(scale) || !(scale > 0.f)) return SPEC_ERR_ARG;
+    if (B == 0) return SPEC_OK;
+    const int H = cache->H, D = cache->D;
+    if (!rows_ok(q, q_stride, Hq, D, dtype) || !rows_ok(k, k_stride, H, D, dtype) ||
+        !rows_ok(v, v_stride, H, D, dtype) || !ctx_len || !anc_mask || !out)
+        return SPEC_ERR_ARG;
+    if (!aligned(ctx_len, 4) || !aligned(anc_mask, 8) || !aligned(out, 2) ||
+        !null_or_aligned(lse, 4) || !null_or_aligned(status, 4))
+        return SPEC_ERR_ARG;
+    if (!workspace || !aligned(workspace, 256) ||
+        workspace_bytes < tree_attn_workspace(B, N, Hq / H, H, D, h->sms))
+        return SPEC_ERR_ARG;
+    DeviceScope ds(h->device);
+    if (!ds.ok()) return SPEC_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    TreeAttnParams p;
+    p.cache = *cache;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.dtype = dtype;
+    p.B = B;
+    p.N = N;
+    p.Hq = Hq;
+    p.G = Hq / H;
+    p.ctx_len = ctx_len;
+    p.mask = anc_mask;
+    p.scale = scale;
+    p.out = out;
+    p.lse = lse;
+    p.status = status;
+    p.ws = static_cast<float *>(workspace);
+    p.arrive = h->arrive;
+    p.sms = h->sms;
+    // a page found outside the cache raises the request's status from zero
+    if (status && cudaMemsetAsync(status, 0, sizeof(int32_t) * (size_t)B, st) != cudaSuccess)
+        return SPEC_ERR_CUDA;
+    return timed(h, SPEC_K_TREE_ATTN, st, [&] { return launch_tree_attn(p, st); });
 }
 
 int spec_row_stats(spec_handle h, const void *logits, int dtype, int rows, int N, int64_t V,

@@ -238,6 +238,66 @@ struct KvCommitParams {
 
 cudaError_t launch_kv_commit(const KvCommitParams &p, bool vec, cudaStream_t st);
 
+// Head norm and rotation of queries and keys (see spec_qk_norm_rope).
+struct QkRopeParams {
+    const void *x[2];             // q, k rows
+    int64_t stride[2];            // elements between tokens
+    void *y[2];
+    int64_t ystride[2];
+    const void *w[2];             // norm weights, or null
+    int H[2];
+    int dtype;                    // 0 f32, 1 bf16, 2 f16
+    int64_t tokens;               // B * N
+    int N, D, rot, pairs;
+    float eps;
+    const float *inv_freq;
+    const int32_t *seq_pos, *depth;
+    int sms;
+};
+
+cudaError_t launch_qk_rope(const QkRopeParams &p, cudaStream_t st);
+
+// K/V rows into the 4-bit cache, and back (see spec_kv_commit_fp4, spec_kv_load_fp4).
+struct KvFp4Params {
+    spec_fp4_cache cache;
+    const void *src[2];           // commit: K and V rows
+    int64_t stride[2];            // ... elements between tokens
+    void *out[2];                 // load: K and V rows, contiguous
+    int dtype;                    // of the rows: 0 f32, 1 bf16, 2 f16
+    int B, N;
+    int64_t max_len;              // load
+    const int32_t *kv_commit, *last, *pos;   // commit: accept_len; load: count; first positions
+    int32_t *status;
+    int sms;
+};
+
+cudaError_t launch_kv_commit_fp4(const KvFp4Params &p, cudaStream_t st);
+cudaError_t launch_kv_load_fp4(const KvFp4Params &p, cudaStream_t st);
+
+// Tree attention over the 4-bit cache (see spec_tree_attention_fp4).
+struct TreeAttnParams {
+    spec_fp4_cache cache;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    int dtype;                    // 1 bf16, 2 f16
+    int B, N, Hq, G;              // G = Hq / cache.H
+    const int32_t *ctx_len;
+    const uint64_t *mask;
+    float scale;
+    void *out;
+    float *lse;
+    int32_t *status;
+    float *ws;                    // partial results (see tree_attn_plan)
+    int32_t *arrive;              // arrivals of split items [kAttnMaxCtas], zero between calls
+    int sms;
+};
+
+constexpr int kAttnMaxCtas = 4096;   // CTAs of an attention launch, at most
+
+// Bytes of partial results that a launch of these sizes may write.
+int64_t tree_attn_workspace(int B, int N, int G, int H, int D, int sms);
+cudaError_t launch_tree_attn(const TreeAttnParams &p, cudaStream_t st);
+
 // Adaptive node-budget update (see spec_budget_update).
 struct BudgetParams {
     spec_budget_params prm;
