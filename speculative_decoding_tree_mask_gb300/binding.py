@@ -67,10 +67,13 @@ class SpecError(RuntimeError):
 def load() -> ctypes.CDLL:
     """Open the CUDA library (raises if it is missing)."""
     global _lib
+    lib = _lib
+    if lib is not None:
+        return lib
     with _lock:
         if _lib is None:
             _lib = _open(LIBRARY)
-    return _lib
+        return _lib
 
 
 @contextlib.contextmanager
@@ -204,6 +207,8 @@ class Handle:
         self.ptr = h
         self.device = int(device)
         self.max_B, self.max_N, self.max_V = int(max_B), int(max_N), int(max_V)
+        self.attention_sizes = None     # sizes that attention_bytes (a workspace) belongs to
+        self.attention_bytes = 0
 
     def close(self):
         if self.ptr is not None and self.ptr.value:
@@ -359,6 +364,8 @@ def spec_kv_commit(h: Handle, src_k, src_v, kv_commit, accept_len, cache_k, cach
 
 
 # ---- the tree step over a 4-bit cache ----------------------------------------------------------
+# A small call of these is shorter on the GPU than its argument checks once were on the host, so
+# the checks compare whole shapes and integer device indices, and find words only on failure.
 
 class Fp4Cache:
     """A 4-bit paged K/V cache (spec_fp4_cache): uint8 codes k, v [num_blocks, block_size, H,
@@ -367,21 +374,25 @@ class Fp4Cache:
     (None = 1). Holds the tensors; block tables come with each call."""
 
     def __init__(self, k, v, k_sf, v_sf, layout: int = SPEC_KV_NHD, k_scale=None, v_scale=None):
-        if layout not in (SPEC_KV_NHD, SPEC_KV_HND):
+        if layout != SPEC_KV_NHD and layout != SPEC_KV_HND:
             raise ValueError("layout must be SPEC_KV_NHD or SPEC_KV_HND")
-        if k.dim() != 4 or any(t.dtype != torch.uint8 for t in (k, v, k_sf, v_sf)):
+        u8 = torch.uint8
+        if k.dtype != u8 or v.dtype != u8 or k_sf.dtype != u8 or v_sf.dtype != u8 or k.dim() != 4:
             raise TypeError("k, v, k_sf and v_sf must be 4-dimensional uint8 tensors")
-        if k.shape != v.shape or k_sf.shape != v_sf.shape or \
-                k.shape[:3] != k_sf.shape[:3] or k.shape[3] != 8 * k_sf.shape[3]:
+        shape = k.shape
+        if shape != v.shape or k_sf.shape != v_sf.shape or \
+                shape != (*k_sf.shape[:-1], 8 * k_sf.shape[-1]):
             raise ValueError("k, v: [..., D/2], k_sf, v_sf: [..., D/16] of one shape")
         for s in (k_scale, v_scale):
             if s is not None and (s.dtype != torch.float32 or s.numel() != 1):
                 raise TypeError("tensor scales must be float32 of one element")
         self.k, self.v, self.k_sf, self.v_sf = k, v, k_sf, v_sf
         self.k_scale, self.v_scale, self.layout = k_scale, v_scale, int(layout)
-        nhd = layout == SPEC_KV_NHD
-        self.num_blocks, self.D = k.shape[0], 2 * k.shape[3]
-        self.block_size, self.H = (k.shape[1], k.shape[2]) if nhd else (k.shape[2], k.shape[1])
+        if layout == SPEC_KV_NHD:
+            self.num_blocks, self.block_size, self.H, half = shape
+        else:
+            self.num_blocks, self.H, self.block_size, half = shape
+        self.D = 2 * half
 
     @classmethod
     def empty(cls, num_blocks: int, block_size: int, H: int, D: int, device,
@@ -395,41 +406,78 @@ class Fp4Cache:
                for n in (D // 2, D // 2, D // 16, D // 16)]
         return cls(*one, layout, k_scale, v_scale)
 
-    def tensors(self):
-        return (self.k, self.v, self.k_sf, self.v_sf, self.k_scale, self.v_scale)
-
-    def struct(self, block_table) -> Fp4CacheStruct:
-        """The library's view of the cache with the block table int32 [B, max_blocks]."""
-        if block_table.dim() != 2:
-            raise ValueError("block_table must be [B, max_blocks]")
+    def struct(self, block_table, B: int, device: int) -> Fp4CacheStruct:
+        """The library's view of the cache on GPU `device`, with the block table int32
+        [B, max_blocks]."""
+        if block_table.dtype != torch.int32:
+            raise TypeError("block_table must be int32")
+        if block_table.dim() != 2 or block_table.shape[0] != B:
+            raise ValueError(f"block_table must be [{B}, max_blocks]")
         return Fp4CacheStruct(
-            *(_ptr(t) for t in self.tensors()), self.num_blocks, self.layout, self.block_size,
-            self.H, self.D, _ptr(_i32(block_table, "block_table")), block_table.shape[1])
+            _addr(self.k, device), _addr(self.v, device), _addr(self.k_sf, device),
+            _addr(self.v_sf, device), _addr(self.k_scale, device), _addr(self.v_scale, device),
+            self.num_blocks, self.layout, self.block_size, self.H, self.D,
+            _addr(block_table, device), block_table.shape[1])
 
 
-def _rows(t, name):
+def _addr(t, device: int):
+    """Address of a contiguous tensor on GPU `device` (None for None)."""
+    if t is None:
+        return None
+    if t.get_device() != device:
+        raise ValueError(f"a tensor is on {t.device}, the call runs on cuda:{device}")
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to the library must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, device: int, name: str):
     """(address, token stride) of rows [B, N, H, D], contiguous or columns of a wider matrix."""
-    if not t.is_cuda:
-        raise ValueError("tensors passed to the library must be CUDA tensors")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{device}")
     B, N, H, D = t.shape
+    if t.is_contiguous():
+        return t.data_ptr(), H * D
     sb, sn, sh, sd = t.stride()
-    token = sn if N > 1 else (sb if B > 1 else H * D)
-    if (D > 1 and sd != 1) or (H > 1 and sh != D) or (B > 1 and N > 1 and sb != N * sn) or \
+    token = sn if N > 1 else sb if B > 1 else H * D
+    if (sd != 1 and D > 1) or (sh != D and H > 1) or (B > 1 and N > 1 and sb != N * sn) or \
             token < H * D:
         raise ValueError(f"{name}: heads and elements must be contiguous, and tokens evenly "
                          "spaced")
-    return ctypes.c_void_p(t.data_ptr()), token
+    return t.data_ptr(), token
 
 
-def _shape(t, want, name):
-    if t is not None and tuple(t.shape) != tuple(want):
-        raise ValueError(f"{name} must be {list(want)}, got {list(t.shape)}")
-    return t
+def _refuse(where: str, **wanted):
+    """Raises for the first tensor that is not what `wanted` gives as name=(tensor, shape,
+    dtype); a tensor may be None, a dtype too (any)."""
+    for name, (t, shape, dtype) in wanted.items():
+        if t is None:
+            continue
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{where}: {name} must be {list(shape)}, got {list(t.shape)}")
 
 
-def _same_dtype(tensors, dtype, where):
-    if any(t is not None and t.dtype != dtype for t in tensors):
-        raise TypeError(f"{where}: row tensors must share one dtype")
+def _bad(t, shape, dtype) -> bool:
+    return t is not None and (t.dtype != dtype or t.shape != shape)
+
+
+def _raw_stream(stream, device: int):
+    """The cudaStream_t of `stream`, or of the device's current stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream
+
+
+_ROW_CODES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
+
+
+def _row_code(dtype, where: str) -> int:
+    code = _ROW_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"{where}: rows must be float32, bfloat16 or float16, got {dtype}")
+    return code
 
 
 def spec_qk_norm_rope(h: Handle, q, k, inv_freq, seq_pos, depth, q_out, k_out, q_weight=None,
@@ -439,28 +487,30 @@ def spec_qk_norm_rope(h: Handle, q, k, inv_freq, seq_pos, depth, q_out, k_out, q
     pass. q [B, N, Hq, D], k [B, N, Hkv, D]; inv_freq float32 [rot/2] (None: no rotation);
     depth int32 [B, N] or None (n itself); weights [D] or None (no norm). q_out, k_out may be
     q and k."""
-    where = "spec_qk_norm_rope"
-    B, N, Hq, D = q.shape
+    where, i32, dt = "spec_qk_norm_rope", torch.int32, q.dtype
+    qs = q.shape
+    B, N, Hq, D = qs
     Hkv = k.shape[2]
-    _shape(k, (B, N, Hkv, D), "k")
-    _shape(q_out, q.shape, "q_out")
-    _shape(k_out, k.shape, "k_out")
-    _same_device((q, k, inv_freq, seq_pos, depth, q_out, k_out, q_weight, k_weight), _hdev(h),
-                 where)
-    _same_dtype((k, q_out, k_out, q_weight, k_weight), q.dtype, where)
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        _shape(w, (D,), name)
-    if inv_freq is not None and inv_freq.dtype != torch.float32:
-        raise TypeError("inv_freq must be float32")
-    _shape(_i32(seq_pos, "seq_pos"), (B,), "seq_pos")
-    if depth is not None:
-        _shape(_i32(depth, "depth"), (B, N), "depth")
-    (qp, qs), (kp, ks), (qo, qos), (ko, kos) = (
-        _rows(t, n) for t, n in ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out")))
+    ks = (B, N, Hkv, D)
+    if _bad(k, ks, dt) or _bad(q_out, qs, dt) or _bad(k_out, ks, dt) or \
+            _bad(q_weight, (D,), dt) or _bad(k_weight, (D,), dt) or \
+            _bad(seq_pos, (B,), i32) or _bad(depth, (B, N), i32) or \
+            (inv_freq is not None and inv_freq.dtype != torch.float32):
+        _refuse(where, k=(k, ks, dt), q_out=(q_out, qs, dt), k_out=(k_out, ks, dt),
+                q_weight=(q_weight, (D,), dt), k_weight=(k_weight, (D,), dt),
+                seq_pos=(seq_pos, (B,), i32), depth=(depth, (B, N), i32),
+                inv_freq=(inv_freq, inv_freq.shape if inv_freq is not None else (),
+                          torch.float32))
+    dev = h.device
+    qa, qt = _rows(q, dev, "q")
+    ka, kt = _rows(k, dev, "k")
+    qo, qot = _rows(q_out, dev, "q_out")
+    ko, kot = _rows(k_out, dev, "k_out")
     _check(load().spec_qk_norm_rope(
-        h.ptr, qp, qs, kp, ks, _kv_dtype(q), B, N, Hq, Hkv, D, _ptr(q_weight), _ptr(k_weight),
-        float(eps), _ptr(inv_freq), 0 if inv_freq is None else 2 * inv_freq.numel(), int(style),
-        _ptr(seq_pos), _ptr(depth), qo, qos, ko, kos, _stream(stream, q.device)), where)
+        h.ptr, qa, qt, ka, kt, _row_code(dt, where), B, N, Hq, Hkv, D, _addr(q_weight, dev),
+        _addr(k_weight, dev), eps, _addr(inv_freq, dev),
+        0 if inv_freq is None else 2 * inv_freq.numel(), style, _addr(seq_pos, dev),
+        _addr(depth, dev), qo, qot, ko, kot, _raw_stream(stream, dev)), where)
 
 
 def spec_kv_commit_fp4(h: Handle, src_k, src_v, cache: Fp4Cache, block_table, seq_pos,
@@ -468,45 +518,39 @@ def spec_kv_commit_fp4(h: Handle, src_k, src_v, cache: Fp4Cache, block_table, se
     """K/V rows [B, N, H, D] into the 4-bit cache: the root and the accepted nodes of a verify
     call (kv_commit, accept_len), or rows 0..accept_len[b] in order (kv_commit None; all N
     without accept_len), at positions seq_pos[b] + j."""
-    where = "spec_kv_commit_fp4"
-    B, N, H, D = src_k.shape
-    _shape(src_k, (B, N, cache.H, cache.D), "src_k")
-    _shape(src_v, src_k.shape, "src_v")
-    _same_device((src_k, src_v, block_table, seq_pos, kv_commit, accept_len, commit_status,
-                  *cache.tensors()), _hdev(h), where)
-    _same_dtype((src_v,), src_k.dtype, where)
-    _shape(block_table, (B, block_table.shape[-1]), "block_table")
-    for t, want, name in ((seq_pos, (B,), "seq_pos"), (kv_commit, (B, N), "kv_commit"),
-                          (accept_len, (B,), "accept_len"),
-                          (commit_status, (B,), "commit_status")):
-        if t is not None:
-            _shape(_i32(t, name), want, name)
-    (kp, ks), (vp, vs) = _rows(src_k, "src_k"), _rows(src_v, "src_v")
+    where, i32, dt = "spec_kv_commit_fp4", torch.int32, src_k.dtype
+    B, N = src_k.shape[:2]
+    rows, one, dev = (B, N, cache.H, cache.D), (B,), h.device
+    if _bad(src_k, rows, dt) or _bad(src_v, rows, dt) or _bad(seq_pos, one, i32) or \
+            _bad(kv_commit, (B, N), i32) or _bad(accept_len, one, i32) or \
+            _bad(commit_status, one, i32):
+        _refuse(where, src_k=(src_k, rows, dt), src_v=(src_v, rows, dt),
+                seq_pos=(seq_pos, one, i32), kv_commit=(kv_commit, (B, N), i32),
+                accept_len=(accept_len, one, i32), commit_status=(commit_status, one, i32))
+    view = cache.struct(block_table, B, dev)
+    ka, kt = _rows(src_k, dev, "src_k")
+    va, vt = _rows(src_v, dev, "src_v")
     _check(load().spec_kv_commit_fp4(
-        h.ptr, kp, ks, vp, vs, _kv_dtype(src_k), B, N, ctypes.byref(cache.struct(block_table)),
-        _ptr(kv_commit), _ptr(accept_len), _ptr(seq_pos), _ptr(commit_status),
-        _stream(stream, src_k.device)), where)
+        h.ptr, ka, kt, va, vt, _row_code(dt, where), B, N, view, _addr(kv_commit, dev),
+        _addr(accept_len, dev), _addr(seq_pos, dev), _addr(commit_status, dev),
+        _raw_stream(stream, dev)), where)
 
 
 def spec_kv_load_fp4(h: Handle, cache: Fp4Cache, block_table, start, count, out_k, out_v,
                      status=None, stream=None):
     """Positions start[b] .. start[b] + count[b] - 1 of the 4-bit cache into out_k, out_v
     [B, max_len, H, D]; rows at and after count[b] become zero."""
-    where = "spec_kv_load_fp4"
-    B, max_len = out_k.shape[0], out_k.shape[1]
-    _shape(out_k, (B, max_len, cache.H, cache.D), "out_k")
-    _shape(out_v, out_k.shape, "out_v")
-    _same_device((out_k, out_v, block_table, start, count, status, *cache.tensors()), _hdev(h),
-                 where)
-    _same_dtype((out_v,), out_k.dtype, where)
-    _shape(block_table, (B, block_table.shape[-1]), "block_table")
-    for t, name in ((start, "start"), (count, "count"), (status, "status")):
-        if t is not None:
-            _shape(_i32(t, name), (B,), name)
+    where, i32, dt = "spec_kv_load_fp4", torch.int32, out_k.dtype
+    B, max_len = out_k.shape[:2]
+    rows, one, dev = (B, max_len, cache.H, cache.D), (B,), h.device
+    if _bad(out_k, rows, dt) or _bad(out_v, rows, dt) or _bad(start, one, i32) or \
+            _bad(count, one, i32) or _bad(status, one, i32):
+        _refuse(where, out_k=(out_k, rows, dt), out_v=(out_v, rows, dt),
+                start=(start, one, i32), count=(count, one, i32), status=(status, one, i32))
     _check(load().spec_kv_load_fp4(
-        h.ptr, ctypes.byref(cache.struct(block_table)), B, _ptr(start), _ptr(count), max_len,
-        _ptr(out_k), _ptr(out_v), _kv_dtype(out_k), _ptr(status),
-        _stream(stream, out_k.device)), where)
+        h.ptr, cache.struct(block_table, B, dev), B, _addr(start, dev), _addr(count, dev),
+        max_len, _addr(out_k, dev), _addr(out_v, dev), _row_code(dt, where), _addr(status, dev),
+        _raw_stream(stream, dev)), where)
 
 
 def spec_tree_attention_workspace(h: Handle, B: int, N: int, Hq: int, H: int, D: int) -> int:
@@ -523,31 +567,25 @@ def spec_tree_attention_fp4(h: Handle, q, k, v, cache: Fp4Cache, block_table, ct
     """Attention of the tree's nodes q [B, N, Hq, D] over positions 0..ctx_len[b]-1 of the
     4-bit cache and over the nodes k, v [B, N, H, D] that anc_mask (int64 [B, N] bit patterns,
     build_tree_mask) lets each see."""
-    where = "spec_tree_attention_fp4"
+    where, i32, dt = "spec_tree_attention_fp4", torch.int32, q.dtype
     B, N, Hq, D = q.shape
-    _shape(q, (B, N, Hq, cache.D), "q")
-    _shape(k, (B, N, cache.H, D), "k")
-    _shape(v, k.shape, "v")
-    _shape(out, q.shape, "out")
-    _same_device((q, k, v, block_table, ctx_len, anc_mask, out, workspace, lse, status,
-                  *cache.tensors()), _hdev(h), where)
-    _same_dtype((k, v, out), q.dtype, where)
-    _shape(block_table, (B, block_table.shape[-1]), "block_table")
-    _shape(_i32(ctx_len, "ctx_len"), (B,), "ctx_len")
-    if anc_mask.dtype not in (torch.int64, getattr(torch, "uint64", torch.int64)):
-        raise TypeError("anc_mask must be a 64-bit integer tensor")
-    _shape(anc_mask, (B, N), "anc_mask")
-    if lse is not None and lse.dtype != torch.float32:
-        raise TypeError("lse must be float32")
-    _shape(lse, (B, N, Hq), "lse")
-    if status is not None:
-        _shape(_i32(status, "status"), (B,), "status")
-    (qp, qs), (kp, ks), (vp, vs) = (_rows(t, n) for t, n in ((q, "q"), (k, "k"), (v, "v")))
+    full, rows, one, dev = (B, N, Hq, cache.D), (B, N, cache.H, cache.D), (B,), h.device
+    bits = torch.int64 if anc_mask.dtype != getattr(torch, "uint64", None) else torch.uint64
+    if _bad(q, full, dt) or _bad(k, rows, dt) or _bad(v, rows, dt) or _bad(out, full, dt) or \
+            _bad(ctx_len, one, i32) or _bad(anc_mask, (B, N), bits) or \
+            _bad(lse, (B, N, Hq), torch.float32) or _bad(status, one, i32):
+        _refuse(where, q=(q, full, dt), k=(k, rows, dt), v=(v, rows, dt), out=(out, full, dt),
+                ctx_len=(ctx_len, one, i32), anc_mask=(anc_mask, (B, N), bits),
+                lse=(lse, (B, N, Hq), torch.float32), status=(status, one, i32))
+    view = cache.struct(block_table, B, dev)
+    qa, qt = _rows(q, dev, "q")
+    ka, kt = _rows(k, dev, "k")
+    va, vt = _rows(v, dev, "v")
     _check(load().spec_tree_attention_fp4(
-        h.ptr, qp, qs, kp, ks, vp, vs, _kv_dtype(q), B, N, Hq,
-        ctypes.byref(cache.struct(block_table)), _ptr(ctx_len), _ptr(anc_mask), float(scale),
-        _ptr(out), _ptr(lse), _ptr(status), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream, q.device)), where)
+        h.ptr, qa, qt, ka, kt, va, vt, _row_code(dt, where), B, N, Hq, view, _addr(ctx_len, dev),
+        _addr(anc_mask, dev), scale, _addr(out, dev), _addr(lse, dev), _addr(status, dev),
+        _addr(workspace, dev), workspace.numel() * workspace.element_size(),
+        _raw_stream(stream, dev)), where)
 
 
 def spec_set_node_budget(h: Handle, n_active):
@@ -660,7 +698,7 @@ def build_tree_mask(h: Handle, parent, stream=None) -> dict:
 def qk_norm_rope(h: Handle, q, k, inv_freq, seq_pos, depth=None, q_weight=None, k_weight=None,
                  eps: float = 1e-6, style: int = SPEC_ROPE_HALVES, stream=None):
     """-> new contiguous (q, k), normalised and rotated (see spec_qk_norm_rope)."""
-    qo, ko = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+    qo, ko = q.new_empty(q.shape), k.new_empty(k.shape)
     spec_qk_norm_rope(h, q, k, inv_freq, seq_pos, depth, qo, ko, q_weight, k_weight, eps, style,
                       stream)
     return qo, ko
@@ -670,7 +708,7 @@ def kv_load_fp4(h: Handle, cache: Fp4Cache, block_table, start, count, max_len: 
                 dtype=torch.bfloat16, stream=None):
     """-> (k, v) rows [B, max_len, H, D] of ``dtype`` (see spec_kv_load_fp4)."""
     shape = (block_table.shape[0], int(max_len), cache.H, cache.D)
-    k, v = (torch.empty(shape, dtype=dtype, device=cache.k.device) for _ in range(2))
+    k, v = cache.k.new_empty(shape, dtype=dtype), cache.k.new_empty(shape, dtype=dtype)
     spec_kv_load_fp4(h, cache, block_table, start, count, k, v, stream=stream)
     return k, v
 
@@ -679,14 +717,17 @@ def tree_attention_fp4(h: Handle, q, k, v, cache: Fp4Cache, block_table, ctx_len
                        scale: float, workspace=None, stream=None):
     """-> (out [B, N, Hq, D], lse float32 [B, N, Hq]) (see spec_tree_attention_fp4). Without a
     workspace one is taken from torch's allocator for the call."""
-    B, N, Hq, D = q.shape
     if workspace is None:
-        size = spec_tree_attention_workspace(h, B, N, Hq, cache.H, D)
-        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+        B, N, Hq, D = q.shape
+        sizes = (B, N, Hq, cache.H, D)
+        if h.attention_sizes != sizes:      # the size depends on these alone
+            h.attention_bytes = spec_tree_attention_workspace(h, *sizes)
+            h.attention_sizes = sizes
+        workspace = q.new_empty(h.attention_bytes, dtype=torch.uint8)
         if stream is not None:
             workspace.record_stream(stream)
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
+    out = q.new_empty(q.shape)
+    lse = q.new_empty(q.shape[:3], dtype=torch.float32)
     spec_tree_attention_fp4(h, q, k, v, cache, block_table, ctx_len, anc_mask, scale, out,
                             workspace, lse, stream=stream)
     return out, lse
