@@ -206,6 +206,7 @@ class Handle:
                                        int(device)), "spec_verify_init")
         self.ptr = h
         self.device = int(device)
+        self.torch_device = torch.device("cuda", self.device)
         self.max_B, self.max_N, self.max_V = int(max_B), int(max_N), int(max_V)
         self.attention_sizes = None     # sizes that attention_bytes (a workspace) belongs to
         self.attention_bytes = 0
@@ -695,10 +696,14 @@ def build_tree_mask(h: Handle, parent, stream=None) -> dict:
     return out
 
 
+def _empty(shape, dtype, h: Handle):
+    return torch.empty(shape, dtype=dtype, device=h.torch_device)
+
+
 def qk_norm_rope(h: Handle, q, k, inv_freq, seq_pos, depth=None, q_weight=None, k_weight=None,
                  eps: float = 1e-6, style: int = SPEC_ROPE_HALVES, stream=None):
     """-> new contiguous (q, k), normalised and rotated (see spec_qk_norm_rope)."""
-    qo, ko = q.new_empty(q.shape), k.new_empty(k.shape)
+    qo, ko = _empty(q.shape, q.dtype, h), _empty(k.shape, k.dtype, h)
     spec_qk_norm_rope(h, q, k, inv_freq, seq_pos, depth, qo, ko, q_weight, k_weight, eps, style,
                       stream)
     return qo, ko
@@ -708,7 +713,7 @@ def kv_load_fp4(h: Handle, cache: Fp4Cache, block_table, start, count, max_len: 
                 dtype=torch.bfloat16, stream=None):
     """-> (k, v) rows [B, max_len, H, D] of ``dtype`` (see spec_kv_load_fp4)."""
     shape = (block_table.shape[0], int(max_len), cache.H, cache.D)
-    k, v = cache.k.new_empty(shape, dtype=dtype), cache.k.new_empty(shape, dtype=dtype)
+    k, v = _empty(shape, dtype, h), _empty(shape, dtype, h)
     spec_kv_load_fp4(h, cache, block_table, start, count, k, v, stream=stream)
     return k, v
 
@@ -723,11 +728,11 @@ def tree_attention_fp4(h: Handle, q, k, v, cache: Fp4Cache, block_table, ctx_len
         if h.attention_sizes != sizes:      # the size depends on these alone
             h.attention_bytes = spec_tree_attention_workspace(h, *sizes)
             h.attention_sizes = sizes
-        workspace = q.new_empty(h.attention_bytes, dtype=torch.uint8)
+        workspace = _empty((h.attention_bytes,), torch.uint8, h)
         if stream is not None:
             workspace.record_stream(stream)
-    out = q.new_empty(q.shape)
-    lse = q.new_empty(q.shape[:3], dtype=torch.float32)
+    out = _empty(q.shape, q.dtype, h)
+    lse = _empty(q.shape[:3], torch.float32, h)
     spec_tree_attention_fp4(h, q, k, v, cache, block_table, ctx_len, anc_mask, scale, out,
                             workspace, lse, stream=stream)
     return out, lse

@@ -853,7 +853,7 @@ int spec_tree_attention_workspace(spec_handle h, int B, int N, int Hq, int H, in
     const int rc = check_attention(h, B, N, Hq, H, D);
     if (rc != SPEC_OK) return rc;
     if (!bytes) return SPEC_ERR_ARG;
-    *bytes = tree_attn_workspace(B, N, Hq / H, H, D, h->sms);
+    *bytes = tree_attn_workspace(N * (Hq / H), D, h->sms);
     return SPEC_OK;
 }
 
@@ -880,7 +880,7 @@ int spec_tree_attention_fp4(spec_handle h, const void *q, int64_t q_stride, cons
         !null_or_aligned(lse, 4) || !null_or_aligned(status, 4))
         return SPEC_ERR_ARG;
     if (!workspace || !aligned(workspace, 256) ||
-        workspace_bytes < tree_attn_workspace(B, N, Hq / H, H, D, h->sms))
+        workspace_bytes < tree_attn_workspace(N * (Hq / H), D, h->sms))
         return SPEC_ERR_ARG;
     DeviceScope ds(h->device);
     if (!ds.ok()) return SPEC_ERR_CUDA;

@@ -287,16 +287,19 @@ struct TreeAttnParams {
     void *out;
     float *lse;
     int32_t *status;
-    float *ws;                    // partial results (see tree_attn_plan)
+    float *ws;                    // parts of items (see tree_attn.cuh)
     int32_t *arrive;              // arrivals of split items [kAttnMaxCtas], zero between calls
     int sms;
 };
 
 constexpr int kAttnMaxCtas = 4096;   // CTAs of an attention launch, at most
 
-// Bytes of partial results that a launch of these sizes may write.
-int64_t tree_attn_workspace(int B, int N, int G, int H, int D, int sms);
+// Bytes of parts that a launch with R rows of a K/V head may write.
+int64_t tree_attn_workspace(int R, int D, int sms);
 cudaError_t launch_tree_attn(const TreeAttnParams &p, cudaStream_t st);
+// On the tcgen05 tensor cores: row tiles of 128 that a CTA takes at a time, and the launch.
+int tree_attn_tc_tiles(int R);
+cudaError_t launch_tree_attn_tc(const TreeAttnParams &p, int grid, cudaStream_t st);
 
 // Adaptive node-budget update (see spec_budget_update).
 struct BudgetParams {

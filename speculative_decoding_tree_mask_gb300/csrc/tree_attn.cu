@@ -735,15 +735,20 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
     }
 }
 
-// Groups of 16 rows of an item, and CTAs an SM holds.
-int row_groups(int R, int D) { return R > 16 && D <= 128 ? 2 : 1; }
-int ctas_per_sm(int R, int D) { return row_groups(R, D) == 2 || D == 256 ? 2 : 3; }
-
-int grid_size(int B, int R, int H, int D, int sms) {
-    const int64_t cap = (int64_t)sms * ctas_per_sm(R, D);
-    (void)B;
-    (void)H;
-    return (int)(cap < kAttnMaxCtas ? cap : kAttnMaxCtas);
+// How a call is run: by this file's warps (groups of 16 rows of an item, CTAs an SM holds), or,
+// with more rows than two groups, on the tcgen05 tensor cores.
+struct Plan {
+    bool tc;
+    int groups, rows, grid;   // rows of an item
+};
+Plan plan(int R, int D, int sms) {
+    Plan p;
+    p.tc = R > 32 && D <= 128;
+    p.groups = R > 16 && D <= 128 ? 2 : 1;
+    p.rows = p.tc ? 128 * tree_attn_tc_tiles(R) : 16 * p.groups;
+    const int64_t cap = (int64_t)sms * (p.tc ? 1 : p.groups == 2 || D == 256 ? 2 : 3);
+    p.grid = (int)(cap < kAttnMaxCtas ? cap : kAttnMaxCtas);
+    return p;
 }
 
 template <int T, int D, int MT>
@@ -758,27 +763,27 @@ cudaError_t launch(const TreeAttnParams &p, int grid, cudaStream_t st) {
 }
 
 template <int T>
-cudaError_t launch_type(const TreeAttnParams &p, cudaStream_t st) {
-    const int D = p.cache.D, R = p.N * p.G;
-    const int grid = grid_size(p.B, R, p.cache.H, D, p.sms);
-    if (D == 256) return launch<T, 256, 1>(p, grid, st);
-    if (row_groups(R, D) == 2)
-        return D == 64 ? launch<T, 64, 2>(p, grid, st) : launch<T, 128, 2>(p, grid, st);
-    return D == 64 ? launch<T, 64, 1>(p, grid, st) : launch<T, 128, 1>(p, grid, st);
+cudaError_t launch_type(const TreeAttnParams &p, const Plan &n, cudaStream_t st) {
+    const int D = p.cache.D;
+    if (D == 256) return launch<T, 256, 1>(p, n.grid, st);
+    if (n.groups == 2)
+        return D == 64 ? launch<T, 64, 2>(p, n.grid, st) : launch<T, 128, 2>(p, n.grid, st);
+    return D == 64 ? launch<T, 64, 1>(p, n.grid, st) : launch<T, 128, 1>(p, n.grid, st);
 }
 
 }  // namespace
 
-int64_t tree_attn_workspace(int B, int N, int G, int H, int D, int sms) {
-    const int R = N * G;
-    const int64_t rows = 16 * row_groups(R, D);
-    const int64_t bytes = grid_size(B, R, H, D, sms) * 2 * rows * (D + 2) * (int64_t)sizeof(float);
+int64_t tree_attn_workspace(int R, int D, int sms) {
+    const Plan n = plan(R, D, sms);
+    const int64_t bytes = (int64_t)n.grid * 2 * n.rows * (D + 2) * (int64_t)sizeof(float);
     return (bytes + 255) / 256 * 256;
 }
 
 cudaError_t launch_tree_attn(const TreeAttnParams &p, cudaStream_t st) {
     if (p.B <= 0) return cudaSuccess;
-    return p.dtype == 1 ? launch_type<1>(p, st) : launch_type<2>(p, st);
+    const Plan n = plan(p.N * p.G, p.cache.D, p.sms);
+    if (n.tc) return launch_tree_attn_tc(p, n.grid, st);
+    return p.dtype == 1 ? launch_type<1>(p, n, st) : launch_type<2>(p, n, st);
 }
 
 }  // namespace specv
