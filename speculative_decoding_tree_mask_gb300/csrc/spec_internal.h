@@ -297,8 +297,8 @@ constexpr int kAttnMaxCtas = 4096;   // CTAs of an attention launch, at most
 // Bytes of parts that a launch with R rows of a K/V head may write.
 int64_t tree_attn_workspace(int R, int D, int sms);
 cudaError_t launch_tree_attn(const TreeAttnParams &p, cudaStream_t st);
-// On the tcgen05 tensor cores: row tiles of 128 that a CTA takes at a time, and the launch.
-int tree_attn_tc_tiles(int R);
+// On the tcgen05 tensor cores: rows of an item, and the launch.
+int tree_attn_tc_rows(int R);
 cudaError_t launch_tree_attn_tc(const TreeAttnParams &p, int grid, cudaStream_t st);
 
 // Adaptive node-budget update (see spec_budget_update).

@@ -33,6 +33,7 @@ constexpr int kThreads = kWarps * 32;
 // Tiles in the ring: the one at work and those in flight (two warps' worth of D = 256 take the
 // shared memory of three of D = 128).
 constexpr int stages(int D) { return D == 256 ? 2 : 3; }
+constexpr int kTreeCost = 1;      // the tree's tile and an item's rest, in context tiles
 constexpr float kRescale = 8.f;   // a maximum is followed once it rises by 2^8
 
 template <int D>
@@ -193,20 +194,18 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
     const float v_scale = C.v_scale ? __ldg(C.v_scale) : 1.f;
     const float unit = P.scale * kLog2e;
 
-    const AttnRange range = attn_range(P, C.H * row_tiles);
-    int b = range.b, item = range.item, tile = range.tile;
+    AttnWalk walk(P, C.H * row_tiles, kTreeCost);
+    AttnPart A;
     Acc<D, MT> acc;
 
-    for (int64_t at = range.begin; at < range.end;) {
-        const int ctx = attn_ctx(P, b), nt = (ctx + kTile - 1) / kTile + 1;
-        const int head = item / row_tiles, row0 = (item - head * row_tiles) * RT;
+    while (walk.next(P, A)) {
+        const int b = A.b, ctx = A.ctx, tile = A.tile;
+        const int head = A.item / row_tiles, row0 = (A.item - head * row_tiles) * RT;
         const int rows = min(RT, R - row0);
-        const int64_t first = at - tile;
-        const int stop = (int)min((int64_t)nt, tile + (range.end - at));
-        const int n = min(stop, nt - 1) - tile;        // context tiles of this CTA's part
-        const int32_t *table = C.block_table + (int64_t)b * C.max_blocks;
+        const int n = min(A.stop, A.nt - 1) - tile;    // context tiles of this CTA's part
         if (P.status && tid == 0 && tile == 0 && __ldg(P.ctx_len + b) != ctx)
             P.status[b] = SPEC_REQ_BAD_SLOT;
+        const int32_t *table = C.block_table + (int64_t)b * C.max_blocks;
 
         // The block of this lane's position in the part's i-th tile; -1 past the context.
         auto page = [&](int i) -> int {
@@ -498,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
                 for (int e = 0; e < 4; ++e) acc.o[mt][j][e] *= v_scale;
         __syncthreads();      // the ring is free
 
-        if (stop == nt) {
+        if (A.stop == A.nt) {
             // The tree's own nodes: their rows in shared memory, 16 nodes a warp.
             unsigned short *tk = reinterpret_cast<unsigned short *>(smem);
             unsigned short *tv = tk + kMaxN * S::kTreeStride;
@@ -699,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
             }
             __syncthreads();
         }
-        const bool whole = tile == 0 && stop == nt;
+        const bool whole = tile == 0 && A.stop == A.nt;
         float *part = attn_slot(P, blockIdx.x, tile == 0, RT, D);
         for (int i = tid; i < rows * (D / 4); i += kThreads) {
             const int r = i / (D / 4), d4 = i - r * (D / 4), cc = d4 / (D / 16), q = d4 % (D / 16);
@@ -723,15 +722,10 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
                 }
             }
         }
-        if (!whole) attn_join<T, D>(P, range, first, nt, b, head, row0, rows, RT, s_flag);
+        if (!whole)
+            attn_join<T, D>(P, walk.r, A, head, row0, rows, RT, s_flag, tid, kThreads,
+                            [] { __syncthreads(); });
         __syncthreads();      // shared memory is free for the next item
-
-        at += stop - tile;
-        tile = 0;
-        if (++item == C.H * row_tiles) {
-            item = 0;
-            ++b;
-        }
     }
 }
 
@@ -745,7 +739,7 @@ Plan plan(int R, int D, int sms) {
     Plan p;
     p.tc = R > 32 && D <= 128;
     p.groups = R > 16 && D <= 128 ? 2 : 1;
-    p.rows = p.tc ? 128 * tree_attn_tc_tiles(R) : 16 * p.groups;
+    p.rows = p.tc ? tree_attn_tc_rows(R) : 16 * p.groups;
     const int64_t cap = (int64_t)sms * (p.tc ? 1 : p.groups == 2 || D == 256 ? 2 : 3);
     p.grid = (int)(cap < kAttnMaxCtas ? cap : kAttnMaxCtas);
     return p;

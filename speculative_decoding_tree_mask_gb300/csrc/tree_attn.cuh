@@ -2,9 +2,11 @@
 // of an item are joined. Internal.
 //
 // The work of a call is a list of items (request, K/V head, tile of query rows), each a row of
-// tiles: its context in tiles of kTile positions, then one tile for the tree's own nodes. The
-// tiles of all items, in order, are cut into equal ranges, one for each CTA of a single wave,
-// whatever the requests' lengths (which only the device knows). A CTA therefore works on the
+// tiles: its context in tiles of kTile positions, then one tile for the tree's own nodes. A
+// context tile counts as one unit of work; the tree's tile, with what an item costs besides
+// (its queries in, its result out), as `cost` units, of which the tile takes place in the first.
+// The units of all items, in order, are cut into equal ranges, one for each CTA of a single
+// wave, whatever the requests' lengths (which only the device knows). A CTA therefore works on
 // end of one item, some whole items, and the start of another. Whole items are finished in
 // place. The parts of an item that a cut goes through are written to the workspace (row sums
 // and maxima and the unnormalised rows, float32); the CTA that arrives last joins them in
@@ -22,24 +24,22 @@ __device__ __forceinline__ int attn_ctx(const TreeAttnParams &P, int b) {
     const int most = P.cache.max_blocks * P.cache.block_size;   // fits: checked on the host
     return min(max(__ldg(P.ctx_len + b), 0), most);
 }
-__device__ __forceinline__ int attn_tiles(const TreeAttnParams &P, int b) {
-    return (attn_ctx(P, b) + kTile - 1) / kTile + 1;
-}
 
-// A CTA's range of tiles, and where it begins.
+// A CTA's range of units, and where it begins.
 struct AttnRange {
-    int64_t total, begin, end;   // tiles of the call; this CTA's [begin, end)
-    int ctas;                    // CTAs that have a range: each has at least one tile
-    int b, item, tile;           // place of `begin`
+    int64_t total, begin, end;   // units of the call; this CTA's [begin, end)
+    int ctas;                    // CTAs that have a range: each has at least one unit
+    int b, item, tile;           // place of `begin`: request, item in it, unit in that
 };
 
 // `items`: items of a request. Every warp computes it for itself (one warp scan).
-__device__ __forceinline__ AttnRange attn_range(const TreeAttnParams &P, int items) {
+__device__ __forceinline__ AttnRange attn_range(const TreeAttnParams &P, int items, int cost) {
+    auto units = [&](int b) { return (attn_ctx(P, b) + kTile - 1) / kTile + cost; };
     const unsigned full = 0xffffffffu;
     const int lane = threadIdx.x & 31;
     const int per = (P.B + 31) / 32, b0 = lane * per, b1 = min(P.B, b0 + per);
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += (int64_t)attn_tiles(P, b) * items;
+    for (int b = b0; b < b1; ++b) mine += (int64_t)units(b) * items;
     int64_t sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -60,7 +60,7 @@ __device__ __forceinline__ AttnRange attn_range(const TreeAttnParams &P, int ite
         int64_t left = r.begin - before;
         int b = b0;
         for (;; ++b) {
-            const int n = attn_tiles(P, b);
+            const int n = units(b);
             if (left < (int64_t)n * items) {
                 r.item = (int)(left / n);
                 r.tile = (int)(left - (int64_t)r.item * n);
@@ -77,10 +77,50 @@ __device__ __forceinline__ AttnRange attn_range(const TreeAttnParams &P, int ite
     return r;
 }
 
-// The CTA whose range holds tile s.
+// The CTA whose range holds unit s.
 __device__ __forceinline__ int attn_owner(const AttnRange &r, int64_t s) {
     return (int)(((s + 1) * r.ctas - 1) / r.total);
 }
+
+// A CTA's part of an item: its tiles [tile, stop) of the item's nt.
+struct AttnPart {
+    int b, item, tile, stop, nt, ctx;
+    int64_t first;                // unit of the item's first tile
+};
+
+// Steps through a CTA's parts, in order.
+struct AttnWalk {
+    AttnRange r;
+    int64_t at;
+    int b, item, tile, items, cost;
+
+    __device__ __forceinline__ AttnWalk(const TreeAttnParams &P, int items_, int cost_)
+        : r(attn_range(P, items_, cost_)), at(r.begin), b(r.b), item(r.item), tile(r.tile),
+          items(items_), cost(cost_) {}
+    // The next part, or false. Units past the tree's first start nothing.
+    __device__ __forceinline__ bool next(const TreeAttnParams &P, AttnPart &p) {
+        while (at < r.end) {
+            const int ctx = attn_ctx(P, b), nt = (ctx + kTile - 1) / kTile + 1;
+            const int left = nt - 1 + cost - tile;
+            const bool starts = tile < nt;
+            p.b = b;
+            p.item = item;
+            p.tile = tile;
+            p.nt = nt;
+            p.ctx = ctx;
+            p.first = at - tile;
+            p.stop = (int)min((int64_t)nt, tile + (r.end - at));
+            at += left;
+            tile = 0;
+            if (++item == items) {
+                item = 0;
+                ++b;
+            }
+            if (starts) return true;
+        }
+        return false;
+    }
+};
 
 // Where CTA `cta` leaves a part of an item: slot 0 if it came into the item from the middle,
 // slot 1 if it began the item. rows x (d values, then max and sum apart).
@@ -127,47 +167,71 @@ __device__ __forceinline__ float attn_lse(float m, float l) {
     return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-// The last of an item's parts to arrive joins them. Called by all threads of the CTA after they
-// have written their part; `first` = the item's first tile, `n` its tiles. Returns after the
+// The last of an item's parts to arrive joins them. Called by `threads` threads of the CTA
+// (`tid` of them), `sync` their barrier, after they have written their part. Returns after the
 // join, or at once when other parts are still missing.
-template <int T, int D>
+template <int T, int D, typename Sync>
 __device__ __forceinline__ void attn_join(const TreeAttnParams &P, const AttnRange &R,
-                                          int64_t first, int n, int b, int head, int row0,
-                                          int rows, int rows_tile, int *s_flag) {
-    const int c0 = attn_owner(R, first), c1 = attn_owner(R, first + n - 1);
+                                          const AttnPart &A, int head, int row0, int rows,
+                                          int rows_tile, int *s_flag, int tid, int threads,
+                                          Sync sync) {
+    const int c0 = attn_owner(R, A.first), c1 = attn_owner(R, A.first + A.nt - 1);
     __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
+    sync();
+    if (tid == 0) {
         const int seen = atomicAdd(P.arrive + c0, 1);
         const int last = seen == c1 - c0;
         if (last) P.arrive[c0] = 0;   // for the next call
         __threadfence();
         *s_flag = last;
     }
-    __syncthreads();
+    sync();
     if (!*s_flag) return;
-    for (int i = threadIdx.x; i < rows * (D / 4); i += blockDim.x) {
-        const int r = i / (D / 4), d4 = i - r * (D / 4);
-        float m = kNoMax, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+    // four float4 of a thread at a time, so that their loads are in flight together
+    constexpr int U = 4;
+    const int n = rows * (D / 4);
+    for (int i0 = tid; i0 < n; i0 += U * threads) {
+        float m[U], l[U];
+        float4 o[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            m[u] = kNoMax;
+            l[u] = 0.f;
+            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll 2
         for (int c = c0; c <= c1; ++c) {
             const float *part = attn_slot(P, c, c == c0, rows_tile, D);
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(part + r * D) + d4);
-            const float pm = __ldcg(part + rows_tile * D + r);
-            const float pl = __ldcg(part + rows_tile * (D + 1) + r);
-            const float mx = fmaxf(m, pm), a = exp2f(m - mx), w = exp2f(pm - mx);
-            o.x = o.x * a + v.x * w;
-            o.y = o.y * a + v.y * w;
-            o.z = o.z * a + v.z * w;
-            o.w = o.w * a + v.w * w;
-            l = l * a + pl * w;
-            m = mx;
+            float4 v[U];
+            float pm[U], pl[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = min(i0 + u * threads, n - 1), r = i / (D / 4);
+                v[u] = __ldcg(reinterpret_cast<const float4 *>(part) + i);
+                pm[u] = __ldcg(part + rows_tile * D + r);
+                pl[u] = __ldcg(part + rows_tile * (D + 1) + r);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float mx = fmaxf(m[u], pm[u]), a = exp2f(m[u] - mx), w = exp2f(pm[u] - mx);
+                o[u].x = o[u].x * a + v[u].x * w;
+                o[u].y = o[u].y * a + v[u].y * w;
+                o[u].z = o[u].z * a + v[u].z * w;
+                o[u].w = o[u].w * a + v[u].w * w;
+                l[u] = l[u] * a + pl[u] * w;
+                m[u] = mx;
+            }
         }
-        const float f = l == 0.f ? 0.f : 1.f / l;
-        const int64_t at = attn_row(P, b, head, row0 + r);
-        store_out4<T>(P.out, at * D + d4 * 4, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
-        if (P.lse && d4 == 0) P.lse[at] = attn_lse(m, l);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * threads, r = i / (D / 4), d4 = i - r * (D / 4);
+            if (i >= n) break;
+            const float f = l[u] == 0.f ? 0.f : 1.f / l[u];
+            const int64_t at = attn_row(P, A.b, head, row0 + r);
+            store_out4<T>(P.out, at * D + d4 * 4,
+                          make_float4(o[u].x * f, o[u].y * f, o[u].z * f, o[u].w * f));
+            if (P.lse && d4 == 0) P.lse[at] = attn_lse(m[u], l[u]);
+        }
     }
 }
 

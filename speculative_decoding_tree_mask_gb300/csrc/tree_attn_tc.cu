@@ -3,21 +3,24 @@
 // The same operator as tree_attn.cu, for items of more rows (nodes x query heads of a K/V
 // head) than its warps can serve at the speed of the cache: then the two products bound it,
 // 4 rows D operations a position, and next to them the exponentials and the conversion of the
-// codes. One CTA an SM takes NT tiles of 128 rows of an item against tiles of 128 positions:
+// codes. One CTA an SM; its warps have one part each and meet at mbarriers only:
 //
 //   convert  (4 warps) a position each: codes to 16-bit elements in shared memory, exact, laid
 //            out for the tensor core (128-byte swizzle; K contiguous along D, and V as it is,
 //            read transposed). K becomes the type of Q, V halves; two tiles of each in a ring;
-//   multiply (1 thread) S = Q K^T and O += P V, sums in tensor memory (all 512 columns for two
-//            row tiles of D = 128: S and O of each); P overwrites the half of S it came from;
-//   softmax  (4 warps a row tile, a row a thread, no exchange between threads) S to P with the
+//   multiply (1 thread) S = Q K^T and O += P V, sums in tensor memory: S and O twice, up to
+//            all 512 columns; P overwrites the half of S it came from;
+//   softmax  (2 groups of 4 warps) S to P, a row a thread, no exchange between threads, the
 //            running maximum and sum in registers. A maximum is followed only once it rises by
-//            2^8 (then O is rescaled in place), which is rare. S is read twice, for the maximum
-//            and for P, since it does not fit in a thread's registers.
-// With two row tiles the tensor core works on one while the other is in softmax. The tree's own
-// nodes are the last tile of an item: their rows are copied instead of converted and P is
-// multiplied in their type; for bfloat16 as a sum of two terms, since eight bits are too few.
-// Every wait gives up after two seconds; the request's status then says so.
+//            2^8 (then O is rescaled in place), which is rare.
+//
+// The two softmax groups keep the tensor core busy: it multiplies for one while the other works.
+// Items of more than 128 rows give each group 128 rows of its own and every tile; items of up
+// to 128 rows give both groups all rows and every other tile (SPLIT), and the two results are
+// joined at the end: tensor memory is read by lanes, and both groups own the same lanes.
+// The tree's own nodes are the last tile of an item: their rows are copied instead of converted
+// and P is multiplied in their type; for bfloat16 as a sum of two terms, since eight bits are
+// too few. Every wait gives up after two seconds; the request's status then says so.
 
 #include "tc_device.cuh"
 #include "tree_attn.cuh"
@@ -28,26 +31,36 @@ namespace {
 constexpr float kRescale = 8.f;
 constexpr int kConvert = 128;     // converting threads
 
-template <int D, int NT>
+constexpr int kSoftmax = 256;     // threads of the two softmax groups
+constexpr int kThreads = kSoftmax + kConvert + 128;   // the last warpgroup: one warp multiplies
+constexpr int kMmaWarp = (kSoftmax + kConvert) / 32;
+constexpr int kTreeCost = 4;      // the tree's tile and an item's rest, in context tiles
+
+template <int D, bool SPLIT>
 struct Tc {
-    static constexpr int kThreads = NT * 128 + kConvert + 32;
+    static constexpr int kRows = SPLIT ? 128 : 256;              // of an item
     static constexpr int kOperand = 128 * D * 2;                 // a 128 x D operand of 16 bits
-    static constexpr int kK = NT * kOperand;                     // Q first, then K and V rings
+    static constexpr int kK = kRows / 128 * kOperand;            // Q first, then K and V rings
     static constexpr int kV = kK + 2 * kOperand;
     static constexpr int kSmall = kV + 2 * kOperand;             // barriers and words
-    static constexpr int kBytes = kSmall + 512 + 1024;           // and room to align by 1024
-    static constexpr int kColumns = NT * (128 + D) > 256 ? 512 : 256;
+    static constexpr int kBytes = kSmall + 4096 + 1024;          // and room to align by 1024
+    static constexpr int kColumns = 512;                         // 2 (128 + D), a power of two
 };
 
 struct Words {
-    uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2], drain;
-    // positions of a K/V tile that are attended; a tile's words are written again only after
-    // the scores of the tile three before, whose P the multiplying thread has waited for
+    uint64_t q_full, q_free, k_full[2], k_free[2], v_full[2], v_free[2], drain;
+    uint64_t s_full[2], p_full[2], o_full[2];                    // of a softmax group
+    // Positions of a K/V tile that are attended. A tile's words are written again for the
+    // fourth after it, once the scores of the second after it are done: those were issued
+    // after its P was waited for.
     unsigned seen[4][4];
-    unsigned long long odd;       // tree nodes with NaN or infinities in V
+    unsigned long long odd[4];    // tree nodes with NaN or infinities in V; part by part likewise
     uint32_t tmem;
     int gave_up, flag;
+    int state[2];                 // SPLIT: 0 no tile, 1 O in the cache's units, 2 in V's
+    float top[2][128], sum[2][128];
 };
+static_assert(sizeof(Words) <= 4096, "room for the words");
 
 // Byte of 16-byte chunk `j` of row r of an operand of D elements a row.
 __device__ __forceinline__ uint32_t chunk_at(int r, int j) {
@@ -148,11 +161,71 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, bar_wait(bar, parity, gave_up));
 }
 
-template <int T, int D, int NT>
-__global__ void __launch_bounds__(Tc<D, NT>::kThreads, 1)
+__device__ __forceinline__ void cp_async16(uint32_t smem, const void *gmem) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
+}
+
+// One tile's S to P, the thread's row: kTree, 64 nodes to type T; else 128 positions to halves.
+template <int T, bool kTree>
+struct RowTile {
+    static constexpr int kChunks = kTree ? 2 : 4;
+    uint32_t s[kChunks][32];
+
+    // The scores, -inf where `see` has no bit; returns their largest.
+    __device__ __forceinline__ float load(uint32_t s_tm, const unsigned (&see)[4]) {
+#pragma unroll
+        for (int q = 0; q < kChunks; ++q) tmem_ld32(s_tm + q * 32, s[q]);
+        tmem_wait_ld(s[0]);
+#pragma unroll
+        for (int q = 1; q < kChunks; ++q) tmem_loaded(s[q]);
+        if (kTree || (see[0] & see[1] & see[2] & see[3]) != 0xffffffffu) {
+#pragma unroll
+            for (int q = 0; q < kChunks; ++q)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (!((see[q] >> e) & 1)) s[q][e] = 0xff800000u;
+        }
+        float big[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int q = 0; q < kChunks; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) big[e & 3] = fmaxf(big[e & 3], __uint_as_float(s[q][e]));
+        return fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
+    }
+    // P = 2^(f s - top) over the scores in tensor memory; returns the row's sum.
+    __device__ __forceinline__ float store(uint32_t s_tm, float f, float top) {
+        const uint64_t f2 = pack_f32x2(f, f), t2 = pack_f32x2(-top, -top);
+        uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+        for (int q = 0; q < kChunks; ++q) {
+            uint32_t lo[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                float a, b;
+                unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[q][e]),
+                                                  __uint_as_float(s[q][e + 1])), f2, t2), a, b);
+                a = ex2(a);
+                b = ex2(b);
+                sum[e / 2 & 1] = add_f32x2(sum[e / 2 & 1], pack_f32x2(a, b));
+                const uint32_t h = pack2<kTree ? T : 2>(a, b);
+                s[q][e / 2] = h;
+                if (kTree && T == 1) lo[e / 2] = pack2<1>(a - bf_lo(h), b - bf_hi(h));
+            }
+            tmem_st16(s_tm + q * 16, s[q]);
+            // what bfloat16 leaves, behind the 64 columns of scores
+            if (kTree && T == 1) tmem_st16(s_tm + 64 + q * 16, lo);
+        }
+        float a, b;
+        unpack_f32x2(add_f32x2(sum[0], sum[1]), a, b);
+        return a + b;
+    }
+};
+
+template <int T, int D, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
     tree_attn_tc_kernel(TreeAttnParams P, int row_tiles, int vec) {
-    using C_ = Tc<D, NT>;
-    constexpr int RT = NT * 128, KS = D / 16;
+    using C_ = Tc<D, SPLIT>;
+    constexpr int RT = C_::kRows, KS = D / 16;
     constexpr int kType = T == 1 ? 1 : 0;                        // of the descriptors
     extern __shared__ char raw[];
     char *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
@@ -160,9 +233,10 @@ __global__ void __launch_bounds__(Tc<D, NT>::kThreads, 1)
     const uint32_t base = smem_addr(smem);
     const spec_fp4_cache &C = P.cache;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int R = P.N * P.G;
-    constexpr int kMmaWarp = NT * 4 + kConvert / 32;
     if (tid == 0) {
+        bar_init(&W.q_full, kConvert);
+        bar_init(&W.q_free, 1);
+        bar_init(&W.drain, 1);
         for (int i = 0; i < 2; ++i) {
             bar_init(&W.k_full[i], kConvert);
             bar_init(&W.v_full[i], kConvert);
@@ -172,7 +246,6 @@ __global__ void __launch_bounds__(Tc<D, NT>::kThreads, 1)
             bar_init(&W.p_full[i], 128);
             bar_init(&W.o_full[i], 1);
         }
-        bar_init(&W.drain, 1);
         W.gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -182,134 +255,33 @@ __global__ void __launch_bounds__(Tc<D, NT>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = W.tmem;
     volatile int *gave_up = &W.gave_up;
-    // tensor memory of row tile m: S (and P over it) at 128 m, O behind all of S
+    // tensor memory of softmax group m: S (and P over it) at 128 m, O behind both
     auto s_at = [&](int m) { return tmem + 128 * m; };
-    auto o_at = [&](int m) { return tmem + 128 * NT + D * m; };
-    const float k_scale = C.k_scale ? __ldg(C.k_scale) : 1.f;
-    const float v_scale = C.v_scale ? __ldg(C.v_scale) : 1.f;
-    const float unit = P.scale * kLog2e;
+    auto o_at = [&](int m) { return tmem + 256 + D * m; };
+    uint32_t done = 0, parts = 0;     // tiles and parts before this one: the phases count them
+    AttnPart A;
 
-    const AttnRange range = attn_range(P, C.H * row_tiles);
-    int b = range.b, item = range.item, tile = range.tile;
-    uint32_t done = 0;            // tiles before this item: the barriers' phases count them
-
-    for (int64_t at = range.begin; at < range.end;) {
-        const int ctx = attn_ctx(P, b), nt = (ctx + kTile - 1) / kTile + 1;
-        const int head = item / row_tiles, row0 = (item - head * row_tiles) * RT;
-        const int rows = min(RT, R - row0);
-        const int64_t first = at - tile;
-        const int stop = (int)min((int64_t)nt, tile + (range.end - at));
-        const int n = stop - tile;                    // tiles of this part
-        const int tree = nt - 1 - tile;               // the tree's place among them, or >= n
-        if (P.status && tid == 0 && tile == 0 && __ldg(P.ctx_len + b) != ctx)
-            P.status[b] = SPEC_REQ_BAD_SLOT;
-
-        // Q into shared memory
-        for (int i = tid; i < RT * (D / 8); i += C_::kThreads) {
-            const int r = i / (D / 8), j = i - r * (D / 8);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (r < rows) {
-                const int rr = row0 + r, node = rr / P.G;
-                v = load8(reinterpret_cast<const unsigned short *>(P.q) +
-                              ((int64_t)b * P.N + node) * P.q_stride +
-                              (int64_t)(head * P.G + rr - node * P.G) * D + j * 8,
-                          vec);
-            }
-            *reinterpret_cast<uint4 *>(smem + (r >> 7) * C_::kOperand + chunk_at(r & 127, j)) = v;
-        }
-        fence_async_smem();
-        if (tid == 0) W.odd = 0ull;
-        __syncthreads();
-
-        if (warp >= NT * 4 && warp < kMmaWarp) {
-            // ---- convert ----
-            const int t = tid - NT * 128;
-            const int32_t *table = C.block_table + (int64_t)b * C.max_blocks;
-            auto page = [&](int i) -> int {
-                const int p = (tile + i) * kTile + t;
-                return i < n && i < tree && p < ctx
-                           ? __ldg(table + (uint32_t)p / (uint32_t)C.block_size)
-                           : -1;
-            };
-            Row4<D> kr, vr;
-            bool ok = false;
-            auto fetch = [&](int i, int blk) {
-                const int p = (tile + i) * kTile + t;
-                ok = blk >= 0 && blk < C.num_blocks;
-                const uint32_t row =
-                    ok ? fp4_row(C, blk, p % (uint32_t)C.block_size, head) : 0u;
-                if (i < n && i < tree && p < ctx && !ok && P.status)
-                    P.status[b] = SPEC_REQ_BAD_SLOT;
-                load_row<D>(C.k, C.k_sf, row, ok, kr);
-                load_row<D>(C.v, C.v_sf, row, ok, vr);
-            };
-            int next = page(1);
-            fetch(0, page(0));
-            for (int i = 0; i < n; ++i) {
-                const uint32_t c = done + i;
-                const int st = c & 1;
-                const uint32_t parity = ((c >> 1) & 1) ^ 1;
-                char *ks = smem + C_::kK + st * C_::kOperand;
-                char *vs = smem + C_::kV + st * C_::kOperand;
-                if (i == tree) {
-                    // the nodes' own rows, zeros up to 64; two threads a row
-                    const int r = t >> 1;
-                    if (!warp_wait(&W.k_free[st], parity, gave_up) ||
-                        !warp_wait(&W.v_free[st], parity, gave_up))
-                        break;
-                    const int64_t row = (int64_t)b * P.N + min(r, P.N - 1);
-                    const unsigned short *k =
-                        reinterpret_cast<const unsigned short *>(P.k) + row * P.k_stride + head * D;
-                    const unsigned short *v =
-                        reinterpret_cast<const unsigned short *>(P.v) + row * P.v_stride + head * D;
-                    for (int j = t & 1; j < D / 8; j += 2) {
-                        uint4 a = make_uint4(0, 0, 0, 0), x = a;
-                        if (r < P.N) {
-                            a = load8(k + j * 8, vec);
-                            x = load8(v + j * 8, vec);
-                            uint32_t *w = reinterpret_cast<uint32_t *>(&x);
-                            bool odd = false;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if (odd16<T>(w[e])) {
-                                    w[e] &= 0xffff0000u;
-                                    odd = true;
-                                }
-                                if (odd16<T>(w[e] >> 16)) {
-                                    w[e] &= 0xffffu;
-                                    odd = true;
-                                }
-                            }
-                            if (odd) atomicOr(&W.odd, 1ull << r);
-                        }
-                        *reinterpret_cast<uint4 *>(ks + chunk_at(r, j)) = a;
-                        *reinterpret_cast<uint4 *>(vs + chunk_at(r, j)) = x;
-                    }
-                    fence_async_smem();
-                    bar_arrive(&W.k_full[st]);
-                    bar_arrive(&W.v_full[st]);
-                    break;        // it is the last
-                }
-                const unsigned seen = __ballot_sync(0xffffffffu, ok);
-                if (!warp_wait(&W.k_free[st], parity, gave_up)) break;
-                if (lane == 0) W.seen[c & 3][t >> 5] = seen;
-                convert_row<D, T == 1>(kr, ks, t);
-                fence_async_smem();
-                bar_arrive(&W.k_full[st]);
-                if (!warp_wait(&W.v_free[st], parity, gave_up)) break;
-                convert_row<D, false>(vr, vs, t);
-                fence_async_smem();
-                bar_arrive(&W.v_full[st]);
-                const int cur = next;
-                next = page(i + 2);
-                fetch(i + 1, cur);
-            }
-        } else if (warp == kMmaWarp) {
-            // ---- multiply ----
-            if (lane == 0) {
-                auto scores = [&](int m, int i) {
+    // Launched with 128 registers a thread, 16 warps: 8 x 184 + 4 x 104 + 4 x 40 = 16 x 128.
+    if (tid >= kSoftmax + kConvert) {
+        fewer_registers<40>();
+        // ---- multiply ----
+        // A job is a tile for a softmax group. Job j: tile j for group j % 2 (SPLIT), or tile
+        // j / 2 for group j % 2. Scores are issued two jobs ahead of the products with V.
+        if (warp == kMmaWarp) {
+          AttnWalk walk(P, C.H * row_tiles, kTreeCost);     // by the whole warp
+          if (lane == 0) {
+            uint32_t jobs[2] = {0, 0};   // of a group so far
+            bool ok = true;
+            while (ok && walk.next(P, A)) {
+                const int n = A.stop - A.tile, tree = A.nt - 1 - A.tile;
+                const int count = SPLIT ? n : 2 * n;
+                auto scores = [&](int j) {
+                    const int m = j & 1, i = SPLIT ? j : j >> 1;
                     const uint32_t c = done + i;
-                    const uint32_t a = base + m * C_::kOperand;
+                    ok = ok && bar_wait(&W.k_full[c & 1], (c >> 1) & 1, gave_up);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint32_t a = base + (SPLIT ? 0 : m * C_::kOperand);
                     const uint32_t k = base + C_::kK + (c & 1) * C_::kOperand;
                     const uint32_t d = i == tree ? mma_desc(kType, 64, false)
                                                  : mma_desc(kType, 128, false);
@@ -320,186 +292,330 @@ __global__ void __launch_bounds__(Tc<D, NT>::kThreads, 1)
                                d, s > 0);
                     }
                     mma_commit(&W.s_full[m]);
+                    if (SPLIT || m == 1) mma_commit(&W.k_free[c & 1]);
+                    if (j == count - 1) mma_commit(&W.q_free);
                 };
-                bool ok = bar_wait(&W.k_full[done & 1], (done >> 1) & 1, gave_up);
-                tc_fence_after();
-                if (ok) {
-                    for (int m = 0; m < NT; ++m) scores(m, 0);
-                    mma_commit(&W.k_free[done & 1]);
-                }
-                for (int i = 0; ok && i < n; ++i) {
+                ok = ok && bar_wait(&W.q_full, parts & 1, gave_up);
+                scores(0);
+                if (count > 1) scores(1);
+                for (int j = 0; ok && j < count; ++j) {
+                    const int m = j & 1, i = SPLIT ? j : j >> 1;
                     const uint32_t c = done + i;
                     const uint32_t v = base + C_::kV + (c & 1) * C_::kOperand;
-                    for (int m = 0; m < NT; ++m) {
-                        if (m == 0) ok = bar_wait(&W.v_full[c & 1], (c >> 1) & 1, gave_up);
-                        ok = ok && bar_wait(&W.p_full[m], c & 1, gave_up);
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (i == tree) {
-                            // 64 nodes; bfloat16: the two terms of P, 64 columns apart
-                            for (int part = 0; part < (T == 1 ? 2 : 1); ++part)
+                    ok = bar_wait(&W.v_full[c & 1], (c >> 1) & 1, gave_up) &&
+                         bar_wait(&W.p_full[m], jobs[m] & 1, gave_up);
+                    if (!ok) break;
+                    ++jobs[m];
+                    tc_fence_after();
+                    const bool add = SPLIT ? j > 1 : i > 0;
+                    if (i == tree) {
+                        // 64 nodes; bfloat16: the two terms of P, 64 columns apart
 #pragma unroll
-                                for (int s = 0; s < 4; ++s)
-                                    mma_ts(o_at(m), s_at(m) + part * 64 + s * 8,
-                                           smem_desc(v + s * 2048, 128 * 128, 1024),
-                                           mma_desc(kType, D, true), i > 0 || part > 0 || s > 0);
-                        } else {
+                        for (int s = 0; s < (T == 1 ? 8 : 4); ++s)
+                            mma_ts(o_at(m), s_at(m) + (s >> 2) * 64 + (s & 3) * 8,
+                                   smem_desc(v + (s & 3) * 2048, 128 * 128, 1024),
+                                   mma_desc(kType, D, true), add || s > 0);
+                    } else {
 #pragma unroll
-                            for (int s = 0; s < 8; ++s)
-                                mma_ts(o_at(m), s_at(m) + s * 8,
-                                       smem_desc(v + s * 2048, 128 * 128, 1024),
-                                       mma_desc(0, D, true), i > 0 || s > 0);
-                        }
-                        mma_commit(&W.o_full[m]);
-                        if (m == NT - 1) mma_commit(&W.v_free[c & 1]);
-                        if (i + 1 < n) {
-                            const uint32_t d = c + 1;
-                            if (m == 0) ok = bar_wait(&W.k_full[d & 1], (d >> 1) & 1, gave_up);
-                            if (!ok) break;
-                            tc_fence_after();
-                            scores(m, i + 1);
-                            if (m == NT - 1) mma_commit(&W.k_free[d & 1]);
-                        }
+                        for (int s = 0; s < 8; ++s)
+                            mma_ts(o_at(m), s_at(m) + s * 8,
+                                   smem_desc(v + s * 2048, 128 * 128, 1024), mma_desc(0, D, true),
+                                   add || s > 0);
                     }
+                    mma_commit(&W.o_full[m]);
+                    if (SPLIT || m == 1) mma_commit(&W.v_free[c & 1]);
+                    if (j + 2 < count) scores(j + 2);
+                }
+                done += n;
+                ++parts;
+            }
+            if (!ok) {
+                // products in flight end before tensor memory is freed
+                mma_commit(&W.drain);
+                for (int i = 0; i < (1 << 20) && !bar_try(&W.drain, 0); ++i) {
                 }
             }
-        } else if (warp < NT * 4) {
-            // ---- softmax: this thread's row ----
-            const int m = warp >> 2, r = m * 128 + (warp & 3) * 32 + lane;
+          }
+        }
+    } else if (tid >= kSoftmax) {
+        fewer_registers<104>();
+        // ---- convert ----
+        const int t = tid - kSoftmax, R = P.N * P.G;
+        AttnWalk walk(P, C.H * row_tiles, kTreeCost);
+        bool go = true;               // no wait has given up
+        while (walk.next(P, A)) {
+            const int b = A.b, ctx = A.ctx, n = A.stop - A.tile, tree = A.nt - 1 - A.tile;
+            const int head = A.item / row_tiles, row0 = (A.item - head * row_tiles) * RT;
+            const int rows = min(RT, R - row0);
+            if (P.status && t == 0 && A.tile == 0 && __ldg(P.ctx_len + b) != ctx)
+                P.status[b] = SPEC_REQ_BAD_SLOT;
+            const int32_t *table = C.block_table + (int64_t)b * C.max_blocks;
+            auto page = [&](int i) -> int {
+                const int p = (A.tile + i) * kTile + t;
+                return i < n && i < tree && p < ctx
+                           ? __ldg(table + (uint32_t)p / (uint32_t)C.block_size)
+                           : -1;
+            };
+            Row4<D> kr, vr;
+            bool ok = false;
+            auto fetch = [&](int i, int blk) {
+                const int p = (A.tile + i) * kTile + t;
+                ok = blk >= 0 && blk < C.num_blocks;
+                const uint32_t row =
+                    ok ? fp4_row(C, blk, p % (uint32_t)C.block_size, head) : 0u;
+                if (i < n && i < tree && p < ctx && !ok && P.status)
+                    P.status[b] = SPEC_REQ_BAD_SLOT;
+                load_row<D>(C.k, C.k_sf, row, ok, kr);
+                load_row<D>(C.v, C.v_sf, row, ok, vr);
+            };
+            const int page0 = page(0);
+            int next = page(1);
+            go = go && warp_wait(&W.q_free, (parts & 1) ^ 1, gave_up);
+            if (go) {
+                // Q: rows of an operand a thread, neighbours' chunks side by side
+#pragma unroll 4
+                for (int i = t; i < RT * (D / 8); i += kConvert) {
+                    const int r = i / (D / 8), j = i - r * (D / 8);
+                    const uint32_t to = (r >> 7) * C_::kOperand + chunk_at(r & 127, j);
+                    const int rr = row0 + (r < rows ? r : 0), node = rr / P.G;
+                    const unsigned short *from =
+                        reinterpret_cast<const unsigned short *>(P.q) +
+                        ((int64_t)b * P.N + node) * P.q_stride +
+                        (int64_t)(head * P.G + rr - node * P.G) * D + j * 8;
+                    if (r >= rows)
+                        *reinterpret_cast<uint4 *>(smem + to) = make_uint4(0, 0, 0, 0);
+                    else if (vec)
+                        cp_async16(base + to, from);
+                    else
+                        *reinterpret_cast<uint4 *>(smem + to) = load8(from, false);
+                }
+            }
+            fetch(0, page0);
+            if (t == 0) W.odd[parts & 3] = 0ull;
+            named_sync(2, kConvert);
+            auto q_done = [&]() {
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                fence_async_smem();
+                if (go) bar_arrive(&W.q_full);
+            };
+            for (int i = 0; i < n; ++i) {
+                const uint32_t c = done + i;
+                const int st = c & 1;
+                const uint32_t parity = ((c >> 1) & 1) ^ 1;
+                char *ks = smem + C_::kK + st * C_::kOperand;
+                char *vs = smem + C_::kV + st * C_::kOperand;
+                if (i == tree) {
+                    // the nodes' own rows, zeros up to 64; two threads a row, half of it each
+                    const int r = t >> 1, j0 = (t & 1) * (D / 16);
+                    const int64_t row = (int64_t)b * P.N + min(r, P.N - 1);
+                    const unsigned short *k = reinterpret_cast<const unsigned short *>(P.k) +
+                                              row * P.k_stride + head * D + j0 * 8;
+                    const unsigned short *v = reinterpret_cast<const unsigned short *>(P.v) +
+                                              row * P.v_stride + head * D + j0 * 8;
+                    uint4 x[D / 16];
+                    auto rows_in = [&](const unsigned short *from) {
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j)
+                            x[j] = r < P.N ? load8(from + j * 8, vec) : make_uint4(0, 0, 0, 0);
+                    };
+                    rows_in(k);
+                    go = go && warp_wait(&W.k_free[st], parity, gave_up);
+                    if (go) {
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j)
+                            *reinterpret_cast<uint4 *>(ks + chunk_at(r, j0 + j)) = x[j];
+                        fence_async_smem();
+                        bar_arrive(&W.k_full[st]);
+                    }
+                    if (i == 0) q_done();
+                    rows_in(v);
+                    bool odd = false;
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        uint32_t *w = reinterpret_cast<uint32_t *>(&x[j]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (odd16<T>(w[e])) {
+                                w[e] &= 0xffff0000u;
+                                odd = true;
+                            }
+                            if (odd16<T>(w[e] >> 16)) {
+                                w[e] &= 0xffffu;
+                                odd = true;
+                            }
+                        }
+                    }
+                    if (odd) atomicOr(&W.odd[parts & 3], 1ull << r);
+                    go = go && warp_wait(&W.v_free[st], parity, gave_up);
+                    if (go) {
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j)
+                            *reinterpret_cast<uint4 *>(vs + chunk_at(r, j0 + j)) = x[j];
+                        fence_async_smem();
+                        bar_arrive(&W.v_full[st]);
+                    }
+                    break;        // it is the last
+                }
+                const unsigned seen = __ballot_sync(0xffffffffu, ok);
+                go = go && warp_wait(&W.k_free[st], parity, gave_up);
+                if (go) {
+                    if (lane == 0) W.seen[c & 3][t >> 5] = seen;
+                    convert_row<D, T == 1>(kr, ks, t);
+                    fence_async_smem();
+                    bar_arrive(&W.k_full[st]);
+                }
+                if (i == 0) q_done();
+                go = go && warp_wait(&W.v_free[st], parity, gave_up);
+                if (go) {
+                    convert_row<D, false>(vr, vs, t);
+                    fence_async_smem();
+                    bar_arrive(&W.v_full[st]);
+                }
+                const int cur = next;
+                next = page(i + 2);
+                fetch(i + 1, cur);
+            }
+            done += n;
+            ++parts;
+        }
+    } else {
+        more_registers<184>();
+        // ---- softmax: this thread's row. A wait that gives up is followed by none, but the
+        // groups' barriers are kept.
+        const int m = warp >> 2, R = P.N * P.G;
+        const int r = (SPLIT ? 0 : m * 128) + (warp & 3) * 32 + lane;    // of the item
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_tm = s_at(m) + lanes, o_tm = o_at(m) + lanes;
+        const float v_scale = C.v_scale ? __ldg(C.v_scale) : 1.f;
+        const float unit = P.scale * kLog2e;
+        const float cache_unit = unit * (C.k_scale ? __ldg(C.k_scale) : 1.f);
+        AttnWalk walk(P, C.H * row_tiles, kTreeCost);
+        uint32_t jobs = 0;            // of this group so far
+        bool go = true;
+        while (walk.next(P, A)) {
+            const int b = A.b, n = A.stop - A.tile, tree = A.nt - 1 - A.tile;
+            const int head = A.item / row_tiles, row0 = (A.item - head * row_tiles) * RT;
+            const int rows = min(RT, R - row0);
             const bool live = r < rows;
-            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-            const uint32_t s_tm = s_at(m) + lanes, o_tm = o_at(m) + lanes;
             float top = kNoMax, sum = 0.f;
             const unsigned long long mask =
                 live ? __ldg(P.mask + (int64_t)b * P.N + (row0 + r) / P.G) &
                            (P.N < 64 ? (1ull << P.N) - 1ull : ~0ull)
                      : 0ull;
-            bool ok = true;
-            for (int i = 0; i < n && ok; ++i) {
-                const uint32_t c = done + i;
-                ok = warp_wait(&W.s_full[m], c & 1, gave_up);
-                if (!ok) break;
-                tc_fence_after();
-                const bool is_tree = i == tree;
-                unsigned see[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    see[q] = is_tree ? (q < 2 ? (unsigned)(mask >> (q * 32)) : 0u) : W.seen[c & 3][q];
-                const bool all = (see[0] & see[1] & see[2] & see[3]) == 0xffffffffu;
-                const float f = is_tree ? unit : unit * k_scale;
-                const int chunks = is_tree ? 2 : 4;
-                auto scores = [&](int q, uint32_t (&s)[32]) {   // of 32 positions; -inf: not seen
-                    tmem_ld32(s_tm + q * 32, s);
-                    tmem_wait_ld(s);
-                    if (!all) {
-                        const unsigned w = q == 0 ? see[0] : q == 1 ? see[1] : q == 2 ? see[2] : see[3];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!((w >> e) & 1)) s[e] = 0xff800000u;
-                    }
-                };
-                float big = -INFINITY;
-                for (int q = 0; q < chunks; ++q) {
-                    uint32_t s[32];
-                    scores(q, s);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) big = fmaxf(big, __uint_as_float(s[e]));
-                }
-                const float x = fmaxf(kNoMax, big * f);
+            int mine = 0;             // tiles of this group in this part
+            // follows the maximum x; `scale` O where it stands
+            auto follow = [&](float x, bool units) {
                 const bool raise = __any_sync(0xffffffffu, x > top + kRescale);
-                const bool units = is_tree && i > 0;      // O leaves the cache's units
-                if (raise || units) {
-                    float a = 1.f;
-                    if (raise) {
-                        const float to = fmaxf(top, x);
-                        a = ex2(top - to);
-                        top = to;
-                        sum *= a;
-                    }
-                    if (units) a *= v_scale;
-                    if (i > 0) {
-                        ok = warp_wait(&W.o_full[m], (c - 1) & 1, gave_up);
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int q = 0; q < D / 32; ++q) {
-                            uint32_t o[32];
-                            tmem_ld32(o_tm + q * 32, o);
-                            tmem_wait_ld(o);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-                            tmem_st32(o_tm + q * 32, o);
-                        }
-                    }
+                if (!raise && !units) return;
+                float a = 1.f;
+                if (raise) {
+                    const float to = fmaxf(top, x);
+                    a = ex2(top - to);
+                    top = to;
+                    sum *= a;
                 }
-                // P over the scores that have been read: chunk q's 16 columns lie in chunk q / 2
-                for (int q = 0; q < chunks; ++q) {
-                    uint32_t s[32], p[16];
-                    scores(q, s);
-                    float l = 0.f;
+                if (units) a *= v_scale;
+                if (mine == 0) return;
+                go = go && warp_wait(&W.o_full[m], (jobs - 1) & 1, gave_up);
+                tc_fence_after();
+#pragma unroll 1
+                for (int q = 0; q < D / 16; ++q) {      // S stays in registers meanwhile
+                    uint32_t o[16];
+                    tmem_ld16(o_tm + q * 16, o);
+                    tmem_wait_ld16(o);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float p0 = ex2(fmaf(__uint_as_float(s[e]), f, -top));
-                        const float p1 = ex2(fmaf(__uint_as_float(s[e + 1]), f, -top));
-                        l += p0 + p1;
-                        s[e] = __float_as_uint(p0);
-                        s[e + 1] = __float_as_uint(p1);
-                    }
-                    sum += l;
-                    if (!is_tree) {
+                    for (int e = 0; e < 16; ++e)
+                        o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                    tmem_st16(o_tm + q * 16, o);
+                }
+            };
+            for (int i = SPLIT ? m : 0; i < n; i += SPLIT ? 2 : 1) {
+                const uint32_t c = done + i;
+                go = go && warp_wait(&W.s_full[m], jobs & 1, gave_up);
+                if (!go) break;
+                tc_fence_after();
+                unsigned see[4];
+                if (i == tree) {
+                    see[0] = (unsigned)mask;
+                    see[1] = (unsigned)(mask >> 32);
+                    see[2] = see[3] = 0;
+                    RowTile<T, true> tile;
+                    const float x = fmaxf(kNoMax, tile.load(s_tm, see) * unit);
+                    follow(x, true);      // O leaves the cache's units
+                    sum += tile.store(s_tm, unit, top);
+                } else {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            p[e] = pack2<2>(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-                        tmem_st16(s_tm + q * 16, p);
-                    } else {
-                        // the nodes' P in their type; what bfloat16 leaves in a second term,
-                        // behind the 64 columns of scores
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            p[e] = pack2<T>(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-                            if (T == 1)
-                                s[e] = pack2<1>(__uint_as_float(s[2 * e]) - bf_lo(p[e]),
-                                                __uint_as_float(s[2 * e + 1]) - bf_hi(p[e]));
-                        }
-                        tmem_st16(s_tm + q * 16, p);
-                        if (T == 1) tmem_st16(s_tm + 64 + q * 16, s);
-                    }
+                    for (int q = 0; q < 4; ++q) see[q] = W.seen[c & 3][q];
+                    RowTile<T, false> tile;
+                    const float x = fmaxf(kNoMax, tile.load(s_tm, see) * cache_unit);
+                    follow(x, false);
+                    sum += tile.store(s_tm, cache_unit, top);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 bar_arrive(&W.p_full[m]);
+                ++jobs;
+                ++mine;
             }
-            // the result: O is done after the last tile's product
-            ok = ok && warp_wait(&W.o_full[m], (done + n - 1) & 1, gave_up);
+            // the result: O is done after the group's last product
+            if (mine > 0) go = go && warp_wait(&W.o_full[m], (jobs - 1) & 1, gave_up);
             tc_fence_after();
-            const bool whole = tile == 0 && stop == nt;
-            const float in_cache = tree < n ? 1.f : v_scale;
-            const float norm = in_cache * (whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f);
+            if (!go && P.status && lane == 0) P.status[b] = SPEC_REQ_INTERNAL;
+            const bool whole = A.tile == 0 && A.stop == A.nt;
+            // the group's O is in V's units once the tree's tile was among its tiles
+            const bool in_v = tree < n && (!SPLIT || (tree & 1) == m);
+            float f[2] = {in_v ? 1.f : v_scale, 0.f};     // of this group's O; of the other's
+            bool has[2] = {mine > 0, false};
+            if (SPLIT) {
+                const int row = (warp & 3) * 32 + lane;
+                W.top[m][row] = top;
+                W.sum[m][row] = sum;
+                if (row == 0) W.state[m] = mine == 0 ? 0 : in_v ? 2 : 1;
+                named_sync(1, kSoftmax);
+                const float other = W.top[m ^ 1][row], most = fmaxf(top, other);
+                const int state = W.state[m ^ 1];
+                has[1] = state != 0;
+                f[0] *= ex2(top - most);
+                f[1] = ex2(other - most) * (state == 2 ? 1.f : v_scale);
+                sum = sum * ex2(top - most) + W.sum[m ^ 1][row] * ex2(other - most);
+                top = most;
+            }
+            const float norm = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+            f[0] *= norm;
+            f[1] *= norm;
             const int64_t to = live ? attn_row(P, b, head, row0 + r) : 0;
-            float *part = attn_slot(P, blockIdx.x, tile == 0, RT, D);
-            const unsigned long long odd = tree < n ? W.odd & mask : 0ull;
-#pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-                uint32_t o[32];
-                tmem_ld32(o_tm + q * 32, o);
-                tmem_wait_ld(o);
-                if (!live || !ok) continue;
+            float *part = attn_slot(P, blockIdx.x, A.tile == 0, RT, D);
+            const unsigned long long odd = tree < n ? W.odd[parts & 3] & mask : 0ull;
+            // SPLIT: the groups take half of the columns each, of both Os
+            const uint32_t other_tm = o_at(m ^ 1) + lanes;
+            for (int q = SPLIT ? m * (D / 64) : 0; q < (SPLIT ? (m + 1) * (D / 64) : D / 32); ++q) {
                 float v[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * norm;
+                for (int e = 0; e < 32; ++e) v[e] = 0.f;
+#pragma unroll
+                for (int g = 0; g < (SPLIT ? 2 : 1); ++g) {
+                    if (!has[g]) continue;      // the same for the whole group
+                    uint32_t o[32];
+                    tmem_ld32((g ? other_tm : o_tm) + q * 32, o);
+                    tmem_wait_ld(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = fmaf(__uint_as_float(o[e]), f[g], v[e]);
+                }
+                if (!live) continue;
                 // NaN and infinities of nodes that this row sees
                 for (unsigned long long left = odd; left; left &= left - 1) {
                     const int j = __ffsll(left) - 1;
+                    const int node = (row0 + r) / P.G;
                     const unsigned short *qp =
                         reinterpret_cast<const unsigned short *>(P.q) +
-                        ((int64_t)b * P.N + (row0 + r) / P.G) * P.q_stride +
-                        (int64_t)(head * P.G + (row0 + r) % P.G) * D;
+                        ((int64_t)b * P.N + node) * P.q_stride +
+                        (int64_t)(head * P.G + row0 + r - node * P.G) * D;
                     const unsigned short *kp = reinterpret_cast<const unsigned short *>(P.k) +
                                                ((int64_t)b * P.N + j) * P.k_stride + head * D;
                     const unsigned short *vp = reinterpret_cast<const unsigned short *>(P.v) +
                                                ((int64_t)b * P.N + j) * P.v_stride + head * D;
                     float dot = 0.f;
+#pragma unroll 1
                     for (int d = 0; d < D; ++d)
                         dot = fmaf(value16<T>(__ldg(qp + d)), value16<T>(__ldg(kp + d)), dot);
                     const float w = ex2(dot * unit - top);
@@ -521,7 +637,7 @@ __global__ void __launch_bounds__(Tc<D, NT>::kThreads, 1)
                             make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                 }
             }
-            if (live && ok) {
+            if (live && (!SPLIT || m == 0)) {
                 if (whole) {
                     if (P.lse) P.lse[to] = attn_lse(top, sum);
                 } else {
@@ -530,28 +646,12 @@ __global__ void __launch_bounds__(Tc<D, NT>::kThreads, 1)
                 }
             }
             tc_fence_before();
-        }
-        __syncthreads();
-        if (*gave_up) {
-            if (P.status && tid == 0) P.status[b] = SPEC_REQ_INTERNAL;
-            break;
-        }
-        if (!(tile == 0 && stop == nt))
-            attn_join<T, D>(P, range, first, nt, b, head, row0, rows, RT, &W.flag);
-        __syncthreads();      // Q and the words are free for the next item
-        done += n;
-        at += stop - tile;
-        tile = 0;
-        if (++item == C.H * row_tiles) {
-            item = 0;
-            ++b;
-        }
-    }
-    // every product has been waited for, unless a wait gave up: then those in flight are, for
-    // as long as they can take
-    if (warp == kMmaWarp && lane == 0 && *gave_up) {
-        mma_commit(&W.drain);
-        for (int i = 0; i < (1 << 20) && !bar_try(&W.drain, 0); ++i) {
+            if (SPLIT) named_sync(1, kSoftmax);    // both Os have been read
+            if (!whole)
+                attn_join<T, D>(P, walk.r, A, head, row0, rows, RT, &W.flag, tid, kSoftmax,
+                                [] { named_sync(1, kSoftmax); });
+            done += n;
+            ++parts;
         }
     }
     tc_fence_before();
@@ -559,35 +659,36 @@ __global__ void __launch_bounds__(Tc<D, NT>::kThreads, 1)
     if (warp == kMmaWarp) tmem_free(tmem, C_::kColumns);
 }
 
-template <int T, int D, int NT>
+template <int T, int D, bool SPLIT>
 cudaError_t launch(const TreeAttnParams &p, int grid, cudaStream_t st) {
-    using C_ = Tc<D, NT>;
-    const cudaError_t e = cudaFuncSetAttribute(tree_attn_tc_kernel<T, D, NT>,
+    using C_ = Tc<D, SPLIT>;
+    const cudaError_t e = cudaFuncSetAttribute(tree_attn_tc_kernel<T, D, SPLIT>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                C_::kBytes);
     if (e != cudaSuccess) return e;
-    const int row_tiles = (p.N * p.G + NT * 128 - 1) / (NT * 128);
+    const int row_tiles = (p.N * p.G + C_::kRows - 1) / C_::kRows;
     auto vec16 = [](const void *q, int64_t stride) {
         return reinterpret_cast<uintptr_t>(q) % 16 == 0 && stride % 8 == 0;
     };
     const int vec = vec16(p.q, p.q_stride) && vec16(p.k, p.k_stride) && vec16(p.v, p.v_stride);
-    tree_attn_tc_kernel<T, D, NT><<<grid, C_::kThreads, C_::kBytes, st>>>(p, row_tiles, vec);
+    tree_attn_tc_kernel<T, D, SPLIT><<<grid, kThreads, C_::kBytes, st>>>(p, row_tiles, vec);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-// Row tiles of 128 that a CTA takes at a time.
-int tree_attn_tc_tiles(int R) { return R > 128 ? 2 : 1; }
+int tree_attn_tc_rows(int R) { return R > 128 ? 256 : 128; }
 
 cudaError_t launch_tree_attn_tc(const TreeAttnParams &p, int grid, cudaStream_t st) {
-    const bool two = tree_attn_tc_tiles(p.N * p.G) == 2;
+    const bool split = tree_attn_tc_rows(p.N * p.G) == 128;
     if (p.cache.D == 64) {
-        if (p.dtype == 1) return two ? launch<1, 64, 2>(p, grid, st) : launch<1, 64, 1>(p, grid, st);
-        return two ? launch<2, 64, 2>(p, grid, st) : launch<2, 64, 1>(p, grid, st);
+        if (p.dtype == 1)
+            return split ? launch<1, 64, true>(p, grid, st) : launch<1, 64, false>(p, grid, st);
+        return split ? launch<2, 64, true>(p, grid, st) : launch<2, 64, false>(p, grid, st);
     }
-    if (p.dtype == 1) return two ? launch<1, 128, 2>(p, grid, st) : launch<1, 128, 1>(p, grid, st);
-    return two ? launch<2, 128, 2>(p, grid, st) : launch<2, 128, 1>(p, grid, st);
+    if (p.dtype == 1)
+        return split ? launch<1, 128, true>(p, grid, st) : launch<1, 128, false>(p, grid, st);
+    return split ? launch<2, 128, true>(p, grid, st) : launch<2, 128, false>(p, grid, st);
 }
 
 }  // namespace specv
