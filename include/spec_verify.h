@@ -108,7 +108,7 @@ enum {
 /*
  * Create a handle for `device` able to serve calls with B <= max_B, N <= max_N (<= 64) and
  * V <= max_V (<= 2^21). Allocates a device workspace of 232 * max_B * max_N + 4 * max_B
- * + 16384 bytes with cudaMalloc (released by spec_verify_destroy). Returns SPEC_ERR_ARG for out-of-range limits,
+ * bytes with cudaMalloc (released by spec_verify_destroy). Returns SPEC_ERR_ARG for out-of-range limits,
  * SPEC_ERR_CUDA if the device cannot be used, SPEC_ERR_WORKSPACE if allocation fails.
  */
 int spec_verify_init(spec_handle *h, int max_B, int max_N, int64_t max_V, int device);
@@ -327,7 +327,9 @@ int spec_kv_load_fp4(spec_handle h, const spec_fp4_cache *cache, int B, const in
  *   (its positions are not attended), else 0;
  *   workspace: device memory of the size that spec_tree_attention_workspace gives for these
  *   sizes, 256-byte aligned; its contents need not be kept or cleared between calls, and calls
- *   that share it or the handle are serialised by the caller.
+ *   that share it are serialised by the caller.
+ * A wait between the kernel's warps that does not end within two seconds gives the request
+ * SPEC_REQ_INTERNAL, in every build.
  * Scores and softmax statistics are float32; probabilities are rounded to 16 bits with the
  * largest of a row scaled near 1, for the product with V, which is exact in 16 bits.
  */

@@ -50,7 +50,6 @@ struct spec_ctx {
     RowPart *piece = nullptr;             // small batches: per-piece row statistics
     int32_t *count = nullptr;             // ... and per-row arrivals (zero between calls)
     int32_t *dbg = nullptr;               // debug builds: violation bits per request [max_B]
-    int32_t *arrive = nullptr;            // tree attention: arrivals of split items (zero between)
     int inject_row = -1, inject_value = 0;   // debug builds: one armed counter injection
     int slots = 0;                        // CTAs of the split row-statistics kernel in a wave
     int sms = 0;                          // streaming multiprocessors of the device
@@ -276,7 +275,7 @@ int spec_verify_init(spec_handle *out, int max_B, int max_N, int64_t max_V, int 
     const size_t rows = (size_t)max_B * max_N;
     const size_t bytes =
         rows * (9 * 4 + kRowChunks * sizeof(float2) + kRowChunks * sizeof(RowPart) + 4) +
-        sizeof(int32_t) * (size_t)max_B + sizeof(int32_t) * kAttnMaxCtas;
+        sizeof(int32_t) * (size_t)max_B;
     if (cudaMalloc(&h->ws, bytes) != cudaSuccess) {
         cudaGetLastError();
         delete h;
@@ -301,12 +300,10 @@ int spec_verify_init(spec_handle *out, int max_B, int max_N, int64_t max_V, int 
     h->dflags = reinterpret_cast<int32_t *>(take(rows * 4));
     h->count = reinterpret_cast<int32_t *>(take(rows * 4));
     h->dbg = reinterpret_cast<int32_t *>(take(sizeof(int32_t) * (size_t)max_B));
-    h->arrive = reinterpret_cast<int32_t *>(take(sizeof(int32_t) * kAttnMaxCtas));
     int sms = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
         cudaMemset(h->count, 0, rows * 4) != cudaSuccess ||
-        cudaMemset(h->dbg, 0, sizeof(int32_t) * (size_t)max_B) != cudaSuccess ||
-        cudaMemset(h->arrive, 0, sizeof(int32_t) * kAttnMaxCtas) != cudaSuccess) {
+        cudaMemset(h->dbg, 0, sizeof(int32_t) * (size_t)max_B) != cudaSuccess) {
         cudaGetLastError();
         cudaFree(h->ws);
         delete h;
@@ -904,8 +901,7 @@ int spec_tree_attention_fp4(spec_handle h, const void *q, int64_t q_stride, cons
     p.out = out;
     p.lse = lse;
     p.status = status;
-    p.ws = static_cast<float *>(workspace);
-    p.arrive = h->arrive;
+    p.workspace = workspace;
     p.sms = h->sms;
     // a page found outside the cache raises the request's status from zero
     if (status && cudaMemsetAsync(status, 0, sizeof(int32_t) * (size_t)B, st) != cudaSuccess)

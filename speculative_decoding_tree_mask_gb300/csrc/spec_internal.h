@@ -287,14 +287,13 @@ struct TreeAttnParams {
     void *out;
     float *lse;
     int32_t *status;
-    float *ws;                    // parts of items (see tree_attn.cuh)
-    int32_t *arrive;              // arrivals of split items [kAttnMaxCtas], zero between calls
+    void *workspace;
+    int4 *notes;                  // in the workspace: cut items [CTAs] (see tree_attn.cuh)
+    float *ws;                    // ... and their parts
     int sms;
 };
 
-constexpr int kAttnMaxCtas = 4096;   // CTAs of an attention launch, at most
-
-// Bytes of parts that a launch with R rows of a K/V head may write.
+// Bytes of notes and parts that a launch with R rows of a K/V head may write.
 int64_t tree_attn_workspace(int R, int D, int sms);
 cudaError_t launch_tree_attn(const TreeAttnParams &p, cudaStream_t st);
 // On the tcgen05 tensor cores: rows of an item, and the launch.

@@ -183,6 +183,14 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// True in one thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(one));
+    return one != 0;
+}
+
 // ---- products --------------------------------------------------------------------------------
 
 // Shared-memory operand descriptor, 128-byte swizzle. K-major: rows of 128 bytes, groups of 8
@@ -196,6 +204,10 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
 constexpr uint32_t mma_desc(int type, int n, bool b_mn_major) {
     return 1u << 4 | (uint32_t)type << 7 | (uint32_t)type << 10 | (b_mn_major ? 1u << 16 : 0u) |
            (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
+}
+// A descriptor's operand moved by `bytes` (a constant: the descriptor's low word takes it).
+__device__ __forceinline__ uint64_t desc_plus(uint64_t desc, int bytes) {
+    return desc + (uint64_t)(bytes >> 4);
 }
 // d (+)= a b^T, 16 deep; one thread issues. a in shared memory or in tensor memory.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,

@@ -59,8 +59,8 @@ struct Smem {
     static constexpr int kFac = kQt + (T == 1 ? kRows * D * 2 : 0);
     static constexpr int kM = kFac + kRows * 4;
     static constexpr int kL = kM + kWarps * kRows * 4;
-    static constexpr int kFlag = kL + kWarps * kRows * 4;                  // join flag, odd nodes
-    static constexpr int kBytes = kFlag + 32;
+    static constexpr int kOdd = kL + kWarps * kRows * 4;
+    static constexpr int kBytes = kOdd + 16;
 };
 
 // 16-byte unit u of position t's codes lies at unit swizzle(t, u).
@@ -186,8 +186,7 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
     float *s_fac = reinterpret_cast<float *>(smem + S::kFac);
     float *s_m = reinterpret_cast<float *>(smem + S::kM);
     float *s_l = reinterpret_cast<float *>(smem + S::kL);
-    int *s_flag = reinterpret_cast<int *>(smem + S::kFlag);
-    unsigned long long *s_odd = reinterpret_cast<unsigned long long *>(smem + S::kFlag + 8);
+    unsigned long long *s_odd = reinterpret_cast<unsigned long long *>(smem + S::kOdd);
     char *ring = smem + warp * kStages * Rg::kBytes;
     const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
     const float k_scale = C.k_scale ? __ldg(C.k_scale) : 1.f;
@@ -196,6 +195,7 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
 
     AttnWalk walk(P, C.H * row_tiles, kTreeCost);
     AttnPart A;
+    bool any = false;
     Acc<D, MT> acc;
 
     while (walk.next(P, A)) {
@@ -722,11 +722,55 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
                 }
             }
         }
-        if (!whole)
-            attn_join<T, D>(P, walk.r, A, head, row0, rows, RT, s_flag, tid, kThreads,
-                            [] { __syncthreads(); });
         __syncthreads();      // shared memory is free for the next item
+        any = true;
     }
+    if (tid == 0) attn_note(P, walk.r, A, any);
+}
+
+// The parts of cut items into the result: a CTA has 256 float4s of an item's rows, a thread one
+// of each part, eight parts' loads in flight together.
+constexpr int kJoinThreads = 256;
+template <int T, int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(TreeAttnParams P, int rows_tile) {
+    grid_dep_wait();
+    const int c0 = blockIdx.y;
+    const int4 note = P.notes[c0];
+    if (note.x < 0) return;
+    const int b = note.x, c1 = note.z, row_tiles = (P.N * P.G + rows_tile - 1) / rows_tile;
+    const int head = note.y / row_tiles, row0 = (note.y - head * row_tiles) * rows_tile;
+    const int rows = min(rows_tile, P.N * P.G - row0);
+    const int i = blockIdx.x * kJoinThreads + threadIdx.x, r = i / (D / 4), d4 = i - r * (D / 4);
+    if (r >= rows) return;
+    float m = kNoMax, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c0; c <= c1; c += 8) {
+        float4 v[8];
+        float pm[8], pl[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int k = min(c + u, c1);
+            const float *part = attn_slot(P, k, k == c0, rows_tile, D);
+            v[u] = __ldcg(reinterpret_cast<const float4 *>(part) + i);
+            pm[u] = __ldcg(part + rows_tile * D + r);
+            pl[u] = __ldcg(part + rows_tile * (D + 1) + r);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (c + u > c1) break;
+            const float mx = fmaxf(m, pm[u]), a = exp2f(m - mx), w = exp2f(pm[u] - mx);
+            o.x = o.x * a + v[u].x * w;
+            o.y = o.y * a + v[u].y * w;
+            o.z = o.z * a + v[u].z * w;
+            o.w = o.w * a + v[u].w * w;
+            l = l * a + pl[u] * w;
+            m = mx;
+        }
+    }
+    const float f = l == 0.f ? 0.f : 1.f / l;
+    const int64_t at = attn_row(P, b, head, row0 + r);
+    store_out4<T>(P.out, at * D + d4 * 4, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
+    if (P.lse && d4 == 0) P.lse[at] = attn_lse(m, l);
 }
 
 // How a call is run: by this file's warps (groups of 16 rows of an item, CTAs an SM holds), or,
@@ -740,8 +784,7 @@ Plan plan(int R, int D, int sms) {
     p.tc = R > 32 && D <= 128;
     p.groups = R > 16 && D <= 128 ? 2 : 1;
     p.rows = p.tc ? tree_attn_tc_rows(R) : 16 * p.groups;
-    const int64_t cap = (int64_t)sms * (p.tc ? 1 : p.groups == 2 || D == 256 ? 2 : 3);
-    p.grid = (int)(cap < kAttnMaxCtas ? cap : kAttnMaxCtas);
+    p.grid = sms * (p.tc ? 1 : p.groups == 2 || D == 256 ? 2 : 3);
     return p;
 }
 
@@ -767,17 +810,42 @@ cudaError_t launch_type(const TreeAttnParams &p, const Plan &n, cudaStream_t st)
 
 }  // namespace
 
+namespace {
+
+int64_t notes_bytes(const Plan &n) { return ((int64_t)n.grid * sizeof(int4) + 255) / 256 * 256; }
+
+template <int T, int D>
+cudaError_t launch_join(const TreeAttnParams &p, const Plan &n, cudaStream_t st) {
+    const dim3 grid((n.rows * (D / 4) + kJoinThreads - 1) / kJoinThreads, n.grid);
+    return launch_dependent(join_kernel<T, D>, grid, dim3(kJoinThreads), 0, st, p, n.rows);
+}
+
+}  // namespace
+
 int64_t tree_attn_workspace(int R, int D, int sms) {
     const Plan n = plan(R, D, sms);
     const int64_t bytes = (int64_t)n.grid * 2 * n.rows * (D + 2) * (int64_t)sizeof(float);
-    return (bytes + 255) / 256 * 256;
+    return notes_bytes(n) + (bytes + 255) / 256 * 256;
 }
 
-cudaError_t launch_tree_attn(const TreeAttnParams &p, cudaStream_t st) {
-    if (p.B <= 0) return cudaSuccess;
-    const Plan n = plan(p.N * p.G, p.cache.D, p.sms);
-    if (n.tc) return launch_tree_attn_tc(p, n.grid, st);
-    return p.dtype == 1 ? launch_type<1>(p, n, st) : launch_type<2>(p, n, st);
+cudaError_t launch_tree_attn(const TreeAttnParams &given, cudaStream_t st) {
+    if (given.B <= 0) return cudaSuccess;
+    TreeAttnParams p = given;
+    const int D = p.cache.D;
+    const Plan n = plan(p.N * p.G, D, p.sms);
+    p.notes = static_cast<int4 *>(p.workspace);
+    p.ws = reinterpret_cast<float *>(static_cast<char *>(p.workspace) + notes_bytes(n));
+    const cudaError_t e = n.tc             ? launch_tree_attn_tc(p, n.grid, st)
+                          : p.dtype == 1 ? launch_type<1>(p, n, st)
+                                         : launch_type<2>(p, n, st);
+    if (e != cudaSuccess) return e;
+    if (p.dtype == 1)
+        return D == 64    ? launch_join<1, 64>(p, n, st)
+               : D == 128 ? launch_join<1, 128>(p, n, st)
+                          : launch_join<1, 256>(p, n, st);
+    return D == 64    ? launch_join<2, 64>(p, n, st)
+           : D == 128 ? launch_join<2, 128>(p, n, st)
+                      : launch_join<2, 256>(p, n, st);
 }
 
 }  // namespace specv

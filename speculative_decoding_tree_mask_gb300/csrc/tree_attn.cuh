@@ -9,8 +9,9 @@
 // wave, whatever the requests' lengths (which only the device knows). A CTA therefore works on
 // end of one item, some whole items, and the start of another. Whole items are finished in
 // place. The parts of an item that a cut goes through are written to the workspace (row sums
-// and maxima and the unnormalised rows, float32); the CTA that arrives last joins them in
-// their order, so the result does not depend on which that is.
+// and maxima and the unnormalised rows, float32), and a second kernel joins them in their
+// order: all SMs share that, where the last CTA to arrive at an item of many parts would take
+// longer for it than for its own part (80 us of 180 for 8 items of 256 rows in 19 parts each).
 #pragma once
 
 #include "fp4_device.cuh"
@@ -129,6 +130,16 @@ __device__ __forceinline__ float *attn_slot(const TreeAttnParams &P, int cta, in
     return P.ws + ((int64_t)cta * 2 + slot) * rows * (d + 2);
 }
 
+// A CTA's note for the joining kernel: the item it began and did not finish (its last), if any,
+// and the CTA that has the item's last part. One thread calls it, at the CTA's end.
+__device__ __forceinline__ void attn_note(const TreeAttnParams &P, const AttnRange &r,
+                                          const AttnPart &last, bool any) {
+    int4 note = make_int4(-1, 0, 0, 0);
+    if (any && last.tile == 0 && last.stop < last.nt)
+        note = make_int4(last.b, last.item, attn_owner(r, last.first + last.nt - 1), 0);
+    P.notes[blockIdx.x] = note;
+}
+
 // Four values of an output row.
 template <int T>
 __device__ __forceinline__ void store_out4(void *out, int64_t e, float4 v) {
@@ -165,74 +176,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 // log sum exp from a maximum in powers of two and a sum.
 __device__ __forceinline__ float attn_lse(float m, float l) {
     return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-}
-
-// The last of an item's parts to arrive joins them. Called by `threads` threads of the CTA
-// (`tid` of them), `sync` their barrier, after they have written their part. Returns after the
-// join, or at once when other parts are still missing.
-template <int T, int D, typename Sync>
-__device__ __forceinline__ void attn_join(const TreeAttnParams &P, const AttnRange &R,
-                                          const AttnPart &A, int head, int row0, int rows,
-                                          int rows_tile, int *s_flag, int tid, int threads,
-                                          Sync sync) {
-    const int c0 = attn_owner(R, A.first), c1 = attn_owner(R, A.first + A.nt - 1);
-    __threadfence();
-    sync();
-    if (tid == 0) {
-        const int seen = atomicAdd(P.arrive + c0, 1);
-        const int last = seen == c1 - c0;
-        if (last) P.arrive[c0] = 0;   // for the next call
-        __threadfence();
-        *s_flag = last;
-    }
-    sync();
-    if (!*s_flag) return;
-    // four float4 of a thread at a time, so that their loads are in flight together
-    constexpr int U = 4;
-    const int n = rows * (D / 4);
-    for (int i0 = tid; i0 < n; i0 += U * threads) {
-        float m[U], l[U];
-        float4 o[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            m[u] = kNoMax;
-            l[u] = 0.f;
-            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll 2
-        for (int c = c0; c <= c1; ++c) {
-            const float *part = attn_slot(P, c, c == c0, rows_tile, D);
-            float4 v[U];
-            float pm[U], pl[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = min(i0 + u * threads, n - 1), r = i / (D / 4);
-                v[u] = __ldcg(reinterpret_cast<const float4 *>(part) + i);
-                pm[u] = __ldcg(part + rows_tile * D + r);
-                pl[u] = __ldcg(part + rows_tile * (D + 1) + r);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const float mx = fmaxf(m[u], pm[u]), a = exp2f(m[u] - mx), w = exp2f(pm[u] - mx);
-                o[u].x = o[u].x * a + v[u].x * w;
-                o[u].y = o[u].y * a + v[u].y * w;
-                o[u].z = o[u].z * a + v[u].z * w;
-                o[u].w = o[u].w * a + v[u].w * w;
-                l[u] = l[u] * a + pl[u] * w;
-                m[u] = mx;
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * threads, r = i / (D / 4), d4 = i - r * (D / 4);
-            if (i >= n) break;
-            const float f = l[u] == 0.f ? 0.f : 1.f / l[u];
-            const int64_t at = attn_row(P, A.b, head, row0 + r);
-            store_out4<T>(P.out, at * D + d4 * 4,
-                          make_float4(o[u].x * f, o[u].y * f, o[u].z * f, o[u].w * f));
-            if (P.lse && d4 == 0) P.lse[at] = attn_lse(m[u], l[u]);
-        }
-    }
 }
 
 }  // namespace specv

@@ -8,8 +8,9 @@
 //   convert  (4 warps) a position each: codes to 16-bit elements in shared memory, exact, laid
 //            out for the tensor core (128-byte swizzle; K contiguous along D, and V as it is,
 //            read transposed). K becomes the type of Q, V halves; two tiles of each in a ring;
-//   multiply (1 thread) S = Q K^T and O += P V, sums in tensor memory: S and O twice, up to
-//            all 512 columns; P overwrites the half of S it came from;
+//   multiply (2 threads, one for each softmax group) S = Q K^T and O += P V, sums in tensor
+//            memory: S and O twice, up to all 512 columns; P overwrites the half of S it came
+//            from. One thread for both groups could not issue as fast as the products end;
 //   softmax  (2 groups of 4 warps) S to P, a row a thread, no exchange between threads, the
 //            running maximum and sum in registers. A maximum is followed only once it rises by
 //            2^8 (then O is rescaled in place), which is rare.
@@ -32,7 +33,7 @@ constexpr float kRescale = 8.f;
 constexpr int kConvert = 128;     // converting threads
 
 constexpr int kSoftmax = 256;     // threads of the two softmax groups
-constexpr int kThreads = kSoftmax + kConvert + 128;   // the last warpgroup: one warp multiplies
+constexpr int kThreads = kSoftmax + kConvert + 128;   // the last warpgroup: two warps multiply
 constexpr int kMmaWarp = (kSoftmax + kConvert) / 32;
 constexpr int kTreeCost = 4;      // the tree's tile and an item's rest, in context tiles
 
@@ -47,8 +48,13 @@ struct Tc {
     static constexpr int kColumns = 512;                         // 2 (128 + D), a power of two
 };
 
+template <int n>
+struct Const {
+    static constexpr int value = n;
+};
+
 struct Words {
-    uint64_t q_full, q_free, k_full[2], k_free[2], v_full[2], v_free[2], drain;
+    uint64_t q_full, q_free, k_full[2], k_free[2], v_full[2], v_free[2], drain[2];
     uint64_t s_full[2], p_full[2], o_full[2];                    // of a softmax group
     // Positions of a K/V tile that are attended. A tile's words are written again for the
     // fourth after it, once the scores of the second after it are done: those were issued
@@ -56,7 +62,7 @@ struct Words {
     unsigned seen[4][4];
     unsigned long long odd[4];    // tree nodes with NaN or infinities in V; part by part likewise
     uint32_t tmem;
-    int gave_up, flag;
+    int gave_up;
     int state[2];                 // SPLIT: 0 no tile, 1 O in the cache's units, 2 in V's
     float top[2][128], sum[2][128];
 };
@@ -235,13 +241,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
         bar_init(&W.q_full, kConvert);
-        bar_init(&W.q_free, 1);
-        bar_init(&W.drain, 1);
+        bar_init(&W.q_free, 2);
         for (int i = 0; i < 2; ++i) {
             bar_init(&W.k_full[i], kConvert);
             bar_init(&W.v_full[i], kConvert);
-            bar_init(&W.k_free[i], 1);
-            bar_init(&W.v_free[i], 1);
+            bar_init(&W.k_free[i], SPLIT ? 1 : 2);
+            bar_init(&W.v_free[i], SPLIT ? 1 : 2);
+            bar_init(&W.drain[i], 1);
             bar_init(&W.s_full[i], 1);
             bar_init(&W.p_full[i], 128);
             bar_init(&W.o_full[i], 1);
@@ -261,84 +267,92 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t done = 0, parts = 0;     // tiles and parts before this one: the phases count them
     AttnPart A;
 
-    // Launched with 128 registers a thread, 16 warps: 8 x 184 + 4 x 104 + 4 x 40 = 16 x 128.
+    // Launched with 128 registers a thread, 16 warps: 8 x 176 + 4 x 112 + 4 x 48 = 16 x 128.
     if (tid >= kSoftmax + kConvert) {
-        fewer_registers<40>();
-        // ---- multiply ----
-        // A job is a tile for a softmax group. Job j: tile j for group j % 2 (SPLIT), or tile
-        // j / 2 for group j % 2. Scores are issued two jobs ahead of the products with V.
-        if (warp == kMmaWarp) {
-          AttnWalk walk(P, C.H * row_tiles, kTreeCost);     // by the whole warp
-          if (lane == 0) {
-            uint32_t jobs[2] = {0, 0};   // of a group so far
+        fewer_registers<48>();
+        // ---- multiply: for softmax group m, its tiles: all, or (SPLIT) every other one ----
+        // The whole warp runs the loop and waits, one thread of it issues: what the products
+        // are given is then the same in all of the warp, as their uniform operands want it.
+        const int m = warp - kMmaWarp;
+        if (m < 2) {
+            AttnWalk walk(P, C.H * row_tiles, kTreeCost);
+            const bool lead = elect_one();
+            constexpr int kStep = SPLIT ? 2 : 1;
+            const uint32_t p = s_at(m), o = o_at(m);
+            uint32_t jobs = 0;           // tiles of this group so far
             bool ok = true;
             while (ok && walk.next(P, A)) {
-                const int n = A.stop - A.tile, tree = A.nt - 1 - A.tile;
-                const int count = SPLIT ? n : 2 * n;
-                auto scores = [&](int j) {
-                    const int m = j & 1, i = SPLIT ? j : j >> 1;
+                const int n = A.stop - A.tile, tree = A.nt - 1 - A.tile, i0 = SPLIT ? m : 0;
+                auto scores = [&](int i) {
                     const uint32_t c = done + i;
-                    ok = ok && bar_wait(&W.k_full[c & 1], (c >> 1) & 1, gave_up);
+                    ok = ok && warp_wait(&W.k_full[c & 1], (c >> 1) & 1, gave_up);
                     if (!ok) return;
                     tc_fence_after();
-                    const uint32_t a = base + (SPLIT ? 0 : m * C_::kOperand);
-                    const uint32_t k = base + C_::kK + (c & 1) * C_::kOperand;
+                    const uint64_t a = smem_desc(base + (SPLIT ? 0 : m * C_::kOperand), 16, 1024);
+                    const uint64_t k =
+                        smem_desc(base + C_::kK + (c & 1) * C_::kOperand, 16, 1024);
                     const uint32_t d = i == tree ? mma_desc(kType, 64, false)
                                                  : mma_desc(kType, 128, false);
+                    if (lead) {
 #pragma unroll
-                    for (int s = 0; s < KS; ++s) {
-                        const uint32_t off = (s >> 2) * (128 * 128) + (s & 3) * 32;
-                        mma_ss(s_at(m), smem_desc(a + off, 16, 1024), smem_desc(k + off, 16, 1024),
-                               d, s > 0);
+                        for (int s = 0; s < KS; ++s) {
+                            const int off = (s >> 2) * (128 * 128) + (s & 3) * 32;
+                            mma_ss(p, desc_plus(a, off), desc_plus(k, off), d, s > 0);
+                        }
+                        mma_commit(&W.s_full[m]);
+                        mma_commit(&W.k_free[c & 1]);
+                        if (i + kStep >= n) mma_commit(&W.q_free);
                     }
-                    mma_commit(&W.s_full[m]);
-                    if (SPLIT || m == 1) mma_commit(&W.k_free[c & 1]);
-                    if (j == count - 1) mma_commit(&W.q_free);
+                    __syncwarp();
                 };
-                ok = ok && bar_wait(&W.q_full, parts & 1, gave_up);
-                scores(0);
-                if (count > 1) scores(1);
-                for (int j = 0; ok && j < count; ++j) {
-                    const int m = j & 1, i = SPLIT ? j : j >> 1;
+                ok = ok && warp_wait(&W.q_full, parts & 1, gave_up);
+                if (i0 < n)
+                    scores(i0);
+                else if (lead)
+                    bar_arrive(&W.q_free);
+                for (int i = i0; ok && i < n; i += kStep) {
                     const uint32_t c = done + i;
-                    const uint32_t v = base + C_::kV + (c & 1) * C_::kOperand;
-                    ok = bar_wait(&W.v_full[c & 1], (c >> 1) & 1, gave_up) &&
-                         bar_wait(&W.p_full[m], jobs[m] & 1, gave_up);
+                    ok = warp_wait(&W.v_full[c & 1], (c >> 1) & 1, gave_up) &&
+                         warp_wait(&W.p_full[m], jobs & 1, gave_up);
                     if (!ok) break;
-                    ++jobs[m];
+                    ++jobs;
                     tc_fence_after();
-                    const bool add = SPLIT ? j > 1 : i > 0;
-                    if (i == tree) {
-                        // 64 nodes; bfloat16: the two terms of P, 64 columns apart
+                    const uint64_t v =
+                        smem_desc(base + C_::kV + (c & 1) * C_::kOperand, 128 * 128, 1024);
+                    const bool add = i > i0;
+                    if (lead) {
+                        if (i == tree) {
+                            // 64 nodes; bfloat16: the two terms of P, 64 columns apart
 #pragma unroll
-                        for (int s = 0; s < (T == 1 ? 8 : 4); ++s)
-                            mma_ts(o_at(m), s_at(m) + (s >> 2) * 64 + (s & 3) * 8,
-                                   smem_desc(v + (s & 3) * 2048, 128 * 128, 1024),
-                                   mma_desc(kType, D, true), add || s > 0);
-                    } else {
+                            for (int s = 0; s < (T == 1 ? 8 : 4); ++s)
+                                mma_ts(o, p + (s >> 2) * 64 + (s & 3) * 8,
+                                       desc_plus(v, (s & 3) * 2048), mma_desc(kType, D, true),
+                                       add || s > 0);
+                        } else {
 #pragma unroll
-                        for (int s = 0; s < 8; ++s)
-                            mma_ts(o_at(m), s_at(m) + s * 8,
-                                   smem_desc(v + s * 2048, 128 * 128, 1024), mma_desc(0, D, true),
-                                   add || s > 0);
+                            for (int s = 0; s < 8; ++s)
+                                mma_ts(o, p + s * 8, desc_plus(v, s * 2048), mma_desc(0, D, true),
+                                       add || s > 0);
+                        }
+                        mma_commit(&W.o_full[m]);
+                        mma_commit(&W.v_free[c & 1]);
                     }
-                    mma_commit(&W.o_full[m]);
-                    if (SPLIT || m == 1) mma_commit(&W.v_free[c & 1]);
-                    if (j + 2 < count) scores(j + 2);
+                    __syncwarp();
+                    if (i + kStep < n) scores(i + kStep);
                 }
                 done += n;
                 ++parts;
             }
             if (!ok) {
                 // products in flight end before tensor memory is freed
-                mma_commit(&W.drain);
-                for (int i = 0; i < (1 << 20) && !bar_try(&W.drain, 0); ++i) {
+                if (lead) mma_commit(&W.drain[m]);
+                for (int i = 0; i < (1 << 20) && !bar_try(&W.drain[m], 0); ++i) {
                 }
             }
-          }
+            __syncwarp();
         }
     } else if (tid >= kSoftmax) {
-        fewer_registers<104>();
+        fewer_registers<112>();
         // ---- convert ----
         const int t = tid - kSoftmax, R = P.N * P.G;
         AttnWalk walk(P, C.H * row_tiles, kTreeCost);
@@ -356,20 +370,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                            ? __ldg(table + (uint32_t)p / (uint32_t)C.block_size)
                            : -1;
             };
-            Row4<D> kr, vr;
-            bool ok = false;
-            auto fetch = [&](int i, int blk) {
+            // two tiles' rows are in flight: set i % 2 is tile i's
+            Row4<D> kr[2], vr[2];
+            uint32_t row[2];
+            bool ok[2];
+            auto find = [&](int i, int blk, int set) {
                 const int p = (A.tile + i) * kTile + t;
-                ok = blk >= 0 && blk < C.num_blocks;
-                const uint32_t row =
-                    ok ? fp4_row(C, blk, p % (uint32_t)C.block_size, head) : 0u;
-                if (i < n && i < tree && p < ctx && !ok && P.status)
+                ok[set] = blk >= 0 && blk < C.num_blocks;
+                row[set] = ok[set] ? fp4_row(C, blk, p % (uint32_t)C.block_size, head) : 0u;
+                if (i < n && i < tree && p < ctx && !ok[set] && P.status)
                     P.status[b] = SPEC_REQ_BAD_SLOT;
-                load_row<D>(C.k, C.k_sf, row, ok, kr);
-                load_row<D>(C.v, C.v_sf, row, ok, vr);
             };
-            const int page0 = page(0);
-            int next = page(1);
+            const int page0 = page(0), page1 = page(1);
+            int next = page(2);
             go = go && warp_wait(&W.q_free, (parts & 1) ^ 1, gave_up);
             if (go) {
                 // Q: rows of an operand a thread, neighbours' chunks side by side
@@ -390,7 +403,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<uint4 *>(smem + to) = load8(from, false);
                 }
             }
-            fetch(0, page0);
+            find(0, page0, 0);
+            load_row<D>(C.k, C.k_sf, row[0], ok[0], kr[0]);
+            load_row<D>(C.v, C.v_sf, row[0], ok[0], vr[0]);
+            find(1, page1, 1);
+            load_row<D>(C.k, C.k_sf, row[1], ok[1], kr[1]);
+            load_row<D>(C.v, C.v_sf, row[1], ok[1], vr[1]);
             if (t == 0) W.odd[parts & 3] = 0ull;
             named_sync(2, kConvert);
             auto q_done = [&]() {
@@ -398,88 +416,101 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_async_smem();
                 if (go) bar_arrive(&W.q_full);
             };
-            for (int i = 0; i < n; ++i) {
+            auto step = [&](int i, auto set_) {
+                constexpr int set = decltype(set_)::value;
                 const uint32_t c = done + i;
                 const int st = c & 1;
                 const uint32_t parity = ((c >> 1) & 1) ^ 1;
                 char *ks = smem + C_::kK + st * C_::kOperand;
                 char *vs = smem + C_::kV + st * C_::kOperand;
-                if (i == tree) {
-                    // the nodes' own rows, zeros up to 64; two threads a row, half of it each
-                    const int r = t >> 1, j0 = (t & 1) * (D / 16);
-                    const int64_t row = (int64_t)b * P.N + min(r, P.N - 1);
-                    const unsigned short *k = reinterpret_cast<const unsigned short *>(P.k) +
-                                              row * P.k_stride + head * D + j0 * 8;
-                    const unsigned short *v = reinterpret_cast<const unsigned short *>(P.v) +
-                                              row * P.v_stride + head * D + j0 * 8;
-                    uint4 x[D / 16];
-                    auto rows_in = [&](const unsigned short *from) {
-#pragma unroll
-                        for (int j = 0; j < D / 16; ++j)
-                            x[j] = r < P.N ? load8(from + j * 8, vec) : make_uint4(0, 0, 0, 0);
-                    };
-                    rows_in(k);
-                    go = go && warp_wait(&W.k_free[st], parity, gave_up);
-                    if (go) {
-#pragma unroll
-                        for (int j = 0; j < D / 16; ++j)
-                            *reinterpret_cast<uint4 *>(ks + chunk_at(r, j0 + j)) = x[j];
-                        fence_async_smem();
-                        bar_arrive(&W.k_full[st]);
-                    }
-                    if (i == 0) q_done();
-                    rows_in(v);
-                    bool odd = false;
-#pragma unroll
-                    for (int j = 0; j < D / 16; ++j) {
-                        uint32_t *w = reinterpret_cast<uint32_t *>(&x[j]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (odd16<T>(w[e])) {
-                                w[e] &= 0xffff0000u;
-                                odd = true;
-                            }
-                            if (odd16<T>(w[e] >> 16)) {
-                                w[e] &= 0xffffu;
-                                odd = true;
-                            }
-                        }
-                    }
-                    if (odd) atomicOr(&W.odd[parts & 3], 1ull << r);
-                    go = go && warp_wait(&W.v_free[st], parity, gave_up);
-                    if (go) {
-#pragma unroll
-                        for (int j = 0; j < D / 16; ++j)
-                            *reinterpret_cast<uint4 *>(vs + chunk_at(r, j0 + j)) = x[j];
-                        fence_async_smem();
-                        bar_arrive(&W.v_full[st]);
-                    }
-                    break;        // it is the last
-                }
-                const unsigned seen = __ballot_sync(0xffffffffu, ok);
+                const unsigned seen = __ballot_sync(0xffffffffu, ok[set]);
+                const int cur = next;
+                next = page(i + 3);
                 go = go && warp_wait(&W.k_free[st], parity, gave_up);
                 if (go) {
                     if (lane == 0) W.seen[c & 3][t >> 5] = seen;
-                    convert_row<D, T == 1>(kr, ks, t);
+                    convert_row<D, T == 1>(kr[set], ks, t);
+                    fence_async_smem();
+                    bar_arrive(&W.k_full[st]);
+                }
+                find(i + 2, cur, set);
+                load_row<D>(C.k, C.k_sf, row[set], ok[set], kr[set]);
+                if (i == 0) q_done();
+                go = go && warp_wait(&W.v_free[st], parity, gave_up);
+                if (go) {
+                    convert_row<D, false>(vr[set], vs, t);
+                    fence_async_smem();
+                    bar_arrive(&W.v_full[st]);
+                }
+                load_row<D>(C.v, C.v_sf, row[set], ok[set], vr[set]);
+            };
+            const int contexts = min(n, tree);
+            for (int i = 0; i < contexts; i += 2) {
+                step(i, Const<0>{});
+                if (i + 1 < contexts) step(i + 1, Const<1>{});
+            }
+            if (tree < n) {
+                const int i = tree;
+                const uint32_t c = done + i;
+                const int st = c & 1;
+                const uint32_t parity = ((c >> 1) & 1) ^ 1;
+                char *ks = smem + C_::kK + st * C_::kOperand;
+                char *vs = smem + C_::kV + st * C_::kOperand;
+                    // the nodes' own rows, zeros up to 64; two threads a row, half of it each
+                const int r = t >> 1, j0 = (t & 1) * (D / 16);
+                const int64_t row = (int64_t)b * P.N + min(r, P.N - 1);
+                const unsigned short *k = reinterpret_cast<const unsigned short *>(P.k) +
+                                          row * P.k_stride + head * D + j0 * 8;
+                const unsigned short *v = reinterpret_cast<const unsigned short *>(P.v) +
+                                          row * P.v_stride + head * D + j0 * 8;
+                uint4 x[D / 16];
+                auto rows_in = [&](const unsigned short *from) {
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j)
+                        x[j] = r < P.N ? load8(from + j * 8, vec) : make_uint4(0, 0, 0, 0);
+                };
+                rows_in(k);
+                go = go && warp_wait(&W.k_free[st], parity, gave_up);
+                if (go) {
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j)
+                        *reinterpret_cast<uint4 *>(ks + chunk_at(r, j0 + j)) = x[j];
                     fence_async_smem();
                     bar_arrive(&W.k_full[st]);
                 }
                 if (i == 0) q_done();
+                rows_in(v);
+                bool odd = false;
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    uint32_t *w = reinterpret_cast<uint32_t *>(&x[j]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (odd16<T>(w[e])) {
+                            w[e] &= 0xffff0000u;
+                            odd = true;
+                        }
+                        if (odd16<T>(w[e] >> 16)) {
+                            w[e] &= 0xffffu;
+                            odd = true;
+                        }
+                    }
+                }
+                if (odd) atomicOr(&W.odd[parts & 3], 1ull << r);
                 go = go && warp_wait(&W.v_free[st], parity, gave_up);
                 if (go) {
-                    convert_row<D, false>(vr, vs, t);
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j)
+                        *reinterpret_cast<uint4 *>(vs + chunk_at(r, j0 + j)) = x[j];
                     fence_async_smem();
                     bar_arrive(&W.v_full[st]);
                 }
-                const int cur = next;
-                next = page(i + 2);
-                fetch(i + 1, cur);
             }
             done += n;
             ++parts;
         }
     } else {
-        more_registers<184>();
+        more_registers<176>();
         // ---- softmax: this thread's row. A wait that gives up is followed by none, but the
         // groups' barriers are kept.
         const int m = warp >> 2, R = P.N * P.G;
@@ -647,12 +678,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before();
             if (SPLIT) named_sync(1, kSoftmax);    // both Os have been read
-            if (!whole)
-                attn_join<T, D>(P, walk.r, A, head, row0, rows, RT, &W.flag, tid, kSoftmax,
-                                [] { named_sync(1, kSoftmax); });
             done += n;
             ++parts;
         }
+        if (tid == 0) attn_note(P, walk.r, A, parts > 0);
     }
     tc_fence_before();
     __syncthreads();
