@@ -15,10 +15,12 @@
 //            running maximum and sum in registers. A maximum is followed only once it rises by
 //            2^8 (then O is rescaled in place), which is rare.
 //
-// The two softmax groups keep the tensor core busy: it multiplies for one while the other works.
-// Items of more than 128 rows give each group 128 rows of its own and every tile; items of up
-// to 128 rows give both groups all rows and every other tile (SPLIT), and the two results are
-// joined at the end: tensor memory is read by lanes, and both groups own the same lanes.
+// A softmax group takes 64 positions at a time, out of two S in turn: while it works on one, the
+// tensor core finishes the products with the P before and makes the next scores (with one S of
+// 128 columns the group waited about as long as it worked). Items of more than 128 rows give
+// each group 128 rows of its own and all positions; items of up to 128 rows give both groups all
+// rows and half of each tile's positions (SPLIT), and the two results are joined at the end:
+// tensor memory is read by lanes, and both groups own the same lanes.
 // The tree's own nodes are the last tile of an item: their rows are copied instead of converted
 // and P is multiplied in their type; for bfloat16 as a sum of two terms, since eight bits are
 // too few. Every wait gives up after two seconds; the request's status then says so.
@@ -55,7 +57,7 @@ struct Const {
 
 struct Words {
     uint64_t q_full, q_free, k_full[2], k_free[2], v_full[2], v_free[2], drain[2];
-    uint64_t s_full[2], p_full[2], o_full[2];                    // of a softmax group
+    uint64_t s_full[2][2], p_full[2][2], o_full[2];              // of a softmax group; buffers
     // Positions of a K/V tile that are attended. A tile's words are written again for the
     // fourth after it, once the scores of the second after it are done: those were issued
     // after its P was waited for.
@@ -162,6 +164,14 @@ __device__ __forceinline__ float value16(uint32_t x) {
     return T == 1 ? __uint_as_float(x << 16) : __half2float(__ushort_as_half((unsigned short)x));
 }
 
+constexpr int kHalf = 64 * 128;   // bytes from the first 64 rows of an operand to the others
+
+// Jobs of softmax group m in a part of n tiles, the tree's at `tree` (at or past n: not in it).
+__device__ __forceinline__ int group_jobs(bool split, int m, int n, int tree) {
+    const int contexts = min(n, tree);
+    return split ? contexts + (tree < n && m == 0) : 2 * contexts + (tree < n);
+}
+
 // A wait of a whole warp: all of it goes on or none.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *gave_up) {
     return __all_sync(0xffffffffu, bar_wait(bar, parity, gave_up));
@@ -171,20 +181,20 @@ __device__ __forceinline__ void cp_async16(uint32_t smem, const void *gmem) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
 }
 
-// One tile's S to P, the thread's row: kTree, 64 nodes to type T; else 128 positions to halves.
+// S to P of 64 positions, the thread's row: to halves, or (kTree) of 64 nodes to type T.
 template <int T, bool kTree>
 struct RowTile {
-    static constexpr int kChunks = kTree ? 2 : 4;
+    static constexpr int kChunks = 2;
     uint32_t s[kChunks][32];
 
     // The scores, -inf where `see` has no bit; returns their largest.
-    __device__ __forceinline__ float load(uint32_t s_tm, const unsigned (&see)[4]) {
+    __device__ __forceinline__ float load(uint32_t s_tm, const unsigned (&see)[2]) {
 #pragma unroll
         for (int q = 0; q < kChunks; ++q) tmem_ld32(s_tm + q * 32, s[q]);
         tmem_wait_ld(s[0]);
 #pragma unroll
         for (int q = 1; q < kChunks; ++q) tmem_loaded(s[q]);
-        if (kTree || (see[0] & see[1] & see[2] & see[3]) != 0xffffffffu) {
+        if (kTree || (see[0] & see[1]) != 0xffffffffu) {
 #pragma unroll
             for (int q = 0; q < kChunks; ++q)
 #pragma unroll
@@ -195,7 +205,9 @@ struct RowTile {
 #pragma unroll
         for (int q = 0; q < kChunks; ++q)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) big[e & 3] = fmaxf(big[e & 3], __uint_as_float(s[q][e]));
+            for (int e = 0; e < 32; e += 2)
+                big[e / 2 & 3] = fmaxf(fmaxf(big[e / 2 & 3], __uint_as_float(s[q][e])),
+                                       __uint_as_float(s[q][e + 1]));
         return fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
     }
     // P = 2^(f s - top) over the scores in tensor memory; returns the row's sum.
@@ -218,8 +230,8 @@ struct RowTile {
                 if (kTree && T == 1) lo[e / 2] = pack2<1>(a - bf_lo(h), b - bf_hi(h));
             }
             tmem_st16(s_tm + q * 16, s[q]);
-            // what bfloat16 leaves, behind the 64 columns of scores
-            if (kTree && T == 1) tmem_st16(s_tm + 64 + q * 16, lo);
+            // what bfloat16 leaves, behind the 32 columns of P
+            if (kTree && T == 1) tmem_st16(s_tm + 32 + q * 16, lo);
         }
         float a, b;
         unpack_f32x2(add_f32x2(sum[0], sum[1]), a, b);
@@ -245,12 +257,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             bar_init(&W.k_full[i], kConvert);
             bar_init(&W.v_full[i], kConvert);
-            bar_init(&W.k_free[i], SPLIT ? 1 : 2);
-            bar_init(&W.v_free[i], SPLIT ? 1 : 2);
+            bar_init(&W.k_free[i], 2);
+            bar_init(&W.v_free[i], 2);
             bar_init(&W.drain[i], 1);
-            bar_init(&W.s_full[i], 1);
-            bar_init(&W.p_full[i], 128);
             bar_init(&W.o_full[i], 1);
+            for (int j = 0; j < 2; ++j) {
+                bar_init(&W.s_full[i][j], 1);
+                bar_init(&W.p_full[i][j], 128);
+            }
         }
         W.gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -261,85 +275,100 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = W.tmem;
     volatile int *gave_up = &W.gave_up;
-    // tensor memory of softmax group m: S (and P over it) at 128 m, O behind both
+    // tensor memory of softmax group m: two S of 64 columns (and P over each) at 128 m, O behind
+    // both groups'
     auto s_at = [&](int m) { return tmem + 128 * m; };
     auto o_at = [&](int m) { return tmem + 256 + D * m; };
     uint32_t done = 0, parts = 0;     // tiles and parts before this one: the phases count them
     AttnPart A;
 
-    // Launched with 128 registers a thread, 16 warps: 8 x 176 + 4 x 112 + 4 x 48 = 16 x 128.
+    // Launched with 128 registers a thread, 16 warps: 8 x 128 + 4 x 200 + 4 x 56 = 16 x 128.
     if (tid >= kSoftmax + kConvert) {
-        fewer_registers<48>();
-        // ---- multiply: for softmax group m, its tiles: all, or (SPLIT) every other one ----
+        fewer_registers<56>();
+        // ---- multiply: for softmax group m. A job is 64 positions (or nodes): two of a tile,
+        // one (the group's) if SPLIT, and one of the tree's tile, which SPLIT leaves to group 0.
         // The whole warp runs the loop and waits, one thread of it issues: what the products
         // are given is then the same in all of the warp, as their uniform operands want it.
         const int m = warp - kMmaWarp;
         if (m < 2) {
             AttnWalk walk(P, C.H * row_tiles, kTreeCost);
             const bool lead = elect_one();
-            constexpr int kStep = SPLIT ? 2 : 1;
-            const uint32_t p = s_at(m), o = o_at(m);
-            uint32_t jobs = 0;           // tiles of this group so far
+            const uint32_t o = o_at(m);
+            uint32_t jobs = 0;           // of this group before this part
             bool ok = true;
             while (ok && walk.next(P, A)) {
-                const int n = A.stop - A.tile, tree = A.nt - 1 - A.tile, i0 = SPLIT ? m : 0;
-                auto scores = [&](int i) {
-                    const uint32_t c = done + i;
+                const int n = A.stop - A.tile, tree = A.nt - 1 - A.tile;
+                const int count = group_jobs(SPLIT, m, n, tree);
+                auto scores = [&](int j) {
+                    const int i = SPLIT ? j : j >> 1, half = SPLIT ? m : j & 1;
+                    const uint32_t c = done + i, buf = (jobs + j) & 1;
                     ok = ok && warp_wait(&W.k_full[c & 1], (c >> 1) & 1, gave_up);
                     if (!ok) return;
                     tc_fence_after();
                     const uint64_t a = smem_desc(base + (SPLIT ? 0 : m * C_::kOperand), 16, 1024);
-                    const uint64_t k =
-                        smem_desc(base + C_::kK + (c & 1) * C_::kOperand, 16, 1024);
-                    const uint32_t d = i == tree ? mma_desc(kType, 64, false)
-                                                 : mma_desc(kType, 128, false);
+                    const uint64_t k = smem_desc(
+                        base + C_::kK + (c & 1) * C_::kOperand + half * kHalf, 16, 1024);
+                    const uint32_t s = s_at(m) + buf * 64;
                     if (lead) {
 #pragma unroll
-                        for (int s = 0; s < KS; ++s) {
-                            const int off = (s >> 2) * (128 * 128) + (s & 3) * 32;
-                            mma_ss(p, desc_plus(a, off), desc_plus(k, off), d, s > 0);
+                        for (int d = 0; d < KS; ++d) {
+                            const int off = (d >> 2) * (128 * 128) + (d & 3) * 32;
+                            mma_ss(s, desc_plus(a, off), desc_plus(k, off),
+                                   mma_desc(kType, 64, false), d > 0);
                         }
-                        mma_commit(&W.s_full[m]);
-                        mma_commit(&W.k_free[c & 1]);
-                        if (i + kStep >= n) mma_commit(&W.q_free);
+                        mma_commit(&W.s_full[m][buf]);
+                        if (SPLIT || half == 1 || i == tree) mma_commit(&W.k_free[c & 1]);
+                        if (j == count - 1) mma_commit(&W.q_free);
                     }
                     __syncwarp();
                 };
                 ok = ok && warp_wait(&W.q_full, parts & 1, gave_up);
-                if (i0 < n)
-                    scores(i0);
-                else if (lead)
-                    bar_arrive(&W.q_free);
-                for (int i = i0; ok && i < n; i += kStep) {
-                    const uint32_t c = done + i;
+                if (count > 0) scores(0);
+                if (count > 1) scores(1);
+                if (count == 0 && ok && lead) bar_arrive(&W.q_free);
+                __syncwarp();
+                for (int j = 0; ok && j < count; ++j) {
+                    const int i = SPLIT ? j : j >> 1, half = SPLIT ? m : j & 1;
+                    const uint32_t c = done + i, buf = (jobs + j) & 1;
                     ok = warp_wait(&W.v_full[c & 1], (c >> 1) & 1, gave_up) &&
-                         warp_wait(&W.p_full[m], jobs & 1, gave_up);
+                         warp_wait(&W.p_full[m][buf], ((jobs + j) >> 1) & 1, gave_up);
                     if (!ok) break;
-                    ++jobs;
                     tc_fence_after();
-                    const uint64_t v =
-                        smem_desc(base + C_::kV + (c & 1) * C_::kOperand, 128 * 128, 1024);
-                    const bool add = i > i0;
+                    const uint64_t v = smem_desc(
+                        base + C_::kV + (c & 1) * C_::kOperand + half * kHalf, 128 * 128, 1024);
+                    const uint32_t p = s_at(m) + buf * 64;
                     if (lead) {
                         if (i == tree) {
-                            // 64 nodes; bfloat16: the two terms of P, 64 columns apart
+                            // bfloat16: the two terms of P, 32 columns each
 #pragma unroll
                             for (int s = 0; s < (T == 1 ? 8 : 4); ++s)
-                                mma_ts(o, p + (s >> 2) * 64 + (s & 3) * 8,
-                                       desc_plus(v, (s & 3) * 2048), mma_desc(kType, D, true),
-                                       add || s > 0);
+                                mma_ts(o, p + s * 8, desc_plus(v, (s & 3) * 2048),
+                                       mma_desc(kType, D, true), j > 0 || s > 0);
                         } else {
 #pragma unroll
-                            for (int s = 0; s < 8; ++s)
+                            for (int s = 0; s < 4; ++s)
                                 mma_ts(o, p + s * 8, desc_plus(v, s * 2048), mma_desc(0, D, true),
-                                       add || s > 0);
+                                       j > 0 || s > 0);
                         }
                         mma_commit(&W.o_full[m]);
-                        mma_commit(&W.v_free[c & 1]);
+                        if (SPLIT || half == 1 || i == tree) mma_commit(&W.v_free[c & 1]);
                     }
                     __syncwarp();
-                    if (i + kStep < n) scores(i + kStep);
+                    if (j + 2 < count) scores(j + 2);
                 }
+                if (SPLIT && m == 1 && tree < n && ok) {
+                    // the tree's tile passes this group by. It is there, so its places' earlier
+                    // phases are over, and this arrival counts for the right one.
+                    const uint32_t c = done + tree;
+                    ok = warp_wait(&W.k_full[c & 1], (c >> 1) & 1, gave_up) &&
+                         warp_wait(&W.v_full[c & 1], (c >> 1) & 1, gave_up);
+                    if (ok && lead) {
+                        bar_arrive(&W.k_free[c & 1]);
+                        bar_arrive(&W.v_free[c & 1]);
+                    }
+                    __syncwarp();
+                }
+                jobs += count;
                 done += n;
                 ++parts;
             }
@@ -352,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         }
     } else if (tid >= kSoftmax) {
-        fewer_registers<112>();
+        more_registers<200>();
         // ---- convert ----
         const int t = tid - kSoftmax, R = P.N * P.G;
         AttnWalk walk(P, C.H * row_tiles, kTreeCost);
@@ -510,13 +539,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++parts;
         }
     } else {
-        more_registers<176>();
         // ---- softmax: this thread's row. A wait that gives up is followed by none, but the
         // groups' barriers are kept.
         const int m = warp >> 2, R = P.N * P.G;
         const int r = (SPLIT ? 0 : m * 128) + (warp & 3) * 32 + lane;    // of the item
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t s_tm = s_at(m) + lanes, o_tm = o_at(m) + lanes;
+        const uint32_t o_tm = o_at(m) + lanes;
         const float v_scale = C.v_scale ? __ldg(C.v_scale) : 1.f;
         const float unit = P.scale * kLog2e;
         const float cache_unit = unit * (C.k_scale ? __ldg(C.k_scale) : 1.f);
@@ -533,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 live ? __ldg(P.mask + (int64_t)b * P.N + (row0 + r) / P.G) &
                            (P.N < 64 ? (1ull << P.N) - 1ull : ~0ull)
                      : 0ull;
-            int mine = 0;             // tiles of this group in this part
+            int mine = 0;             // jobs of this group in this part, so far
             // follows the maximum x; `scale` O where it stands
             auto follow = [&](float x, bool units) {
                 const bool raise = __any_sync(0xffffffffu, x > top + kRescale);
@@ -560,23 +588,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_st16(o_tm + q * 16, o);
                 }
             };
-            for (int i = SPLIT ? m : 0; i < n; i += SPLIT ? 2 : 1) {
-                const uint32_t c = done + i;
-                go = go && warp_wait(&W.s_full[m], jobs & 1, gave_up);
+            const int count = group_jobs(SPLIT, m, n, tree);
+            for (int j = 0; j < count; ++j) {
+                const int i = SPLIT ? j : j >> 1, half = SPLIT ? m : j & 1;
+                const uint32_t buf = jobs & 1, s_tm = s_at(m) + buf * 64 + lanes;
+                go = go && warp_wait(&W.s_full[m][buf], (jobs >> 1) & 1, gave_up);
                 if (!go) break;
                 tc_fence_after();
-                unsigned see[4];
+                unsigned see[2];
                 if (i == tree) {
                     see[0] = (unsigned)mask;
                     see[1] = (unsigned)(mask >> 32);
-                    see[2] = see[3] = 0;
                     RowTile<T, true> tile;
                     const float x = fmaxf(kNoMax, tile.load(s_tm, see) * unit);
                     follow(x, true);      // O leaves the cache's units
                     sum += tile.store(s_tm, unit, top);
                 } else {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) see[q] = W.seen[c & 3][q];
+                    see[0] = W.seen[(done + i) & 3][half * 2];
+                    see[1] = W.seen[(done + i) & 3][half * 2 + 1];
                     RowTile<T, false> tile;
                     const float x = fmaxf(kNoMax, tile.load(s_tm, see) * cache_unit);
                     follow(x, false);
@@ -584,17 +613,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                bar_arrive(&W.p_full[m]);
+                bar_arrive(&W.p_full[m][buf]);
                 ++jobs;
                 ++mine;
             }
-            // the result: O is done after the group's last product
+            // the result: O is done after the group's last product. The one before may be under way
+            // too, and a barrier tells only two phases apart: first that one, then the last.
+            if (mine > 1) go = go && warp_wait(&W.o_full[m], (jobs - 2) & 1, gave_up);
             if (mine > 0) go = go && warp_wait(&W.o_full[m], (jobs - 1) & 1, gave_up);
             tc_fence_after();
             if (!go && P.status && lane == 0) P.status[b] = SPEC_REQ_INTERNAL;
             const bool whole = A.tile == 0 && A.stop == A.nt;
             // the group's O is in V's units once the tree's tile was among its tiles
-            const bool in_v = tree < n && (!SPLIT || (tree & 1) == m);
+            const bool in_v = tree < n && (!SPLIT || m == 0);
             float f[2] = {in_v ? 1.f : v_scale, 0.f};     // of this group's O; of the other's
             bool has[2] = {mine > 0, false};
             if (SPLIT) {
@@ -602,7 +633,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 W.top[m][row] = top;
                 W.sum[m][row] = sum;
                 if (row == 0) W.state[m] = mine == 0 ? 0 : in_v ? 2 : 1;
+                tc_fence_before();
                 named_sync(1, kSoftmax);
+                tc_fence_after();
                 const float other = W.top[m ^ 1][row], most = fmaxf(top, other);
                 const int state = W.state[m ^ 1];
                 has[1] = state != 0;
