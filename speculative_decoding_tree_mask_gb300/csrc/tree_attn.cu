@@ -746,25 +746,34 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(TreeAttnParams P, in
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c = c0; c <= c1; c += 8) {
         float4 v[8];
-        float pm[8], pl[8];
+        float pm[8], pl[8], top = m;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const int k = min(c + u, c1);
-            const float *part = attn_slot(P, k, k == c0, rows_tile, D);
+            pm[u] = kNoMax;
+            if (c + u > c1) continue;
+            const float *part = attn_slot(P, c + u, c + u == c0, rows_tile, D);
             v[u] = __ldcg(reinterpret_cast<const float4 *>(part) + i);
             pm[u] = __ldcg(part + rows_tile * D + r);
             pl[u] = __ldcg(part + rows_tile * (D + 1) + r);
         }
 #pragma unroll
+        for (int u = 0; u < 8; ++u) top = fmaxf(top, pm[u]);
+        const float a = ex2(m - top);
+        m = top;
+        l *= a;
+        o.x *= a;
+        o.y *= a;
+        o.z *= a;
+        o.w *= a;
+#pragma unroll
         for (int u = 0; u < 8; ++u) {
-            if (c + u > c1) break;
-            const float mx = fmaxf(m, pm[u]), a = exp2f(m - mx), w = exp2f(pm[u] - mx);
-            o.x = o.x * a + v[u].x * w;
-            o.y = o.y * a + v[u].y * w;
-            o.z = o.z * a + v[u].z * w;
-            o.w = o.w * a + v[u].w * w;
-            l = l * a + pl[u] * w;
-            m = mx;
+            if (c + u > c1) continue;
+            const float w = ex2(pm[u] - top);
+            o.x = fmaf(v[u].x, w, o.x);
+            o.y = fmaf(v[u].y, w, o.y);
+            o.z = fmaf(v[u].z, w, o.z);
+            o.w = fmaf(v[u].w, w, o.w);
+            l = fmaf(pl[u], w, l);
         }
     }
     const float f = l == 0.f ? 0.f : 1.f / l;

@@ -5,9 +5,10 @@
 // 4 rows D operations a position, and next to them the exponentials and the conversion of the
 // codes. One CTA an SM; its warps have one part each and meet at mbarriers only:
 //
-//   convert  (4 warps) a position each: codes to 16-bit elements in shared memory, exact, laid
-//            out for the tensor core (128-byte swizzle; K contiguous along D, and V as it is,
-//            read transposed). K becomes the type of Q, V halves; two tiles of each in a ring;
+//   convert  (4 warps for K, 4 for V) a position a thread: codes to 16-bit elements in shared
+//            memory, exact, laid out for the tensor core (128-byte swizzle; K contiguous along
+//            D, and V as it is, read transposed). K becomes the type of Q, V halves; two tiles
+//            of each in a ring, and the rows of two more on their way;
 //   multiply (2 threads, one for each softmax group) S = Q K^T and O += P V, sums in tensor
 //            memory: S and O twice, up to all 512 columns; P overwrites the half of S it came
 //            from. One thread for both groups could not issue as fast as the products end;
@@ -32,7 +33,7 @@ namespace specv {
 namespace {
 
 constexpr float kRescale = 8.f;
-constexpr int kConvert = 128;     // converting threads
+constexpr int kConvert = 256;     // converting threads: K's, then V's
 
 constexpr int kSoftmax = 256;     // threads of the two softmax groups
 constexpr int kThreads = kSoftmax + kConvert + 128;   // the last warpgroup: two warps multiply
@@ -58,6 +59,7 @@ struct Const {
 struct Words {
     uint64_t q_full, q_free, k_full[2], k_free[2], v_full[2], v_free[2], drain[2];
     uint64_t s_full[2][2], p_full[2][2], o_full[2];              // of a softmax group; buffers
+    uint64_t o_last[2];                                          // once a part
     // Positions of a K/V tile that are attended. A tile's words are written again for the
     // fourth after it, once the scores of the second after it are done: those were issued
     // after its P was waited for.
@@ -172,6 +174,13 @@ __device__ __forceinline__ int group_jobs(bool split, int m, int n, int tree) {
     return split ? contexts + (tree < n && m == 0) : 2 * contexts + (tree < n);
 }
 
+// 32 bytes to a 32-byte boundary.
+__device__ __forceinline__ void store32(void *to, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 // A wait of a whole warp: all of it goes on or none.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *gave_up) {
     return __all_sync(0xffffffffu, bar_wait(bar, parity, gave_up));
@@ -255,12 +264,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_init(&W.q_full, kConvert);
         bar_init(&W.q_free, 2);
         for (int i = 0; i < 2; ++i) {
-            bar_init(&W.k_full[i], kConvert);
-            bar_init(&W.v_full[i], kConvert);
+            bar_init(&W.k_full[i], kConvert / 2);
+            bar_init(&W.v_full[i], kConvert / 2);
             bar_init(&W.k_free[i], 2);
             bar_init(&W.v_free[i], 2);
             bar_init(&W.drain[i], 1);
             bar_init(&W.o_full[i], 1);
+            bar_init(&W.o_last[i], 1);
             for (int j = 0; j < 2; ++j) {
                 bar_init(&W.s_full[i][j], 1);
                 bar_init(&W.p_full[i][j], 128);
@@ -282,9 +292,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t done = 0, parts = 0;     // tiles and parts before this one: the phases count them
     AttnPart A;
 
-    // Launched with 128 registers a thread, 16 warps: 8 x 128 + 4 x 200 + 4 x 56 = 16 x 128.
+    // Launched with 96 registers a thread, 20 warps: 8 x 128 + 8 x 80 + 4 x 64 = 20 x 96.
     if (tid >= kSoftmax + kConvert) {
-        fewer_registers<56>();
+        fewer_registers<64>();
         // ---- multiply: for softmax group m. A job is 64 positions (or nodes): two of a tile,
         // one (the group's) if SPLIT, and one of the tree's tile, which SPLIT leaves to group 0.
         // The whole warp runs the loop and waits, one thread of it issues: what the products
@@ -302,9 +312,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto scores = [&](int j) {
                     const int i = SPLIT ? j : j >> 1, half = SPLIT ? m : j & 1;
                     const uint32_t c = done + i, buf = (jobs + j) & 1;
-                    ok = ok && warp_wait(&W.k_full[c & 1], (c >> 1) & 1, gave_up);
-                    if (!ok) return;
-                    tc_fence_after();
+                    if (SPLIT || half == 0) {     // a tile's second half came with its first
+                        ok = ok && warp_wait(&W.k_full[c & 1], (c >> 1) & 1, gave_up);
+                        if (!ok) return;
+                    }
                     const uint64_t a = smem_desc(base + (SPLIT ? 0 : m * C_::kOperand), 16, 1024);
                     const uint64_t k = smem_desc(
                         base + C_::kK + (c & 1) * C_::kOperand + half * kHalf, 16, 1024);
@@ -323,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 };
                 ok = ok && warp_wait(&W.q_full, parts & 1, gave_up);
+                tc_fence_after();
                 if (count > 0) scores(0);
                 if (count > 1) scores(1);
                 if (count == 0 && ok && lead) bar_arrive(&W.q_free);
@@ -330,8 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; ok && j < count; ++j) {
                     const int i = SPLIT ? j : j >> 1, half = SPLIT ? m : j & 1;
                     const uint32_t c = done + i, buf = (jobs + j) & 1;
-                    ok = warp_wait(&W.v_full[c & 1], (c >> 1) & 1, gave_up) &&
-                         warp_wait(&W.p_full[m][buf], ((jobs + j) >> 1) & 1, gave_up);
+                    if (SPLIT || half == 0) ok = warp_wait(&W.v_full[c & 1], (c >> 1) & 1, gave_up);
+                    ok = ok && warp_wait(&W.p_full[m][buf], ((jobs + j) >> 1) & 1, gave_up);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t v = smem_desc(
@@ -351,6 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        j > 0 || s > 0);
                         }
                         mma_commit(&W.o_full[m]);
+                        if (j == count - 1) mma_commit(&W.o_last[m]);
                         if (SPLIT || half == 1 || i == tree) mma_commit(&W.v_free[c & 1]);
                     }
                     __syncwarp();
@@ -381,42 +394,51 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         }
     } else if (tid >= kSoftmax) {
-        more_registers<200>();
-        // ---- convert ----
-        const int t = tid - kSoftmax, R = P.N * P.G;
+        fewer_registers<80>();
+        // ---- convert: K or V, a position a thread ----
+        const bool of_v = tid >= kSoftmax + kConvert / 2;
+        const int t = (tid - kSoftmax) % (kConvert / 2), R = P.N * P.G;
+        const void *codes = of_v ? C.v : C.k, *scales = of_v ? C.v_sf : C.k_sf;
+        const unsigned short *nodes = reinterpret_cast<const unsigned short *>(of_v ? P.v : P.k);
+        const int64_t node_stride = of_v ? P.v_stride : P.k_stride;
+        uint64_t *full = of_v ? W.v_full : W.k_full, *free = of_v ? W.v_free : W.k_free;
+        char *ring = smem + (of_v ? C_::kV : C_::kK);
         AttnWalk walk(P, C.H * row_tiles, kTreeCost);
         bool go = true;               // no wait has given up
         while (walk.next(P, A)) {
             const int b = A.b, ctx = A.ctx, n = A.stop - A.tile, tree = A.nt - 1 - A.tile;
             const int head = A.item / row_tiles, row0 = (A.item - head * row_tiles) * RT;
-            const int rows = min(RT, R - row0);
-            if (P.status && t == 0 && A.tile == 0 && __ldg(P.ctx_len + b) != ctx)
+            const int rows = min(RT, R - row0), contexts = min(n, tree);
+            if (P.status && tid == kSoftmax && A.tile == 0 && __ldg(P.ctx_len + b) != ctx)
                 P.status[b] = SPEC_REQ_BAD_SLOT;
             const int32_t *table = C.block_table + (int64_t)b * C.max_blocks;
             auto page = [&](int i) -> int {
                 const int p = (A.tile + i) * kTile + t;
-                return i < n && i < tree && p < ctx
+                return i < contexts && p < ctx
                            ? __ldg(table + (uint32_t)p / (uint32_t)C.block_size)
                            : -1;
             };
             // two tiles' rows are in flight: set i % 2 is tile i's
-            Row4<D> kr[2], vr[2];
-            uint32_t row[2];
+            Row4<D> in[2];
             bool ok[2];
-            auto find = [&](int i, int blk, int set) {
+            auto fetch = [&](int i, int blk, int set) {
                 const int p = (A.tile + i) * kTile + t;
                 ok[set] = blk >= 0 && blk < C.num_blocks;
-                row[set] = ok[set] ? fp4_row(C, blk, p % (uint32_t)C.block_size, head) : 0u;
-                if (i < n && i < tree && p < ctx && !ok[set] && P.status)
+                if (i < contexts && p < ctx && !ok[set] && P.status)
                     P.status[b] = SPEC_REQ_BAD_SLOT;
+                load_row<D>(codes, scales,
+                            ok[set] ? fp4_row(C, blk, p % (uint32_t)C.block_size, head) : 0u,
+                            ok[set], in[set]);
             };
             const int page0 = page(0), page1 = page(1);
             int next = page(2);
+            fetch(0, page0, 0);
+            fetch(1, page1, 1);
             go = go && warp_wait(&W.q_free, (parts & 1) ^ 1, gave_up);
             if (go) {
-                // Q: rows of an operand a thread, neighbours' chunks side by side
+                // Q: neighbours' chunks side by side
 #pragma unroll 4
-                for (int i = t; i < RT * (D / 8); i += kConvert) {
+                for (int i = tid - kSoftmax; i < RT * (D / 8); i += kConvert) {
                     const int r = i / (D / 8), j = i - r * (D / 8);
                     const uint32_t to = (r >> 7) * C_::kOperand + chunk_at(r & 127, j);
                     const int rr = row0 + (r < rows ? r : 0), node = rr / P.G;
@@ -432,14 +454,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<uint4 *>(smem + to) = load8(from, false);
                 }
             }
-            find(0, page0, 0);
-            load_row<D>(C.k, C.k_sf, row[0], ok[0], kr[0]);
-            load_row<D>(C.v, C.v_sf, row[0], ok[0], vr[0]);
-            find(1, page1, 1);
-            load_row<D>(C.k, C.k_sf, row[1], ok[1], kr[1]);
-            load_row<D>(C.v, C.v_sf, row[1], ok[1], vr[1]);
-            if (t == 0) W.odd[parts & 3] = 0ull;
-            named_sync(2, kConvert);
+            if (of_v) {
+                if (t == 0) W.odd[parts & 3] = 0ull;
+                named_sync(2, kConvert / 2);
+            }
             auto q_done = [&]() {
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_async_smem();
@@ -449,96 +467,74 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr int set = decltype(set_)::value;
                 const uint32_t c = done + i;
                 const int st = c & 1;
-                const uint32_t parity = ((c >> 1) & 1) ^ 1;
-                char *ks = smem + C_::kK + st * C_::kOperand;
-                char *vs = smem + C_::kV + st * C_::kOperand;
+                char *to = ring + st * C_::kOperand;
                 const unsigned seen = __ballot_sync(0xffffffffu, ok[set]);
                 const int cur = next;
                 next = page(i + 3);
-                go = go && warp_wait(&W.k_free[st], parity, gave_up);
+                go = go && warp_wait(&free[st], ((c >> 1) & 1) ^ 1, gave_up);
                 if (go) {
-                    if (lane == 0) W.seen[c & 3][t >> 5] = seen;
-                    convert_row<D, T == 1>(kr[set], ks, t);
+                    if (!of_v && lane == 0) W.seen[c & 3][t >> 5] = seen;
+                    if (T == 1 && !of_v)
+                        convert_row<D, true>(in[set], to, t);
+                    else
+                        convert_row<D, false>(in[set], to, t);
                     fence_async_smem();
-                    bar_arrive(&W.k_full[st]);
+                    bar_arrive(&full[st]);
                 }
-                find(i + 2, cur, set);
-                load_row<D>(C.k, C.k_sf, row[set], ok[set], kr[set]);
+                fetch(i + 2, cur, set);
                 if (i == 0) q_done();
-                go = go && warp_wait(&W.v_free[st], parity, gave_up);
-                if (go) {
-                    convert_row<D, false>(vr[set], vs, t);
-                    fence_async_smem();
-                    bar_arrive(&W.v_full[st]);
-                }
-                load_row<D>(C.v, C.v_sf, row[set], ok[set], vr[set]);
             };
-            const int contexts = min(n, tree);
             for (int i = 0; i < contexts; i += 2) {
                 step(i, Const<0>{});
                 if (i + 1 < contexts) step(i + 1, Const<1>{});
             }
             if (tree < n) {
-                const int i = tree;
-                const uint32_t c = done + i;
+                // the nodes' own rows, zeros up to 64; two threads a row, half of it each
+                const uint32_t c = done + tree;
                 const int st = c & 1;
-                const uint32_t parity = ((c >> 1) & 1) ^ 1;
-                char *ks = smem + C_::kK + st * C_::kOperand;
-                char *vs = smem + C_::kV + st * C_::kOperand;
-                    // the nodes' own rows, zeros up to 64; two threads a row, half of it each
+                char *to = ring + st * C_::kOperand;
                 const int r = t >> 1, j0 = (t & 1) * (D / 16);
-                const int64_t row = (int64_t)b * P.N + min(r, P.N - 1);
-                const unsigned short *k = reinterpret_cast<const unsigned short *>(P.k) +
-                                          row * P.k_stride + head * D + j0 * 8;
-                const unsigned short *v = reinterpret_cast<const unsigned short *>(P.v) +
-                                          row * P.v_stride + head * D + j0 * 8;
+                const unsigned short *from =
+                    nodes + ((int64_t)b * P.N + min(r, P.N - 1)) * node_stride + head * D + j0 * 8;
                 uint4 x[D / 16];
-                auto rows_in = [&](const unsigned short *from) {
 #pragma unroll
-                    for (int j = 0; j < D / 16; ++j)
-                        x[j] = r < P.N ? load8(from + j * 8, vec) : make_uint4(0, 0, 0, 0);
-                };
-                rows_in(k);
-                go = go && warp_wait(&W.k_free[st], parity, gave_up);
-                if (go) {
+                for (int j = 0; j < D / 16; ++j)
+                    x[j] = r < P.N ? load8(from + j * 8, vec) : make_uint4(0, 0, 0, 0);
+                if (tree == 0) q_done();
+                if (of_v) {
+                    // NaN and infinities are left out of the products
+                    bool odd = false;
 #pragma unroll
-                    for (int j = 0; j < D / 16; ++j)
-                        *reinterpret_cast<uint4 *>(ks + chunk_at(r, j0 + j)) = x[j];
-                    fence_async_smem();
-                    bar_arrive(&W.k_full[st]);
-                }
-                if (i == 0) q_done();
-                rows_in(v);
-                bool odd = false;
+                    for (int j = 0; j < D / 16; ++j) {
+                        uint32_t *w = reinterpret_cast<uint32_t *>(&x[j]);
 #pragma unroll
-                for (int j = 0; j < D / 16; ++j) {
-                    uint32_t *w = reinterpret_cast<uint32_t *>(&x[j]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (odd16<T>(w[e])) {
-                            w[e] &= 0xffff0000u;
-                            odd = true;
-                        }
-                        if (odd16<T>(w[e] >> 16)) {
-                            w[e] &= 0xffffu;
-                            odd = true;
+                        for (int e = 0; e < 4; ++e) {
+                            if (odd16<T>(w[e])) {
+                                w[e] &= 0xffff0000u;
+                                odd = true;
+                            }
+                            if (odd16<T>(w[e] >> 16)) {
+                                w[e] &= 0xffffu;
+                                odd = true;
+                            }
                         }
                     }
+                    if (odd) atomicOr(&W.odd[parts & 3], 1ull << r);
                 }
-                if (odd) atomicOr(&W.odd[parts & 3], 1ull << r);
-                go = go && warp_wait(&W.v_free[st], parity, gave_up);
+                go = go && warp_wait(&free[st], ((c >> 1) & 1) ^ 1, gave_up);
                 if (go) {
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j)
-                        *reinterpret_cast<uint4 *>(vs + chunk_at(r, j0 + j)) = x[j];
+                        *reinterpret_cast<uint4 *>(to + chunk_at(r, j0 + j)) = x[j];
                     fence_async_smem();
-                    bar_arrive(&W.v_full[st]);
+                    bar_arrive(&full[st]);
                 }
             }
             done += n;
             ++parts;
         }
     } else {
+        more_registers<128>();
         // ---- softmax: this thread's row. A wait that gives up is followed by none, but the
         // groups' barriers are kept.
         const int m = warp >> 2, R = P.N * P.G;
@@ -549,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float unit = P.scale * kLog2e;
         const float cache_unit = unit * (C.k_scale ? __ldg(C.k_scale) : 1.f);
         AttnWalk walk(P, C.H * row_tiles, kTreeCost);
-        uint32_t jobs = 0;            // of this group so far
+        uint32_t jobs = 0, results = 0;   // of this group so far; parts with any
         bool go = true;
         while (walk.next(P, A)) {
             const int b = A.b, n = A.stop - A.tile, tree = A.nt - 1 - A.tile;
@@ -575,6 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (units) a *= v_scale;
                 if (mine == 0) return;
+                // the scores at hand were made after the product two before this one's
                 go = go && warp_wait(&W.o_full[m], (jobs - 1) & 1, gave_up);
                 tc_fence_after();
 #pragma unroll 1
@@ -617,10 +614,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++jobs;
                 ++mine;
             }
-            // the result: O is done after the group's last product. The one before may be under way
-            // too, and a barrier tells only two phases apart: first that one, then the last.
-            if (mine > 1) go = go && warp_wait(&W.o_full[m], (jobs - 2) & 1, gave_up);
-            if (mine > 0) go = go && warp_wait(&W.o_full[m], (jobs - 1) & 1, gave_up);
+            // The result: O is done after the group's last product. Its own barrier tells that:
+            // two products may be under way here, and o_full tells only two phases apart.
+            if (mine > 0) go = go && warp_wait(&W.o_last[m], results++ & 1, gave_up);
             tc_fence_after();
             if (!go && P.status && lane == 0) P.status[b] = SPEC_REQ_INTERNAL;
             const bool whole = A.tile == 0 && A.stop == A.nt;
@@ -649,6 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             f[1] *= norm;
             const int64_t to = live ? attn_row(P, b, head, row0 + r) : 0;
             float *part = attn_slot(P, blockIdx.x, A.tile == 0, RT, D);
+            const bool out32 = (reinterpret_cast<uintptr_t>(P.out) & 31) == 0;
             const unsigned long long odd = tree < n ? W.odd[parts & 3] & mask : 0ull;
             // SPLIT: the groups take half of the columns each, of both Os
             const uint32_t other_tm = o_at(m ^ 1) + lanes;
@@ -689,16 +686,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (odd16<T>(y)) v[e] += w * value16<T>(y);
                     }
                 }
-                if (whole) {
+                if (whole && out32) {
+                    unsigned short *p = reinterpret_cast<unsigned short *>(P.out) + to * D + q * 32;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 16) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) w[k] = pack2<T>(v[e + 2 * k], v[e + 2 * k + 1]);
+                        store32(p + e, w);
+                    }
+                } else if (whole) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
                         store_out4<T>(P.out, to * D + q * 32 + e,
                                       make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4 *>(part + (int64_t)r * D + q * 32 + e) =
-                            make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[e + k]);
+                        store32(part + (int64_t)r * D + q * 32 + e, w);
+                    }
                 }
             }
             if (live && (!SPLIT || m == 0)) {
