@@ -7,8 +7,10 @@
 //
 //   convert  (4 warps for K, 4 for V) a position a thread: codes to 16-bit elements in shared
 //            memory, exact, laid out for the tensor core (128-byte swizzle; K contiguous along
-//            D, and V as it is, read transposed). K becomes the type of Q, V halves; two tiles
-//            of each in a ring, and the rows of two more on their way;
+//            D, and V as it is, read transposed). All become halves; two tiles of each in a
+//            ring, the rows of the next on their way by asynchronous copies. Q, and the K of the tree's nodes, are
+//            brought to halves by a power of two for each row, exact for what is within 2^-32
+//            of the row's largest element (bfloat16 for all of K cost twice the conversion);
 //   multiply (2 threads, one for each softmax group) S = Q K^T and O += P V, sums in tensor
 //            memory: S and O twice, up to all 512 columns; P overwrites the half of S it came
 //            from. One thread for both groups could not issue as fast as the products end;
@@ -22,9 +24,8 @@
 // each group 128 rows of its own and all positions; items of up to 128 rows give both groups all
 // rows and half of each tile's positions (SPLIT), and the two results are joined at the end:
 // tensor memory is read by lanes, and both groups own the same lanes.
-// The tree's own nodes are the last tile of an item: their rows are copied instead of converted
-// and P is multiplied in their type; for bfloat16 as a sum of two terms, since eight bits are
-// too few. Every wait gives up after two seconds; the request's status then says so.
+// The tree's own nodes are the last tile of an item: V stays as it is and P is multiplied in its
+// type; for bfloat16 as a sum of two terms, since eight bits are too few. Every wait gives up after two seconds; the request's status then says so.
 
 #include "tc_device.cuh"
 #include "tree_attn.cuh"
@@ -46,14 +47,15 @@ struct Tc {
     static constexpr int kOperand = 128 * D * 2;                 // a 128 x D operand of 16 bits
     static constexpr int kK = kRows / 128 * kOperand;            // Q first, then K and V rings
     static constexpr int kV = kK + 2 * kOperand;
-    static constexpr int kSmall = kV + 2 * kOperand;             // barriers and words
-    static constexpr int kBytes = kSmall + 4096 + 1024;          // and room to align by 1024
+    // Rows of codes and scales as they come, a thread its own: D / 2 and D / 16 bytes, the
+    // pitch free of bank conflicts. As many tiles of them as fit.
+    static constexpr int kPitch = D / 2 + 16;
+    static constexpr int kRaws = kOperand * (kRows / 128 + 4) > 192 * 1024 - 1 ? 1 : 2;
+    static constexpr int kRaw = kV + 2 * kOperand;               // [K, V][kRaws][128][kPitch]
+    static constexpr int kSmall = kRaw + 2 * kRaws * 128 * kPitch;   // barriers and words
+    static constexpr int kBytes = kSmall + 6144 + 1024;          // and room to align by 1024
+    static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
     static constexpr int kColumns = 512;                         // 2 (128 + D), a power of two
-};
-
-template <int n>
-struct Const {
-    static constexpr int value = n;
 };
 
 struct Words {
@@ -69,22 +71,15 @@ struct Words {
     int gave_up;
     int state[2];                 // SPLIT: 0 no tile, 1 O in the cache's units, 2 in V's
     float top[2][128], sum[2][128];
+    // 1 / the power of two of each row of Q and of each node's K; a part's are written again for
+    // the second after it, once the scores of the one between are done
+    float q_down[2][256], k_down[2][64];
 };
-static_assert(sizeof(Words) <= 4096, "room for the words");
+static_assert(sizeof(Words) <= 6144, "room for the words");
 
 // Byte of 16-byte chunk `j` of row r of an operand of D elements a row.
 __device__ __forceinline__ uint32_t chunk_at(int r, int j) {
     return (uint32_t)(j >> 3) * (128 * 128) + r * 128 + (((j & 7) ^ (r & 7)) << 4);
-}
-
-// A pair of halves that hold e2m1 values, times a block scale, as bfloat16 (exact): the bits of
-// a normal half shifted into a bfloat16's place are the value times 2^-112, which the factor
-// (scale * 2^112) restores. Zero stays zero; 0.5 is the smallest other magnitude.
-__device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h, uint32_t factor) {
-    const uint32_t t = ((h >> 3) & 0x0fff0fffu) | (h & 0x80008000u);
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(t), "r"(factor));
-    return r;
 }
 
 template <int D>
@@ -93,42 +88,55 @@ struct Row4 {                     // a position's codes and block scales of one 
     uint32_t sf[D / 64];
 };
 
-template <int D>
-__device__ __forceinline__ void load_row(const void *codes, const void *scales, uint32_t row,
-                                         bool ok, Row4<D> &r) {
-    const uint4 *c = reinterpret_cast<const uint4 *>(codes) + (int64_t)row * (D / 32);
-    const uint32_t *s = reinterpret_cast<const uint32_t *>(scales) + (int64_t)row * (D / 64);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) r.w[i] = ok ? __ldg(c + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) r.sf[i] = ok ? __ldg(s + i) : 0u;
+template <int n>
+__device__ __forceinline__ void cp_async(uint32_t smem, const void *gmem) {
+    if constexpr (n == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem), "l"(gmem), "n"(n)
+                     : "memory");
 }
 
-// The row's elements into row t of an operand; BF: as bfloat16, else as halves.
-template <int D, bool BF>
+// Starts the copy of a row to `to`. (Registers as the landing place cost more: a wait for an
+// older load there was a wait for these too.)
+template <int D>
+__device__ __forceinline__ void start_row(const void *codes, const void *scales, uint32_t row,
+                                          uint32_t to) {
+    const char *c = reinterpret_cast<const char *>(codes) + (int64_t)row * (D / 2);
+    const char *s = reinterpret_cast<const char *>(scales) + (int64_t)row * (D / 16);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) cp_async<16>(to + i * 16, c + i * 16);
+    cp_async<D / 16>(to + D / 2, s);
+}
+
+template <int D>
+__device__ __forceinline__ void take_row(const char *from, bool ok, Row4<D> &r) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) r.w[i] = *reinterpret_cast<const uint4 *>(from + i * 16);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+        const uint32_t sf = *reinterpret_cast<const uint32_t *>(from + D / 2 + i * 4);
+        r.sf[i] = ok ? sf : 0u;      // zeros for a position that is not there
+        // the scales are the last to be read: once they are used, the row has been read, and
+        // its place can be filled again
+        asm volatile("mov.b32 %0, %0;" : "+r"(r.sf[i]));
+    }
+}
+
+// The row's elements, as halves, into row t of an operand.
+template <int D>
 __device__ __forceinline__ void convert_row(const Row4<D> &r, char *to, int t) {
 #pragma unroll
     for (int q = 0; q < D / 32; ++q) {               // 32 elements: two blocks
         const uint32_t two = e4m3x2_to_f16x2((r.sf[q / 2] >> (q % 2 * 16)) & 0xffffu);
-        uint32_t f[2];
-        if constexpr (BF) {
-            const float2 s = __half22float2(*reinterpret_cast<const __half2 *>(&two));
-            const __nv_bfloat162 a = __float2bfloat162_rn(s.x * 0x1p112f);
-            const __nv_bfloat162 b = __float2bfloat162_rn(s.y * 0x1p112f);
-            f[0] = *reinterpret_cast<const uint32_t *>(&a);
-            f[1] = *reinterpret_cast<const uint32_t *>(&b);
-        } else {
-            f[0] = __byte_perm(two, two, 0x1010);
-            f[1] = __byte_perm(two, two, 0x3232);
-        }
+        const uint32_t f[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
         const uint32_t w[4] = {r.w[q].x, r.w[q].y, r.w[q].z, r.w[q].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t h[4];
             e2m1x8_to_f16x2(w[i], h);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                h[e] = BF ? scaled_bf16x2(h[e], f[i / 2]) : hmul2(h[e], f[i / 2]);
+            for (int e = 0; e < 4; ++e) h[e] = hmul2(h[e], f[i / 2]);
             *reinterpret_cast<uint4 *>(to + chunk_at(t, q * 4 + i)) =
                 make_uint4(h[0], h[1], h[2], h[3]);
         }
@@ -166,6 +174,35 @@ __device__ __forceinline__ float value16(uint32_t x) {
     return T == 1 ? __uint_as_float(x << 16) : __half2float(__ushort_as_half((unsigned short)x));
 }
 
+// Eight elements of type T as halves times `up`, and their largest finite magnitude.
+template <int T>
+__device__ __forceinline__ float largest8(const uint4 &x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float big = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float a = fabsf(value16<T>((w[e / 2] >> (e % 2 * 16)) & 0xffffu));
+        if (a < INFINITY) big = fmaxf(big, a);
+    }
+    return big;
+}
+template <int T>
+__device__ __forceinline__ uint4 halves8(const uint4 &x, float up) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        h[e] = pack2<2>(value16<T>(w[e] & 0xffffu) * up, value16<T>(w[e] >> 16) * up);
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+// The power of two that brings `big` into [2^14, 2^15), 2^126 at most (a row of zeros, or of
+// almost nothing), and its reciprocal.
+__device__ __forceinline__ float scale_up(float big, float &down) {
+    const uint32_t e = max(__float_as_uint(big) >> 23, 15u);   // exponent fields add up to 268
+    down = __uint_as_float((e - 14u) << 23);
+    return __uint_as_float((268u - e) << 23);
+}
+
 constexpr int kHalf = 64 * 128;   // bytes from the first 64 rows of an operand to the others
 
 // Jobs of softmax group m in a part of n tiles, the tree's at `tree` (at or past n: not in it).
@@ -186,23 +223,27 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, bar_wait(bar, parity, gave_up));
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t smem, const void *gmem) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
-}
-
 // S to P of 64 positions, the thread's row: to halves, or (kTree) of 64 nodes to type T.
 template <int T, bool kTree>
 struct RowTile {
     static constexpr int kChunks = 2;
     uint32_t s[kChunks][32];
 
-    // The scores, -inf where `see` has no bit; returns their largest.
-    __device__ __forceinline__ float load(uint32_t s_tm, const unsigned (&see)[2]) {
+    // The scores (kTree: times down[node]), -inf where `see` has no bit; returns their largest.
+    __device__ __forceinline__ float load(uint32_t s_tm, const unsigned (&see)[2],
+                                          const float *down) {
 #pragma unroll
         for (int q = 0; q < kChunks; ++q) tmem_ld32(s_tm + q * 32, s[q]);
         tmem_wait_ld(s[0]);
 #pragma unroll
         for (int q = 1; q < kChunks; ++q) tmem_loaded(s[q]);
+        if (kTree) {
+#pragma unroll
+            for (int q = 0; q < kChunks; ++q)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    s[q][e] = __float_as_uint(__uint_as_float(s[q][e]) * down[q * 32 + e]);
+        }
         if (kTree || (see[0] & see[1]) != 0xffffffffu) {
 #pragma unroll
             for (int q = 0; q < kChunks; ++q)
@@ -292,9 +333,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t done = 0, parts = 0;     // tiles and parts before this one: the phases count them
     AttnPart A;
 
-    // Launched with 96 registers a thread, 20 warps: 8 x 128 + 8 x 80 + 4 x 64 = 20 x 96.
+    // Launched with 96 registers a thread, 20 warps: 8 x 128 + 8 x 88 + 4 x 48 = 20 x 96.
     if (tid >= kSoftmax + kConvert) {
-        fewer_registers<64>();
+        fewer_registers<48>();
         // ---- multiply: for softmax group m. A job is 64 positions (or nodes): two of a tile,
         // one (the group's) if SPLIT, and one of the tree's tile, which SPLIT leaves to group 0.
         // The whole warp runs the loop and waits, one thread of it issues: what the products
@@ -325,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int d = 0; d < KS; ++d) {
                             const int off = (d >> 2) * (128 * 128) + (d & 3) * 32;
                             mma_ss(s, desc_plus(a, off), desc_plus(k, off),
-                                   mma_desc(kType, 64, false), d > 0);
+                                   mma_desc(0, 64, false), d > 0);
                         }
                         mma_commit(&W.s_full[m][buf]);
                         if (SPLIT || half == 1 || i == tree) mma_commit(&W.k_free[c & 1]);
@@ -394,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         }
     } else if (tid >= kSoftmax) {
-        fewer_registers<80>();
+        fewer_registers<88>();
         // ---- convert: K or V, a position a thread ----
         const bool of_v = tid >= kSoftmax + kConvert / 2;
         const int t = (tid - kSoftmax) % (kConvert / 2), R = P.N * P.G;
@@ -403,6 +444,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t node_stride = of_v ? P.v_stride : P.k_stride;
         uint64_t *full = of_v ? W.v_full : W.k_full, *free = of_v ? W.v_free : W.k_free;
         char *ring = smem + (of_v ? C_::kV : C_::kK);
+        constexpr int kRaws = C_::kRaws;
+        char *mine = smem + C_::kRaw + ((of_v ? kRaws : 0) * 128 + t) * C_::kPitch;
+        const uint32_t mine_s = smem_addr(mine);
         AttnWalk walk(P, C.H * row_tiles, kTreeCost);
         bool go = true;               // no wait has given up
         while (walk.next(P, A)) {
@@ -412,82 +456,92 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (P.status && tid == kSoftmax && A.tile == 0 && __ldg(P.ctx_len + b) != ctx)
                 P.status[b] = SPEC_REQ_BAD_SLOT;
             const int32_t *table = C.block_table + (int64_t)b * C.max_blocks;
+            // the block of this thread's position in the i-th tile (of some position past them)
             auto page = [&](int i) -> int {
-                const int p = (A.tile + i) * kTile + t;
-                return i < contexts && p < ctx
-                           ? __ldg(table + (uint32_t)p / (uint32_t)C.block_size)
-                           : -1;
+                const uint32_t p = (uint32_t)((A.tile + i) * kTile + t);
+                return __ldg(table + min(p / (uint32_t)C.block_size, (uint32_t)C.max_blocks - 1u));
             };
-            // two tiles' rows are in flight: set i % 2 is tile i's
-            Row4<D> in[2];
-            bool ok[2];
-            auto fetch = [&](int i, int blk, int set) {
+            // the rows of the next kRaws tiles are in flight; bit i % 2 of `there`: tile i's is
+            unsigned there = 0;
+            auto start = [&](int i, int blk) {
                 const int p = (A.tile + i) * kTile + t;
-                ok[set] = blk >= 0 && blk < C.num_blocks;
-                if (i < contexts && p < ctx && !ok[set] && P.status)
-                    P.status[b] = SPEC_REQ_BAD_SLOT;
-                load_row<D>(codes, scales,
-                            ok[set] ? fp4_row(C, blk, p % (uint32_t)C.block_size, head) : 0u,
-                            ok[set], in[set]);
+                const bool in = i < contexts && p < ctx, ok = in && blk >= 0 && blk < C.num_blocks;
+                if (in && !ok && P.status) P.status[b] = SPEC_REQ_BAD_SLOT;
+                there = (there & ~(1u << (i & 1))) | (ok ? 1u << (i & 1) : 0u);
+                if (i < contexts)
+                    start_row<D>(codes, scales,
+                                 ok ? fp4_row(C, blk, p % (uint32_t)C.block_size, head) : 0u,
+                                 mine_s + i % kRaws * 128 * C_::kPitch);
+                asm volatile("cp.async.commit_group;" ::: "memory");
             };
             const int page0 = page(0), page1 = page(1);
-            int next = page(2);
-            fetch(0, page0, 0);
-            fetch(1, page1, 1);
-            go = go && warp_wait(&W.q_free, (parts & 1) ^ 1, gave_up);
-            if (go) {
-                // Q: neighbours' chunks side by side
-#pragma unroll 4
-                for (int i = tid - kSoftmax; i < RT * (D / 8); i += kConvert) {
+            int next = kRaws == 1 ? page1 : page(2);
+            // Q: the D / 8 chunks of a row side by side, four of a thread at a time
+            constexpr int kMine = RT * (D / 8) / kConvert, kBatch = kMine < 4 ? kMine : 4;
+            uint4 x[kBatch];
+            auto q_in = [&](int at) {
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int i = (at + u) * kConvert + tid - kSoftmax;
                     const int r = i / (D / 8), j = i - r * (D / 8);
-                    const uint32_t to = (r >> 7) * C_::kOperand + chunk_at(r & 127, j);
-                    const int rr = row0 + (r < rows ? r : 0), node = rr / P.G;
-                    const unsigned short *from =
-                        reinterpret_cast<const unsigned short *>(P.q) +
-                        ((int64_t)b * P.N + node) * P.q_stride +
-                        (int64_t)(head * P.G + rr - node * P.G) * D + j * 8;
-                    if (r >= rows)
-                        *reinterpret_cast<uint4 *>(smem + to) = make_uint4(0, 0, 0, 0);
-                    else if (vec)
-                        cp_async16(base + to, from);
-                    else
-                        *reinterpret_cast<uint4 *>(smem + to) = load8(from, false);
+                    const int rr = row0 + min(r, rows - 1), node = rr / P.G;
+                    x[u] = load8(reinterpret_cast<const unsigned short *>(P.q) +
+                                     ((int64_t)b * P.N + node) * P.q_stride +
+                                     (int64_t)(head * P.G + rr - node * P.G) * D + j * 8,
+                                 vec);
+                }
+            };
+            q_in(0);
+            start(0, page0);
+            if (kRaws == 2) start(1, page1);
+            go = go && warp_wait(&W.q_free, (parts & 1) ^ 1, gave_up);
+#pragma unroll
+            for (int at = 0; at < kMine; at += kBatch) {
+                if (at > 0) q_in(at);
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int i = (at + u) * kConvert + tid - kSoftmax;
+                    const int r = i / (D / 8), j = i - r * (D / 8);
+                    if (r >= rows) x[u] = make_uint4(0, 0, 0, 0);
+                    float big = largest8<T>(x[u]);
+#pragma unroll
+                    for (int o = D / 16; o > 0; o >>= 1)
+                        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                    float down;
+                    const float up = scale_up(big, down);
+                    if (go) {
+                        *reinterpret_cast<uint4 *>(smem + (r >> 7) * C_::kOperand +
+                                                   chunk_at(r & 127, j)) = halves8<T>(x[u], up);
+                        if (j == 0) W.q_down[parts & 1][r] = down;
+                    }
                 }
             }
             if (of_v) {
                 if (t == 0) W.odd[parts & 3] = 0ull;
                 named_sync(2, kConvert / 2);
             }
-            auto q_done = [&]() {
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                fence_async_smem();
-                if (go) bar_arrive(&W.q_full);
-            };
-            auto step = [&](int i, auto set_) {
-                constexpr int set = decltype(set_)::value;
+            fence_async_smem();
+            if (go) bar_arrive(&W.q_full);
+            for (int i = 0; i < contexts; ++i) {
                 const uint32_t c = done + i;
                 const int st = c & 1;
-                char *to = ring + st * C_::kOperand;
-                const unsigned seen = __ballot_sync(0xffffffffu, ok[set]);
+                asm volatile("cp.async.wait_group %0;" ::"n"(kRaws - 1) : "memory");
+                const bool ok = there >> (i & 1) & 1;
+                const unsigned seen = __ballot_sync(0xffffffffu, ok);
+                Row4<D> row;
+                take_row<D>(mine + i % kRaws * 128 * C_::kPitch, ok, row);
                 const int cur = next;
-                next = page(i + 3);
+                next = page(i + kRaws + 1);
+                start(i + kRaws, cur);
                 go = go && warp_wait(&free[st], ((c >> 1) & 1) ^ 1, gave_up);
                 if (go) {
                     if (!of_v && lane == 0) W.seen[c & 3][t >> 5] = seen;
-                    if (T == 1 && !of_v)
-                        convert_row<D, true>(in[set], to, t);
-                    else
-                        convert_row<D, false>(in[set], to, t);
+                    convert_row<D>(row, ring + st * C_::kOperand, t);
                     fence_async_smem();
                     bar_arrive(&full[st]);
                 }
-                fetch(i + 2, cur, set);
-                if (i == 0) q_done();
-            };
-            for (int i = 0; i < contexts; i += 2) {
-                step(i, Const<0>{});
-                if (i + 1 < contexts) step(i + 1, Const<1>{});
             }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
             if (tree < n) {
                 // the nodes' own rows, zeros up to 64; two threads a row, half of it each
                 const uint32_t c = done + tree;
@@ -496,17 +550,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int r = t >> 1, j0 = (t & 1) * (D / 16);
                 const unsigned short *from =
                     nodes + ((int64_t)b * P.N + min(r, P.N - 1)) * node_stride + head * D + j0 * 8;
-                uint4 x[D / 16];
+                uint4 y[D / 16];
+                float down = 1.f;
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j)
-                    x[j] = r < P.N ? load8(from + j * 8, vec) : make_uint4(0, 0, 0, 0);
-                if (tree == 0) q_done();
+                    y[j] = r < P.N ? load8(from + j * 8, vec) : make_uint4(0, 0, 0, 0);
                 if (of_v) {
                     // NaN and infinities are left out of the products
                     bool odd = false;
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) {
-                        uint32_t *w = reinterpret_cast<uint32_t *>(&x[j]);
+                        uint32_t *w = reinterpret_cast<uint32_t *>(&y[j]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             if (odd16<T>(w[e])) {
@@ -520,12 +574,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (odd) atomicOr(&W.odd[parts & 3], 1ull << r);
+                } else {
+                    float big = 0.f;
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) big = fmaxf(big, largest8<T>(y[j]));
+                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                    const float up = scale_up(big, down);
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) y[j] = halves8<T>(y[j], up);
                 }
                 go = go && warp_wait(&free[st], ((c >> 1) & 1) ^ 1, gave_up);
                 if (go) {
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j)
-                        *reinterpret_cast<uint4 *>(to + chunk_at(r, j0 + j)) = x[j];
+                        *reinterpret_cast<uint4 *>(to + chunk_at(r, j0 + j)) = y[j];
+                    if (!of_v && (t & 1) == 0) W.k_down[parts & 1][r] = down;
                     fence_async_smem();
                     bar_arrive(&full[st]);
                 }
@@ -552,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int head = A.item / row_tiles, row0 = (A.item - head * row_tiles) * RT;
             const int rows = min(RT, R - row0);
             const bool live = r < rows;
-            float top = kNoMax, sum = 0.f;
+            float top = kNoMax, sum = 0.f, down = 1.f;   // down: 1 / Q's power of two
             const unsigned long long mask =
                 live ? __ldg(P.mask + (int64_t)b * P.N + (row0 + r) / P.G) &
                            (P.N < 64 ? (1ull << P.N) - 1ull : ~0ull)
@@ -592,21 +655,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 go = go && warp_wait(&W.s_full[m][buf], (jobs >> 1) & 1, gave_up);
                 if (!go) break;
                 tc_fence_after();
+                if (mine == 0) down = W.q_down[parts & 1][r];
                 unsigned see[2];
                 if (i == tree) {
                     see[0] = (unsigned)mask;
                     see[1] = (unsigned)(mask >> 32);
                     RowTile<T, true> tile;
-                    const float x = fmaxf(kNoMax, tile.load(s_tm, see) * unit);
+                    const float x = fmaxf(kNoMax, tile.load(s_tm, see, W.k_down[parts & 1]) * (unit * down));
                     follow(x, true);      // O leaves the cache's units
-                    sum += tile.store(s_tm, unit, top);
+                    sum += tile.store(s_tm, unit * down, top);
                 } else {
                     see[0] = W.seen[(done + i) & 3][half * 2];
                     see[1] = W.seen[(done + i) & 3][half * 2 + 1];
                     RowTile<T, false> tile;
-                    const float x = fmaxf(kNoMax, tile.load(s_tm, see) * cache_unit);
+                    const float x =
+                        fmaxf(kNoMax, tile.load(s_tm, see, nullptr) * (cache_unit * down));
                     follow(x, false);
-                    sum += tile.store(s_tm, cache_unit, top);
+                    sum += tile.store(s_tm, cache_unit * down, top);
                 }
                 tmem_wait_st();
                 tc_fence_before();
