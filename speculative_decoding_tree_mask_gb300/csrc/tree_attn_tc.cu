@@ -39,7 +39,7 @@ constexpr int kConvert = 256;     // converting threads: K's, then V's
 constexpr int kSoftmax = 256;     // threads of the two softmax groups
 constexpr int kThreads = kSoftmax + kConvert + 128;   // the last warpgroup: two warps multiply
 constexpr int kMmaWarp = (kSoftmax + kConvert) / 32;
-constexpr int kTreeCost = 4;      // the tree's tile and an item's rest, in context tiles
+constexpr int kTreeCost = 8;      // the tree's tile and an item's rest, in context tiles
 
 template <int D, bool SPLIT>
 struct Tc {
@@ -476,44 +476,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             const int page0 = page(0), page1 = page(1);
             int next = kRaws == 1 ? page1 : page(2);
-            // Q: the D / 8 chunks of a row side by side, four of a thread at a time
-            constexpr int kMine = RT * (D / 8) / kConvert, kBatch = kMine < 4 ? kMine : 4;
-            uint4 x[kBatch];
-            auto q_in = [&](int at) {
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const int i = (at + u) * kConvert + tid - kSoftmax;
-                    const int r = i / (D / 8), j = i - r * (D / 8);
-                    const int rr = row0 + min(r, rows - 1), node = rr / P.G;
-                    x[u] = load8(reinterpret_cast<const unsigned short *>(P.q) +
-                                     ((int64_t)b * P.N + node) * P.q_stride +
-                                     (int64_t)(head * P.G + rr - node * P.G) * D + j * 8,
-                                 vec);
-                }
-            };
-            q_in(0);
             start(0, page0);
             if (kRaws == 2) start(1, page1);
             go = go && warp_wait(&W.q_free, (parts & 1) ^ 1, gave_up);
-#pragma unroll
-            for (int at = 0; at < kMine; at += kBatch) {
-                if (at > 0) q_in(at);
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const int i = (at + u) * kConvert + tid - kSoftmax;
+            if (go) {
+                // Q, the D / 8 chunks of a row side by side: all of it copied to its place, and
+                // there made halves
+                constexpr int kMine = RT * (D / 8) / kConvert;
+#pragma unroll 4
+                for (int u = 0; u < kMine; ++u) {
+                    const int i = u * kConvert + tid - kSoftmax;
                     const int r = i / (D / 8), j = i - r * (D / 8);
-                    if (r >= rows) x[u] = make_uint4(0, 0, 0, 0);
-                    float big = largest8<T>(x[u]);
+                    const uint32_t to = (r >> 7) * C_::kOperand + chunk_at(r & 127, j);
+                    const int rr = row0 + min(r, rows - 1), node = rr / P.G;
+                    const unsigned short *from =
+                        reinterpret_cast<const unsigned short *>(P.q) +
+                        ((int64_t)b * P.N + node) * P.q_stride +
+                        (int64_t)(head * P.G + rr - node * P.G) * D + j * 8;
+                    if (r >= rows)
+                        *reinterpret_cast<uint4 *>(smem + to) = make_uint4(0, 0, 0, 0);
+                    else if (vec)
+                        cp_async<16>(base + to, from);
+                    else
+                        *reinterpret_cast<uint4 *>(smem + to) = load8(from, false);
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 4
+                for (int u = 0; u < kMine; ++u) {
+                    const int i = u * kConvert + tid - kSoftmax;
+                    const int r = i / (D / 8), j = i - r * (D / 8);
+                    uint4 *at = reinterpret_cast<uint4 *>(smem + (r >> 7) * C_::kOperand +
+                                                          chunk_at(r & 127, j));
+                    const uint4 x = *at;
+                    float big = largest8<T>(x), down;
 #pragma unroll
                     for (int o = D / 16; o > 0; o >>= 1)
                         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-                    float down;
                     const float up = scale_up(big, down);
-                    if (go) {
-                        *reinterpret_cast<uint4 *>(smem + (r >> 7) * C_::kOperand +
-                                                   chunk_at(r & 127, j)) = halves8<T>(x[u], up);
-                        if (j == 0) W.q_down[parts & 1][r] = down;
-                    }
+                    *at = halves8<T>(x, up);
+                    if (j == 0) W.q_down[parts & 1][r] = down;
                 }
             }
             if (of_v) {
