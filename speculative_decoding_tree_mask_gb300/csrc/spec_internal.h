@@ -290,6 +290,7 @@ struct TreeAttnParams {
     void *workspace;
     int4 *notes;                  // in the workspace: cut items [CTAs] (see tree_attn.cuh)
     float *ws;                    // ... and their parts
+    int columns;                  // columns of CTAs
     int sms;
 };
 

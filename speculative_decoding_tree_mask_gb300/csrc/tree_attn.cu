@@ -11,17 +11,20 @@
 // it is exact as a half; the tensor scales are applied to the scores and to the result. Q is
 // brought to halves by a power of two for each row (exact for what is within 2^-32 of the row's
 // largest element) and p is rounded to a half with the row's largest near 1. The products are
-// m16n8k16 of halves with float32 sums.
+// m16n8k16 of halves with float32 sums, transposed: S^T = K Q^T and O^T = V^T P^T, so that rows
+// come in groups of eight (with Q as the 16-row operand, one token of up to eight heads paid
+// for 16 rows, and 24 rows for 32).
 //
 // A CTA is four warps; each takes 32 of a tile's 128 positions and keeps its own maxima, sums
 // and output in registers, so that the main loop has no barrier. Codes and scales come through
-// a ring in shared memory by asynchronous copies. Both products contract over
-// an index whose order is free: the head's elements for K, the positions for V. So lane (g, c)
-// takes the elements [c D/4, (c+1) D/4) of position g as its share of the K operand, one wide
-// load, and the elements [g D/8, (g+1) D/8) of its four positions for V, whose pairs of
-// positions are put together by a byte permute. The positions of a group of eight are taken in
-// the order 0 1 3 2 4 5 7 6, which with the swizzle of 16-byte units makes both loads free of
-// bank conflicts.
+// a ring in shared memory by asynchronous copies. Both products contract over an index whose
+// order is free: the head's elements for K, the positions for V. So lane (g, c) takes the
+// elements [c D/4, (c+1) D/4) of the positions g and g + 8 as its share of the K operand, wide
+// loads, and the elements [g D/8, (g+1) D/8) of its four positions for V, whose pairs of
+// positions are put together by a byte permute; P^T is S^T through movmatrix. The positions of
+// a group of eight are taken in the order 0 1 3 2 4 5 7 6, which with the swizzle of 16-byte
+// units makes both loads free of bank conflicts. A row's maximum is followed only when a score
+// passes it by 2^8, so that the lanes need not agree on it for every tile.
 
 #include "tree_attn.cuh"
 
@@ -30,15 +33,19 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-// Tiles in the ring: the one at work and those in flight (two warps' worth of D = 256 take the
-// shared memory of three of D = 128).
-constexpr int stages(int D) { return D == 256 ? 2 : 3; }
-constexpr int kTreeCost = 1;      // the tree's tile and an item's rest, in context tiles
-constexpr float kRescale = 8.f;   // a maximum is followed once it rises by 2^8
+constexpr int kTreeCost = 4;      // the tree's tile and an item's rest, in context tiles
+constexpr float kRescale = 8.f;   // a maximum is followed once it is passed by 2^8
 
-template <int D>
+// CTAs an SM holds, by the registers of the output (D x 8 RG floats a warp) and the ring.
+constexpr int ctas_per_sm(int D, int RG) {
+    return D * RG <= 64 ? 5 : D * RG <= 128 ? 4 : D * RG <= 256 ? 3 : 2;
+}
+// Tiles in the ring: the one at work and those in flight.
+constexpr int stages(int D, int RG) { return D == 256 ? 2 : 3; }
+
+template <int D, int RG>
 struct Ring {
-    static constexpr int kStages = stages(D);
+    static constexpr int kStages = stages(D, RG);
     static constexpr int kCodes = 32 * D / 2;             // bytes of K (and of V) codes
     static constexpr int kScales = 32 * D / 16;
     static constexpr int kV = kCodes, kKs = 2 * kCodes, kVs = kKs + kScales, kSeen = kVs + kScales;
@@ -46,13 +53,13 @@ struct Ring {
 };
 
 // Shared memory of a CTA, in bytes from its start.
-template <int T, int D, int MT>
+template <int T, int D, int RG>
 struct Smem {
-    static constexpr int kRows = 16 * MT;
-    static constexpr int kRing = kWarps * stages(D) * Ring<D>::kBytes;
+    static constexpr int kRows = 8 * RG;
+    static constexpr int kRing = kWarps * stages(D, RG) * Ring<D, RG>::kBytes;
     static constexpr int kTreeStride = D + 8;                              // elements
     static constexpr int kTree = 2 * kMaxN * kTreeStride * 2;              // in the ring's place
-    static constexpr int kJoin = kRows * D * 4;                            // likewise
+    static constexpr int kJoin = D / 4 * (kRows + 1) * 16;                 // likewise
     static constexpr int kFirst = kRing > kTree ? kRing : kTree;
     static constexpr int kQ = kFirst > kJoin ? kFirst : kJoin;
     static constexpr int kQt = kQ + kRows * D * 2;                         // Q in its own type
@@ -123,65 +130,73 @@ __device__ __forceinline__ float half_bits(uint32_t h) {
     return __half2float(__ushort_as_half((unsigned short)h));
 }
 
-// The state of an item in one warp: rows g and g + 8 of each of its MT groups of 16.
-template <int D, int MT>
+// An 8 x 8 matrix of 16-bit elements, transposed: lane (g, c) has elements 2c, 2c + 1 of row g.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
+}
+
+// The state of an item in one warp. Lane (g, c) has rows 2c and 2c + 1 of each of RG groups of
+// eight; of these the elements [g D/8, (g+1) D/8): o[i][j][2 h + e] is element g D/8 + 2 j + h of
+// row 8 i + 2 c + e.
+template <int D, int RG>
 struct Acc {
-    float o[MT][D / 8][4];
-    float m[MT][2], l[MT][2];   // l: this lane's share of the row sums
+    float o[RG][D / 16][4];
+    float m[RG][2], l[RG][2];   // m: the same in all lanes of a row; l: this lane's share
 
     __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
+        for (int i = 0; i < RG; ++i) {
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j)
+            for (int j = 0; j < D / 16; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
             m[i][0] = m[i][1] = kNoMax;
             l[i][0] = l[i][1] = 0.f;
         }
     }
-    // Takes new row maxima in: rescales when one has risen far enough (for the whole warp).
-    __device__ __forceinline__ void raise(float (&x)[MT][2]) {
+    // Takes this lane's largest scores in: when one in the warp has passed its row's maximum
+    // far enough, all rows follow theirs.
+    __device__ __forceinline__ void raise(float (&x)[RG][2]) {
         bool up = false;
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < RG; ++i)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                x[i][r] = fmaxf(x[i][r], __shfl_xor_sync(0xffffffffu, x[i][r], 1));
-                x[i][r] = fmaxf(x[i][r], __shfl_xor_sync(0xffffffffu, x[i][r], 2));
-                up |= x[i][r] > m[i][r] + kRescale;
-            }
+            for (int e = 0; e < 2; ++e) up |= x[i][e] > m[i][e] + kRescale;
         if (!__any_sync(0xffffffffu, up)) return;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
+        for (int i = 0; i < RG; ++i) {
             float a[2];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float to = fmaxf(m[i][r], x[i][r]);
-                a[r] = ex2(m[i][r] - to);
-                m[i][r] = to;
-                l[i][r] *= a[r];
+            for (int e = 0; e < 2; ++e) {
+                float to = fmaxf(m[i][e], x[i][e]);
+#pragma unroll
+                for (int s = 4; s < 32; s <<= 1) to = fmaxf(to, __shfl_xor_sync(~0u, to, s));
+                a[e] = ex2(m[i][e] - to);
+                m[i][e] = to;
+                l[i][e] *= a[e];
             }
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j)
+            for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[i][j][e] *= a[e >> 1];
+                for (int e = 0; e < 4; ++e) o[i][j][e] *= a[e & 1];
         }
     }
 };
 
-// T: 1 bf16, 2 f16; MT: groups of 16 query rows of an item.
-template <int T, int D, int MT>
-__global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
+// T: 1 bf16, 2 f16; RG: groups of 8 query rows of an item.
+template <int T, int D, int RG>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, RG))
     tree_attn_kernel(TreeAttnParams P, int row_tiles) {
-    using S = Smem<T, D, MT>;
-    using Rg = Ring<D>;
+    using S = Smem<T, D, RG>;
+    using Rg = Ring<D, RG>;
     constexpr int RT = S::kRows, KS = D / 16, kStages = Rg::kStages;
     extern __shared__ __align__(128) char smem[];
     const spec_fp4_cache &C = P.cache;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-    const int pg = g ^ ((g >> 1) & 1);                 // position of the g-th column of eight
-    const int pt0 = 2 * c + (c & 1), pt1 = 2 * c + 1 - (c & 1);   // ... of columns 2c, 2c + 1
+    const int pg = g ^ ((g >> 1) & 1);                 // position of the g-th of eight
+    const int pt0 = 2 * c + (c & 1), pt1 = 2 * c + 1 - (c & 1);   // ... of 2c and 2c + 1
     const int R = P.N * P.G;
     float *s_fac = reinterpret_cast<float *>(smem + S::kFac);
     float *s_m = reinterpret_cast<float *>(smem + S::kM);
@@ -193,10 +208,10 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
     const float v_scale = C.v_scale ? __ldg(C.v_scale) : 1.f;
     const float unit = P.scale * kLog2e;
 
-    AttnWalk walk(P, C.H * row_tiles, kTreeCost);
+    AttnWalk walk(P, C.H * row_tiles, kTreeCost, P.columns);
     AttnPart A;
     bool any = false;
-    Acc<D, MT> acc;
+    Acc<D, RG> acc;
 
     while (walk.next(P, A)) {
         const int b = A.b, ctx = A.ctx, tile = A.tile;
@@ -206,7 +221,6 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
         if (P.status && tid == 0 && tile == 0 && __ldg(P.ctx_len + b) != ctx)
             P.status[b] = SPEC_REQ_BAD_SLOT;
         const int32_t *table = C.block_table + (int64_t)b * C.max_blocks;
-
         // The block of this lane's position in the part's i-th tile; -1 past the context.
         auto page = [&](int i) -> int {
             const int p = (tile + i) * kTile + warp * 32 + lane;
@@ -253,8 +267,8 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
             issue(i, cur);
         }
 
-        // Q, in the order of the products' operands: row r of 16, element d belongs to lane
-        // (r % 8, d / (D/4)), step (d % (D/4)) / 4.
+        // Q, in the order of the products' operands: element d of row r belongs to lane
+        // (r % 8, d / (D/4)); two steps of 16 elements make one 16-byte word of a lane.
         for (int r = warp; r < RT; r += kWarps) {
             constexpr int E = D / 32;                  // elements of a lane, neighbours
             const bool live = r < rows;
@@ -274,44 +288,35 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
-            // 2^k brings the largest into [2^14, 2^15); a row of zeros is left alone
-            const int ex = big > 0.f ? ilogbf(big) : 14;
-            const float up = ldexpf(1.f, max(-126, min(127, 14 - ex)));
-            const int step0 = (lane * E % (D / 4)) / 4, cc = lane * E / (D / 4);
+            // 2^k brings the largest into [2^14, 2^15), at most 2^126
+            const uint32_t ex = max(__float_as_uint(big) >> 23, 15u);
+            const float up = __uint_as_float((268u - ex) << 23);
+            const int cc = lane * E / (D / 4);
             char *q16 = smem + S::kQ, *qt = smem + S::kQt;
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
                 const int in = lane * E % (D / 4) + e;   // element within the lane's quarter
-                const int reg = ((in & 2) ? 2 : 0) + ((r & 8) ? 1 : 0);
-                const int off = (((r / 16) * KS + (E >= 4 ? step0 + e / 4 : in / 4)) * 32 +
-                                 (r % 8) * 4 + cc) * 16 + reg * 4;
+                const int kk = in / 4;                   // step; its words are elements 0 1, 2 3
+                const int off = (((r / 8) * (KS / 2) + kk / 2) * 32 + (r % 8) * 4 + cc) * 16 +
+                                (kk & 1) * 8 + (in & 2) * 2;
                 *reinterpret_cast<uint32_t *>(q16 + off) = f16x2(x[e] * up, x[e + 1] * up);
                 if (T == 1)
                     *reinterpret_cast<uint32_t *>(qt + off) =
                         (uint32_t)raw[e] | (uint32_t)raw[e + 1] << 16;
             }
-            if (lane == 0) s_fac[r] = unit / up;
+            if (lane == 0) s_fac[r] = unit * __uint_as_float((ex - 14u) << 23);
         }
         __syncthreads();
 
-        float fac[MT][2];
+        float fac[RG][2];
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < RG; ++i)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) fac[i][r] = s_fac[i * 16 + g + r * 8];
-        constexpr bool kQRegs = MT == 1 && D <= 128;
-        uint32_t qf[kQRegs ? KS : 1][4];
-        auto q_frag = [&](const char *base, int i, int kk, uint32_t (&a)[4]) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(base + ((i * KS + kk) * 32 + lane) * 16);
-            a[0] = v.x;
-            a[1] = v.y;
-            a[2] = v.z;
-            a[3] = v.w;
+            for (int e = 0; e < 2; ++e) fac[i][e] = s_fac[i * 8 + 2 * c + e];
+        // two steps of Q for group i
+        auto q_frag = [&](const char *base, int i, int kk2) -> uint4 {
+            return *reinterpret_cast<const uint4 *>(base + ((i * (KS / 2) + kk2) * 32 + lane) * 16);
         };
-        if (kQRegs) {
-#pragma unroll
-            for (int kk = 0; kk < (kQRegs ? KS : 1); ++kk) q_frag(smem + S::kQ, 0, kk, qf[kk]);
-        }
         acc.clear();
 
         for (int i = 0; i < n; ++i) {
@@ -324,14 +329,15 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
             }
             const char *st = ring + (i % kStages) * Rg::kBytes;
             const unsigned seen = *reinterpret_cast<const unsigned *>(st + Rg::kSeen);
-            float s[MT][4][4];
+            // two groups of 16 positions, 8 j + pg of which are this lane's for K
+            float s[2][RG][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int r = 0; r < RG; ++r)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[mt][j][e] = 0.f;
-            // scores: the elements of eight codes (a word) at a time, for all 32 positions
+                    for (int e = 0; e < 4; ++e) s[h][r][e] = 0.f;
+            // scores: the elements of eight codes (a word) at a time
             constexpr int KW = D / 32;                 // words of a lane's share of a position
             uint32_t kw[4][KW], ks[4][KW / 2];
 #pragma unroll
@@ -367,67 +373,62 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
             }
 #pragma unroll
             for (int w = 0; w < KW; ++w) {
-                uint32_t a[MT][2][4];
-                if (!kQRegs) {
+                uint4 qv[RG];
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
+                for (int r = 0; r < RG; ++r) qv[r] = q_frag(smem + S::kQ, r, w);
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) q_frag(smem + S::kQ, mt, 2 * w + q, a[mt][q]);
-                }
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t x[4], y[4];
+                    e2m1x8_to_f16x2(kw[2 * h][w], x);
+                    e2m1x8_to_f16x2(kw[2 * h + 1][w], y);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t r[4];
-                    e2m1x8_to_f16x2(kw[j][w], r);
+                    for (int e = 0; e < 4; ++e) {
+                        x[e] = hmul2(x[e], ks[2 * h][w / 2]);
+                        y[e] = hmul2(y[e], ks[2 * h + 1][w / 2]);
+                    }
+                    const uint32_t a0[4] = {x[0], y[0], x[1], y[1]}, a1[4] = {x[2], y[2], x[3], y[3]};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) r[e] = hmul2(r[e], ks[j][w / 2]);
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        if constexpr (kQRegs) {
-                            mma<2>(s[mt][j], qf[2 * w], r[0], r[1]);
-                            mma<2>(s[mt][j], qf[2 * w + 1], r[2], r[3]);
-                        } else {
-                            mma<2>(s[mt][j], a[mt][0], r[0], r[1]);
-                            mma<2>(s[mt][j], a[mt][1], r[2], r[3]);
-                        }
+                    for (int r = 0; r < RG; ++r) {
+                        mma<2>(s[h][r], a0, qv[r].x, qv[r].y);
+                        mma<2>(s[h][r], a1, qv[r].z, qv[r].w);
                     }
                 }
             }
-            float top[MT][2];
+            float top[RG][2];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                top[mt][0] = top[mt][1] = kNoMax;
+            for (int r = 0; r < RG; ++r) {
+                const float f[2] = {fac[r][0] * k_scale, fac[r][1] * k_scale};
+                top[r][0] = top[r][1] = kNoMax;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float x = s[mt][j][e] * (fac[mt][e >> 1] * k_scale);
-                        if (seen != 0xffffffffu && !((seen >> (8 * j + ((e & 1) ? pt1 : pt0))) & 1))
+                        float x = s[h][r][e] * f[e & 1];
+                        if (seen != 0xffffffffu && !((seen >> (16 * h + 8 * (e >> 1) + pg)) & 1))
                             x = -INFINITY;
-                        s[mt][j][e] = x;
-                        top[mt][e >> 1] = fmaxf(top[mt][e >> 1], x);
+                        s[h][r][e] = x;
+                        top[r][e & 1] = fmaxf(top[r][e & 1], x);
                     }
             }
             acc.raise(top);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int r = 0; r < RG; ++r)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float p = ex2(s[mt][j][e] - acc.m[mt][e >> 1]);
-                        s[mt][j][e] = p;
-                        acc.l[mt][e >> 1] += p;
+                        const float p = ex2(s[h][r][e] - acc.m[r][e & 1]);
+                        s[h][r][e] = p;
+                        acc.l[r][e & 1] += p;
                     }
             // values: two groups of 16 positions
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                uint32_t a[MT][4];
+                uint32_t p0[RG], p1[RG];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    a[mt][0] = f16x2(s[mt][2 * h][0], s[mt][2 * h][1]);
-                    a[mt][1] = f16x2(s[mt][2 * h][2], s[mt][2 * h][3]);
-                    a[mt][2] = f16x2(s[mt][2 * h + 1][0], s[mt][2 * h + 1][1]);
-                    a[mt][3] = f16x2(s[mt][2 * h + 1][2], s[mt][2 * h + 1][3]);
+                for (int r = 0; r < RG; ++r) {
+                    p0[r] = transpose8(f16x2(s[h][r][0], s[h][r][1]));
+                    p1[r] = transpose8(f16x2(s[h][r][2], s[h][r][3]));
                 }
                 const int ts[4] = {16 * h + pt0, 16 * h + pt1, 16 * h + 8 + pt0, 16 * h + 8 + pt1};
                 constexpr int VW = D / 64;             // words of a lane's share of a position
@@ -475,26 +476,26 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
                     e2m1x8_to_f16x2(vw[3][w], vd);
                     const uint32_t f0 = sab[w / 2], f1 = scd[w / 2];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
+                    for (int y = 0; y < 4; ++y) {
+                        // elements 8 w + 2 y and the next, of positions 2c, 2c + 1 and + 8
+                        const uint32_t a[4] = {hmul2(prmt(va[y], vb[y], 0x5410), f0),
+                                               hmul2(prmt(va[y], vb[y], 0x7632), f0),
+                                               hmul2(prmt(vc[y], vd[y], 0x5410), f1),
+                                               hmul2(prmt(vc[y], vd[y], 0x7632), f1)};
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t sel = e ? 0x7632 : 0x5410;
-                            const uint32_t b0 = hmul2(prmt(va[y], vb[y], sel), f0);
-                            const uint32_t b1 = hmul2(prmt(vc[y], vd[y], sel), f1);
-#pragma unroll
-                            for (int mt = 0; mt < MT; ++mt)
-                                mma<2>(acc.o[mt][8 * w + 2 * y + e], a[mt], b0, b1);
-                        }
+                        for (int r = 0; r < RG; ++r)
+                            mma<2>(acc.o[r][4 * w + y], a, p0[r], p1[r]);
+                    }
                 }
             }
         }
         cp_async_wait<0>();
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int r = 0; r < RG; ++r)
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j)
+            for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc.o[mt][j][e] *= v_scale;
+                for (int e = 0; e < 4; ++e) acc.o[r][j][e] *= v_scale;
         __syncthreads();      // the ring is free
 
         if (A.stop == A.nt) {
@@ -504,6 +505,7 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
             if (tid == 0) *s_odd = 0ull;
             __syncthreads();
             const int keys = min(kMaxN, (P.N + 15) / 16 * 16);
+#pragma unroll 4
             for (int i = tid; i < keys * (D / 2); i += kThreads) {
                 const int t = i / (D / 2), d = (i - t * (D / 2)) * 2;
                 uint32_t kv[2] = {0, 0};
@@ -527,92 +529,100 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
             const int key0 = warp * 16;
             if (key0 < P.N) {
                 const unsigned odd = (unsigned)(*s_odd >> key0) & 0xffffu;
-                unsigned bits[MT][2];
-                float s[MT][2][4], top[MT][2];
+                unsigned bits[RG][2];
+                float s[RG][4], top[RG][2];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int r = 0; r < RG; ++r)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int rr = mt * 16 + g + r * 8;
-                        bits[mt][r] =
+                    for (int e = 0; e < 2; ++e) {
+                        const int rr = r * 8 + 2 * c + e;
+                        bits[r][e] =
                             rr < rows ? (unsigned)(__ldg(P.mask + (int64_t)b * P.N +
                                                          (row0 + rr) / P.G) >> key0) &
                                             (P.N - key0 >= 16 ? 0xffffu : (1u << (P.N - key0)) - 1u)
                                       : 0u;
-                        top[mt][r] = kNoMax;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[mt][r][e] = 0.f;
+                        top[r][e] = kNoMax;
+                        s[r][e] = s[r][e + 2] = 0.f;
                     }
 #pragma unroll
-                for (int kk = 0; kk < KS; ++kk) {
-                    uint32_t a[MT][4];
+                for (int kk2 = 0; kk2 < KS / 2; ++kk2) {
+                    uint4 qv[RG];
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-                        q_frag(smem + (T == 1 ? S::kQt : S::kQ), mt, kk, a[mt]);
+                    for (int r = 0; r < RG; ++r)
+                        qv[r] = q_frag(smem + (T == 1 ? S::kQt : S::kQ), r, kk2);
+                    // elements 8 kk2 .. + 7 of this lane's quarter, of nodes g and g + 8
+                    uint2 x[2], y[2];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint2 kv = *reinterpret_cast<const uint2 *>(
-                            tk + (key0 + 8 * j + g) * S::kTreeStride + c * (D / 4) + 4 * kk);
+                    for (int e = 0; e < 2; ++e) {
+                        const unsigned short *k = tk + (key0 + g) * S::kTreeStride + c * (D / 4) +
+                                                  8 * kk2 + 4 * e;
+                        x[e] = *reinterpret_cast<const uint2 *>(k);
+                        y[e] = *reinterpret_cast<const uint2 *>(k + 8 * S::kTreeStride);
+                    }
+                    const uint32_t a0[4] = {x[0].x, y[0].x, x[0].y, y[0].y};
+                    const uint32_t a1[4] = {x[1].x, y[1].x, x[1].y, y[1].y};
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) mma<T>(s[mt][j], a[mt], kv.x, kv.y);
+                    for (int r = 0; r < RG; ++r) {
+                        mma<T>(s[r], a0, qv[r].x, qv[r].y);
+                        mma<T>(s[r], a1, qv[r].z, qv[r].w);
                     }
                 }
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int r = 0; r < RG; ++r)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float f = T == 1 ? unit : fac[mt][e >> 1];
-                            const bool on = (bits[mt][e >> 1] >> (8 * j + 2 * c + (e & 1))) & 1;
-                            s[mt][j][e] = on ? s[mt][j][e] * f : -INFINITY;
-                            top[mt][e >> 1] = fmaxf(top[mt][e >> 1], s[mt][j][e]);
-                        }
-                acc.raise(top);
-                uint32_t hi[MT][4], lo[MT][4];
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float p = ex2(s[mt][j][e] - acc.m[mt][e >> 1]);
-                            s[mt][j][e] = p;
-                            acc.l[mt][e >> 1] += p;
-                        }
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float p0 = s[mt][j][2 * r], p1 = s[mt][j][2 * r + 1];
-                            if (T == 2) {
-                                hi[mt][2 * j + r] = f16x2(p0, p1);
-                            } else {
-                                // eight bits are too few for p: a second product has the rest
-                                const uint32_t w = bf16x2(p0, p1);
-                                hi[mt][2 * j + r] = w;
-                                lo[mt][2 * j + r] = bf16x2(p0 - bf_lo(w), p1 - bf_hi(w));
-                            }
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        const float f = T == 1 ? unit : fac[r][e & 1];
+                        const bool on = (bits[r][e & 1] >> (g + 8 * (e >> 1))) & 1;
+                        s[r][e] = on ? s[r][e] * f : -INFINITY;
+                        top[r][e & 1] = fmaxf(top[r][e & 1], s[r][e]);
                     }
+                acc.raise(top);
+                uint32_t hi[RG][2], lo[RG][2];
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    const unsigned short *v = tv + g * (D / 8) + j;
-                    uint32_t w[2];
+                for (int r = 0; r < RG; ++r) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float p = ex2(s[r][e] - acc.m[r][e & 1]);
+                        s[r][e] = p;
+                        acc.l[r][e & 1] += p;
+                    }
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        const int t = 2 * c + 8 * q;
-                        uint32_t x = v[(key0 + t) * S::kTreeStride];
-                        uint32_t y = v[(key0 + t + 1) * S::kTreeStride];
+                        const float x = s[r][2 * q], y = s[r][2 * q + 1];
+                        if (T == 2) {
+                            hi[r][q] = transpose8(f16x2(x, y));
+                        } else {
+                            // eight bits are too few for p: a second product has the rest
+                            const uint32_t w = bf16x2(x, y);
+                            hi[r][q] = transpose8(w);
+                            lo[r][q] = transpose8(bf16x2(x - bf_lo(w), y - bf_hi(w)));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    uint32_t a[4];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        // elements 2 j, 2 j + 1 of nodes 2c + 8 q and the next
+                        const unsigned short *v = tv + (key0 + 2 * c + 8 * q) * S::kTreeStride +
+                                                  g * (D / 8) + 2 * j;
+                        uint32_t x = *reinterpret_cast<const uint32_t *>(v);
+                        uint32_t y = *reinterpret_cast<const uint32_t *>(v + S::kTreeStride);
                         if (odd) {
                             constexpr uint32_t ex = T == 1 ? 0x7f80u : 0x7c00u;
-                            if ((x & ex) == ex) x = 0;
-                            if ((y & ex) == ex) y = 0;
+                            if ((x & ex) == ex) x &= 0xffff0000u;
+                            if ((x >> 16 & ex) == ex) x &= 0xffffu;
+                            if ((y & ex) == ex) y &= 0xffff0000u;
+                            if ((y >> 16 & ex) == ex) y &= 0xffffu;
                         }
-                        w[q] = x | y << 16;
+                        a[2 * q] = prmt(x, y, 0x5410);
+                        a[2 * q + 1] = prmt(x, y, 0x7632);
                     }
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        mma<T>(acc.o[mt][j], hi[mt], w[0], w[1]);
-                        if (T == 1) mma<T>(acc.o[mt][j], lo[mt], w[0], w[1]);
+                    for (int r = 0; r < RG; ++r) {
+                        mma<T>(acc.o[r][j], a, hi[r][0], hi[r][1]);
+                        if (T == 1) mma<T>(acc.o[r][j], a, lo[r][0], lo[r][1]);
                     }
                 }
                 // nodes with NaN or infinities in V: only for the rows that see them
@@ -621,24 +631,21 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
                     for (int t = 0; t < 16; ++t) {
                         if (!((odd >> t) & 1)) continue;
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
+                        for (int r = 0; r < RG; ++r)
 #pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                const float p = __shfl_sync(
-                                    0xffffffffu, s[mt][t >> 3][2 * r + (t & 1)],
-                                    (lane & ~3) | ((t >> 1) & 3));
-                                if (!((bits[mt][r] >> t) & 1)) continue;
+                            for (int e = 0; e < 2; ++e) {
+                                const float p = __shfl_sync(0xffffffffu, s[r][2 * (t >> 3) + e],
+                                                            (t & 7) * 4 + c);
+                                if (!((bits[r][e] >> t) & 1)) continue;
 #pragma unroll
-                                for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-                                    for (int e = 0; e < 2; ++e) {
-                                        const uint32_t x =
-                                            tv[(key0 + t) * S::kTreeStride + (2 * c + e) * (D / 8) + j];
-                                        constexpr uint32_t ex = T == 1 ? 0x7f80u : 0x7c00u;
-                                        if ((x & ex) == ex)
-                                            acc.o[mt][j][2 * r + e] +=
-                                                p * (T == 1 ? __uint_as_float(x << 16) : half_bits(x));
-                                    }
+                                for (int j = 0; j < D / 8; ++j) {
+                                    const uint32_t x =
+                                        tv[(key0 + t) * S::kTreeStride + g * (D / 8) + j];
+                                    constexpr uint32_t ex = T == 1 ? 0x7f80u : 0x7c00u;
+                                    if ((x & ex) == ex)
+                                        acc.o[r][j / 2][2 * (j & 1) + e] +=
+                                            p * (T == 1 ? __uint_as_float(x << 16) : half_bits(x));
+                                }
                             }
                     }
                 }
@@ -648,44 +655,44 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
 
         // The four warps' states become one.
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int r = 0; r < RG; ++r)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float l = acc.l[mt][r];
-                l += __shfl_xor_sync(0xffffffffu, l, 1);
-                l += __shfl_xor_sync(0xffffffffu, l, 2);
-                if (c == 0) {
-                    s_m[warp * RT + mt * 16 + g + 8 * r] = acc.m[mt][r];
-                    s_l[warp * RT + mt * 16 + g + 8 * r] = l;
+            for (int e = 0; e < 2; ++e) {
+                float l = acc.l[r][e];
+#pragma unroll
+                for (int s = 4; s < 32; s <<= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+                if (g == 0) {
+                    s_m[warp * RT + r * 8 + 2 * c + e] = acc.m[r][e];
+                    s_l[warp * RT + r * 8 + 2 * c + e] = l;
                 }
             }
         __syncthreads();
-        float4 *join = reinterpret_cast<float4 *>(smem);   // [D/16][RT][4]: row r, quarter c
-        float f[MT][2];
+        // [D/32 of a lane][g][row]: four elements of a row each; the pitch avoids bank conflicts
+        float4 *join = reinterpret_cast<float4 *>(smem);
+        float f[RG][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int r = 0; r < RG; ++r)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int rr = mt * 16 + g + 8 * r;
+            for (int e = 0; e < 2; ++e) {
+                const int rr = r * 8 + 2 * c + e;
                 float m = s_m[rr];
 #pragma unroll
                 for (int w = 1; w < kWarps; ++w) m = fmaxf(m, s_m[w * RT + rr]);
-                f[mt][r] = exp2f(acc.m[mt][r] - m);
+                f[r][e] = exp2f(acc.m[r][e] - m);
             }
         for (int w = 0; w < kWarps; ++w) {
             if (warp == w) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int r = 0; r < RG; ++r)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r)
+                    for (int e = 0; e < 2; ++e)
 #pragma unroll
-                        for (int q = 0; q < D / 16; ++q) {
-                            // columns 2c + e of all the products: elements (2c + e) D/8 + j
-                            const int e = q / (D / 32), j = (q % (D / 32)) * 4;
-                            float4 v = make_float4(
-                                acc.o[mt][j][2 * r + e] * f[mt][r], acc.o[mt][j + 1][2 * r + e] * f[mt][r],
-                                acc.o[mt][j + 2][2 * r + e] * f[mt][r], acc.o[mt][j + 3][2 * r + e] * f[mt][r]);
-                            float4 &to = join[(q * RT + mt * 16 + g + 8 * r) * 4 + c];
+                        for (int q = 0; q < D / 32; ++q) {
+                            float4 v = make_float4(acc.o[r][2 * q][e] * f[r][e],
+                                                   acc.o[r][2 * q][2 + e] * f[r][e],
+                                                   acc.o[r][2 * q + 1][e] * f[r][e],
+                                                   acc.o[r][2 * q + 1][2 + e] * f[r][e]);
+                            float4 &to = join[(q * 8 + g) * (RT + 1) + r * 8 + 2 * c + e];
                             if (w > 0) {
                                 const float4 o = to;
                                 v.x += o.x;
@@ -701,8 +708,8 @@ __global__ void __launch_bounds__(kThreads, MT == 2 || D == 256 ? 2 : 3)
         const bool whole = tile == 0 && A.stop == A.nt;
         float *part = attn_slot(P, blockIdx.x, tile == 0, RT, D);
         for (int i = tid; i < rows * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), d4 = i - r * (D / 4), cc = d4 / (D / 16), q = d4 % (D / 16);
-            const float4 v = join[(q * RT + r) * 4 + cc];
+            const int r = i / (D / 4), d4 = i - r * (D / 4), gg = d4 / (D / 32), q = d4 % (D / 32);
+            const float4 v = join[(q * 8 + gg) * (RT + 1) + r];
             float m = s_m[r], l = 0.f;
 #pragma unroll
             for (int w = 1; w < kWarps; ++w) m = fmaxf(m, s_m[w * RT + r]);
@@ -737,21 +744,22 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(TreeAttnParams P, in
     const int c0 = blockIdx.y;
     const int4 note = P.notes[c0];
     if (note.x < 0) return;
-    const int b = note.x, c1 = note.z, row_tiles = (P.N * P.G + rows_tile - 1) / rows_tile;
+    const int b = note.x, c1 = note.z, step = P.columns, row_tiles = (P.N * P.G + rows_tile - 1) / rows_tile;
     const int head = note.y / row_tiles, row0 = (note.y - head * row_tiles) * rows_tile;
     const int rows = min(rows_tile, P.N * P.G - row0);
     const int i = blockIdx.x * kJoinThreads + threadIdx.x, r = i / (D / 4), d4 = i - r * (D / 4);
     if (r >= rows) return;
     float m = kNoMax, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; c += 8) {
+    for (int c = c0; c <= c1; c += 8 * step) {
         float4 v[8];
         float pm[8], pl[8], top = m;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             pm[u] = kNoMax;
-            if (c + u > c1) continue;
-            const float *part = attn_slot(P, c + u, c + u == c0, rows_tile, D);
+            const int k = c + u * step;
+            if (k > c1) continue;
+            const float *part = attn_slot(P, k, k == c0, rows_tile, D);
             v[u] = __ldcg(reinterpret_cast<const float4 *>(part) + i);
             pm[u] = __ldcg(part + rows_tile * D + r);
             pl[u] = __ldcg(part + rows_tile * (D + 1) + r);
@@ -767,7 +775,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(TreeAttnParams P, in
         o.w *= a;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            if (c + u > c1) continue;
+            if (c + u * step > c1) continue;
             const float w = ex2(pm[u] - top);
             o.x = fmaf(v[u].x, w, o.x);
             o.y = fmaf(v[u].y, w, o.y);
@@ -782,8 +790,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(TreeAttnParams P, in
     if (P.lse && d4 == 0) P.lse[at] = attn_lse(m, l);
 }
 
-// How a call is run: by this file's warps (groups of 16 rows of an item, CTAs an SM holds), or,
-// with more rows than two groups, on the tcgen05 tensor cores.
+// How a call is run: by this file's warps (groups of 8 rows of an item), or, with more rows
+// than four groups, on the tcgen05 tensor cores.
 struct Plan {
     bool tc;
     int groups, rows, grid;   // rows of an item
@@ -791,30 +799,40 @@ struct Plan {
 Plan plan(int R, int D, int sms) {
     Plan p;
     p.tc = R > 32 && D <= 128;
-    p.groups = R > 16 && D <= 128 ? 2 : 1;
-    p.rows = p.tc ? tree_attn_tc_rows(R) : 16 * p.groups;
-    p.grid = sms * (p.tc ? 1 : p.groups == 2 || D == 256 ? 2 : 3);
+    const int most = D == 256 ? 2 : 4;
+    p.groups = (R + 7) / 8 < most ? (R + 7) / 8 : most;
+    p.rows = p.tc ? tree_attn_tc_rows(R) : 8 * p.groups;
+    p.grid = sms * (p.tc ? 1 : ctas_per_sm(D, p.groups));
     return p;
 }
 
-template <int T, int D, int MT>
+template <int T, int D, int RG>
 cudaError_t launch(const TreeAttnParams &p, int grid, cudaStream_t st) {
-    const int smem = Smem<T, D, MT>::kBytes;
-    const cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<T, D, MT>,
+    const int smem = Smem<T, D, RG>::kBytes;
+    const cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<T, D, RG>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int row_tiles = (p.N * p.G + 16 * MT - 1) / (16 * MT);
-    tree_attn_kernel<T, D, MT><<<grid, kThreads, smem, st>>>(p, row_tiles);
+    const int row_tiles = (p.N * p.G + 8 * RG - 1) / (8 * RG);
+    tree_attn_kernel<T, D, RG><<<grid, kThreads, smem, st>>>(p, row_tiles);
     return cudaGetLastError();
+}
+
+template <int T, int D>
+cudaError_t launch_groups(const TreeAttnParams &p, const Plan &n, cudaStream_t st) {
+    if (n.groups == 1) return launch<T, D, 1>(p, n.grid, st);
+    if (n.groups == 2) return launch<T, D, 2>(p, n.grid, st);
+    if constexpr (D <= 128) {
+        if (n.groups == 3) return launch<T, D, 3>(p, n.grid, st);
+        return launch<T, D, 4>(p, n.grid, st);
+    }
+    return cudaErrorInvalidValue;
 }
 
 template <int T>
 cudaError_t launch_type(const TreeAttnParams &p, const Plan &n, cudaStream_t st) {
-    const int D = p.cache.D;
-    if (D == 256) return launch<T, 256, 1>(p, n.grid, st);
-    if (n.groups == 2)
-        return D == 64 ? launch<T, 64, 2>(p, n.grid, st) : launch<T, 128, 2>(p, n.grid, st);
-    return D == 64 ? launch<T, 64, 1>(p, n.grid, st) : launch<T, 128, 1>(p, n.grid, st);
+    if (p.cache.D == 64) return launch_groups<T, 64>(p, n, st);
+    if (p.cache.D == 128) return launch_groups<T, 128>(p, n, st);
+    return launch_groups<T, 256>(p, n, st);
 }
 
 }  // namespace
@@ -822,6 +840,13 @@ cudaError_t launch_type(const TreeAttnParams &p, const Plan &n, cudaStream_t st)
 namespace {
 
 int64_t notes_bytes(const Plan &n) { return ((int64_t)n.grid * sizeof(int4) + 255) / 256 * 256; }
+
+// Columns of CTAs (see tree_attn.cuh): one for each item of a request, unless that leaves more
+// than one CTA in sixteen without work.
+int columns(const TreeAttnParams &p, const Plan &n) {
+    const int64_t items = (int64_t)p.cache.H * ((p.N * p.G + n.rows - 1) / n.rows);
+    return items <= n.grid && n.grid % items * 16 <= n.grid ? (int)items : 1;
+}
 
 template <int T, int D>
 cudaError_t launch_join(const TreeAttnParams &p, const Plan &n, cudaStream_t st) {
@@ -842,6 +867,7 @@ cudaError_t launch_tree_attn(const TreeAttnParams &given, cudaStream_t st) {
     TreeAttnParams p = given;
     const int D = p.cache.D;
     const Plan n = plan(p.N * p.G, D, p.sms);
+    p.columns = columns(p, n);
     p.notes = static_cast<int4 *>(p.workspace);
     p.ws = reinterpret_cast<float *>(static_cast<char *>(p.workspace) + notes_bytes(n));
     const cudaError_t e = n.tc             ? launch_tree_attn_tc(p, n.grid, st)

@@ -6,7 +6,11 @@
 // context tile counts as one unit of work; the tree's tile, with what an item costs besides
 // (its queries in, its result out), as `cost` units, of which the tile takes place in the first.
 // The units of all items, in order, are cut into equal ranges, one for each CTA of a single
-// wave, whatever the requests' lengths (which only the device knows). A CTA therefore works on
+// wave, whatever the requests' lengths (which only the device knows). The CTAs may stand in
+// columns, one for each item of a request (K/V head and row tile), each column cutting all
+// requests alike: then the heads of a position are read at the same time. In the NHD layout they
+// lie side by side, eight bytes of block scales each, and were fetched over and over when every
+// head passed a position at a time of its own (64 chains, 8 heads: 1.14 GB for 0.54). A CTA therefore works on
 // end of one item, some whole items, and the start of another. Whole items are finished in
 // place. The parts of an item that a cut goes through are written to the workspace (row sums
 // and maxima and the unnormalised rows, float32), and a second kernel joins them in their
@@ -28,13 +32,14 @@ __device__ __forceinline__ int attn_ctx(const TreeAttnParams &P, int b) {
 
 // A CTA's range of units, and where it begins.
 struct AttnRange {
-    int64_t total, begin, end;   // units of the call; this CTA's [begin, end)
-    int ctas;                    // CTAs that have a range: each has at least one unit
+    int64_t total, begin, end;   // units of a column; this CTA's [begin, end)
+    int ctas;                    // CTAs of a column that have a range: each at least one unit
     int b, item, tile;           // place of `begin`: request, item in it, unit in that
 };
 
-// `items`: items of a request. Every warp computes it for itself (one warp scan).
-__device__ __forceinline__ AttnRange attn_range(const TreeAttnParams &P, int items, int cost) {
+// `items`: items of a request in a column. Every warp computes it for itself (one warp scan).
+__device__ __forceinline__ AttnRange attn_range(const TreeAttnParams &P, int items, int cost,
+                                                int columns) {
     auto units = [&](int b) { return (attn_ctx(P, b) + kTile - 1) / kTile + cost; };
     const unsigned full = 0xffffffffu;
     const int lane = threadIdx.x & 31;
@@ -49,12 +54,13 @@ __device__ __forceinline__ AttnRange attn_range(const TreeAttnParams &P, int ite
     }
     AttnRange r;
     r.total = __shfl_sync(full, sum, 31);
-    r.ctas = (int)min((int64_t)gridDim.x, r.total);
+    const int cta = blockIdx.x / columns;
+    r.ctas = (int)min((int64_t)(gridDim.x / columns), r.total);
     r.b = r.item = r.tile = 0;
     r.begin = r.end = 0;
-    if ((int)blockIdx.x >= r.ctas) return r;
-    r.begin = r.total * blockIdx.x / r.ctas;
-    r.end = r.total * (blockIdx.x + 1) / r.ctas;
+    if (cta >= r.ctas) return r;
+    r.begin = r.total * cta / r.ctas;
+    r.end = r.total * (cta + 1) / r.ctas;
     const int64_t before = sum - mine;
     const bool here = before <= r.begin && r.begin < sum;
     if (here) {
@@ -78,7 +84,7 @@ __device__ __forceinline__ AttnRange attn_range(const TreeAttnParams &P, int ite
     return r;
 }
 
-// The CTA whose range holds unit s.
+// The CTA (of a column) whose range holds unit s.
 __device__ __forceinline__ int attn_owner(const AttnRange &r, int64_t s) {
     return (int)(((s + 1) * r.ctas - 1) / r.total);
 }
@@ -93,11 +99,13 @@ struct AttnPart {
 struct AttnWalk {
     AttnRange r;
     int64_t at;
-    int b, item, tile, items, cost;
+    int b, item, tile, items, cost, column;   // column: 0 if there is one only
 
-    __device__ __forceinline__ AttnWalk(const TreeAttnParams &P, int items_, int cost_)
-        : r(attn_range(P, items_, cost_)), at(r.begin), b(r.b), item(r.item), tile(r.tile),
-          items(items_), cost(cost_) {}
+    // `all`: items of a request.
+    __device__ __forceinline__ AttnWalk(const TreeAttnParams &P, int all, int cost_, int columns)
+        : r(attn_range(P, columns > 1 ? 1 : all, cost_, columns)), at(r.begin), b(r.b),
+          item(r.item), tile(r.tile), items(columns > 1 ? 1 : all), cost(cost_),
+          column(blockIdx.x % columns) {}
     // The next part, or false. Units past the tree's first start nothing.
     __device__ __forceinline__ bool next(const TreeAttnParams &P, AttnPart &p) {
         while (at < r.end) {
@@ -105,7 +113,7 @@ struct AttnWalk {
             const int left = nt - 1 + cost - tile;
             const bool starts = tile < nt;
             p.b = b;
-            p.item = item;
+            p.item = item + column;
             p.tile = tile;
             p.nt = nt;
             p.ctx = ctx;
@@ -136,7 +144,10 @@ __device__ __forceinline__ void attn_note(const TreeAttnParams &P, const AttnRan
                                           const AttnPart &last, bool any) {
     int4 note = make_int4(-1, 0, 0, 0);
     if (any && last.tile == 0 && last.stop < last.nt)
-        note = make_int4(last.b, last.item, attn_owner(r, last.first + last.nt - 1), 0);
+        note = make_int4(last.b, last.item,
+                         attn_owner(r, last.first + last.nt - 1) * P.columns +
+                             (int)blockIdx.x % P.columns,
+                         0);
     P.notes[blockIdx.x] = note;
 }
 

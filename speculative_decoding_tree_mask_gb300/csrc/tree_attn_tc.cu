@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // are given is then the same in all of the warp, as their uniform operands want it.
         const int m = warp - kMmaWarp;
         if (m < 2) {
-            AttnWalk walk(P, C.H * row_tiles, kTreeCost);
+            AttnWalk walk(P, C.H * row_tiles, kTreeCost, P.columns);
             const bool lead = elect_one();
             const uint32_t o = o_at(m);
             uint32_t jobs = 0;           // of this group before this part
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kRaws = C_::kRaws;
         char *mine = smem + C_::kRaw + ((of_v ? kRaws : 0) * 128 + t) * C_::kPitch;
         const uint32_t mine_s = smem_addr(mine);
-        AttnWalk walk(P, C.H * row_tiles, kTreeCost);
+        AttnWalk walk(P, C.H * row_tiles, kTreeCost, P.columns);
         bool go = true;               // no wait has given up
         while (walk.next(P, A)) {
             const int b = A.b, ctx = A.ctx, n = A.stop - A.tile, tree = A.nt - 1 - A.tile;
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float v_scale = C.v_scale ? __ldg(C.v_scale) : 1.f;
         const float unit = P.scale * kLog2e;
         const float cache_unit = unit * (C.k_scale ? __ldg(C.k_scale) : 1.f);
-        AttnWalk walk(P, C.H * row_tiles, kTreeCost);
+        AttnWalk walk(P, C.H * row_tiles, kTreeCost, P.columns);
         uint32_t jobs = 0, results = 0;   // of this group so far; parts with any
         bool go = true;
         while (walk.next(P, A)) {
