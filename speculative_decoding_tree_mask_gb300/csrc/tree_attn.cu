@@ -41,7 +41,7 @@ constexpr int ctas_per_sm(int D, int RG) {
     return D * RG <= 64 ? 5 : D * RG <= 128 ? 4 : D * RG <= 256 ? 3 : 2;
 }
 // Tiles in the ring: the one at work and those in flight.
-constexpr int stages(int D, int RG) { return D == 256 ? 2 : 3; }
+constexpr int stages(int D, int RG) { return D == 256 || (D == 128 && RG == 1) ? 2 : 3; }
 
 template <int D, int RG>
 struct Ring {
@@ -404,7 +404,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, RG))
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float x = s[h][r][e] * f[e & 1];
-                        if (seen != 0xffffffffu && !((seen >> (16 * h + 8 * (e >> 1) + pg)) & 1))
+                        if (seen != 0xffffffffu &&
+                            !((seen >> (16 * h + 8 * (e >> 1) + pg)) & 1))
                             x = -INFINITY;
                         s[h][r][e] = x;
                         top[r][e & 1] = fmaxf(top[r][e & 1], x);
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, RG))
                         s[h][r][e] = p;
                         acc.l[r][e & 1] += p;
                     }
-            // values: two groups of 16 positions
+            // values
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t p0[RG], p1[RG];
@@ -430,7 +431,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, RG))
                     p0[r] = transpose8(f16x2(s[h][r][0], s[h][r][1]));
                     p1[r] = transpose8(f16x2(s[h][r][2], s[h][r][3]));
                 }
-                const int ts[4] = {16 * h + pt0, 16 * h + pt1, 16 * h + 8 + pt0, 16 * h + 8 + pt1};
+                const int t0 = 16 * h;
+                const int ts[4] = {t0 + pt0, t0 + pt1, t0 + 8 + pt0, t0 + 8 + pt1};
                 constexpr int VW = D / 64;             // words of a lane's share of a position
                 constexpr int VG = D == 256 ? 2 : 1;   // block scales of that share
                 uint32_t vw[4][VW], sab[VG], scd[VG];
@@ -735,32 +737,38 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, RG))
     if (tid == 0) attn_note(P, walk.r, A, any);
 }
 
-// The parts of cut items into the result: a CTA has 256 float4s of an item's rows, a thread one
-// of each part, eight parts' loads in flight together.
+// The parts of cut items into the result. A thread has a float4 of a row and, of the parts,
+// every PG-th, eight of them in flight together; the PG threads of a float4 meet in shared
+// memory. PG is 1 for items of few parts and many rows.
 constexpr int kJoinThreads = 256;
-template <int T, int D>
+template <int T, int D, int PG>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(TreeAttnParams P, int rows_tile) {
+    constexpr int F = D / 4, kPer = kJoinThreads / (F * PG);       // rows of a CTA
+    __shared__ float4 s_o[PG > 1 ? kJoinThreads : 1];
+    __shared__ float2 s_ml[PG > 1 ? kJoinThreads : 1];
     grid_dep_wait();
     const int c0 = blockIdx.y;
     const int4 note = P.notes[c0];
     if (note.x < 0) return;
-    const int b = note.x, c1 = note.z, step = P.columns, row_tiles = (P.N * P.G + rows_tile - 1) / rows_tile;
+    const int b = note.x, c1 = note.z, step = P.columns;
+    const int row_tiles = (P.N * P.G + rows_tile - 1) / rows_tile;
     const int head = note.y / row_tiles, row0 = (note.y - head * row_tiles) * rows_tile;
     const int rows = min(rows_tile, P.N * P.G - row0);
-    const int i = blockIdx.x * kJoinThreads + threadIdx.x, r = i / (D / 4), d4 = i - r * (D / 4);
-    if (r >= rows) return;
+    const int d4 = threadIdx.x % F, group = threadIdx.x / F % PG;
+    const int r = blockIdx.x * kPer + threadIdx.x / (F * PG);
+    if (PG == 1 && r >= rows) return;
     float m = kNoMax, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; c += 8 * step) {
+    for (int c = c0 + group * step; c <= c1 && r < rows; c += 8 * PG * step) {
         float4 v[8];
         float pm[8], pl[8], top = m;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             pm[u] = kNoMax;
-            const int k = c + u * step;
+            const int k = c + u * PG * step;
             if (k > c1) continue;
             const float *part = attn_slot(P, k, k == c0, rows_tile, D);
-            v[u] = __ldcg(reinterpret_cast<const float4 *>(part) + i);
+            v[u] = __ldcg(reinterpret_cast<const float4 *>(part + r * D) + d4);
             pm[u] = __ldcg(part + rows_tile * D + r);
             pl[u] = __ldcg(part + rows_tile * (D + 1) + r);
         }
@@ -775,13 +783,37 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(TreeAttnParams P, in
         o.w *= a;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            if (c + u * step > c1) continue;
+            if (c + u * PG * step > c1) continue;
             const float w = ex2(pm[u] - top);
             o.x = fmaf(v[u].x, w, o.x);
             o.y = fmaf(v[u].y, w, o.y);
             o.z = fmaf(v[u].z, w, o.z);
             o.w = fmaf(v[u].w, w, o.w);
             l = fmaf(pl[u], w, l);
+        }
+    }
+    if (PG > 1) {
+        s_o[threadIdx.x] = o;
+        s_ml[threadIdx.x] = make_float2(m, l);
+        __syncthreads();
+        if (group != 0 || r >= rows) return;
+        float top = m;
+#pragma unroll
+        for (int u = 1; u < PG; ++u) top = fmaxf(top, s_ml[threadIdx.x + u * F].x);
+        const float a = ex2(m - top);
+        o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
+        l *= a;
+        m = top;
+#pragma unroll
+        for (int u = 1; u < PG; ++u) {
+            const float2 ml = s_ml[threadIdx.x + u * F];
+            const float4 v = s_o[threadIdx.x + u * F];
+            const float w = ex2(ml.x - top);
+            o.x = fmaf(v.x, w, o.x);
+            o.y = fmaf(v.y, w, o.y);
+            o.z = fmaf(v.z, w, o.z);
+            o.w = fmaf(v.w, w, o.w);
+            l = fmaf(ml.y, w, l);
         }
     }
     const float f = l == 0.f ? 0.f : 1.f / l;
@@ -850,8 +882,16 @@ int columns(const TreeAttnParams &p, const Plan &n) {
 
 template <int T, int D>
 cudaError_t launch_join(const TreeAttnParams &p, const Plan &n, cudaStream_t st) {
-    const dim3 grid((n.rows * (D / 4) + kJoinThreads - 1) / kJoinThreads, n.grid);
-    return launch_dependent(join_kernel<T, D>, grid, dim3(kJoinThreads), 0, st, p, n.rows);
+    constexpr int F = D / 4, PG = D == 256 ? 4 : 8;
+    // all CTAs' work in items of about this many parts: over eight, the parts are shared out
+    const int R = p.N * p.G, rows = R < n.rows ? R : n.rows;
+    const int64_t items = (int64_t)p.B * p.cache.H * ((R + n.rows - 1) / n.rows);
+    const int per = kJoinThreads / F;
+    if (n.grid > 8 * items && rows <= 32)
+        return launch_dependent(join_kernel<T, D, PG>, dim3((rows * PG + per - 1) / per, n.grid),
+                                dim3(kJoinThreads), 0, st, p, n.rows);
+    return launch_dependent(join_kernel<T, D, 1>, dim3((rows + per - 1) / per, n.grid),
+                            dim3(kJoinThreads), 0, st, p, n.rows);
 }
 
 }  // namespace
