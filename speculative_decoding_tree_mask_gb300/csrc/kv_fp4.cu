@@ -15,10 +15,11 @@ namespace specv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kItems = 4;          // blocks of 16 elements a thread handles at a time
-constexpr int kUnit = kThreads * kItems;
-constexpr int kSmemRequests = 2048;
-constexpr int kCtasPerSm = 8;
+constexpr int kSmemRequests = 2048;   // requests whose last slot and position fit in shared memory
+// Commit: blocks of 16 elements a thread handles at a time, CTAs an SM holds.
+constexpr int kCommitItems = 2, kCommitUnit = kThreads * kCommitItems, kCommitCtas = 3;
+// Load: likewise.
+constexpr int kItems = 4, kUnit = kThreads * kItems, kCtasPerSm = 8;
 
 // A thread's 16 elements as floats. vec: 32, 16 (byte alignment of every block) or 0.
 template <int T>
@@ -80,10 +81,10 @@ __device__ __forceinline__ uint32_t quantise16(const float (&x)[16], float r, ui
     // the scale's float: exact through a half
     const uint32_t h = e4m3x2_to_f16x2(sf);
     const float s = __half2float(__ushort_as_half((unsigned short)h));
-    const float m = s > 0.f ? __frcp_rn(s) * r : 0.f;
+    const float m = s > 0.f ? __frcp_rn(s) * r : 0.f;   // s 0: codes 0; s NaN: any codes
     float y[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = m > 0.f ? x[i] * m : 0.f;
+    for (int i = 0; i < 16; ++i) y[i] = x[i] * m;
     c.x = f32x8_to_e2m1x8(y);
     c.y = f32x8_to_e2m1x8(y + 8);
     return sf;
@@ -111,85 +112,102 @@ __device__ __forceinline__ void commit_status(const KvFp4Params &P, int b, int l
 }
 
 // Units of `slots` consecutive slots x all 16-element blocks of K and V of a request (or a
-// piece of one slot when that is more than kUnit), slot groups outermost: the slots that every
+// piece of one slot when that is more than a unit), slot groups outermost: the slots that every
 // request writes come first, and the CTAs, a wave of them striding over the units, stop at the
-// last slot that any request writes.
+// last slot that any request writes. A unit costs two round trips, its nodes and cache blocks
+// and then its rows; the first is made while the unit before waits for its rows.
 template <int T>
-__global__ void __launch_bounds__(kThreads) commit_kernel(KvFp4Params P, int slots, int pieces,
-                                                          int vec) {
-    extern __shared__ int s_last[];
+__global__ void __launch_bounds__(kThreads, kCommitCtas)
+    commit_kernel(KvFp4Params P, int slots, int pieces, int vec) {
+    extern __shared__ int2 s_req[];      // (last slot, position) of each request
     __shared__ int s_max;
+    constexpr int I = kCommitItems;
     const spec_fp4_cache &c = P.cache;
     const int tid = threadIdx.x, B = P.B;
     const bool cached = B <= kSmemRequests;
     const int per_head = c.D / 16, row = c.H * per_head;   // blocks of a head, of a K row
     int most = P.N - 1;
-    if (cached && P.last) {
+    if (cached) {
         if (tid == 0) s_max = -1;
         __syncthreads();
         int m = -1;
         for (int b = tid; b < B; b += kThreads) {
-            const int l = last_slot(P, b);
-            s_last[b] = l;
-            m = max(m, l);
+            const int2 r = make_int2(last_slot(P, b), __ldg(P.pos + b));
+            s_req[b] = r;
+            m = max(m, r.x);
         }
         m = __reduce_max_sync(0xffffffffu, m);
         if ((tid & 31) == 0) atomicMax(&s_max, m);
         __syncthreads();
         most = s_max;
     }
-    auto last_of = [&](int b) { return cached && P.last ? s_last[b] : last_slot(P, b); };
+    auto request = [&](int b) {
+        return cached ? s_req[b] : make_int2(last_slot(P, b), __ldg(P.pos + b));
+    };
     if (P.status)
         for (int b = (gridDim.x - 1 - blockIdx.x) * (kThreads / 32) + tid / 32; b < B;
              b += gridDim.x * (kThreads / 32))
-            commit_status(P, b, last_of(b), tid & 31);
+            commit_status(P, b, request(b).x, tid & 31);
     const float rk = __frcp_rn(c.k_scale ? __ldg(c.k_scale) : 1.f);
     const float rv = __frcp_rn(c.v_scale ? __ldg(c.v_scale) : 1.f);
-    const int64_t groups = most < 0 ? 0 : most / slots + 1;
-    const int64_t units = groups * B * pieces;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t gb = u / pieces;
-        const int piece = (int)(u - gb * pieces), b = (int)(gb % B);
-        const int j0 = (int)(gb / B) * slots, last = last_of(b);
-        if (j0 > last) continue;
-        const int n = min(slots, last - j0 + 1);
-        const int lo = piece * kUnit, hi = min(n * 2 * row, lo + kUnit);
-        const int pos = __ldg(P.pos + b);
-        uint32_t w[kItems][16];
-        uint32_t at[kItems];     // the block's place: cache row * per_head + block of the head
-        bool isv[kItems], ok[kItems];
+    const int64_t units = (most < 0 ? 0 : most / slots + 1) * (int64_t)B * pieces;
+    // One block of 16 elements: where it comes from and goes.
+    struct Item {
+        int node, blk, off, e;   // e: block of the K row, or of the V row behind it; -1: nothing
+    };
+    int b = 0;
+    // this thread's items of the next unit at or after u that writes something
+    auto find = [&](int64_t u, Item (&it)[I]) -> int64_t {
+        for (; u < units; u += gridDim.x) {
+            const int64_t gb = u / pieces;
+            b = (int)(gb % B);
+            const int2 req = request(b);
+            const int j0 = (int)(gb / B) * slots;
+            if (j0 > req.x) continue;
+            const int n = min(slots, req.x - j0 + 1);
+            const int lo = (int)(u - gb * pieces) * kCommitUnit, hi = min(n * 2 * row, lo + kCommitUnit);
 #pragma unroll
-        for (int q = 0; q < kItems; ++q) {
-            const int i = lo + tid + q * kThreads;
-            ok[q] = i < hi;
-            isv[q] = false;
-            at[q] = 0;
-            if (!ok[q]) continue;
-            const int sl = i / (2 * row), k = i - sl * 2 * row, j = j0 + sl;
-            isv[q] = k >= row;
-            const int e = isv[q] ? k - row : k, head = e / per_head;
-            const int node =
-                P.kv_commit ? __ldg(P.kv_commit + (int64_t)b * P.N + j) : j;
-            int off = 0;
-            const int blk = fp4_block(c, b, (int64_t)pos + j, &off);
-            ok[q] = node >= 0 && node < P.N && blk >= 0;
-            if (!ok[q]) continue;
-            at[q] = fp4_row(c, blk, off, head);
-            load16<T>(P.src[isv[q]], ((int64_t)b * P.N + node) * P.stride[isv[q]] + e * 16, vec,
-                      w[q]);
+            for (int q = 0; q < I; ++q) {
+                const int i = lo + tid + q * kThreads;
+                it[q].e = -1;
+                it[q].node = it[q].blk = it[q].off = 0;
+                if (i >= hi) continue;
+                const int sl = slots == 1 ? 0 : i / (2 * row), j = j0 + sl;
+                it[q].e = i - sl * 2 * row;
+                it[q].node = P.kv_commit ? __ldg(P.kv_commit + (int64_t)b * P.N + j) : j;
+                it[q].blk = fp4_block(c, b, (int64_t)req.y + j, &it[q].off);
+            }
+            return u;
         }
+        return units;
+    };
+    Item it[I];
+    int64_t u = find(blockIdx.x, it);
+    while (u < units) {
+        uint32_t w[I][16];
+        int64_t place[I];        // of the block in the cache, -1: nothing
+        bool isv[I];
 #pragma unroll
-        for (int q = 0; q < kItems; ++q) {
-            if (!ok[q]) continue;
-            const int i = lo + tid + q * kThreads;
-            const int k = i % (2 * row), e = isv[q] ? k - row : k;
-            const int64_t place = (int64_t)at[q] * per_head + e % per_head;
+        for (int q = 0; q < I; ++q) {
+            isv[q] = it[q].e >= row;
+            const int e = isv[q] ? it[q].e - row : it[q].e, head = e / per_head;
+            place[q] = -1;
+            if (it[q].e < 0 || it[q].node < 0 || it[q].node >= P.N || it[q].blk < 0) continue;
+            place[q] = (int64_t)fp4_row(c, it[q].blk, it[q].off, head) * per_head +
+                       (e - head * per_head);
+            load16<T>(P.src[isv[q]], ((int64_t)b * P.N + it[q].node) * P.stride[isv[q]] + e * 16,
+                      vec, w[q]);
+        }
+        u = find(u + gridDim.x, it);
+#pragma unroll
+        for (int q = 0; q < I; ++q) {
+            if (place[q] < 0) continue;
             float x[16];
             floats16<T>(w[q], x);
             uint2 code;
             const uint32_t sf = quantise16(x, isv[q] ? rv : rk, code);
-            reinterpret_cast<uint2 *>(isv[q] ? c.v : c.k)[place] = code;
-            reinterpret_cast<uint8_t *>(isv[q] ? c.v_sf : c.k_sf)[place] = (uint8_t)sf;
+            reinterpret_cast<uint2 *>(isv[q] ? c.v : c.k)[place[q]] = code;
+            reinterpret_cast<uint8_t *>(isv[q] ? c.v_sf : c.k_sf)[place[q]] = (uint8_t)sf;
         }
     }
 }
@@ -314,11 +332,11 @@ cudaError_t commit_type(const KvFp4Params &p, cudaStream_t st) {
     constexpr int es = T == 0 ? 4 : 2;
     const int a = align_of(p.src[0], p.stride[0] * es), b = align_of(p.src[1], p.stride[1] * es);
     const int row2 = 2 * p.cache.H * (p.cache.D / 16);
-    const int slots = row2 >= kUnit ? 1 : kUnit / row2;
-    const int pieces = (slots * row2 + kUnit - 1) / kUnit;
+    const int slots = row2 >= kCommitUnit ? 1 : kCommitUnit / row2;
+    const int pieces = (slots * row2 + kCommitUnit - 1) / kCommitUnit;
     const int64_t units = ((int64_t)(p.N - 1) / slots + 1) * p.B * pieces;
-    const int64_t cap = (int64_t)p.sms * kCtasPerSm;
-    const size_t smem = p.B <= kSmemRequests ? sizeof(int) * (size_t)p.B : 0;
+    const int64_t cap = (int64_t)p.sms * kCommitCtas;
+    const size_t smem = p.B <= kSmemRequests ? sizeof(int2) * (size_t)p.B : 0;
     commit_kernel<T><<<(unsigned)(units < cap ? units : cap), kThreads, smem, st>>>(
         p, slots, pieces, a < b ? a : b);
     return cudaGetLastError();

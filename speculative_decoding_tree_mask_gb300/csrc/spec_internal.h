@@ -297,7 +297,9 @@ struct TreeAttnParams {
 // Bytes of notes and parts that a launch with R rows of a K/V head may write.
 int64_t tree_attn_workspace(int R, int D, int sms);
 cudaError_t launch_tree_attn(const TreeAttnParams &p, cudaStream_t st);
-// On the tcgen05 tensor cores: rows of an item, and the launch.
+// On the tcgen05 tensor cores: rows of an item, what its tree's tile and rest weigh in context
+// tiles, and the launch.
+int tree_attn_tc_cost();
 int tree_attn_tc_rows(int R);
 cudaError_t launch_tree_attn_tc(const TreeAttnParams &p, int grid, cudaStream_t st);
 

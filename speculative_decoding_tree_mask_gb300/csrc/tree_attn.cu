@@ -906,7 +906,12 @@ cudaError_t launch_tree_attn(const TreeAttnParams &given, cudaStream_t st) {
     if (given.B <= 0) return cudaSuccess;
     TreeAttnParams p = given;
     const int D = p.cache.D;
-    const Plan n = plan(p.N * p.G, D, p.sms);
+    Plan n = plan(p.N * p.G, D, p.sms);
+    // no more CTAs than there can be units of work
+    const int64_t units = (int64_t)p.B * p.cache.H * ((p.N * p.G + n.rows - 1) / n.rows) *
+                          ((p.cache.max_blocks * (int64_t)p.cache.block_size + kTile - 1) / kTile +
+                           (n.tc ? tree_attn_tc_cost() : kTreeCost));
+    if (units < n.grid) n.grid = (int)units;
     p.columns = columns(p, n);
     p.notes = static_cast<int4 *>(p.workspace);
     p.ws = reinterpret_cast<float *>(static_cast<char *>(p.workspace) + notes_bytes(n));

@@ -814,6 +814,7 @@ cudaError_t launch(const TreeAttnParams &p, int grid, cudaStream_t st) {
 
 }  // namespace
 
+int tree_attn_tc_cost() { return kTreeCost; }
 int tree_attn_tc_rows(int R) { return R > 128 ? 256 : 128; }
 
 cudaError_t launch_tree_attn_tc(const TreeAttnParams &p, int grid, cudaStream_t st) {
