@@ -242,8 +242,8 @@ int spec_kv_commit(spec_handle h, const void *src_k, const void *src_v, int src_
  *   k_scale, v_scale   device float32, one value per cache (NULL = 1), positive and between
  *                2^-100 and 2^100;
  *   block_table  int32 [B, max_blocks]: cache block of each block_size tokens of request b.
- * An element's value is code * block scale * tensor scale. D is a multiple of 16, at most 512;
- * a cache has fewer than 2^32 rows (num_blocks * block_size * H).
+ * An element's value is code * block scale * tensor scale. D is a multiple of 16, at most 512, H
+ * at most 65536; a cache has fewer than 2^32 rows (num_blocks * block_size * H).
  * Storing x, with r = RN(1 / tensor scale) and all products rounded to float32:
  *   block scale s = e4m3(max|x| * RN(r * RN(1/6))), nearest even, at most 448;
  *   code = e2m1(x * RN(RN(1/s) * r)), nearest even, at most 6 in magnitude; all codes are 0

@@ -684,7 +684,7 @@ bool null_or_aligned(const void *p, size_t a) { return !p || aligned(p, a); }
 // The parts of a 4-bit cache that the host can check; a batch of none needs no block table.
 int check_cache(const spec_fp4_cache *c, int B) {
     if (!c) return SPEC_ERR_ARG;
-    if (c->H < 1 || c->D < 16 || c->D % 16 != 0 || c->D > 512) return SPEC_ERR_ARG;
+    if (c->H < 1 || c->H > (1 << 16) || c->D < 16 || c->D % 16 != 0 || c->D > 512) return SPEC_ERR_ARG;
     if (c->layout != SPEC_KV_NHD && c->layout != SPEC_KV_HND) return SPEC_ERR_ARG;
     if (c->block_size < 1 || c->num_blocks < 1 || c->max_blocks < 1) return SPEC_ERR_ARG;
     if (c->num_blocks > INT32_MAX || (int64_t)c->block_size * c->H > INT32_MAX ||

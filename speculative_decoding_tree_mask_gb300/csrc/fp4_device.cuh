@@ -66,9 +66,10 @@ __device__ __forceinline__ uint32_t fp4_row(const spec_fp4_cache &c, int blk, in
 }
 
 // The cache block of position p of request b, or -1 when it lies outside the table or cache.
-__device__ __forceinline__ int fp4_block(const spec_fp4_cache &c, int b, int64_t p, int *off) {
+__device__ __forceinline__ int fp4_block(const spec_fp4_cache &c, const FastDiv &by_page, int b,
+                                         int64_t p, int *off) {
     if (p < 0 || p > INT32_MAX) return -1;   // the table holds at most INT32_MAX positions
-    const int bi = (int)((uint32_t)p / (uint32_t)c.block_size);
+    const int bi = (int)by_page((uint32_t)p);
     if (bi >= c.max_blocks) return -1;
     *off = (int)p - bi * c.block_size;
     const int blk = __ldg(c.block_table + (int64_t)b * c.max_blocks + bi);

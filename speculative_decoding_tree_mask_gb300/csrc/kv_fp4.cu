@@ -105,7 +105,7 @@ __device__ __forceinline__ void commit_status(const KvFp4Params &P, int b, int l
         const int node = P.kv_commit ? __ldg(P.kv_commit + (int64_t)b * P.N + j) : j;
         int off;
         bad |= node < 0 || node >= P.N ||
-               fp4_block(P.cache, b, (int64_t)P.pos[b] + j, &off) < 0;
+               fp4_block(P.cache, P.by_page, b, (int64_t)P.pos[b] + j, &off) < 0;
     }
     bad = __any_sync(0xffffffffu, bad);
     if (lane == 0) P.status[b] = bad ? SPEC_REQ_BAD_SLOT : 0;
@@ -159,10 +159,10 @@ __global__ void __launch_bounds__(kThreads, kCommitCtas)
     // this thread's items of the next unit at or after u that writes something
     auto find = [&](int64_t u, Item (&it)[I]) -> int64_t {
         for (; u < units; u += gridDim.x) {
-            const int64_t gb = u / pieces;
-            b = (int)(gb % B);
+            const int64_t gb = pieces == 1 ? u : u / pieces, group = gb / B;
+            b = (int)(gb - group * B);
             const int2 req = request(b);
-            const int j0 = (int)(gb / B) * slots;
+            const int j0 = (int)group * slots;
             if (j0 > req.x) continue;
             const int n = min(slots, req.x - j0 + 1);
             const int lo = (int)(u - gb * pieces) * kCommitUnit, hi = min(n * 2 * row, lo + kCommitUnit);
@@ -172,10 +172,10 @@ __global__ void __launch_bounds__(kThreads, kCommitCtas)
                 it[q].e = -1;
                 it[q].node = it[q].blk = it[q].off = 0;
                 if (i >= hi) continue;
-                const int sl = slots == 1 ? 0 : i / (2 * row), j = j0 + sl;
+                const int sl = slots == 1 ? 0 : (int)(P.by_row(i) >> 1), j = j0 + sl;
                 it[q].e = i - sl * 2 * row;
                 it[q].node = P.kv_commit ? __ldg(P.kv_commit + (int64_t)b * P.N + j) : j;
-                it[q].blk = fp4_block(c, b, (int64_t)req.y + j, &it[q].off);
+                it[q].blk = fp4_block(c, P.by_page, b, (int64_t)req.y + j, &it[q].off);
             }
             return u;
         }
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, kCommitCtas)
 #pragma unroll
         for (int q = 0; q < I; ++q) {
             isv[q] = it[q].e >= row;
-            const int e = isv[q] ? it[q].e - row : it[q].e, head = e / per_head;
+            const int e = isv[q] ? it[q].e - row : it[q].e, head = (int)P.by_head(max(e, 0));
             place[q] = -1;
             if (it[q].e < 0 || it[q].node < 0 || it[q].node >= P.N || it[q].blk < 0) continue;
             place[q] = (int64_t)fp4_row(c, it[q].blk, it[q].off, head) * per_head +
@@ -258,7 +258,8 @@ __device__ __forceinline__ void store16(void *base, int64_t e, int vec, const fl
 
 // Units of kUnit consecutive 16-element blocks of one request's K or V output rows.
 template <int T>
-__global__ void __launch_bounds__(kThreads) load_kernel(KvFp4Params P, int64_t per, int vec) {
+__global__ void __launch_bounds__(kThreads, T == 0 ? 6 : kCtasPerSm)
+    load_kernel(KvFp4Params P, int64_t per, int vec) {
     const spec_fp4_cache &c = P.cache;
     const int tid = threadIdx.x;
     const uint32_t per_head = c.D / 16, row = (uint32_t)c.H * per_head;
@@ -278,17 +279,18 @@ __global__ void __launch_bounds__(kThreads) load_kernel(KvFp4Params P, int64_t p
         bool seen = true;
 #pragma unroll
         for (int q = 0; q < kItems; ++q) {
-            const uint32_t i = tid + q * kThreads, k = rem0 + i, tok = k / row, e = k - tok * row;
+            const uint32_t i = tid + q * kThreads, k = rem0 + i, tok = P.by_row(k);
+            const uint32_t e = k - tok * row;
             code[q] = make_uint2(0, 0);
             sf[q] = 0;
             if (lo + i >= each || tok0 + tok >= count) continue;
             int off = 0;
-            const int blk = fp4_block(c, b, start + tok0 + tok, &off);
+            const int blk = fp4_block(c, P.by_page, b, start + tok0 + tok, &off);
             if (blk < 0) {
                 seen = false;
                 continue;
             }
-            const uint32_t head = e / per_head;
+            const uint32_t head = P.by_head(e);
             const int64_t place =
                 (int64_t)fp4_row(c, blk, off, (int)head) * per_head + (e - head * per_head);
             code[q] = __ldg(codes + place);
@@ -319,6 +321,14 @@ __global__ void __launch_bounds__(kThreads) load_kernel(KvFp4Params P, int64_t p
             store16<T>(P.out[isv], (b * each + i) * 16, vec, x);
         }
     }
+}
+
+KvFp4Params with_divisors(const KvFp4Params &given) {
+    KvFp4Params p = given;
+    p.by_head = FastDiv((uint32_t)p.cache.D / 16);
+    p.by_row = FastDiv((uint32_t)p.cache.H * (p.cache.D / 16));
+    p.by_page = FastDiv((uint32_t)p.cache.block_size);
+    return p;
 }
 
 // Alignment that every block's 16 elements share: 32 or 16 bytes, or 0.
@@ -356,15 +366,17 @@ cudaError_t load_type(const KvFp4Params &p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_kv_commit_fp4(const KvFp4Params &p, cudaStream_t st) {
-    if (p.B <= 0) return cudaSuccess;
+cudaError_t launch_kv_commit_fp4(const KvFp4Params &given, cudaStream_t st) {
+    if (given.B <= 0) return cudaSuccess;
+    const KvFp4Params p = with_divisors(given);
     if (p.dtype == 0) return commit_type<0>(p, st);
     if (p.dtype == 1) return commit_type<1>(p, st);
     return commit_type<2>(p, st);
 }
 
-cudaError_t launch_kv_load_fp4(const KvFp4Params &p, cudaStream_t st) {
-    if (p.B <= 0) return cudaSuccess;
+cudaError_t launch_kv_load_fp4(const KvFp4Params &given, cudaStream_t st) {
+    if (given.B <= 0) return cudaSuccess;
+    const KvFp4Params p = with_divisors(given);
     if (p.status) {
         const cudaError_t e = cudaMemsetAsync(p.status, 0, sizeof(int32_t) * (size_t)p.B, st);
         if (e != cudaSuccess) return e;

@@ -257,6 +257,22 @@ struct QkRopeParams {
 
 cudaError_t launch_qk_rope(const QkRopeParams &p, cudaStream_t st);
 
+// Division of n < 2^31 by a number known on the host: a multiplication and a shift (the round-up
+// method of Granlund and Montgomery, "Division by invariant integers using multiplication").
+struct FastDiv {
+    uint32_t d = 1, mul = 1, shift = 0;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t divisor) : d(divisor) {
+        while (shift < 32 && (uint64_t(1) << shift) < d) ++shift;
+        mul = (uint32_t)((((uint64_t(1) << shift) - d) << 32) / d + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+        return (__umulhi(n, mul) + n) >> shift;
+    }
+#endif
+};
+
 // K/V rows into the 4-bit cache, and back (see spec_kv_commit_fp4, spec_kv_load_fp4).
 struct KvFp4Params {
     spec_fp4_cache cache;
@@ -269,6 +285,7 @@ struct KvFp4Params {
     const int32_t *kv_commit, *last, *pos;   // commit: accept_len; load: count; first positions
     int32_t *status;
     int sms;
+    FastDiv by_head, by_row, by_page;   // 16-element blocks of a head, of a row; block_size
 };
 
 cudaError_t launch_kv_commit_fp4(const KvFp4Params &p, cudaStream_t st);
