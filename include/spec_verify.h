@@ -243,7 +243,8 @@ int spec_kv_commit(spec_handle h, const void *src_k, const void *src_v, int src_
  *                2^-100 and 2^100;
  *   block_table  int32 [B, max_blocks]: cache block of each block_size tokens of request b.
  * An element's value is code * block scale * tensor scale. D is a multiple of 16, at most 512, H
- * at most 65536; a cache has fewer than 2^32 rows (num_blocks * block_size * H).
+ * at most 65536; a cache has fewer than 2^32 rows (num_blocks * block_size * H), a request at
+ * most 2^31 - 1025 positions (max_blocks * block_size).
  * Storing x, with r = RN(1 / tensor scale) and all products rounded to float32:
  *   block scale s = e4m3(max|x| * RN(r * RN(1/6))), nearest even, at most 448;
  *   code = e2m1(x * RN(RN(1/s) * r)), nearest even, at most 6 in magnitude; all codes are 0

@@ -689,7 +689,7 @@ int check_cache(const spec_fp4_cache *c, int B) {
     if (c->block_size < 1 || c->num_blocks < 1 || c->max_blocks < 1) return SPEC_ERR_ARG;
     if (c->num_blocks > INT32_MAX || (int64_t)c->block_size * c->H > INT32_MAX ||
         c->num_blocks > int64_t(UINT32_MAX) / ((int64_t)c->block_size * c->H) ||
-        (int64_t)c->max_blocks * c->block_size > INT32_MAX)
+        (int64_t)c->max_blocks * c->block_size > INT32_MAX - 1024)   // tiles past the end count too
         return SPEC_ERR_ARG;
     if (!c->k || !c->v || !c->k_sf || !c->v_sf || (B > 0 && !c->block_table))
         return SPEC_ERR_ARG;

@@ -18,8 +18,10 @@ constexpr int kThreads = 256;
 constexpr int kSmemRequests = 2048;   // requests whose last slot and position fit in shared memory
 // Commit: blocks of 16 elements a thread handles at a time, CTAs an SM holds.
 constexpr int kCommitItems = 2, kCommitUnit = kThreads * kCommitItems, kCommitCtas = 3;
-// Load: likewise.
-constexpr int kItems = 4, kUnit = kThreads * kItems, kCtasPerSm = 8;
+// Load: blocks a thread handles, 4 when that fills the GPU, else 1 (333 positions of two
+// requests, 4 heads x 64: 2.7 us against 4.3); a CTA has one unit of them (16 x 16384 positions,
+// 8 heads x 128: 195 us; 222 with CTAs that stride over the units, 312 with one block a thread).
+constexpr int kLoadItems = 4, kLoadCtas = 8;
 
 // A thread's 16 elements as floats. vec: 32, 16 (byte alignment of every block) or 0.
 template <int T>
@@ -256,9 +258,9 @@ __device__ __forceinline__ void store16(void *base, int64_t e, int vec, const fl
     }
 }
 
-// Units of kUnit consecutive 16-element blocks of one request's K or V output rows.
-template <int T>
-__global__ void __launch_bounds__(kThreads, T == 0 ? 6 : kCtasPerSm)
+// Units of I x kThreads consecutive 16-element blocks of one request's K or V output rows.
+template <int T, int I>
+__global__ void __launch_bounds__(kThreads, T == 0 ? 6 : kLoadCtas)
     load_kernel(KvFp4Params P, int64_t per, int vec) {
     const spec_fp4_cache &c = P.cache;
     const int tid = threadIdx.x;
@@ -267,18 +269,18 @@ __global__ void __launch_bounds__(kThreads, T == 0 ? 6 : kCtasPerSm)
     const float ks = c.k_scale ? __ldg(c.k_scale) : 1.f;
     const float vs = c.v_scale ? __ldg(c.v_scale) : 1.f;
     for (int64_t u = blockIdx.x; u < 2 * per * P.B; u += gridDim.x) {
-        const int64_t bk = u / per, lo = (u - bk * per) * kUnit;
+        const int64_t bk = u / per, lo = (u - bk * per) * (kThreads * I);
         const int b = (int)(bk >> 1), isv = (int)(bk & 1);
         const int64_t tok0 = lo / row;
         const uint32_t rem0 = (uint32_t)(lo - tok0 * row);
         const int start = __ldg(P.pos + b), count = __ldg(P.last + b);
         const uint2 *codes = reinterpret_cast<const uint2 *>(isv ? c.v : c.k);
         const uint8_t *scales = reinterpret_cast<const uint8_t *>(isv ? c.v_sf : c.k_sf);
-        uint2 code[kItems];
-        uint32_t sf[kItems];
+        uint2 code[I];
+        uint32_t sf[I];
         bool seen = true;
 #pragma unroll
-        for (int q = 0; q < kItems; ++q) {
+        for (int q = 0; q < I; ++q) {
             const uint32_t i = tid + q * kThreads, k = rem0 + i, tok = P.by_row(k);
             const uint32_t e = k - tok * row;
             code[q] = make_uint2(0, 0);
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, T == 0 ? 6 : kCtasPerSm)
         if (P.status && (!seen || count < 0 || count > P.max_len))
             P.status[b] = SPEC_REQ_BAD_SLOT;
 #pragma unroll
-        for (int q = 0; q < kItems; ++q) {
+        for (int q = 0; q < I; ++q) {
             const int64_t i = lo + tid + q * kThreads;
             if (i >= each) continue;
             const uint32_t h = e4m3x2_to_f16x2(sf[q]);
@@ -356,11 +358,16 @@ template <int T>
 cudaError_t load_type(const KvFp4Params &p, cudaStream_t st) {
     const int a = align_of(p.out[0], 0), b = align_of(p.out[1], 0);
     const int64_t each = p.max_len * p.cache.H * (p.cache.D / 16);
+    const bool many = 2 * each * p.B >= (int64_t)p.sms * kLoadCtas * kThreads * kLoadItems;
+    const int unit = kThreads * (many ? kLoadItems : 1);
     // a request has a unit even when it has no rows: its count is checked there
-    const int64_t per = each > 0 ? (each + kUnit - 1) / kUnit : 1;
-    const int64_t units = 2 * per * p.B, cap = (int64_t)p.sms * kCtasPerSm;
-    load_kernel<T><<<(unsigned)(units < cap ? units : cap), kThreads, 0, st>>>(p, per,
-                                                                               a < b ? a : b);
+    const int64_t per = each > 0 ? (each + unit - 1) / unit : 1;
+    const int64_t units = 2 * per * p.B;
+    const unsigned grid = (unsigned)(units < INT32_MAX ? units : INT32_MAX);
+    if (many)
+        load_kernel<T, kLoadItems><<<grid, kThreads, 0, st>>>(p, per, a < b ? a : b);
+    else
+        load_kernel<T, 1><<<grid, kThreads, 0, st>>>(p, per, a < b ? a : b);
     return cudaGetLastError();
 }
 

@@ -45,6 +45,7 @@ __device__ __forceinline__ AttnRange attn_range(const TreeAttnParams &P, int ite
     const int lane = threadIdx.x & 31;
     const int per = (P.B + 31) / 32, b0 = lane * per, b1 = min(P.B, b0 + per);
     int64_t mine = 0;
+#pragma unroll 8
     for (int b = b0; b < b1; ++b) mine += (int64_t)units(b) * items;
     int64_t sum = mine;
 #pragma unroll

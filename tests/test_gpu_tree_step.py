@@ -633,3 +633,63 @@ def test_example_decodes_and_keeps_the_accepted_path():
         # half of the widest step (2 of 6) under a scale within 2^-4 of amax / 6, cut at 6 of it,
         # and the projection's and the rows' own bf16 roundings
         assert np.all(np.abs(x - y) <= amax * (1 / 6 * (1 + 2.0 ** -4) + 2.0 ** -4 + 2.0 ** -5))
+
+
+# ---- schedules and paths of the attention kernels ----------------------------------------------
+
+@pytest.mark.parametrize("H", [1, 3, 7, 16])
+@pytest.mark.parametrize("N,Gq,D", [(2, 2, 64), (20, 3, 128), (64, 3, 64)])
+def test_attention_head_counts(h, H, N, Gq, D):
+    """Heads that divide the CTAs into columns and heads that do not, for both kernels."""
+    rng = np.random.default_rng(1000 * H + N)
+    Case(rng, 2, N, H, Gq, D, "f16", S.NHD, 16, [700, 130]).check(h)
+
+
+@pytest.mark.parametrize("pad", [0, 3, 8])
+@pytest.mark.parametrize("layout,bs", [(S.NHD, 1), (S.NHD, 48), (S.HND, 7), (S.HND, 200)])
+@pytest.mark.parametrize("dt,N", [("bf16", 40), ("f16", 64)])
+def test_attention_many_rows_pages_and_strides(h, layout, bs, pad, dt, N):
+    rng = np.random.default_rng(bs + 1000 * layout + pad + N)
+    Case(rng, 2, N, 2, 3, 128, dt, layout, bs, [211, 150], pad=pad).check(h)
+
+
+@pytest.mark.parametrize("N,Gq,D,dt", [(6, 4, 128, "bf16"), (40, 2, 64, "bf16"),
+                                       (40, 2, 128, "f16"), (64, 4, 128, "bf16"),
+                                       (64, 4, 64, "f16")])
+def test_attention_bits_do_not_change(h, N, Gq, D, dt):
+    """Many runs of one batch whose items are cut in many places: the same bits each time, whole
+    batches of requests without a context among them."""
+    rng = np.random.default_rng(117)
+    ctx = [0, 1, 3000, 0] + [int(x) for x in rng.integers(0, 700, 36)]
+    c = Case(rng, 40, N, 2, Gq, D, dt, S.NHD, 32, ctx)
+    first, first_lse = c.check(h)
+    for _ in range(10):
+        out, lse = c.run(h)
+        assert torch.equal(out, first) and torch.equal(lse, first_lse)
+
+
+@pytest.mark.parametrize("N,Gq,D", [(1, 1, 256), (3, 4, 64), (8, 4, 128)])
+def test_attention_few_items_of_many_parts(h, N, Gq, D):
+    """One request over many CTAs: the parts of an item are joined by several threads a value."""
+    rng = np.random.default_rng(118)
+    Case(rng, 1, N, 2, Gq, D, "bf16", S.HND, 32, [6000], chain=True).check(h)
+
+
+def test_attention_all_rows_finite_with_negative_and_large_scores(h):
+    """Scores that rise along the context, so that the running maximum is followed again and
+    again, and scores that fall, so that it is not."""
+    rng = np.random.default_rng(119)
+    for N, Gq in ((2, 4), (40, 2), (64, 4)):
+        c = Case(rng, 2, N, 1, Gq, 64, "f16", S.HND, 16, [900, 901])
+        # a key direction shared by all queries, growing (request 0) or shrinking (request 1)
+        x = rng.standard_normal(c.codes[0].shape).astype(np.float32) * 0.1
+        for b in range(2):
+            for p in range(int(c.ctx[b])):
+                blk, off = S.place(c.table, x.shape[0], 16, b, p)
+                x[blk, :, off] += (p if b == 0 else 900 - p) * 0.01
+        c.codes[0], c.sf[0] = S.quantise(x, 0.75)
+        c.cache.k.copy_(gpu(S.pack(c.codes[0])))
+        c.cache.k_sf.copy_(gpu(c.sf[0]))
+        c.q.fill_(1.0)
+        c.q64 = c.q.double().cpu().numpy()
+        c.check(h)
