@@ -72,7 +72,8 @@ enum {
     SPEC_REQ_BAD_SLOT = 5,      /* KV commit: a slot maps outside the block table or cache */
     SPEC_REQ_BAD_BUDGET = 6,    /* the request's node budget (spec_set_node_budget) is
                                    outside [1, N] */
-    SPEC_REQ_INTERNAL = 7       /* debug builds only (SPEC_DEBUG): one of the kernels' own
+    SPEC_REQ_INTERNAL = 7       /* spec_tree_attention_fp4: a wait inside the kernel gave up.
+                                   Otherwise debug builds only (SPEC_DEBUG): one of the kernels' own
                                    consistency checks failed for this request -- an index
                                    outside its array (the access was skipped), a split row's
                                    arrival counter outside [0, split), or an accepted path that
@@ -329,8 +330,8 @@ int spec_kv_load_fp4(spec_handle h, const spec_fp4_cache *cache, int B, const in
  *   workspace: device memory of the size that spec_tree_attention_workspace gives for these
  *   sizes, 256-byte aligned; its contents need not be kept or cleared between calls, and calls
  *   that share it are serialised by the caller.
- * A wait between the kernel's warps that does not end within two seconds gives the request
- * SPEC_REQ_INTERNAL, in every build.
+ * Every wait between the kernel's warps ends after two seconds at most; a request whose result
+ * is lost that way gets SPEC_REQ_INTERNAL, in every build (no such case is known).
  * Scores and softmax statistics are float32; probabilities are rounded to 16 bits with the
  * largest of a row scaled near 1, for the product with V, which is exact in 16 bits.
  */
