@@ -12,7 +12,7 @@
 // keeps its lanes' own in registers for all its rows. Heads are shared out over more warps
 // when there are few tokens, so that a small call still fills the GPU. 16384 tokens of 40 heads
 // x 128 in bfloat16 take 58 us, 5.8 TB/s in and out (86% of the measured copy); 256 tokens 4.1 us.
-// Sizes and alignments that 16-byte vectors or the halves' pairs do not fit take a warp per row.
+// Sizes and alignments that 16-byte vectors do not fit take a warp per row.
 //
 // The angle: turns = position * inv_freq / (2 pi). inv_freq / (2 pi) becomes a 64-bit fixed
 // point fraction of a turn (one integer product with floor(2^64 / (2 pi))), the product with the
@@ -141,9 +141,16 @@ __device__ __forceinline__ Share warp_share(const QkRopeParams &P, int shares, i
     return s;
 }
 
-// T: element type; LPR: lanes per head row; PAIRS: the rotation's style.
-template <int T, int LPR, bool PAIRS>
+// How a lane's two vectors rotate: with each other (halves whose length is a multiple of a
+// vector), each within itself (pairs), or with elements of other lanes, through shared memory
+// (other halves: 16384 tokens of 40 heads x 128 with 90 rotated take 86 us, 181 with a warp per
+// row and its two-byte loads).
+enum Mode { M_HALVES = 0, M_PAIRS = 1, M_ACROSS = 2 };
+
+// T: element type; LPR: lanes per head row.
+template <int T, int LPR, int MODE>
 __global__ void __launch_bounds__(kWarps * 32) qk_rope_vec(QkRopeParams P, int shares, int per) {
+    constexpr bool PAIRS = MODE == M_PAIRS, ACROSS = MODE == M_ACROSS;
     constexpr int E = T == 0 ? 4 : 8;    // elements of a vector
     constexpr int G = 32 / LPR;          // rows a warp holds at a time
     extern __shared__ float2 s_cs[];
@@ -153,7 +160,7 @@ __global__ void __launch_bounds__(kWarps * 32) qk_rope_vec(QkRopeParams P, int s
     const Share sh = warp_share(P, shares, per);
     // this lane's vectors, -1 if none
     int va, vb;
-    if (PAIRS) {
+    if (PAIRS || ACROSS) {
         va = 2 * j;
         vb = 2 * j + 1;
     } else if (j < hv) {
@@ -178,16 +185,25 @@ __global__ void __launch_bounds__(kWarps * 32) qk_rope_vec(QkRopeParams P, int s
     fetch(sh.row0 + g);      // in flight while the angles are formed
     for (int i = lane; i < half; i += 32) cs[i] = cos_sin(P.inv_freq, i, sh.pos);
     __syncwarp();
-    // element e of the lane's vectors rotates with (c, s)[e]: pair e of the halves, or pair
-    // e of the E pairs in the two neighbouring vectors
-    float c[E], s[E];
+    // Element e of the lane's vectors rotates with (c, s)[e]: pair e of the halves, or pair
+    // e of the E pairs in the two neighbouring vectors. ACROSS: element e becomes itself times
+    // c plus its partner times s, and s has the sign.
+    constexpr int K = ACROSS ? 2 * E : E;
+    float c[K], s[K];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int i = PAIRS ? j * E + e : (j < hv ? j * E + e : half);
+    for (int e = 0; e < K; ++e) {
+        const int at = j * K + e;
+        const int i = ACROSS ? (at < half ? at : at < P.rot ? at - half : half)
+                             : (PAIRS || j < hv ? at : half);
         const float2 v = i < half ? cs[i] : make_float2(1.f, 0.f);
         c[e] = v.x;
-        s[e] = v.y;
+        s[e] = ACROSS && at < half ? -v.y : v.y;
     }
+    // ACROSS: the rows between norm and rotation. A word is left out after each lane's share, so
+    // that the lanes' equal elements lie in different banks.
+    const int pitch = P.D + P.D / (2 * E) + 1;
+    float *buf = reinterpret_cast<float *>(s_cs + kWarps * half) +
+                 ((threadIdx.x >> 5) * G + g) * pitch;
     const float inv_d = 1.f / (float)P.D;
     for (int r0 = sh.row0; r0 < sh.row1; r0 += G) {
         const int r = r0 + g;
@@ -220,7 +236,28 @@ __global__ void __launch_bounds__(kWarps * 32) qk_rope_vec(QkRopeParams P, int s
                 for (int e = 0; e < E; ++e) y[e] = y[e] * n * u[e];
             }
         }
-        if (PAIRS) {
+        if (ACROSS) {
+            float *mine = buf + j * (2 * E + 1);
+            if (va >= 0) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) mine[e] = x[e];
+            }
+            if (vb >= 0) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) mine[E + e] = y[e];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 2 * E; ++e) {
+                const int at = j * 2 * E + e;
+                if (at >= P.rot) continue;
+                const int to = at < half ? at + half : at - half;
+                const float p = buf[to + to / (2 * E)];
+                float &v = e < E ? x[e % E] : y[e % E];
+                v = v * c[e] + p * s[e];
+            }
+            __syncwarp();
+        } else if (PAIRS) {
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
                 const float p = x[e], q = x[e + 1];
@@ -247,7 +284,7 @@ __global__ void __launch_bounds__(kWarps * 32) qk_rope_vec(QkRopeParams P, int s
     }
 }
 
-// Any head size, split and alignment: a warp per row, its elements in shared memory between
+// Any head size and alignment: a warp per row, its elements in shared memory between
 // the norm and the rotation.
 template <int T>
 __global__ void __launch_bounds__(kWarps * 32) qk_rope_any(QkRopeParams P, int shares, int per) {
@@ -296,18 +333,25 @@ bool vec16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 template <int T, int LPR>
 cudaError_t launch_vec(const QkRopeParams &p, int64_t grid, int shares, int per,
                        cudaStream_t st) {
+    constexpr int E = T == 0 ? 4 : 8;
     const size_t smem = sizeof(float2) * (size_t)(kWarps * (p.rot / 2));
-    if (p.pairs)
-        qk_rope_vec<T, LPR, true><<<(unsigned)grid, kWarps * 32, smem, st>>>(p, shares, per);
-    else
-        qk_rope_vec<T, LPR, false><<<(unsigned)grid, kWarps * 32, smem, st>>>(p, shares, per);
+    if (p.pairs) {
+        qk_rope_vec<T, LPR, M_PAIRS><<<(unsigned)grid, kWarps * 32, smem, st>>>(p, shares, per);
+    } else if (p.rot / 2 % E == 0) {
+        qk_rope_vec<T, LPR, M_HALVES><<<(unsigned)grid, kWarps * 32, smem, st>>>(p, shares, per);
+    } else {
+        const size_t rows = sizeof(float) * (size_t)(kWarps * (32 / LPR) *
+                                                     (p.D + p.D / (2 * E) + 1));
+        qk_rope_vec<T, LPR, M_ACROSS><<<(unsigned)grid, kWarps * 32, smem + rows, st>>>(p, shares,
+                                                                                      per);
+    }
     return cudaGetLastError();
 }
 
 template <int T>
 cudaError_t launch_type(const QkRopeParams &p, cudaStream_t st) {
     constexpr int E = T == 0 ? 4 : 8, es = T == 0 ? 4 : 2;
-    bool vec = p.D % E == 0 && (p.pairs || (p.rot / 2) % E == 0) && p.D / E <= 64;
+    bool vec = p.D % E == 0 && p.D / E <= 64;
     for (int i = 0; i < 2; ++i)
         vec = vec && vec16(p.x[i]) && vec16(p.y[i]) && vec16(p.w[i]) &&
               p.stride[i] * es % 16 == 0 && p.ystride[i] * es % 16 == 0;

@@ -93,6 +93,32 @@ def test_norm_rope(h, dt, D, rot, pairs, norm, pad):
     assert torch.equal(q1, q) and torch.equal(k1, k)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("D,rot,pad", [(128, 90, 0), (64, 2, 8), (512, 250, 0), (256, 254, 16),
+                                       (72, 70, 0), (16, 14, 0), (8, 6, 8)])
+def test_rotation_across_vectors(h, dt, D, rot, pad):
+    """Halves whose length is no multiple of a 16-byte vector, in place, with one head and many."""
+    rng = np.random.default_rng(D + rot)
+    B, N, Hq, Hk = 2, 3, 9, 1
+    q, q64 = rows(rng, B, N, Hq, D, dt, pad, 2.0)
+    k, k64 = rows(rng, B, N, Hk, D, dt, pad)
+    f = (10000.0 ** -(np.arange(rot // 2) / (rot // 2))).astype(np.float32)
+    pos = np.array([7, 500000], np.int32)
+    w = torch.from_numpy(rng.uniform(0.5, 2, D).astype(np.float32)).to(TDT[dt])
+    G.spec_qk_norm_rope(h, q, k, gpu(f), gpu(pos), None, q, k, w.to(DEV), w.to(DEV), 1e-6)
+    torch.cuda.synchronize()
+    where = pos[:, None].astype(np.int64) + np.arange(N)
+    for got, x in ((q, q64), (k, k64)):
+        ref = S.norm_rope(x, w.double().numpy(), 1e-6, f, where, False)
+        plain = np.abs(S.norm_rope(x, w.double().numpy(), 1e-6, f[:0], where, False))
+        size = plain.copy()
+        a = np.arange(rot // 2)
+        size[..., a] = size[..., a + rot // 2] = plain[..., a] + plain[..., a + rot // 2]
+        tol = torch.finfo(TDT[dt]).eps / 2 * np.abs(ref) + 2.0 ** -19 * size
+        tol += 2.0 ** -25 if dt == "f16" else 0.0
+        assert np.all(np.abs(got.double().cpu().numpy() - ref) <= tol)
+
+
 def test_norm_rope_many_tokens_and_special_values(h):
     """A prompt longer than the handle's trees; a NaN stays in its head; a row of zeros is zero."""
     rng = np.random.default_rng(5)
