@@ -126,10 +126,8 @@ __device__ __forceinline__ void take_row(const char *from, bool ok, Row4<D> &r) 
     for (int i = 0; i < D / 64; ++i) {
         const uint32_t sf = *reinterpret_cast<const uint32_t *>(from + D / 2 + i * 4);
         r.sf[i] = ok ? sf : 0u;      // zeros for a position that is not there
-        // the scales are the last to be read: once they are used, the row has been read, and
-        // its place can be filled again
-        asm volatile("mov.b32 %0, %0;" : "+r"(r.sf[i]));
     }
+    __syncwarp();                    // the row has been read: its place can be filled again
 }
 
 // The row's elements, as halves, into row t of an operand.
