@@ -332,8 +332,10 @@ int spec_kv_load_fp4(spec_handle h, const spec_fp4_cache *cache, int B, const in
  *   that share it are serialised by the caller.
  * Every wait between the kernel's warps ends after two seconds at most; a request whose result
  * is lost that way gets SPEC_REQ_INTERNAL, in every build (no such case is known).
- * Scores and softmax statistics are float32; probabilities are rounded to 16 bits with the
- * largest of a row scaled near 1, for the product with V, which is exact in 16 bits.
+ * Scores and softmax statistics are float32; probabilities are rounded to 16 bits for the product
+ * with V, which is exact in 16 bits: with the largest of a row scaled to between 2^7 and 2^15, so
+ * that a key counts down to 2^-31 of it (a bfloat16 tree's own: as two 16-bit terms). The sums
+ * before the division are float32: (ctx_len[b] + N) * max|v| must stay below 2^112.
  */
 int spec_tree_attention_workspace(spec_handle h, int B, int N, int Hq, int H, int D,
                                   int64_t *bytes);

@@ -1,7 +1,7 @@
 // Tree attention over the 4-bit paged cache.
 //
 //   out_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = 2^(x_ij - m_i),  x_ij = log2(e) scale q_i.k_j,
-// over the context positions and the nodes that node i may see; m_i is a running maximum.
+// over the context positions and the nodes that node i may see; m_i follows the row's maximum.
 // The rows of an item are the N nodes times the G query heads that share one K/V head, so K and
 // V are read once for all of them: 0.5625 bytes an element. With few rows DRAM should bound it;
 // what stands in the way is the conversion of the codes, about 2.5 instructions for two
@@ -14,7 +14,8 @@
 // A code times its block scale has at most six significant bits and lies in [2^-10, 2688], so
 // it is exact as a half; the tensor scales are applied to the scores and to the result. Q is
 // brought to halves by a power of two for each row (exact for what is within 2^-32 of the row's
-// largest element) and p is rounded to a half with the row's largest near 1. The products are
+// largest element) and p is rounded to a half with the row's largest at 2^7 or more (kHeadroom:
+// what is 2^-31 of it still counts). The products are
 // m16n8k16 of halves with float32 sums, transposed: S^T = K Q^T and O^T = V^T P^T, so that rows
 // come in groups of eight (with Q as the 16-row operand, one token of up to eight heads paid
 // for 16 rows, and 24 rows for 32).
@@ -27,8 +28,8 @@
 // loads, and the elements [g D/8, (g+1) D/8) of its four positions for V, whose pairs of
 // positions are put together by a byte permute; P^T is S^T through movmatrix. The positions of
 // a group of eight are taken in the order 0 1 3 2 4 5 7 6, which with the swizzle of 16-byte
-// units makes both loads free of bank conflicts. A row's maximum is followed only when a score
-// passes it by 2^8, so that the lanes need not agree on it for every tile.
+// units makes both loads free of bank conflicts. A row's maximum is followed only once it has
+// risen by 2^8, so that the lanes need not agree on it for every tile.
 
 #include "tree_attn.cuh"
 
@@ -38,7 +39,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTreeCost = 4;      // the tree's tile and an item's rest, in context tiles
-constexpr float kRescale = 8.f;   // a maximum is followed once it is passed by 2^8
 
 // CTAs an SM holds, by the registers of the output (D x 8 RG floats a warp) and the ring. One
 // more each spills: 24 rows of D = 128 took 378 us with three CTAs, 205 with two.
@@ -148,7 +148,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
 template <int D, int RG>
 struct Acc {
     float o[RG][D / 16][4];
-    float m[RG][2], l[RG][2];   // m: the same in all lanes of a row; l: this lane's share
+    float m[RG][2], l[RG][2];   // m: the reference, the same in all lanes of a row; l: this lane's
 
     __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -161,23 +161,24 @@ struct Acc {
             l[i][0] = l[i][1] = 0.f;
         }
     }
-    // Takes this lane's largest scores in: when one in the warp has passed its row's maximum
+    // Takes this lane's largest scores in: when one in the warp has passed its row's reference
     // far enough, all rows follow theirs.
     __device__ __forceinline__ void raise(float (&x)[RG][2]) {
         bool up = false;
 #pragma unroll
         for (int i = 0; i < RG; ++i)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) up |= x[i][e] > m[i][e] + kRescale;
+            for (int e = 0; e < 2; ++e) up |= x[i][e] - m[i][e] > kRescale;
         if (!__any_sync(0xffffffffu, up)) return;
 #pragma unroll
         for (int i = 0; i < RG; ++i) {
             float a[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float to = fmaxf(m[i][e], x[i][e]);
+                float to = x[i][e];
 #pragma unroll
                 for (int s = 4; s < 32; s <<= 1) to = fmaxf(to, __shfl_xor_sync(~0u, to, s));
+                to = attn_reference(m[i][e], to);
                 a[e] = ex2(m[i][e] - to);
                 m[i][e] = to;
                 l[i][e] *= a[e];

@@ -182,7 +182,21 @@ __device__ __forceinline__ int64_t attn_row(const TreeAttnParams &P, int b, int 
     return ((int64_t)b * P.N + n) * P.Hq + head * P.G + g;
 }
 
-constexpr float kNoMax = -1e30f;            // running maximum before the first key
+constexpr float kNoMax = -1e30f;            // a row's reference before the first key
+
+// A row's probabilities are 2^(x - m) with a reference m that is raised to its largest score less
+// kHeadroom, and raised again only when a score passes m by kRescale. So the largest score met
+// when m was raised stands at 2^7 and none above 2^15, which a half holds; a half's last step is
+// 2^-24, so keys down to 2^-31 of that one keep their weight in the product with V. (With m at the
+// largest score they ended at 2^-24: the result lost what many such keys weigh together, while
+// the row's sum had it.) The factor cancels in the result and in m + log2(sum).
+constexpr float kHeadroom = 7.f, kRescale = 15.f;
+
+// The reference for a largest score x that passed m. Rounded up: m steps by more than the
+// headroom where scores are beyond 2^27, and no probability may pass 2^15.
+__device__ __forceinline__ float attn_reference(float m, float x) {
+    return fmaxf(m, __fadd_ru(x, -kHeadroom));
+}
 constexpr float kLn2 = 0.6931471805599453f;
 
 // log sum exp from a maximum in powers of two and a sum.

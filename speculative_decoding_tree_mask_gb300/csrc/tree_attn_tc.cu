@@ -17,7 +17,8 @@
 //            from. One thread for both groups could not issue as fast as the products end;
 //   softmax  (2 groups of 4 warps) S to P, a row a thread, no exchange between threads, the
 //            running maximum and sum in registers. A maximum is followed only once it rises by
-//            2^8 (then O is rescaled in place), which is rare.
+//            2^8 (then O is rescaled in place), which is rare; P has the row's largest at 2^7 or
+//            more, so that a half keeps what is 2^-31 of it (kHeadroom).
 //
 // A softmax group takes 64 positions at a time, out of two S in turn: while it works on one, the
 // tensor core finishes the products with the P before and makes the next scores (with one S of
@@ -41,7 +42,6 @@
 namespace specv {
 namespace {
 
-constexpr float kRescale = 8.f;
 constexpr int kConvert = 256;     // converting threads: K's, then V's
 constexpr int kSoftmax = 256;     // threads of the two softmax groups
 constexpr int kThreads = kSoftmax + kConvert + 128;   // the last warpgroup: two warps multiply
@@ -623,19 +623,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int head = A.item / row_tiles, row0 = (A.item - head * row_tiles) * RT;
             const int rows = min(RT, R - row0);
             const bool live = r < rows;
-            float top = kNoMax, sum = 0.f, down = 1.f;   // down: 1 / Q's power of two
+            // top: the row's reference; down: 1 / Q's power of two
+            float top = kNoMax, sum = 0.f, down = 1.f;
             const unsigned long long mask =
                 live ? __ldg(P.mask + (int64_t)b * P.N + (row0 + r) / P.G) &
                            (P.N < 64 ? (1ull << P.N) - 1ull : ~0ull)
                      : 0ull;
             int mine = 0;             // jobs of this group in this part, so far
-            // follows the maximum x; `scale` O where it stands
+            // follows the largest score x; rescales O where it stands
             auto follow = [&](float x, bool units) {
-                const bool raise = __any_sync(0xffffffffu, x > top + kRescale);
+                const bool raise = __any_sync(0xffffffffu, x - top > kRescale);
                 if (!raise && !units) return;
                 float a = 1.f;
                 if (raise) {
-                    const float to = fmaxf(top, x);
+                    const float to = attn_reference(top, x);
                     a = ex2(top - to);
                     top = to;
                     sum *= a;
