@@ -69,7 +69,7 @@ struct Smem {
     static constexpr int kQ = kFirst > kJoin ? kFirst : kJoin;
     static constexpr int kQt = kQ + kRows * D * 2;                         // Q in its own type
     static constexpr int kFac = kQt + (T == 1 ? kRows * D * 2 : 0);
-    static constexpr int kM = kFac + kRows * 4;
+    static constexpr int kM = kFac + 2 * kRows * 4;   // factors of the context's, the tree's scores
     static constexpr int kL = kM + kWarps * kRows * 4;
     static constexpr int kOdd = kL + kWarps * kRows * 4;
     static constexpr int kBytes = kOdd + 16;
@@ -210,9 +210,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, RG))
     unsigned long long *s_odd = reinterpret_cast<unsigned long long *>(smem + S::kOdd);
     char *ring = smem + warp * kStages * Rg::kBytes;
     const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
-    const float k_scale = C.k_scale ? __ldg(C.k_scale) : 1.f;
     const float v_scale = C.v_scale ? __ldg(C.v_scale) : 1.f;
     const float unit = P.scale * kLog2e;
+    const float cache_unit = unit * (C.k_scale ? __ldg(C.k_scale) : 1.f);
 
     AttnWalk walk(P, C.H * row_tiles, kTreeCost, P.columns);
     AttnPart A;
@@ -310,7 +310,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, RG))
                     *reinterpret_cast<uint32_t *>(qt + off) =
                         (uint32_t)raw[e] | (uint32_t)raw[e + 1] << 16;
             }
-            if (lane == 0) s_fac[r] = unit * __uint_as_float((ex - 14u) << 23);
+            if (lane == 0) {
+                const float down = __uint_as_float((ex - 14u) << 23);
+                s_fac[r] = attn_factor(cache_unit * down);
+                s_fac[RT + r] = attn_factor(T == 1 ? unit : unit * down);   // bf16: Q as it is
+            }
         }
         __syncthreads();
 
@@ -403,13 +407,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, RG))
             float top[RG][2];
 #pragma unroll
             for (int r = 0; r < RG; ++r) {
-                const float f[2] = {fac[r][0] * k_scale, fac[r][1] * k_scale};
                 top[r][0] = top[r][1] = kNoMax;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float x = s[h][r][e] * f[e & 1];
+                        float x = s[h][r][e] * fac[r][e & 1];
                         if (seen != 0xffffffffu &&
                             !((seen >> (16 * h + 8 * (e >> 1) + pg)) & 1))
                             x = -INFINITY;
@@ -579,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, RG))
                 for (int r = 0; r < RG; ++r)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float f = T == 1 ? unit : fac[r][e & 1];
+                        const float f = s_fac[RT + r * 8 + 2 * c + (e & 1)];
                         const bool on = (bits[r][e & 1] >> (g + 8 * (e >> 1))) & 1;
                         s[r][e] = on ? s[r][e] * f : -INFINITY;
                         top[r][e & 1] = fmaxf(top[r][e & 1], s[r][e]);

@@ -199,6 +199,13 @@ __device__ __forceinline__ float attn_reference(float m, float x) {
 }
 constexpr float kLn2 = 0.6931471805599453f;
 
+// The factor of a row's scores, kept a positive float32 number (2^-149 at least): 0, which the
+// smallest factors of a row of zeros come to, would make NaN of the -inf of a masked score, and
+// infinity would of a score of zero.
+__device__ __forceinline__ float attn_factor(float f) {
+    return fminf(fmaxf(f, 1.4e-45f), 3.40282347e38f);
+}
+
 // log sum exp from a maximum in powers of two and a sum.
 __device__ __forceinline__ float attn_lse(float m, float l) {
     return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;

@@ -666,21 +666,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 if (mine == 0) down = W.q_down[parts & 1][r];
                 unsigned see[2];
+                const float f = attn_factor((i == tree ? unit : cache_unit) * down);
                 if (i == tree) {
                     see[0] = (unsigned)mask;
                     see[1] = (unsigned)(mask >> 32);
                     RowTile<T, true> tile;
-                    const float x = fmaxf(kNoMax, tile.load(s_tm, see, W.k_down[parts & 1]) * (unit * down));
+                    const float x = fmaxf(kNoMax, tile.load(s_tm, see, W.k_down[parts & 1]) * f);
                     follow(x, true);      // O leaves the cache's units
-                    sum += tile.store(s_tm, unit * down, top);
+                    sum += tile.store(s_tm, f, top);
                 } else {
                     see[0] = W.seen[(done + i) & 3][half * 2];
                     see[1] = W.seen[(done + i) & 3][half * 2 + 1];
                     RowTile<T, false> tile;
-                    const float x =
-                        fmaxf(kNoMax, tile.load(s_tm, see, nullptr) * (cache_unit * down));
+                    const float x = fmaxf(kNoMax, tile.load(s_tm, see, nullptr) * f);
                     follow(x, false);
-                    sum += tile.store(s_tm, cache_unit * down, top);
+                    sum += tile.store(s_tm, f, top);
                 }
                 tmem_wait_st();
                 tc_fence_before();

@@ -81,3 +81,44 @@ def test_many_keys_far_below_the_largest(h, dt, N, Gq, D, octaves, every):
     assert np.all(np.abs(got - ref[:, None]) <= tol[:, None]), np.abs(got / ref[:, None] - 1).max()
     want = octaves * np.log(2) + np.log(top + rest)
     assert np.all(np.abs(gl - want[:, None]) <= 2.0 ** -20 * 32)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("N,Gq,D", SHAPES)
+@pytest.mark.parametrize("log_ks,log_q,scale", [(-100, 0, None), (-30, 0, None), (100, -100, None),
+                                                (0, 0, 1e-30), (0, 0, 1e-44)])
+def test_scale_factors_at_the_ends_of_float32(h, dt, N, Gq, D, log_ks, log_q, scale):
+    """Rows of zeros among others, under tensor scales and a `scale` that bring the factor of the
+    scores out of float32's range: the scores are numbers, so the results are."""
+    if dt == "f16" and log_q < 0:
+        log_q = -14                    # its range; the scores are then large, but numbers
+        log_ks = 14
+    rng = np.random.default_rng(N + D)
+    c = T.Case(rng, 2, N, 1, Gq, D, dt, S.NHD, 16, [300, 1])
+    c.scales = (2.0 ** log_ks, c.scales[1])
+    c.cache.k_scale.fill_(2.0 ** log_ks)
+    c.q.mul_(2.0 ** log_q)
+    c.q[:, ::3] = 0
+    if log_ks == 100:
+        c.tk.mul_(2.0 ** 100)
+        c.tk64 = c.tk.double().cpu().numpy()
+    c.q64 = c.q.double().cpu().numpy()
+    if scale is not None:
+        c.scale = scale
+    c.check(h)
+
+
+@pytest.mark.parametrize("N,Gq,D", SHAPES)
+def test_large_queries_and_keys_of_zeros(h, N, Gq, D):
+    """Rows of 2^100 under a K scale of 2^100 over keys of zeros: all scores are zero."""
+    rng = np.random.default_rng(N + D)
+    c = T.Case(rng, 2, N, 1, Gq, D, "bf16", S.HND, 16, [300, 1])
+    c.codes[0][:] = 0
+    c.cache.k.zero_()
+    c.scales = (2.0 ** 100, c.scales[1])
+    c.cache.k_scale.fill_(2.0 ** 100)
+    c.q.mul_(2.0 ** 100)
+    c.tk.zero_()
+    c.q64, c.tk64 = c.q.double().cpu().numpy(), c.tk.double().cpu().numpy()
+    # the oracle's bound counts |q k|: zero
+    c.check(h)
