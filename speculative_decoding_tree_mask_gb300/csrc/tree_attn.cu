@@ -168,7 +168,7 @@ struct Acc {
 #pragma unroll
         for (int i = 0; i < RG; ++i)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) up |= x[i][e] - m[i][e] > kRescale;
+            for (int e = 0; e < 2; ++e) up |= x[i][e] > attn_limit(m[i][e]);
         if (!__any_sync(0xffffffffu, up)) return;
 #pragma unroll
         for (int i = 0; i < RG; ++i) {
@@ -412,7 +412,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, RG))
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float x = s[h][r][e] * fac[r][e & 1];
+                        // rounded here, not with the difference from m: p may not pass 2^15
+                        float x = __fmul_rn(s[h][r][e], fac[r][e & 1]);
                         if (seen != 0xffffffffu &&
                             !((seen >> (16 * h + 8 * (e >> 1) + pg)) & 1))
                             x = -INFINITY;
@@ -584,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, RG))
                     for (int e = 0; e < 4; ++e) {
                         const float f = s_fac[RT + r * 8 + 2 * c + (e & 1)];
                         const bool on = (bits[r][e & 1] >> (g + 8 * (e >> 1))) & 1;
-                        s[r][e] = on ? s[r][e] * f : -INFINITY;
+                        s[r][e] = on ? __fmul_rn(s[r][e], f) : -INFINITY;
                         top[r][e & 1] = fmaxf(top[r][e & 1], s[r][e]);
                     }
                 acc.raise(top);

@@ -192,6 +192,10 @@ constexpr float kNoMax = -1e30f;            // a row's reference before the firs
 // the row's sum had it.) The factor cancels in the result and in m + log2(sum).
 constexpr float kHeadroom = 7.f, kRescale = 15.f;
 
+// What a score has to pass for its row's reference m to be raised. Rounded down, for the same reason
+// as the reference is rounded up.
+__device__ __forceinline__ float attn_limit(float m) { return __fadd_rd(m, kRescale); }
+
 // The reference for a largest score x that passed m. Rounded up: m steps by more than the
 // headroom where scores are beyond 2^27, and no probability may pass 2^15.
 __device__ __forceinline__ float attn_reference(float m, float x) {

@@ -210,6 +210,11 @@ __device__ __forceinline__ float scale_up(float big, float &down) {
     return __uint_as_float((268u - e) << 23);
 }
 
+// The reference of a row comes from a rounded product f s, within 2^-24 of it, which f s - top in
+// one rounding brings to light: as 2^-4 at most up to scores of 2^20, beyond as more than a half
+// holds. There the products are rounded alike first (RowTile::apart).
+constexpr float kApart = 1048576.f;
+
 constexpr int kHalf = 64 * 128;   // bytes from the first 64 rows of an operand to the others
 
 // Jobs of softmax group m in a part of n tiles, the tree's at `tree` (at or past n: not in it).
@@ -266,6 +271,15 @@ struct RowTile {
                 big[e / 2 & 3] = fmaxf(fmaxf(big[e / 2 & 3], __uint_as_float(s[q][e])),
                                        __uint_as_float(s[q][e + 1]));
         return fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
+    }
+    // The scores times f, which becomes 1.
+    __device__ __forceinline__ void apart(float &f) {
+#pragma unroll
+        for (int q = 0; q < kChunks; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                s[q][e] = __float_as_uint(__fmul_rn(__uint_as_float(s[q][e]), f));
+        f = 1.f;
     }
     // P = 2^(f s - top) over the scores in tensor memory; returns the row's sum.
     __device__ __forceinline__ float store(uint32_t s_tm, float f, float top) {
@@ -623,16 +637,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int head = A.item / row_tiles, row0 = (A.item - head * row_tiles) * RT;
             const int rows = min(RT, R - row0);
             const bool live = r < rows;
-            // top: the row's reference; down: 1 / Q's power of two
-            float top = kNoMax, sum = 0.f, down = 1.f;
+            // top: the row's reference; limit: what raises it, or calls for apart(); down: 1 / Q's power of two
+            float top = kNoMax, limit = -INFINITY, sum = 0.f, down = 1.f;
             const unsigned long long mask =
                 live ? __ldg(P.mask + (int64_t)b * P.N + (row0 + r) / P.G) &
                            (P.N < 64 ? (1ull << P.N) - 1ull : ~0ull)
                      : 0ull;
             int mine = 0;             // jobs of this group in this part, so far
-            // follows the largest score x; rescales O where it stands
-            auto follow = [&](float x, bool units) {
-                const bool raise = __any_sync(0xffffffffu, x - top > kRescale);
+            // follows the largest score x of a tile; rescales O where it stands
+            auto follow = [&](float x, bool units, auto &tile, float &f) {
+                const bool raise = __any_sync(0xffffffffu, x > limit);
                 if (!raise && !units) return;
                 float a = 1.f;
                 if (raise) {
@@ -640,6 +654,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     a = ex2(top - to);
                     top = to;
                     sum *= a;
+                    limit = attn_limit(top);
+                    if (fabsf(top) > kApart) {
+                        limit = -INFINITY;      // and so for each tile to come
+                        tile.apart(f);
+                    }
                 }
                 if (units) a *= v_scale;
                 if (mine == 0) return;
@@ -666,20 +685,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 if (mine == 0) down = W.q_down[parts & 1][r];
                 unsigned see[2];
-                const float f = attn_factor((i == tree ? unit : cache_unit) * down);
+                float f = attn_factor((i == tree ? unit : cache_unit) * down);
                 if (i == tree) {
                     see[0] = (unsigned)mask;
                     see[1] = (unsigned)(mask >> 32);
                     RowTile<T, true> tile;
                     const float x = fmaxf(kNoMax, tile.load(s_tm, see, W.k_down[parts & 1]) * f);
-                    follow(x, true);      // O leaves the cache's units
+                    follow(x, true, tile, f);      // O leaves the cache's units
                     sum += tile.store(s_tm, f, top);
                 } else {
                     see[0] = W.seen[(done + i) & 3][half * 2];
                     see[1] = W.seen[(done + i) & 3][half * 2 + 1];
                     RowTile<T, false> tile;
                     const float x = fmaxf(kNoMax, tile.load(s_tm, see, nullptr) * f);
-                    follow(x, false);
+                    follow(x, false, tile, f);
                     sum += tile.store(s_tm, f, top);
                 }
                 tmem_wait_st();

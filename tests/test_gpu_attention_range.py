@@ -122,3 +122,27 @@ def test_large_queries_and_keys_of_zeros(h, N, Gq, D):
     c.q64, c.tk64 = c.q.double().cpu().numpy(), c.tk.double().cpu().numpy()
     # the oracle's bound counts |q k|: zero
     c.check(h)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("N,Gq,D", SHAPES)
+@pytest.mark.parametrize("log_q", [14, 15])
+@pytest.mark.parametrize("scale", [0.1, 1e5, 3e9, 7e12, 1.3e20, 1e25, 1e33])
+def test_scores_of_any_size(h, dt, N, Gq, D, log_q, scale):
+    """Scores so large that float32 steps between them pass 2^5: the keys of the largest share the
+    weight evenly. They are equal as products, so they are equal as probabilities: half a step
+    of the result's type, the 2^-11 of the probabilities and the sums."""
+    rng = np.random.default_rng(N + D)
+    ctx = 700
+    code = rng.integers(0, 7, ctx)
+    best = rng.permutation(ctx)[:5]
+    code[best] = 7
+    c = Flat(rng, N, Gq, D, dt, ctx, code)
+    c.q[..., 0] = 2.0 ** log_q
+    c.tk[..., 0] = -1.0
+    got, gl = c.run(h, scale)
+    ref = c.v[best].mean(0)
+    tol = (torch.finfo(T.TDT[dt]).eps / 2 * (1 + 2.0 ** -7) + 2.0 ** -11 + 2.0 ** -18) * ref
+    assert np.all(np.abs(got - ref) <= tol)
+    want = 6 * 2.0 ** log_q * float(np.float32(scale)) + np.log(5)
+    assert np.all(np.abs(gl - want) <= 2.0 ** -21 * want)
