@@ -182,7 +182,9 @@ __device__ __forceinline__ int64_t attn_row(const TreeAttnParams &P, int b, int 
     return ((int64_t)b * P.N + n) * P.Hq + head * P.G + g;
 }
 
-constexpr float kNoMax = -1e30f;            // a row's reference before the first key
+// A row's reference before the first key: the lowest number, so that any score passes it. (Not
+// -inf: its difference from a masked score would be NaN.)
+constexpr float kNoMax = -3.40282347e38f;
 
 // A row's probabilities are 2^(x - m) with a reference m that is raised to its largest score less
 // kHeadroom, and raised again only when a score passes m by kRescale. So the largest score met

@@ -146,3 +146,23 @@ def test_scores_of_any_size(h, dt, N, Gq, D, log_q, scale):
     assert np.all(np.abs(got - ref) <= tol)
     want = 6 * 2.0 ** log_q * float(np.float32(scale)) + np.log(5)
     assert np.all(np.abs(gl - want) <= 2.0 ** -21 * want)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("N,Gq,D", SHAPES)
+@pytest.mark.parametrize("scale", [0.1, 1e20, 1e28, 1e33])
+def test_large_negative_scores(h, dt, N, Gq, D, scale):
+    """Every key's score is the same negative number, however large: the weights are even."""
+    rng = np.random.default_rng(N + D)
+    ctx = 300
+    c = Flat(rng, N, Gq, D, dt, ctx, np.full(ctx, 15))
+    c.q[..., 0] = 64.0
+    c.tk[..., 0] = -6.0
+    got, gl = c.run(h, scale)
+    tv = c.tv[0, :, 0].double().cpu().numpy()
+    keys = (ctx + 1 + np.arange(N))[:, None]
+    ref = (c.v.sum(0) + np.cumsum(tv, 0)) / keys
+    tol = (torch.finfo(T.TDT[dt]).eps / 2 * (1 + 2.0 ** -7) + 2.0 ** -11 + 2.0 ** -18) * ref
+    assert np.all(np.abs(got - ref[:, None]) <= tol[:, None])
+    want = -384 * float(np.float32(scale)) + np.log(keys)
+    assert np.all(np.abs(gl - want) <= 2.0 ** -21 * np.abs(want))
