@@ -641,17 +641,37 @@ def spec_profile_end(h: Handle):
 
 # ---- convenience: allocate outputs -----------------------------------------------------------
 
-def alloc_outputs(B: int, N: int, device) -> dict:
-    opts = dict(dtype=torch.int32, device=device)
-    return dict(accept_len=torch.empty(B, **opts), out_tokens=torch.empty((B, N), **opts),
-                kv_commit=torch.empty((B, N), **opts), bonus=torch.empty(B, **opts),
-                status=torch.empty(B, **opts))
+def _new(device, stream, *specs, returned=True):
+    """Tensors (shape, dtype) for a call on ``stream``, from that stream's memory: torch hands out
+    freed memory again at once on the stream it belongs to, whose earlier work on it may not have
+    run yet when another stream starts. `returned`: the caller gets them and may use and free
+    them on the current stream, which is noted too."""
+    if stream is None:
+        return [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
+    if not isinstance(stream, torch.cuda.Stream):      # anything that has a cudaStream_t
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        new = [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
+    if returned:
+        for t in new:
+            t.record_stream(here)
+    return new
+
+
+def alloc_outputs(B: int, N: int, device, stream=None) -> dict:
+    """The outputs of a verify call on ``stream`` (None: the current one)."""
+    one, all_nodes = ((B,), torch.int32), ((B, N), torch.int32)
+    accept_len, out_tokens, kv_commit, bonus, status = _new(device, stream, one, all_nodes,
+                                                            all_nodes, one, one)
+    return dict(accept_len=accept_len, out_tokens=out_tokens, kv_commit=kv_commit, bonus=bonus,
+                status=status)
 
 
 def verify_greedy(h: Handle, logits, draft_token, parent, out: dict | None = None,
                   stream=None) -> dict:
     B, N, _ = logits.shape
-    out = out or alloc_outputs(B, N, logits.device)
+    out = out or alloc_outputs(B, N, logits.device, stream)
     spec_verify_greedy(h, logits, draft_token, parent, out["accept_len"], out["out_tokens"],
                        out["kv_commit"], out["bonus"], out["status"], stream)
     return out
@@ -660,7 +680,7 @@ def verify_greedy(h: Handle, logits, draft_token, parent, out: dict | None = Non
 def verify_sample(h: Handle, logits, draft_token, parent, temperature, uniforms, draft=None,
                   draft_kind=SPEC_DRAFT_POINT, out: dict | None = None, stream=None) -> dict:
     B, N, _ = logits.shape
-    out = out or alloc_outputs(B, N, logits.device)
+    out = out or alloc_outputs(B, N, logits.device, stream)
     spec_verify_sample(h, logits, draft_token, parent, temperature, uniforms, out["accept_len"],
                        out["out_tokens"], out["kv_commit"], out["bonus"], out["status"], draft,
                        draft_kind, stream)
@@ -670,7 +690,7 @@ def verify_sample(h: Handle, logits, draft_token, parent, temperature, uniforms,
 def verify_greedy_lazy(h: Handle, logits, draft_token, parent, out: dict | None = None,
                        stream=None) -> dict:
     B, N, _ = logits.shape
-    out = out or alloc_outputs(B, N, draft_token.device)
+    out = out or alloc_outputs(B, N, draft_token.device, stream)
     spec_verify_greedy_lazy(h, logits, draft_token, parent, out["accept_len"], out["out_tokens"],
                             out["kv_commit"], out["bonus"], out["status"], stream)
     return out
@@ -679,7 +699,7 @@ def verify_greedy_lazy(h: Handle, logits, draft_token, parent, out: dict | None 
 def verify_sample_lazy(h: Handle, logits, draft_token, parent, temperature, uniforms, draft=None,
                        draft_kind=SPEC_DRAFT_POINT, out: dict | None = None, stream=None) -> dict:
     B, N, _ = logits.shape
-    out = out or alloc_outputs(B, N, draft_token.device)
+    out = out or alloc_outputs(B, N, draft_token.device, stream)
     spec_verify_sample_lazy(h, logits, draft_token, parent, temperature, uniforms,
                             out["accept_len"], out["out_tokens"], out["kv_commit"], out["bonus"],
                             out["status"], draft, draft_kind, stream)
@@ -688,22 +708,17 @@ def verify_sample_lazy(h: Handle, logits, draft_token, parent, temperature, unif
 
 def build_tree_mask(h: Handle, parent, stream=None) -> dict:
     B, N = parent.shape
-    dev = parent.device
-    out = dict(anc_mask=torch.empty((B, N), dtype=torch.int64, device=dev),
-               depth=torch.empty((B, N), dtype=torch.int32, device=dev),
-               status=torch.empty(B, dtype=torch.int32, device=dev))
+    anc_mask, depth, status = _new(parent.device, stream, ((B, N), torch.int64),
+                                   ((B, N), torch.int32), ((B,), torch.int32))
+    out = dict(anc_mask=anc_mask, depth=depth, status=status)
     spec_build_tree_mask(h, parent, out["anc_mask"], out["depth"], out["status"], stream)
     return out
-
-
-def _empty(shape, dtype, h: Handle):
-    return torch.empty(shape, dtype=dtype, device=h.torch_device)
 
 
 def qk_norm_rope(h: Handle, q, k, inv_freq, seq_pos, depth=None, q_weight=None, k_weight=None,
                  eps: float = 1e-6, style: int = SPEC_ROPE_HALVES, stream=None):
     """-> new contiguous (q, k), normalised and rotated (see spec_qk_norm_rope)."""
-    qo, ko = _empty(q.shape, q.dtype, h), _empty(k.shape, k.dtype, h)
+    qo, ko = _new(h.torch_device, stream, (q.shape, q.dtype), (k.shape, k.dtype))
     spec_qk_norm_rope(h, q, k, inv_freq, seq_pos, depth, qo, ko, q_weight, k_weight, eps, style,
                       stream)
     return qo, ko
@@ -713,7 +728,7 @@ def kv_load_fp4(h: Handle, cache: Fp4Cache, block_table, start, count, max_len: 
                 dtype=torch.bfloat16, stream=None):
     """-> (k, v) rows [B, max_len, H, D] of ``dtype`` (see spec_kv_load_fp4)."""
     shape = (block_table.shape[0], int(max_len), cache.H, cache.D)
-    k, v = _empty(shape, dtype, h), _empty(shape, dtype, h)
+    k, v = _new(h.torch_device, stream, (shape, dtype), (shape, dtype))
     spec_kv_load_fp4(h, cache, block_table, start, count, k, v, stream=stream)
     return k, v
 
@@ -728,11 +743,9 @@ def tree_attention_fp4(h: Handle, q, k, v, cache: Fp4Cache, block_table, ctx_len
         if h.attention_sizes != sizes:      # the size depends on these alone
             h.attention_bytes = spec_tree_attention_workspace(h, *sizes)
             h.attention_sizes = sizes
-        workspace = _empty((h.attention_bytes,), torch.uint8, h)
-        if stream is not None:
-            workspace.record_stream(stream)
-    out = _empty(q.shape, q.dtype, h)
-    lse = _empty(q.shape[:3], torch.float32, h)
+        workspace, = _new(h.torch_device, stream, ((h.attention_bytes,), torch.uint8),
+                          returned=False)
+    out, lse = _new(h.torch_device, stream, (q.shape, q.dtype), (q.shape[:3], torch.float32))
     spec_tree_attention_fp4(h, q, k, v, cache, block_table, ctx_len, anc_mask, scale, out,
                             workspace, lse, stream=stream)
     return out, lse
@@ -782,7 +795,7 @@ def spec_debug_inject_arrival(h: Handle, row: int, value: int):
 
 def spec_debug_words(h: Handle, B: int, stream=None) -> torch.Tensor:
     """Debug builds: the violation bits (DBG_*) of requests 0..B-1 in the handle's last call."""
-    words = torch.empty(B, dtype=torch.int32, device=_hdev(h))
+    words, = _new(h.torch_device, stream, ((B,), torch.int32))
     _check(load().spec_debug_words(h.ptr, _ptr(words), int(B), _stream(stream, words.device)),
            "spec_debug_words")
     return words
