@@ -99,15 +99,19 @@ def decode(steps=8, batch=4, nodes=24, vocab=2048, Hq=8, Hkv=2, D=64, block_size
     with G.Handle(batch, nodes, vocab, torch.device(device).index or 0) as h:
         size = G.spec_tree_attention_workspace(h, batch, nodes, Hq, Hkv, D)
         workspace = torch.empty(size, dtype=torch.uint8, device=device)
+        attended, kept = (torch.empty(batch, dtype=torch.int32, device=device) for _ in range(2))
         for _ in range(steps):
             parent, token = draft(model, root, nodes, 3, rng)
             tree = G.build_tree_mask(h, parent)
             q, k, v = model.project(h, token, length, tree["depth"])
             out, _ = G.tree_attention_fp4(h, q, k, v, cache, table, length, tree["anc_mask"],
-                                          D ** -0.5, workspace)
+                                          D ** -0.5, workspace, status=attended)
             res = G.verify_greedy(h, model.logits(token, out), token.int(), parent)
             G.spec_kv_commit_fp4(h, k, v, cache, table, length, res["kv_commit"],
-                                 res["accept_len"])
+                                 res["accept_len"], kept)
+            met = torch.stack((tree["status"], attended, res["status"], kept))
+            if met.any():
+                raise RuntimeError(f"mask, attention, verification, commit: {met.tolist()}")
             length = length + res["accept_len"] + 1
             root = res["bonus"].long()
             n = res["accept_len"].tolist()

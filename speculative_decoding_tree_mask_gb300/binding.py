@@ -725,18 +725,20 @@ def qk_norm_rope(h: Handle, q, k, inv_freq, seq_pos, depth=None, q_weight=None, 
 
 
 def kv_load_fp4(h: Handle, cache: Fp4Cache, block_table, start, count, max_len: int,
-                dtype=torch.bfloat16, stream=None):
-    """-> (k, v) rows [B, max_len, H, D] of ``dtype`` (see spec_kv_load_fp4)."""
+                dtype=torch.bfloat16, stream=None, status=None):
+    """-> (k, v) rows [B, max_len, H, D] of ``dtype`` (see spec_kv_load_fp4). status int32 [B]:
+    what each request met (None: it stays unknown)."""
     shape = (block_table.shape[0], int(max_len), cache.H, cache.D)
     k, v = _new(h.torch_device, stream, (shape, dtype), (shape, dtype))
-    spec_kv_load_fp4(h, cache, block_table, start, count, k, v, stream=stream)
+    spec_kv_load_fp4(h, cache, block_table, start, count, k, v, status, stream)
     return k, v
 
 
 def tree_attention_fp4(h: Handle, q, k, v, cache: Fp4Cache, block_table, ctx_len, anc_mask,
-                       scale: float, workspace=None, stream=None):
+                       scale: float, workspace=None, stream=None, status=None):
     """-> (out [B, N, Hq, D], lse float32 [B, N, Hq]) (see spec_tree_attention_fp4). Without a
-    workspace one is taken from torch's allocator for the call."""
+    workspace one is taken from torch's allocator for the call. status int32 [B]: what each
+    request met (None: it stays unknown)."""
     if workspace is None:
         B, N, Hq, D = q.shape
         sizes = (B, N, Hq, cache.H, D)
@@ -747,7 +749,7 @@ def tree_attention_fp4(h: Handle, q, k, v, cache: Fp4Cache, block_table, ctx_len
                           returned=False)
     out, lse = _new(h.torch_device, stream, (q.shape, q.dtype), (q.shape[:3], torch.float32))
     spec_tree_attention_fp4(h, q, k, v, cache, block_table, ctx_len, anc_mask, scale, out,
-                            workspace, lse, stream=stream)
+                            workspace, lse, status, stream)
     return out, lse
 
 

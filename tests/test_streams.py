@@ -97,3 +97,17 @@ def test_memory_of_a_call_belongs_to_its_stream(monkeypatch, name, stream):
     if stream is not None:
         assert all(t.users == ([here] if any(t is o for o in out) else []) for t in taken)
         assert any(g is stream for g in given)
+
+
+@pytest.mark.parametrize("name", ["kv_load_fp4", "tree_attention_fp4"])
+def test_status_reaches_the_library(monkeypatch, name):
+    """The convenience calls hand a status tensor on."""
+    given, status = [], Tensor(None, (2,))
+    monkeypatch.setattr(torch, "empty", lambda shape, dtype, device: Tensor(None, (1,)))
+    monkeypatch.setattr(G, "spec_tree_attention_workspace", lambda *a: 512)
+    monkeypatch.setattr(G, "spec_" + name, lambda *a, **kw: given.extend([*a, *kw.values()]))
+    if name == "kv_load_fp4":
+        G.kv_load_fp4(Handle(), Cache(), Input(2, 4), x, x, 5, status=status)
+    else:
+        G.tree_attention_fp4(Handle(), x, x, x, Cache(), x, x, x, 1.0, status=status)
+    assert any(g is status for g in given)
