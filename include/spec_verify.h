@@ -331,7 +331,8 @@ int spec_kv_load_fp4(spec_handle h, const spec_fp4_cache *cache, int B, const in
  *   sizes, 256-byte aligned; its contents need not be kept or cleared between calls, and calls
  *   that share it are serialised by the caller.
  * Every wait between the kernel's warps ends after two seconds at most; a request whose result
- * is lost that way gets SPEC_REQ_INTERNAL, in every build (no such case is known).
+ * is lost that way gets SPEC_REQ_INTERNAL, in every build, and NaN in out and lse for the rows
+ * that are lost (no such case is known).
  * Scores and softmax statistics are float32; probabilities are rounded to 16 bits for the product
  * with V, which is exact in 16 bits: with the largest of a row scaled to between 2^7 and 2^15, so
  * that a key counts down to 2^-31 of it (a bfloat16 tree's own: as two 16-bit terms). The sums
@@ -448,12 +449,17 @@ const char *spec_error_string(int code);
  *   on the handle whose row statistics are split over several CTAs per row writes `value`
  *   into the arrival counter of row `row` (b * N + node) after zeroing the counters, so its
  *   check must catch it. Returns SPEC_ERR_UNSUPPORTED in release builds.
+ * spec_debug_inject_lost_wait: arms a one-shot injection for tests: if the next
+ *   spec_tree_attention_fp4 call on the handle runs on the tcgen05 tensor cores (more than 32
+ *   query rows a K/V head, D 64 or 128), every wait between the kernel's warps gives up at once,
+ *   before any product is issued. SPEC_ERR_UNSUPPORTED in release builds.
  * spec_debug_words: copies the debug words of requests 0..B-1 of the handle's last call into
  *   the device int32 array `words` (asynchronously on `stream`). SPEC_ERR_UNSUPPORTED in
  *   release builds.
  */
 int spec_debug_build(void);
 int spec_debug_inject_arrival(spec_handle h, int row, int value);
+int spec_debug_inject_lost_wait(spec_handle h);
 int spec_debug_words(spec_handle h, int32_t *words, int B, void *stream);
 
 /*

@@ -129,6 +129,7 @@ def _open(path: str) -> ctypes.CDLL:
     lib.spec_error_string.restype = ctypes.c_char_p
     lib.spec_debug_build.argtypes = []
     lib.spec_debug_inject_arrival.argtypes = [P, i32, i32]
+    lib.spec_debug_inject_lost_wait.argtypes = [P]
     lib.spec_debug_words.argtypes = [P, P, i32, P]
     return lib
 
@@ -793,6 +794,12 @@ def spec_debug_inject_arrival(h: Handle, row: int, value: int):
     arrival counter of ``row`` (a test of the counter check)."""
     _check(load().spec_debug_inject_arrival(h.ptr, int(row), int(value)),
            "spec_debug_inject_arrival")
+
+
+def spec_debug_inject_lost_wait(h: Handle):
+    """Debug builds: if the next tree attention on ``h`` runs on the tcgen05 tensor cores, all its
+    waits give up at once (a test of lost results)."""
+    _check(load().spec_debug_inject_lost_wait(h.ptr), "spec_debug_inject_lost_wait")
 
 
 def spec_debug_words(h: Handle, B: int, stream=None) -> torch.Tensor:

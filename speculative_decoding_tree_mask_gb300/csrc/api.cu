@@ -51,6 +51,7 @@ struct spec_ctx {
     int32_t *count = nullptr;             // ... and per-row arrivals (zero between calls)
     int32_t *dbg = nullptr;               // debug builds: violation bits per request [max_B]
     int inject_row = -1, inject_value = 0;   // debug builds: one armed counter injection
+    int inject_lost = 0;                  // ... and one armed loss of an attention's waits
     int slots = 0;                        // CTAs of the split row-statistics kernel in a wave
     int sms = 0;                          // streaming multiprocessors of the device
     const int32_t *n_active = nullptr;   // node budget set by spec_set_node_budget
@@ -903,6 +904,8 @@ int spec_tree_attention_fp4(spec_handle h, const void *q, int64_t q_stride, cons
     p.status = status;
     p.workspace = workspace;
     p.sms = h->sms;
+    p.lose = h->inject_lost;
+    h->inject_lost = 0;
     // a page found outside the cache raises the request's status from zero
     if (status && cudaMemsetAsync(status, 0, sizeof(int32_t) * (size_t)B, st) != cudaSuccess)
         return SPEC_ERR_CUDA;
@@ -1010,6 +1013,18 @@ int spec_debug_inject_arrival(spec_handle h, int row, int value) {
     (void)h;
     (void)row;
     (void)value;
+    return SPEC_ERR_UNSUPPORTED;
+#endif
+}
+
+int spec_debug_inject_lost_wait(spec_handle h) {
+    SPEC_RANGE("spec_debug_inject_lost_wait");
+#ifdef SPEC_DEBUG
+    if (!h) return SPEC_ERR_ARG;
+    h->inject_lost = 1;
+    return SPEC_OK;
+#else
+    (void)h;
     return SPEC_ERR_UNSUPPORTED;
 #endif
 }

@@ -308,6 +308,7 @@ struct TreeAttnParams {
     int4 *notes;                  // in the workspace: cut items [CTAs] (see tree_attn.cuh)
     float *ws;                    // ... and their parts
     int columns;                  // columns of CTAs
+    int lose;                     // debug builds: every wait of the tcgen05 kernel gives up at once
     int sms;
 };
 

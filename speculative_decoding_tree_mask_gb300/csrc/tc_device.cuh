@@ -38,6 +38,9 @@ __device__ __forceinline__ uint64_t now_ns() {
 // Waits for the phase of `parity` to complete, at most two seconds: then, or when another
 // warp's wait has run out, sets *gave_up and returns false.
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *gave_up) {
+#ifdef SPEC_DEBUG
+    if (*gave_up) return false;      // at once when a test has set it before the first wait
+#endif
     if (bar_try(bar, parity)) return true;
     const uint64_t t0 = now_ns();
     for (;;) {

@@ -28,7 +28,7 @@
 // tensor memory is read by lanes, and both groups own the same lanes.
 // The tree's own nodes are the last tile of an item: V stays as it is and P is multiplied in its
 // type; for bfloat16 as a sum of two terms, since eight bits are too few. Every wait gives up
-// after two seconds; the request's status then says so.
+// after two seconds; the request's status then says so, and its results are NaN.
 //
 // Bound: at D = 128 the scores of 64 positions read 6 KB of operands for 32 clocks of products,
 // so shared memory allows 80% of the products' rate; the multiplying warps and softmax take
@@ -338,7 +338,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bar_init(&W.p_full[i][j], 128);
             }
         }
+#ifdef SPEC_DEBUG
+        W.gave_up = P.lose;
+#else
         W.gave_up = 0;
+#endif
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMmaWarp) tmem_alloc(&W.tmem, C_::kColumns);
@@ -376,8 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t c = done + i, buf = (jobs + j) & 1;
                     if (SPLIT || half == 0) {     // a tile's second half came with its first
                         ok = ok && warp_wait(&W.k_full[c & 1], (c >> 1) & 1, gave_up);
-                        if (!ok) return;
                     }
+                    if (!ok) return;              // no products of what did not come
                     const uint64_t a = smem_desc(base + (SPLIT ? 0 : m * C_::kOperand), 16, 1024);
                     const uint64_t k = smem_desc(
                         base + C_::kK + (c & 1) * C_::kOperand + half * kHalf, 16, 1024);
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int head = A.item / row_tiles, row0 = (A.item - head * row_tiles) * RT;
             const int rows = min(RT, R - row0), contexts = min(n, tree);
             if (P.status && tid == kSoftmax && A.tile == 0 && __ldg(P.ctx_len + b) != ctx)
-                P.status[b] = SPEC_REQ_BAD_SLOT;
+                atomicMax(P.status + b, SPEC_REQ_BAD_SLOT);    // a lost result (below) outweighs it
             const int32_t *table = C.block_table + (int64_t)b * C.max_blocks;
             // the block of this thread's position in the i-th tile (of some position past them)
             auto page = [&](int i) -> int {
@@ -487,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto start = [&](int i, int blk) {
                 const int p = (A.tile + i) * kTile + t;
                 const bool in = i < contexts && p < ctx, ok = in && blk >= 0 && blk < C.num_blocks;
-                if (in && !ok && P.status) P.status[b] = SPEC_REQ_BAD_SLOT;
+                if (in && !ok && P.status) atomicMax(P.status + b, SPEC_REQ_BAD_SLOT);
                 there = (there & ~(1u << (i & 1))) | (ok ? 1u << (i & 1) : 0u);
                 if (i < contexts)
                     start_row<D>(codes, scales,
@@ -711,7 +715,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // two products may be under way here, and o_full tells only two phases apart.
             if (mine > 0) go = go && warp_wait(&W.o_last[m], results++ & 1, gave_up);
             tc_fence_after();
-            if (!go && P.status && lane == 0) P.status[b] = SPEC_REQ_INTERNAL;
+            if (!go) {      // lost: a sum of NaN makes the rows of this part NaN, and the item's
+                sum = NAN;
+                if (P.status && lane == 0) atomicMax(P.status + b, SPEC_REQ_INTERNAL);
+            }
             const bool whole = A.tile == 0 && A.stop == A.nt;
             // the group's O is in V's units once the tree's tile was among its tiles
             const bool in_v = tree < n && (!SPLIT || m == 0);
@@ -745,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q = SPLIT ? m * (D / 64) : 0; q < (SPLIT ? (m + 1) * (D / 64) : D / 32); ++q) {
                 float v[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                for (int e = 0; e < 32; ++e) v[e] = sum == sum ? 0.f : NAN;
 #pragma unroll
                 for (int g = 0; g < (SPLIT ? 2 : 1); ++g) {
                     if (!has[g]) continue;      // the same for the whole group
