@@ -267,8 +267,10 @@ typedef struct {
  *   q_weight, k_weight   [D] of dtype, or both NULL for no norm:
  *                y = x / sqrt(mean(x^2) + eps) * weight;
  *   inv_freq     float32 [rot / 2]: angle of pair i = position * inv_freq[i], position =
- *                seq_pos[b] + depth[b][n]. The angle's turn is formed in 64-bit fixed point, so
- *                it is exact to 2^-32 of a turn at any 32-bit position;
+ *                seq_pos[b] + depth[b][n]. The angle's turn is formed in 64-bit fixed point,
+ *                within |position| (|inv_freq| + 1) 2^-64 + 2^-34 of a turn (below 2^-31 at any
+ *                32-bit position for frequencies up to 1); its cosine and sine are float32,
+ *                within 2^-22 of themselves;
  *   rot          rotated elements of a head, even, 0 <= rot <= D; the others are only
  *                normalised. Pair i is elements (i, i + rot/2) for SPEC_ROPE_HALVES, (2i, 2i+1)
  *                for SPEC_ROPE_PAIRS; (a, c) becomes (a cos - c sin, c cos + a sin);

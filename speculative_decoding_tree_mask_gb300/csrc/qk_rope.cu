@@ -16,8 +16,10 @@
 //
 // The angle: turns = position * inv_freq / (2 pi). inv_freq / (2 pi) becomes a 64-bit fixed
 // point fraction of a turn (one integer product with floor(2^64 / (2 pi))), the product with the
-// position is taken modulo one turn by 64-bit wrap-around, and the top 32 bits give the angle:
-// no 64-bit floating point, whose rate is low, and no loss at far positions.
+// position is taken modulo one turn by 64-bit wrap-around, its nearest quarter turn is taken off,
+// and 32 bits of the rest become a float: no 64-bit floating point, whose rate is low. The step's
+// two cuts cost |position| (|inv_freq| + 1) 2^-64 of a turn, the rest's 2^-34. (A float of the
+// whole turn would have 24 bits of it: 2^-26 of a turn near a half turn, where the sine is small.)
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -51,11 +53,14 @@ __device__ __forceinline__ uint64_t turn_step(float f) {
 // (cos, sin) of pair i at `pos`.
 __device__ __forceinline__ float2 cos_sin(const float *inv_freq, int i, int pos) {
     const float f = __ldg(inv_freq + i);
-    const int turn = (int)(((uint64_t)(int64_t)pos * turn_step(f)) >> 32);
+    const uint64_t turn = (uint64_t)(int64_t)pos * turn_step(f);
+    const uint32_t quarter = (uint32_t)((turn + (1ull << 61)) >> 62);       // the nearest
+    const int rest = (int)((int64_t)(turn - ((uint64_t)quarter << 62)) >> 30);   // of 2^34
     float s, c;
-    sincospif((float)turn * 4.656612873077393e-10f, &s, &c);   // 2^-31: a turn is 2 half turns
+    sincospif((float)rest * 1.1641532182693481e-10f, &s, &c);   // 2^-33: a turn is 2 half turns
     if (!(fabsf(f) < INFINITY)) s = c = NAN;
-    return make_float2(c, s);
+    const float2 r = quarter & 1 ? make_float2(-s, c) : make_float2(c, s);
+    return quarter & 2 ? make_float2(-r.x, -r.y) : r;
 }
 
 template <int T>
