@@ -8,8 +8,8 @@
 // so a warp reads 1 KB of 16-bit rows and writes 256 bytes of codes and 32 of scales side by
 // side. Reading back is bound by DRAM once there are enough rows (16 x 16384 positions, 8 heads
 // x 128, to bfloat16: 195 us, 6.4 TB/s). A commit writes few slots a request: 2048 slots of 32
-// heads x 128 take about 19 us where their bytes need 6, in dependent loads (length, node and
-// block, row) and about 350 instructions a block before its divisions became multiplications.
+// heads x 128 take 16 us where their bytes need 6, in dependent loads (length, node and block,
+// row) and about 290 instructions a block.
 
 #include "fp4_device.cuh"
 
@@ -18,11 +18,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kSmemRequests = 2048;   // requests whose last slot and position fit in shared memory
-// Commit: blocks of 16 elements a thread handles at a time, CTAs an SM holds (2 and 3: 37.8 us for
-// 2048 slots of 32 heads with their read-back; 1 and 8: 43.7, 4 and 2: 39.5, before the divisions).
+// Commit: blocks of 16 elements a thread handles at a time, CTAs an SM holds. With their read-back,
+// 2048 slots of 32 heads x 128 and 4 x 4097 rows of 8 heads x 80: 33 and 28 us with 2 and 3; 36 and 32
+// with 1 and 6; 40 and 41 with 1 and 8; 35 and 31 with 4 and 2.
 constexpr int kCommitItems = 2, kCommitUnit = kThreads * kCommitItems, kCommitCtas = 3;
 // Load: blocks a thread handles, 4 when that fills the GPU, else 1 (333 positions of two
-// requests, 4 heads x 64: 2.7 us against 4.3); a CTA has one unit of them (16 x 16384 positions,
+// requests, 4 heads x 64: 2.9 us against 4.3); a CTA has one unit of them (16 x 16384 positions,
 // 8 heads x 128: 195 us; 222 with CTAs that stride over the units, 312 with one block a thread).
 constexpr int kLoadItems = 4, kLoadCtas = 8;
 

@@ -11,7 +11,8 @@
 // heads of one token: it forms the token's rot/2 sines and cosines once, in shared memory, and
 // keeps its lanes' own in registers for all its rows. Heads are shared out over more warps
 // when there are few tokens, so that a small call still fills the GPU. 16384 tokens of 40 heads
-// x 128 in bfloat16 take 58 us, 5.8 TB/s in and out (86% of the measured copy); 256 tokens 4.1 us.
+// x 128 in bfloat16 take 58 us, 5.8 TB/s in and out (86% of the measured copy), by pairs 59 us; 256
+// tokens 4.3 us.
 // Sizes and alignments that 16-byte vectors do not fit take a warp per row.
 //
 // The angle: turns = position * inv_freq / (2 pi). inv_freq / (2 pi) becomes a 64-bit fixed
@@ -148,7 +149,7 @@ __device__ __forceinline__ Share warp_share(const QkRopeParams &P, int shares, i
 
 // How a lane's two vectors rotate: with each other (halves whose length is a multiple of a
 // vector), each within itself (pairs), or with elements of other lanes, through shared memory
-// (other halves: 16384 tokens of 40 heads x 128 with 90 rotated take 86 us, 181 with a warp per
+// (other halves: 16384 tokens of 40 heads x 128 with 90 rotated take 84 us, 181 with a warp per
 // row and its two-byte loads).
 enum Mode { M_HALVES = 0, M_PAIRS = 1, M_ACROSS = 2 };
 

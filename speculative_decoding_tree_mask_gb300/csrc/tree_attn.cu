@@ -4,17 +4,19 @@
 // over the context positions and the nodes that node i may see; m_i follows the row's maximum.
 // The rows of an item are the N nodes times the G query heads that share one K/V head, so K and
 // V are read once for all of them: 0.5625 bytes an element. With few rows DRAM should bound it;
-// what stands in the way is the conversion of the codes, about 2.5 instructions for two
-// elements, and the products (the warps' matrix unit does 1024 multiplications a clock and SM).
-// One token over 262000 positions of 8 K/V heads x 128: 69 us, 4.3 TB/s (64% of the measured
-// copy; 62% of the issue slots and 57% of the integer pipe, which converts, are taken). 64 chains
-// of six, 24 rows an item: 205 us where the bytes need 79 and the products about 100; the output
-// of 24 rows leaves registers for eight warps an SM only.
+// what stands in the way is the number of instructions, and the products (the warps' matrix unit
+// does 1024 multiplications a clock and SM). One token over 262000 positions of 8 K/V heads x 128:
+// 70 us, 4.3 TB/s (63% of the measured copy), 62% of the issue slots and 57% of the integer pipe
+// taken. It issues 5.6 instructions for two elements: 2.6 on the integer pipe (conversions, bytes
+// put in place, comparisons), the scale's multiplication, 1.0 more on the FMA pipe (addresses and
+// float32), 0.45 loads and copies, 0.25 products, 0.3 others. 64 chains of six, 24 rows an item:
+// 207 us where the bytes need 79 and the products about 100; the output of 24 rows leaves registers
+// for eight warps an SM only, and it issues 7.0 for two elements.
 //
 // A code times its block scale has at most six significant bits and lies in [2^-10, 2688], so
 // it is exact as a half; the tensor scales are applied to the scores and to the result. Q is
-// brought to halves by a power of two for each row (exact for what is within 2^-32 of the row's
-// largest element) and p is rounded to a half with the row's largest at 2^7 or more (kHeadroom:
+// brought to halves by a power of two for each row (bfloat16: exact for what is within 2^-31 of the
+// row's largest element) and p is rounded to a half with the row's largest at 2^7 or more (kHeadroom:
 // what is 2^-31 of it still counts). The products are
 // m16n8k16 of halves with float32 sums, transposed: S^T = K Q^T and O^T = V^T P^T, so that rows
 // come in groups of eight (with Q as the 16-row operand, one token of up to eight heads paid
@@ -38,10 +40,13 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTreeCost = 4;      // the tree's tile and an item's rest, in context tiles
+// The tree's tile and an item's rest, in context tiles. With 2, 4 and 8: the chains above 211, 207
+// and 204 us; 64 chains over up to 2000 positions, D = 64, 48, 43 and 40; 128 single tokens over up
+// to 1000, 38, 41 and 41; over up to 100, 19 each.
+constexpr int kTreeCost = 4;
 
 // CTAs an SM holds, by the registers of the output (D x 8 RG floats a warp) and the ring. One
-// more each spills: 24 rows of D = 128 took 378 us with three CTAs, 205 with two.
+// more each spills: 24 rows of D = 128 took 378 us with three CTAs, 207 with two.
 constexpr int ctas_per_sm(int D, int RG) {
     return D * RG <= 64 ? 5 : D * RG <= 128 ? 4 : D * RG <= 256 ? 3 : 2;
 }
@@ -833,9 +838,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(TreeAttnParams P, in
 }
 
 // How a call is run: by this file's warps (groups of 8 rows of an item), or, with more rows
-// than four groups, on the tcgen05 tensor cores (16 requests, 16000 positions, 8 heads x 128: 32
-// rows take 106 us here, 36 rows 101 us there). D = 256 has no tcgen05
-// form: its Q, K and V tiles do not fit in shared memory together.
+// than four groups, on the tcgen05 tensor cores. 16 requests of up to 16000 positions, 8 heads,
+// here against there: 20 rows 79 us and 104, 32 rows 105 and 104, 36 rows (which would read the
+// cache twice here) 174 and 105; at D = 64 54 and 76, 68 and 77, 112 and 77; up to 500 positions 18
+// and 23, 23 and 22, 30 and 23. D = 256 has no tcgen05 form: its Q, K and V tiles do not fit in
+// shared memory together.
 struct Plan {
     bool tc;
     int groups, rows, grid;   // rows of an item
@@ -886,7 +893,10 @@ namespace {
 int64_t notes_bytes(const Plan &n) { return ((int64_t)n.grid * sizeof(int4) + 255) / 256 * 256; }
 
 // Columns of CTAs (see tree_attn.cuh): one for each item of a request, unless that leaves more
-// than one CTA in sixteen without work.
+// than one CTA in sixteen without work. Against one column: the 64 chains 207 us and 260, one token
+// 70 and 72, 32 64-node trees 187 and 197, 7 heads 61 and 79. (What the limit gives away: 90 heads of
+// 608 CTAs leave one in nine idle, and take 220 us in one column, 157 in 90, in the NHD layout; 144
+// and 140 in HND.)
 int columns(const TreeAttnParams &p, const Plan &n) {
     const int64_t items = (int64_t)p.cache.H * ((p.N * p.G + n.rows - 1) / n.rows);
     return items <= n.grid && n.grid % items * 16 <= n.grid ? (int)items : 1;
@@ -895,7 +905,10 @@ int columns(const TreeAttnParams &p, const Plan &n) {
 template <int T, int D>
 cudaError_t launch_join(const TreeAttnParams &p, const Plan &n, cudaStream_t st) {
     constexpr int F = D / 4, PG = D == 256 ? 4 : 8;
-    // all CTAs' work in items of about this many parts: over eight, the parts are shared out
+    // all CTAs' work in items of about this many parts: over eight, the parts are shared out (one
+    // token over 262000 positions 70 us, 78 if not; a chain of 6 over 50000, D = 64, 25 and 26; 16
+    // tokens over 8000, which are not, 30, 33 if so; 4 chains of 6 over 8000, nine parts an item,
+    // lose by it: 28 us, 23 if not)
     const int R = p.N * p.G, rows = R < n.rows ? R : n.rows;
     const int64_t items = (int64_t)p.B * p.cache.H * ((R + n.rows - 1) / n.rows);
     const int per = kJoinThreads / F;

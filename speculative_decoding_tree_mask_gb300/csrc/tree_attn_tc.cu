@@ -10,7 +10,7 @@
 //            D, and V as it is, read transposed). All become halves; two tiles of each in a
 //            ring, the rows of the next on their way by asynchronous copies. Q, and the K of the
 //            tree's nodes, are brought to halves by a power of two for each row, exact for what
-//            is within 2^-32 of the row's largest element (bfloat16 for all of K cost twice the
+//            is within 2^-31 of the row's largest element (bfloat16 for all of K cost twice the
 //            conversion);
 //   multiply (2 threads, one for each softmax group) S = Q K^T and O += P V, sums in tensor
 //            memory: S and O twice, up to all 512 columns; P overwrites the half of S it came
@@ -33,8 +33,8 @@
 // Bound: at D = 128 the scores of 64 positions read 6 KB of operands for 32 clocks of products,
 // so shared memory allows 80% of the products' rate; the multiplying warps and softmax take
 // about 1900 clocks for 64 positions of 256 rows where that needs 1280. 32 64-node trees over up
-// to 8192 positions (32 query heads, 8 K/V heads): 188 us, 0.88 PFLOP/s (46% of the measured
-// cuBLAS rate); one over 100000 positions: 108 us.
+// to 8192 positions (32 query heads, 8 K/V heads): 186 us, 0.89 PFLOP/s (47% of the measured
+// cuBLAS rate); one over 100000 positions: 107 us.
 
 #include "tc_device.cuh"
 #include "tree_attn.cuh"
@@ -46,8 +46,9 @@ constexpr int kConvert = 256;     // converting threads: K's, then V's
 constexpr int kSoftmax = 256;     // threads of the two softmax groups
 constexpr int kThreads = kSoftmax + kConvert + 128;   // the last warpgroup: two warps multiply
 constexpr int kMmaWarp = (kSoftmax + kConvert) / 32;
-// The tree's tile and an item's rest, in context tiles (the trees above: 244 us with 4, 211 with
-// 6, 195 with 8, 209 with 16).
+// The tree's tile and an item's rest, in context tiles. With 4, 8 and 16: the trees above 195, 187
+// and 195 us, with D = 64 147, 151 and 159; 32-node trees (SPLIT) 129, 123 and 127, with D = 64 88,
+// 87 and 90; 128 64-node trees over up to 500 positions 183, 174 and 172.
 constexpr int kTreeCost = 8;
 
 template <int D, bool SPLIT>
