@@ -54,7 +54,7 @@ enum {
     SPEC_ERR_WORKSPACE = -4     /* workspace allocation failed */
 };
 
-enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 };  /* element types (F16: K/V only) */
+enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 };  /* element types (F16: not for logits) */
 
 enum {
     SPEC_DRAFT_POINT = 0,       /* deterministic trie: the draft puts mass 1 on each child */
@@ -72,12 +72,15 @@ enum {
     SPEC_REQ_BAD_SLOT = 5,      /* KV commit: a slot maps outside the block table or cache */
     SPEC_REQ_BAD_BUDGET = 6,    /* the request's node budget (spec_set_node_budget) is
                                    outside [1, N] */
-    SPEC_REQ_INTERNAL = 7       /* spec_tree_attention_fp4: a wait inside the kernel gave up.
+    SPEC_REQ_INTERNAL = 7,      /* spec_tree_attention_fp4, spec_paged_attention: a wait inside the
+                                   kernel gave up.
                                    Otherwise debug builds only (SPEC_DEBUG): one of the kernels' own
                                    consistency checks failed for this request -- an index
                                    outside its array (the access was skipped), a split row's
                                    arrival counter outside [0, split), or an accepted path that
                                    is not a chain of parent links; see spec_debug_words */
+    SPEC_REQ_BAD_RANGE = 8      /* paged step: a request's rows row_start[b] .. row_start[b + 1] - 1
+                                   are not within the rows given, or more than max_new */
 };
 
 enum { SPEC_KV_NHD = 0, SPEC_KV_HND = 1 };  /* paged KV cache layouts */
@@ -87,6 +90,8 @@ enum { SPEC_ROPE_HALVES = 0, SPEC_ROPE_PAIRS = 1 };         /* which elements ro
 
 /* Row-statistics flag bits (spec_row_stats row_flags). */
 enum { SPEC_ROW_NAN = 1, SPEC_ROW_POSINF = 2, SPEC_ROW_ALL_NEGINF = 4 };
+/* ... and of spec_token_logprobs, which has these too. */
+enum { SPEC_ROW_BAD_NODE = 8, SPEC_ROW_BAD_TOKEN = 16 };
 
 /* Kernel classes reported by the profiling calls. */
 enum {
@@ -103,7 +108,10 @@ enum {
     SPEC_K_KV_COMMIT_FP4 = 10,  /* K/V rows into the 4-bit cache */
     SPEC_K_KV_LOAD_FP4 = 11,    /* 4-bit cache back to rows */
     SPEC_K_TREE_ATTN = 12,      /* tree attention over the 4-bit cache */
-    SPEC_K_COUNT = 13
+    SPEC_K_KV_APPEND = 13,      /* new tokens' K/V into the paged cache, rotated */
+    SPEC_K_PAGED_ATTN = 14,     /* attention of new tokens over the paged cache */
+    SPEC_K_LOGPROBS = 15,       /* log probabilities, entropy and likeliest tokens of rows */
+    SPEC_K_COUNT = 16
 };
 
 /*
@@ -348,6 +356,130 @@ int spec_tree_attention_fp4(spec_handle h, const void *q, int64_t q_stride, cons
                             const uint64_t *anc_mask, float scale, void *out, float *lse,
                             int32_t *status, void *workspace, int64_t workspace_bytes,
                             void *stream);
+
+/*
+ * The paged step of the target model over a cache of 16 or 8 bits (the one that spec_kv_commit
+ * writes): spec_kv_append turns the projections of new tokens into rotated queries and cached keys
+ * and values, spec_paged_attention is the attention of those tokens over the cache. New tokens are
+ * one a request (decoding), a draft chain, a prompt or a chunk of one, in any mix.
+ *
+ * Rows [T, H, D] of `dtype`: row_start int32 [B + 1] gives request b the rows row_start[b] ..
+ * row_start[b + 1] - 1, its tokens in order (none if the two are equal); NULL gives each T / B rows
+ * (T a multiple of B). Rows may be columns of a wider matrix: each argument comes with the number of
+ * elements from one row to the next, at least H * D. Row i of request b stands at position
+ * seq_pos[b] + i of its sequence; seq_pos int32 [B] is the number of positions before. A request
+ * whose rows are not within 0 .. T - 1 (or with row_start[b] > row_start[b + 1]) takes no part
+ * (SPEC_REQ_BAD_RANGE). Rows of no request are not read, and their results are left as they were.
+ * Requests do not share rows: row_start does not fall. B is limited by the handle, T by 2^31 - 1.
+ *
+ * The paged cache (host struct, copied at the call; the pointers are device memory):
+ *   k, v         SPEC_KV_NHD [num_blocks, block_size, H, D] or SPEC_KV_HND [num_blocks, H,
+ *                block_size, D], 16-byte aligned; a block is contiguous, and blocks stand
+ *                k_block_stride, v_block_stride elements apart (multiples of 16 bytes, so that K and V
+ *                may be interleaved block by block);
+ *   kind         SPEC_CACHE_SAME (elements of the rows' dtype) or SPEC_CACHE_FP8_E4M3 / _E5M2;
+ *   k_scale, v_scale   device float32, one value each (NULL = 1), for fp8: an element's value is
+ *                its code's times the scale; ignored otherwise;
+ *   block_table  int32 [B, max_blocks]: cache block of each block_size positions of request b.
+ * H at most 65536, D at most 1024, a head's bytes a multiple of 16; a request has at most 2^31 - 1025
+ * positions (max_blocks * block_size), the cache at most 2^31 - 1 blocks.
+ */
+typedef struct {
+    void *k, *v;
+    int64_t k_block_stride, v_block_stride;
+    const float *k_scale, *v_scale;
+    int64_t num_blocks;
+    int32_t kind, layout, block_size, H, D;
+    const int32_t *block_table;
+    int32_t max_blocks;
+} spec_kv_cache;
+
+/*
+ * New tokens into the paged cache, the rotation by their positions (and the norm of the heads) on
+ * the way.
+ *   q [T, Hq, D] (NULL with Hq 0: keys and values only), k, v [T, H, D] of dtype (SPEC_F32 /
+ *                SPEC_BF16 / SPEC_F16), H and D the cache's;
+ *   q_weight, k_weight, eps, inv_freq, rot, style   as in spec_qk_norm_rope, of which this is the
+ *                form for new tokens: the same norm, angles and rounding; q_weight may be NULL when
+ *                q is;
+ *   q_out        [T, Hq, D] of dtype; may be q itself with the same stride.
+ * Row i of request b: q normalised and rotated by position seq_pos[b] + i goes to q_out, k
+ * likewise to that position of the cache, v to it as it is. All arithmetic is float32, rounded
+ * once: to dtype, or for fp8 as RN(x / scale), nearest even, saturated (as spec_kv_commit does).
+ * status int32 [B] (may be NULL): SPEC_REQ_BAD_RANGE, or SPEC_REQ_BAD_SLOT if a position is outside
+ * [0, max_blocks * block_size) or its block outside the cache (it is skipped; its q_out is written),
+ * else 0. Where two rows share a slot of the cache, it holds one of them.
+ */
+int spec_kv_append(spec_handle h, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                   const void *v, int64_t v_stride, int dtype, int B, int64_t T, int Hq,
+                   const int32_t *row_start, const int32_t *seq_pos, const spec_kv_cache *cache,
+                   const void *q_weight, const void *k_weight, float eps, const float *inv_freq,
+                   int rot, int style, void *q_out, int64_t q_out_stride, int32_t *status,
+                   void *stream);
+
+/*
+ * Attention of new tokens over the paged cache, their own positions included (spec_kv_append
+ * comes first): row i of request b, at p = seq_pos[b] + i, sees position j of its sequence if
+ *   0 <= j <= p,  and window == 0, or j > p - window, or j < sinks
+ * (a sliding window of `window` positions that ends with the token itself, and `sinks` first
+ * positions that stay visible). For query head h, whose K/V head is h / (Hq / H):
+ *   out = sum_j softmax_j(scale * q.k_j) v_j,   lse = log sum_j exp(scale * q.k_j).
+ * A row that sees nothing gets out 0 and lse -inf. What a row does not see never influences its
+ * result, NaN and infinities included. A row that sees an infinity or a NaN in V gets it (or NaN)
+ * in that element.
+ *   q [T, Hq, D] of dtype (SPEC_BF16 / SPEC_F16), Hq a multiple of the cache's H; D a multiple of 16,
+ *                at most 256 (others: SPEC_ERR_UNSUPPORTED); scale finite, > 0;
+ *   max_new      the most rows of a request, or 0 if that is not known (then T): it chooses the
+ *                kernel and its workspace. A request with more gets SPEC_REQ_BAD_RANGE, and its rows
+ *                are left as they were;
+ *   window, sinks   >= 0; sinks counts only where window > 0;
+ *   out [T, Hq, D] of dtype, lse float32 [T, Hq] (may be NULL), both contiguous;
+ *   status int32 [B] (may be NULL): SPEC_REQ_BAD_RANGE; SPEC_REQ_BAD_SLOT if seq_pos[b] is
+ *   negative, a row's position is outside the table, or a block that is read is outside the cache
+ *   (such positions are not attended); else 0;
+ *   workspace: device memory of the size that spec_paged_attention_workspace gives for these
+ *   sizes, 256-byte aligned; its contents need not be kept or cleared between calls, and calls
+ *   that share it are serialised by the caller.
+ * Every wait between the kernel's warps ends after two seconds at most; a request whose result is
+ * lost that way gets SPEC_REQ_INTERNAL and NaN in the rows that are lost (no such case is known).
+ * Scores, softmax statistics and sums are float32. Probabilities are rounded to 16 bits for the
+ * product with V: to dtype, or to halves over an fp8 cache (whose values a half holds exactly, and
+ * for which bfloat16 queries are brought to halves by a power of two for each row, exact for what is
+ * within 2^-31 of the row's largest element).
+ */
+int spec_paged_attention_workspace(spec_handle h, int B, int64_t T, int max_new, int Hq, int H,
+                                   int D, int64_t *bytes);
+int spec_paged_attention(spec_handle h, const void *q, int64_t q_stride, int dtype, int B,
+                         int64_t T, int Hq, int max_new, const int32_t *row_start,
+                         const int32_t *seq_pos, const spec_kv_cache *cache, float scale,
+                         int window, int sinks, void *out, float *lse, int32_t *status,
+                         void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Log probabilities of given tokens, entropy and the likeliest tokens of logits rows, in one pass
+ * over each row: what an answer's tokens scored.
+ *   logits [B, N, V] of dtype (SPEC_F32 / SPEC_BF16); N is not limited by the handle, B and V are;
+ *   node         int32 [B, P]: slot j of request b scores row node[b][j] (the kv_commit of a verify
+ *                call: out_tokens[b][j] was chosen by that row); -1 is a slot of nothing. NULL: row
+ *                j itself (P = N);
+ *   tokens       int32 [B, P, C]: C tokens for each slot (0 <= C <= 64; NULL with C 0), -1 for none;
+ *   temperature  finite, > 0: p = softmax(z / temperature);
+ *   logprob      float32 [B, P, C]: log p(token); 0 for a token or a slot of nothing, so that a sum
+ *                over a request's slots is its path's;
+ *   entropy      float32 [B, P] (may be NULL): -sum p log p; 0 for a slot of nothing;
+ *   top          0 <= top <= 32; top_ids int32, top_logprobs float32 [B, P, top]: the likeliest
+ *                tokens and their log p, the largest first, the lowest token first among equals. Past
+ *                the tokens with a logit above -inf, and in a slot of nothing: -1 and -inf;
+ *   flags        int32 [B, P] (may be NULL): SPEC_ROW_* bits of the row (NaN, +inf, all -inf:
+ *                logprob, entropy and top_logprobs NaN, top_ids -1), SPEC_ROW_BAD_NODE for a node of
+ *                N or more, or below -1 (likewise), SPEC_ROW_BAD_TOKEN for a token of V or more, or
+ *                below -1 (its logprob is NaN).
+ * Sums are float32 (of at most 2^11 terms a thread, then pairwise). Nothing is kept between calls.
+ */
+int spec_token_logprobs(spec_handle h, const void *logits, int dtype, int B, int64_t N, int64_t V,
+                        const int32_t *node, int P, const int32_t *tokens, int C,
+                        float temperature, float *logprob, float *entropy, int top,
+                        int32_t *top_ids, float *top_logprobs, int32_t *flags, void *stream);
 
 /*
  * The vocabulary-streaming row statistics on their own (the first stage of both verify

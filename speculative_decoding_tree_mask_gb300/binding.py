@@ -25,11 +25,14 @@ SPEC_REQ_OK, SPEC_REQ_BAD_PARENT, SPEC_REQ_BAD_TOKEN, SPEC_REQ_BAD_ROW, SPEC_REQ
 SPEC_ROW_NAN, SPEC_ROW_POSINF, SPEC_ROW_ALL_NEGINF = 1, 2, 4
 KERNEL_CLASSES = ("tree_mask", "row_stats", "draft_stats", "walk_greedy", "walk_sample",
                   "lazy_greedy", "lazy_sample", "kv_commit", "budget", "qk_rope",
-                  "kv_commit_fp4", "kv_load_fp4", "tree_attn")
+                  "kv_commit_fp4", "kv_load_fp4", "tree_attn", "kv_append", "paged_attn",
+                  "logprobs")
+SPEC_ROW_BAD_NODE, SPEC_ROW_BAD_TOKEN = 8, 16
 SPEC_F16 = 2
 SPEC_REQ_BAD_SLOT = 5
 SPEC_REQ_BAD_BUDGET = 6
 SPEC_REQ_INTERNAL = 7   # debug builds: a kernel's own consistency check failed
+SPEC_REQ_BAD_RANGE = 8   # a request's rows are not within the rows given
 DBG_INDEX, DBG_ARRIVAL, DBG_WALK = 1, 2, 4
 SPEC_KV_NHD, SPEC_KV_HND = 0, 1
 SPEC_CACHE_SAME, SPEC_CACHE_FP8_E4M3, SPEC_CACHE_FP8_E5M2 = 0, 1, 2
@@ -42,6 +45,17 @@ class Fp4CacheStruct(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_sf", ctypes.c_void_p),
                 ("v_sf", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int64),
+                ("layout", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("block_table", ctypes.c_void_p), ("max_blocks", ctypes.c_int32)]
+
+
+class KvCacheStruct(ctypes.Structure):
+    """spec_kv_cache: the paged cache of 16 or 8 bits as the library takes it (see KvCache)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_block_stride", ctypes.c_int64), ("v_block_stride", ctypes.c_int64),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("num_blocks", ctypes.c_int64), ("kind", ctypes.c_int32),
                 ("layout", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("H", ctypes.c_int32), ("D", ctypes.c_int32),
                 ("block_table", ctypes.c_void_p), ("max_blocks", ctypes.c_int32)]
@@ -123,6 +137,15 @@ def _open(path: str) -> ctypes.CDLL:
                                                   ctypes.POINTER(i64)]
     lib.spec_tree_attention_fp4.argtypes = [P, P, i64, P, i64, P, i64, i32, i32, i32, i32, C, P,
                                             P, f32, P, P, P, P, i64, P]
+    K = ctypes.POINTER(KvCacheStruct)
+    lib.spec_kv_append.argtypes = [P, P, i64, P, i64, P, i64, i32, i32, i64, i32, P, P, K, P, P,
+                                   f32, P, i32, i32, P, i64, P, P]
+    lib.spec_paged_attention_workspace.argtypes = [P, i32, i64, i32, i32, i32, i32,
+                                                   ctypes.POINTER(i64)]
+    lib.spec_paged_attention.argtypes = [P, P, i64, i32, i32, i64, i32, i32, P, P, K, f32, i32,
+                                         i32, P, P, P, P, i64, P]
+    lib.spec_token_logprobs.argtypes = [P, P, i32, i32, i64, i64, P, i32, P, i32, f32, P, P, i32,
+                                        P, P, P, P]
     lib.spec_profile_begin.argtypes = [P]
     lib.spec_profile_end.argtypes = [P, P, P]
     lib.spec_error_string.argtypes = [i32]
@@ -211,6 +234,7 @@ class Handle:
         self.max_B, self.max_N, self.max_V = int(max_B), int(max_N), int(max_V)
         self.attention_sizes = None     # sizes that attention_bytes (a workspace) belongs to
         self.attention_bytes = 0
+        self.paged_sizes, self.paged_bytes = None, 0      # the same for paged_attention
 
     def close(self):
         if self.ptr is not None and self.ptr.value:
@@ -590,6 +614,201 @@ def spec_tree_attention_fp4(h: Handle, q, k, v, cache: Fp4Cache, block_table, ct
         _raw_stream(stream, dev)), where)
 
 
+# ---- the paged step over a 16-bit or 8-bit cache ------------------------------------------------
+
+_FP8_KINDS = {getattr(torch, "float8_e4m3fn", None): SPEC_CACHE_FP8_E4M3,
+              getattr(torch, "float8_e5m2", None): SPEC_CACHE_FP8_E5M2}
+
+
+class KvCache:
+    """A paged K/V cache (spec_kv_cache), the one that spec_kv_commit writes: k, v [num_blocks,
+    block_size, H, D] (SPEC_KV_NHD) or [num_blocks, H, block_size, D] (SPEC_KV_HND) of float32,
+    bfloat16, float16 or a float8 type, or uint8 with `kind` saying which float8. Blocks may stand
+    apart (kv[:, 0] and kv[:, 1] of one tensor). Tensor scales of fp8: float32 of one element
+    (None = 1). Holds the tensors; block tables come with each call."""
+
+    def __init__(self, k, v, layout: int = SPEC_KV_NHD, k_scale=None, v_scale=None,
+                 kind: int | None = None):
+        if layout != SPEC_KV_NHD and layout != SPEC_KV_HND:
+            raise ValueError("layout must be SPEC_KV_NHD or SPEC_KV_HND")
+        dtype, shape = k.dtype, k.shape
+        if kind is None:
+            kind = _FP8_KINDS.get(dtype, SPEC_CACHE_SAME)
+            if kind == SPEC_CACHE_SAME and dtype not in _ROW_CODES:
+                raise TypeError(f"a cache of {dtype} needs its kind")
+        elif kind == SPEC_CACHE_SAME:
+            if dtype not in _ROW_CODES:
+                raise TypeError(f"SPEC_CACHE_SAME: rows cannot be {dtype}")
+        elif kind != SPEC_CACHE_FP8_E4M3 and kind != SPEC_CACHE_FP8_E5M2:
+            raise ValueError("kind must be SPEC_CACHE_SAME, _FP8_E4M3 or _FP8_E5M2")
+        elif dtype != torch.uint8 and _FP8_KINDS.get(dtype) != kind:
+            raise TypeError(f"kind does not fit a cache of {dtype}")
+        if v.dtype != dtype or len(shape) != 4 or v.shape != shape:
+            raise TypeError("k and v must be 4-dimensional tensors of one shape and type")
+        for s in (k_scale, v_scale):
+            if s is not None and (s.dtype != torch.float32 or s.numel() != 1):
+                raise TypeError("tensor scales must be float32 of one element")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.layout, self.kind = int(layout), int(kind)
+        self.dtype = dtype if kind == SPEC_CACHE_SAME else None      # what rows have to be
+        if layout == SPEC_KV_NHD:
+            self.num_blocks, self.block_size, self.H, self.D = shape
+        else:
+            self.num_blocks, self.H, self.block_size, self.D = shape
+
+    @classmethod
+    def empty(cls, num_blocks: int, block_size: int, H: int, D: int, dtype, device,
+              layout: int = SPEC_KV_NHD, k_scale=None, v_scale=None) -> "KvCache":
+        """A cache of zeros."""
+        shape = (num_blocks, block_size, H, D) if layout == SPEC_KV_NHD else \
+            (num_blocks, H, block_size, D)
+        return cls(*(torch.zeros(shape, dtype=dtype, device=device) for _ in range(2)), layout,
+                   k_scale, v_scale)
+
+    def _blocks(self, t, device: int, name: str):
+        """(address, elements from block to block) of k or v."""
+        if t.get_device() != device:
+            raise ValueError(f"cache {name} is on {t.device}, the call runs on cuda:{device}")
+        s = t.stride()
+        _, b, c, d = t.shape
+        if (d > 1 and s[3] != 1) or (c > 1 and s[2] != d) or (b > 1 and s[1] != c * d):
+            raise ValueError(f"cache {name}: a block must be contiguous")
+        return t.data_ptr(), s[0] if t.shape[0] > 1 else b * c * d
+
+    def struct(self, block_table, B: int, device: int, dtype) -> KvCacheStruct:
+        """The library's view of the cache on GPU `device` for rows of `dtype`, with the block
+        table int32 [B, max_blocks]."""
+        if self.dtype is not None and self.dtype != dtype:
+            raise TypeError(f"the cache holds {self.dtype}, the rows are {dtype}")
+        if block_table.dtype != torch.int32:
+            raise TypeError("block_table must be int32")
+        if block_table.dim() != 2 or block_table.shape[0] != B:
+            raise ValueError(f"block_table must be [{B}, max_blocks]")
+        k, ks = self._blocks(self.k, device, "k")
+        v, vs = self._blocks(self.v, device, "v")
+        return KvCacheStruct(
+            k, v, ks, vs, _addr(self.k_scale, device), _addr(self.v_scale, device),
+            self.num_blocks, self.kind, self.layout, self.block_size, self.H, self.D,
+            _addr(block_table, device), block_table.shape[1])
+
+
+def _batch_rows(t, device: int, name: str):
+    """(address, row stride) of rows [T, H, D], contiguous or columns of a wider matrix."""
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{device}")
+    T, H, D = t.shape
+    if t.is_contiguous():
+        return t.data_ptr(), H * D
+    st, sh, sd = t.stride()
+    row = st if T > 1 else H * D
+    if (sd != 1 and D > 1) or (sh != D and H > 1) or row < H * D:
+        raise ValueError(f"{name}: heads and elements must be contiguous, and rows apart")
+    return t.data_ptr(), row
+
+
+def spec_kv_append(h: Handle, q, k, v, cache: KvCache, block_table, seq_pos, q_out,
+                   row_start=None, inv_freq=None, q_weight=None, k_weight=None,
+                   eps: float = 1e-6, style: int = SPEC_ROPE_HALVES, status=None, stream=None):
+    """New tokens into the paged cache: rows k, v [T, H, D] of request b (row_start[b] ..
+    row_start[b + 1] - 1; None: T / B each) to its positions seq_pos[b] and on, k (and q [T, Hq, D]
+    into q_out, which may be q; both None: no queries) normalised with the weights (None: not)
+    and rotated by inv_freq float32 [rot/2] (None: not)."""
+    where, i32, dt = "spec_kv_append", torch.int32, k.dtype
+    T, B, dev = k.shape[0], seq_pos.shape[0], h.device
+    ks, D = (T, cache.H, cache.D), (cache.D,)
+    qs = (T, q.shape[1], cache.D) if q is not None else None
+    if (q is None) != (q_out is None):
+        raise ValueError(f"{where}: q and q_out come together")
+    if _bad(k, ks, dt) or _bad(v, ks, dt) or _bad(q, qs, dt) or _bad(q_out, qs, dt) or \
+            _bad(q_weight, D, dt) or _bad(k_weight, D, dt) or _bad(seq_pos, (B,), i32) or \
+            _bad(row_start, (B + 1,), i32) or _bad(status, (B,), i32) or \
+            (inv_freq is not None and inv_freq.dtype != torch.float32):
+        _refuse(where, k=(k, ks, dt), v=(v, ks, dt), q=(q, qs, dt), q_out=(q_out, qs, dt),
+                q_weight=(q_weight, D, dt), k_weight=(k_weight, D, dt),
+                seq_pos=(seq_pos, (B,), i32), row_start=(row_start, (B + 1,), i32),
+                status=(status, (B,), i32),
+                inv_freq=(inv_freq, inv_freq.shape if inv_freq is not None else (),
+                          torch.float32))
+    code = _row_code(dt, where)
+    view = cache.struct(block_table, B, dev, dt)
+    ka, kt = _batch_rows(k, dev, "k")
+    va, vt = _batch_rows(v, dev, "v")
+    qa = qt = qo = qot = Hq = 0
+    if q is not None:
+        Hq = q.shape[1]
+        qa, qt = _batch_rows(q, dev, "q")
+        qo, qot = _batch_rows(q_out, dev, "q_out")
+    _check(load().spec_kv_append(
+        h.ptr, qa or None, qt, ka, kt, va, vt, code, B, T, Hq, _addr(row_start, dev),
+        _addr(seq_pos, dev), view, _addr(q_weight, dev), _addr(k_weight, dev), eps,
+        _addr(inv_freq, dev), 0 if inv_freq is None else 2 * inv_freq.numel(), style, qo or None,
+        qot, _addr(status, dev), _raw_stream(stream, dev)), where)
+
+
+def spec_paged_attention_workspace(h: Handle, B: int, T: int, max_new: int, Hq: int, H: int,
+                                   D: int) -> int:
+    """Bytes of workspace that spec_paged_attention needs for these sizes."""
+    n = ctypes.c_int64()
+    _check(load().spec_paged_attention_workspace(h.ptr, int(B), int(T), int(max_new), int(Hq),
+                                                 int(H), int(D), ctypes.byref(n)),
+           "spec_paged_attention_workspace")
+    return n.value
+
+
+def spec_paged_attention(h: Handle, q, cache: KvCache, block_table, seq_pos, scale: float, out,
+                         workspace, row_start=None, max_new: int = 0, window: int = 0,
+                         sinks: int = 0, lse=None, status=None, stream=None):
+    """Attention of new tokens q [T, Hq, D] (rows as in spec_kv_append) over the paged cache, their
+    own positions included: row i of request b sees positions up to p = seq_pos[b] + i, with a
+    window only the last `window` of them and the first `sinks`."""
+    where, i32, dt = "spec_paged_attention", torch.int32, q.dtype
+    T, Hq, _ = q.shape
+    B, full, dev = seq_pos.shape[0], (T, Hq, cache.D), h.device
+    if _bad(q, full, dt) or _bad(out, full, dt) or _bad(seq_pos, (B,), i32) or \
+            _bad(row_start, (B + 1,), i32) or _bad(lse, (T, Hq), torch.float32) or \
+            _bad(status, (B,), i32):
+        _refuse(where, q=(q, full, dt), out=(out, full, dt), seq_pos=(seq_pos, (B,), i32),
+                row_start=(row_start, (B + 1,), i32), lse=(lse, (T, Hq), torch.float32),
+                status=(status, (B,), i32))
+    code = _row_code(dt, where)
+    view = cache.struct(block_table, B, dev, dt)
+    qa, qt = _batch_rows(q, dev, "q")
+    _check(load().spec_paged_attention(
+        h.ptr, qa, qt, code, B, T, Hq, max_new, _addr(row_start, dev), _addr(seq_pos, dev), view,
+        scale, window, sinks, _addr(out, dev), _addr(lse, dev), _addr(status, dev),
+        _addr(workspace, dev), workspace.numel() * workspace.element_size(),
+        _raw_stream(stream, dev)), where)
+
+
+def spec_token_logprobs(h: Handle, logits, node, tokens, temperature: float, logprob, entropy=None,
+                        top_ids=None, top_logprobs=None, flags=None, stream=None):
+    """Log probabilities of tokens [B, P] or [B, P, C] under the rows node [B, P] of logits [B, N,
+    V] (None: row j for slot j, P = N), entropy [B, P], the likeliest tokens top_ids and
+    top_logprobs [B, P, K]. node, tokens: -1 for none (kv_commit and out_tokens of a verify
+    call)."""
+    where, i32, f32 = "spec_token_logprobs", torch.int32, torch.float32
+    B, N, V = logits.shape
+    P = N if node is None else node.shape[1]
+    one = (B, P)
+    C = 0 if tokens is None else tokens.shape[2] if tokens.dim() == 3 else 1
+    ts = one if tokens is None or tokens.dim() == 2 else (B, P, C)
+    K = 0 if top_ids is None else top_ids.shape[-1]
+    if (tokens is None) != (logprob is None) or (top_ids is None) != (top_logprobs is None):
+        raise ValueError(f"{where}: tokens and logprob, top_ids and top_logprobs come together")
+    if _bad(node, one, i32) or _bad(tokens, ts, i32) or _bad(logprob, ts, f32) or \
+            _bad(entropy, one, f32) or _bad(top_ids, (B, P, K), i32) or \
+            _bad(top_logprobs, (B, P, K), f32) or _bad(flags, one, i32):
+        _refuse(where, node=(node, one, i32), tokens=(tokens, ts, i32), logprob=(logprob, ts, f32),
+                entropy=(entropy, one, f32), top_ids=(top_ids, (B, P, K), i32),
+                top_logprobs=(top_logprobs, (B, P, K), f32), flags=(flags, one, i32))
+    dev = h.device
+    _check(load().spec_token_logprobs(
+        h.ptr, _addr(logits, dev), _dtype_code(logits), B, N, V, _addr(node, dev), P,
+        _addr(tokens, dev), C, temperature, _addr(logprob, dev), _addr(entropy, dev), K,
+        _addr(top_ids, dev), _addr(top_logprobs, dev), _addr(flags, dev),
+        _raw_stream(stream, dev)), where)
+
+
 def spec_set_node_budget(h: Handle, n_active):
     """Later verify calls on ``h`` verify request b as its first n_active[b] nodes (device
     int32 [>= B], read when the kernels run); None verifies every node."""
@@ -752,6 +971,56 @@ def tree_attention_fp4(h: Handle, q, k, v, cache: Fp4Cache, block_table, ctx_len
     spec_tree_attention_fp4(h, q, k, v, cache, block_table, ctx_len, anc_mask, scale, out,
                             workspace, lse, status, stream)
     return out, lse
+
+
+def kv_append(h: Handle, q, k, v, cache: KvCache, block_table, seq_pos, row_start=None,
+              inv_freq=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+              style: int = SPEC_ROPE_HALVES, stream=None, status=None):
+    """-> new contiguous q, normalised and rotated (None for None); k and v go to the cache (see
+    spec_kv_append). status int32 [B]: what each request met (None: it stays unknown)."""
+    qo = None
+    if q is not None:
+        qo, = _new(h.torch_device, stream, (q.shape, q.dtype))
+    spec_kv_append(h, q, k, v, cache, block_table, seq_pos, qo, row_start, inv_freq, q_weight,
+                   k_weight, eps, style, status, stream)
+    return qo
+
+
+def paged_attention(h: Handle, q, cache: KvCache, block_table, seq_pos, scale: float,
+                    row_start=None, max_new: int = 0, window: int = 0, sinks: int = 0,
+                    workspace=None, stream=None, status=None):
+    """-> (out [T, Hq, D], lse float32 [T, Hq]) (see spec_paged_attention); rows of no request
+    stay as the allocator gave them. Without a workspace one is taken from torch's allocator for
+    the call. status int32 [B]: what each request met (None: it stays unknown)."""
+    if workspace is None:
+        sizes = (seq_pos.shape[0], q.shape[0], max_new, q.shape[1], cache.H, cache.D)
+        if h.paged_sizes != sizes:          # the size depends on these alone
+            h.paged_bytes = spec_paged_attention_workspace(h, *sizes)
+            h.paged_sizes = sizes
+        workspace, = _new(h.torch_device, stream, ((h.paged_bytes,), torch.uint8), returned=False)
+    out, lse = _new(h.torch_device, stream, (q.shape, q.dtype), (q.shape[:2], torch.float32))
+    spec_paged_attention(h, q, cache, block_table, seq_pos, scale, out, workspace, row_start,
+                         max_new, window, sinks, lse, status, stream)
+    return out, lse
+
+
+def token_logprobs(h: Handle, logits, tokens=None, node=None, temperature: float = 1.0,
+                   top: int = 0, stream=None) -> dict:
+    """-> dict(logprob like tokens, entropy [B, P], top_ids, top_logprobs [B, P, top], flags
+    [B, P]); without tokens no logprob (see spec_token_logprobs)."""
+    B, N, _ = logits.shape
+    one = (B, N if node is None else node.shape[1])
+    f32, i32 = torch.float32, torch.int32
+    specs = [(one, f32), (one, i32), ((*one, top), i32), ((*one, top), f32)]
+    if tokens is not None:
+        specs.append((tokens.shape, f32))
+    entropy, flags, ids, top_lp, *lp = _new(h.torch_device, stream, *specs)
+    spec_token_logprobs(h, logits, node, tokens, temperature, lp[0] if lp else None, entropy, ids,
+                        top_lp, flags, stream)
+    out = dict(entropy=entropy, top_ids=ids, top_logprobs=top_lp, flags=flags)
+    if lp:
+        out["logprob"] = lp[0]
+    return out
 
 
 # ---- greedy verification without device allocation --------------------------------------------

@@ -22,7 +22,9 @@ DEBUG_LIBRARY = os.path.join(HERE, "libspecverify_debug.so")
 SOURCES = ["api.cu", "row_stats.cu", "tree_mask.cu", "walk_greedy.cu", "walk_sample_point.cu",
            "walk_sample_dense.cu", "walk_sample_logits_bf16.cu", "walk_sample_logits_f32.cu",
            "lazy_greedy.cu", "kv_commit.cu", "noalloc.cu", "budget.cu", "qk_rope.cu", "kv_fp4.cu",
-           "tree_attn.cu", "tree_attn_tc.cu"]
+           "tree_attn.cu", "tree_attn_tc.cu", "kv_append.cu", "kv_append_f16.cu",
+           "kv_append_f32.cu", "paged_attn.cu", "paged_few_bf16.cu", "paged_few_f16.cu",
+           "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr"]

@@ -912,6 +912,233 @@ int spec_tree_attention_fp4(spec_handle h, const void *q, int64_t q_stride, cons
     return timed(h, SPEC_K_TREE_ATTN, st, [&] { return launch_tree_attn(p, st); });
 }
 
+// ---- the paged step ---------------------------------------------------------------------------
+
+namespace {
+
+// The parts of a paged cache that the host can check, for rows of `dtype`; a batch of none needs
+// no block table.
+int check_paged(const spec_kv_cache *c, int dtype, int B) {
+    if (!c) return SPEC_ERR_ARG;
+    if (c->kind != SPEC_CACHE_SAME && c->kind != SPEC_CACHE_FP8_E4M3 &&
+        c->kind != SPEC_CACHE_FP8_E5M2)
+        return SPEC_ERR_ARG;
+    if (c->layout != SPEC_KV_NHD && c->layout != SPEC_KV_HND) return SPEC_ERR_ARG;
+    const int e = c->kind != SPEC_CACHE_SAME ? 1 : dtype == SPEC_F32 ? 4 : 2;
+    if (c->H < 1 || c->H > (1 << 16) || c->D < 1 || c->D > 1024 || c->D * e % 16 != 0)
+        return SPEC_ERR_ARG;
+    if (c->block_size < 1 || c->num_blocks < 1 || c->num_blocks > INT32_MAX || c->max_blocks < 1)
+        return SPEC_ERR_ARG;
+    if ((int64_t)c->max_blocks * c->block_size > INT32_MAX - 1024)    // tiles past the end count too
+        return SPEC_ERR_ARG;
+    const int64_t block = (int64_t)c->block_size * c->H;
+    if (block > INT32_MAX) return SPEC_ERR_ARG;
+    for (int64_t s : {c->k_block_stride, c->v_block_stride})
+        if (s < block * c->D || s > (int64_t(1) << 40) || s * e % 16 != 0) return SPEC_ERR_ARG;
+    if (!c->k || !c->v || (B > 0 && !c->block_table)) return SPEC_ERR_ARG;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !null_or_aligned(c->block_table, 4) ||
+        !null_or_aligned(c->k_scale, 4) || !null_or_aligned(c->v_scale, 4))
+        return SPEC_ERR_ARG;
+    return SPEC_OK;
+}
+
+// The rows of a batch: how many, and how they are dealt to the requests.
+bool batch_ok(spec_handle h, int B, int64_t T, const int32_t *row_start, const int32_t *seq_pos) {
+    if (B < 0 || B > h->max_B || T < 0 || T > INT32_MAX) return false;
+    if (B == 0) return true;
+    return seq_pos && aligned(seq_pos, 4) && null_or_aligned(row_start, 4) &&
+           (row_start || T % B == 0);
+}
+
+}  // namespace
+
+int spec_kv_append(spec_handle h, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                   const void *v, int64_t v_stride, int dtype, int B, int64_t T, int Hq,
+                   const int32_t *row_start, const int32_t *seq_pos, const spec_kv_cache *cache,
+                   const void *q_weight, const void *k_weight, float eps, const float *inv_freq,
+                   int rot, int style, void *q_out, int64_t q_out_stride, int32_t *status,
+                   void *stream) {
+    SPEC_RANGE("spec_kv_append");
+    if (!h || !float_type(dtype)) return SPEC_ERR_ARG;
+    const int rc = check_paged(cache, dtype, B);
+    if (rc != SPEC_OK) return rc;
+    const int H = cache->H, D = cache->D;
+    if (Hq < 0 || Hq > (1 << 20) || (Hq > 0) != (q != nullptr) || (Hq > 0) != (q_out != nullptr))
+        return SPEC_ERR_ARG;
+    if (rot < 0 || rot > D || rot % 2 != 0) return SPEC_ERR_ARG;
+    if (style != SPEC_ROPE_HALVES && style != SPEC_ROPE_PAIRS) return SPEC_ERR_ARG;
+    if (!std::isfinite(eps) || eps < 0.f) return SPEC_ERR_ARG;
+    if (Hq > 0 ? (q_weight == nullptr) != (k_weight == nullptr) : q_weight && !k_weight)
+        return SPEC_ERR_ARG;
+    if (!batch_ok(h, B, T, row_start, seq_pos)) return SPEC_ERR_ARG;
+    if (B == 0) return SPEC_OK;
+    const size_t e = dtype == SPEC_F32 ? 4 : 2;
+    if (!null_or_aligned(q_weight, e) || !null_or_aligned(k_weight, e) ||
+        !null_or_aligned(inv_freq, 4) || (rot > 0 && !inv_freq) || !null_or_aligned(status, 4))
+        return SPEC_ERR_ARG;
+    if (T > 0) {
+        if (!rows_ok(k, k_stride, H, D, dtype) || !rows_ok(v, v_stride, H, D, dtype))
+            return SPEC_ERR_ARG;
+        if (Hq > 0 && (!rows_ok(q, q_stride, Hq, D, dtype) ||
+                       !rows_ok(q_out, q_out_stride, Hq, D, dtype) ||
+                       (q_out == q && q_out_stride != q_stride)))
+            return SPEC_ERR_ARG;
+    }
+    DeviceScope ds(h->device);
+    if (!ds.ok()) return SPEC_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    KvAppendParams p = {};
+    p.cache = *cache;
+    p.x[0] = q;
+    p.x[1] = k;
+    p.x[2] = v;
+    p.stride[0] = Hq > 0 ? q_stride : 0;
+    p.stride[1] = k_stride;
+    p.stride[2] = v_stride;
+    p.q_out = q_out;
+    p.q_out_stride = Hq > 0 ? q_out_stride : 0;
+    p.w[0] = q_weight;
+    p.w[1] = k_weight;
+    p.dtype = dtype;
+    p.B = B;
+    p.Hq = Hq;
+    p.N = (int)(T / B);
+    p.T = T;
+    p.row_start = row_start;
+    p.seq_pos = seq_pos;
+    p.rot = rot;
+    p.pairs = style == SPEC_ROPE_PAIRS;
+    p.eps = eps;
+    p.inv_freq = inv_freq;
+    p.status = status;
+    p.sms = h->sms;
+    // a place found outside the cache raises the request's status from zero
+    if (status && cudaMemsetAsync(status, 0, sizeof(int32_t) * (size_t)B, st) != cudaSuccess)
+        return SPEC_ERR_CUDA;
+    return timed(h, SPEC_K_KV_APPEND, st, [&] { return launch_kv_append(p, st); });
+}
+
+namespace {
+
+// Sizes of a paged attention call; max_new becomes what it stands for.
+int check_paged_attention(spec_handle h, int B, int64_t T, int &max_new, int Hq, int H, int D) {
+    if (!h) return SPEC_ERR_ARG;
+    if (B < 0 || B > h->max_B || T < 0 || T > INT32_MAX || max_new < 0) return SPEC_ERR_ARG;
+    if (H < 1 || Hq < H || Hq % H != 0 || Hq > (1 << 16)) return SPEC_ERR_ARG;
+    if (D < 16 || D % 16 != 0 || D > 256) return SPEC_ERR_UNSUPPORTED;
+    if (max_new == 0 || max_new > T) max_new = (int)T;
+    return SPEC_OK;
+}
+
+}  // namespace
+
+int spec_paged_attention_workspace(spec_handle h, int B, int64_t T, int max_new, int Hq, int H,
+                                   int D, int64_t *bytes) {
+    SPEC_RANGE("spec_paged_attention_workspace");
+    const int rc = check_paged_attention(h, B, T, max_new, Hq, H, D);
+    if (rc != SPEC_OK) return rc;
+    if (!bytes) return SPEC_ERR_ARG;
+    *bytes = paged_attn_workspace(T, max_new, Hq / H, D, h->sms);
+    return SPEC_OK;
+}
+
+int spec_paged_attention(spec_handle h, const void *q, int64_t q_stride, int dtype, int B,
+                         int64_t T, int Hq, int max_new, const int32_t *row_start,
+                         const int32_t *seq_pos, const spec_kv_cache *cache, float scale,
+                         int window, int sinks, void *out, float *lse, int32_t *status,
+                         void *workspace, int64_t workspace_bytes, void *stream) {
+    SPEC_RANGE("spec_paged_attention");
+    if (!h || (dtype != SPEC_BF16 && dtype != SPEC_F16)) return SPEC_ERR_ARG;
+    int rc = check_paged(cache, dtype, B);
+    if (rc != SPEC_OK) return rc;
+    const int H = cache->H, D = cache->D;
+    rc = check_paged_attention(h, B, T, max_new, Hq, H, D);
+    if (rc != SPEC_OK) return rc;
+    if (!std::isfinite(scale) || !(scale > 0.f) || window < 0 || sinks < 0) return SPEC_ERR_ARG;
+    if (!batch_ok(h, B, T, row_start, seq_pos)) return SPEC_ERR_ARG;
+    if (B == 0) return SPEC_OK;
+    if (!null_or_aligned(lse, 4) || !null_or_aligned(status, 4)) return SPEC_ERR_ARG;
+    if (T > 0 && (!rows_ok(q, q_stride, Hq, D, dtype) || !out || !aligned(out, 2)))
+        return SPEC_ERR_ARG;
+    if (!workspace || !aligned(workspace, 256) ||
+        workspace_bytes < paged_attn_workspace(T, max_new, Hq / H, D, h->sms))
+        return SPEC_ERR_ARG;
+    DeviceScope ds(h->device);
+    if (!ds.ok()) return SPEC_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    PagedAttnParams p = {};
+    p.cache = *cache;
+    if (p.cache.kind == SPEC_CACHE_SAME) p.cache.k_scale = p.cache.v_scale = nullptr;
+    p.q = q;
+    p.q_stride = q_stride;
+    p.dtype = dtype;
+    p.B = B;
+    p.Hq = Hq;
+    p.G = Hq / H;
+    p.N = (int)(T / B);
+    p.T = T;
+    p.max_new = max_new;
+    p.row_start = row_start;
+    p.seq_pos = seq_pos;
+    p.scale = scale;
+    p.window = window;
+    p.sinks = window > 0 ? sinks : 0;
+    p.out = out;
+    p.lse = lse;
+    p.status = status;
+    p.workspace = workspace;
+    p.sms = h->sms;
+    p.lose = h->inject_lost;
+    h->inject_lost = 0;
+    if (status && cudaMemsetAsync(status, 0, sizeof(int32_t) * (size_t)B, st) != cudaSuccess)
+        return SPEC_ERR_CUDA;
+    return timed(h, SPEC_K_PAGED_ATTN, st, [&] { return launch_paged_attn(p, st); });
+}
+
+int spec_token_logprobs(spec_handle h, const void *logits, int dtype, int B, int64_t N, int64_t V,
+                        const int32_t *node, int P, const int32_t *tokens, int C,
+                        float temperature, float *logprob, float *entropy, int top,
+                        int32_t *top_ids, float *top_logprobs, int32_t *flags, void *stream) {
+    SPEC_RANGE("spec_token_logprobs");
+    if (!h) return SPEC_ERR_ARG;
+    if (B < 0 || B > h->max_B || N < 1 || N > INT32_MAX || V < 1 || V > h->max_V) return SPEC_ERR_ARG;
+    if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_ARG;
+    if (P < 0 || (!node && P != N) || (int64_t)B * P > INT32_MAX / 8) return SPEC_ERR_ARG;
+    if (C < 0 || C > 64 || top < 0 || top > 32) return SPEC_ERR_ARG;
+    if (!std::isfinite(temperature) || !(temperature > 0.f)) return SPEC_ERR_ARG;
+    const float k = kLog2eF / temperature, inv_t = 1.f / temperature;
+    if (!std::isfinite(k) || !(inv_t > 0.f)) return SPEC_ERR_ARG;
+    if (B == 0 || P == 0) return SPEC_OK;
+    if (!logits || (C > 0 && (!tokens || !logprob)) || (top > 0 && (!top_ids || !top_logprobs)))
+        return SPEC_ERR_ARG;
+    if (!aligned(logits, esize(dtype))) return SPEC_ERR_ARG;
+    const void *words[] = {node, tokens, logprob, entropy, top_ids, top_logprobs, flags};
+    for (const void *p : words)
+        if (!null_or_aligned(p, 4)) return SPEC_ERR_ARG;
+    DeviceScope ds(h->device);
+    if (!ds.ok()) return SPEC_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    LogprobsParams p = {};
+    p.logits = logits;
+    p.B = B;
+    p.P = P;
+    p.C = C;
+    p.top = top;
+    p.N = N;
+    p.V = V;
+    p.node = node;
+    p.tokens = tokens;
+    p.k = k;
+    p.inv_t = inv_t;
+    p.logprob = logprob;
+    p.entropy = entropy;
+    p.top_logprobs = top_logprobs;
+    p.top_ids = top_ids;
+    p.flags = flags;
+    p.sms = h->sms;
+    return timed(h, SPEC_K_LOGPROBS, st, [&] { return launch_logprobs(p, dtype, st); });
+}
+
 int spec_row_stats(spec_handle h, const void *logits, int dtype, int rows, int N, int64_t V,
                    float temperature, const int32_t *draft_token, const int32_t *parent,
                    float *row_max, float *row_sum, int32_t *row_argmax, int32_t *row_flags,

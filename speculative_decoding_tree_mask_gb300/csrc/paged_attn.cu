@@ -1,0 +1,157 @@
+// Paged attention: how a call is run, and the joining of items that were cut.
+#include "paged_attn.cuh"
+
+namespace specv {
+namespace {
+
+// The parts of cut items into the result. A thread has a float4 of a row and, of the parts,
+// every PG-th, eight of them in flight together; the PG threads of a float4 meet in shared
+// memory. PG is 1 for items of few parts and many rows.
+constexpr int kJoinThreads = 256;
+template <int T, int DP, int PG>
+__global__ void __launch_bounds__(kJoinThreads)
+    paged_join_kernel(PagedAttnParams P, int rows_tile) {
+    constexpr int F = DP / 4, kPer = kJoinThreads / (F * PG);       // rows of a CTA
+    __shared__ float4 s_o[PG > 1 ? kJoinThreads : 1];
+    __shared__ float2 s_ml[PG > 1 ? kJoinThreads : 1];
+    grid_dep_wait();
+    const int c0 = blockIdx.y;
+    const int4 note = P.notes[c0];
+    if (note.x < 0) return;
+    const int c1 = note.w;
+    PagedReq req;
+    paged_req(P, note.x, req);
+    const int64_t row0 = (int64_t)note.y * rows_tile, all = (int64_t)req.n * P.G;
+    const int rows = (int)min((int64_t)rows_tile, all - row0);
+    const int d4 = threadIdx.x % F, group = threadIdx.x / F % PG;
+    const int r = blockIdx.x * kPer + threadIdx.x / (F * PG);
+    if (PG == 1 && r >= rows) return;
+    float m = kPagedNoMax, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c0 + group; c <= c1 && r < rows; c += 8 * PG) {
+        float4 v[8];
+        float pm[8], pl[8], top = m;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            pm[u] = kPagedNoMax;
+            const int k = c + u * PG;
+            if (k > c1) continue;
+            const float *part = paged_slot(P, k, k == c0, rows_tile, DP);
+            v[u] = __ldcg(reinterpret_cast<const float4 *>(part + r * DP) + d4);
+            pm[u] = __ldcg(part + rows_tile * DP + r);
+            pl[u] = __ldcg(part + rows_tile * (DP + 1) + r);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) top = fmaxf(top, pm[u]);
+        const float a = ex2(m - top);
+        m = top;
+        l *= a;
+        o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (c + u * PG > c1) continue;
+            const float w = ex2(pm[u] - top);
+            o.x = fmaf(v[u].x, w, o.x);
+            o.y = fmaf(v[u].y, w, o.y);
+            o.z = fmaf(v[u].z, w, o.z);
+            o.w = fmaf(v[u].w, w, o.w);
+            l = fmaf(pl[u], w, l);
+        }
+    }
+    if (PG > 1) {
+        s_o[threadIdx.x] = o;
+        s_ml[threadIdx.x] = make_float2(m, l);
+        __syncthreads();
+        if (group != 0 || r >= rows) return;
+        float top = m;
+#pragma unroll
+        for (int u = 1; u < PG; ++u) top = fmaxf(top, s_ml[threadIdx.x + u * F].x);
+        const float a = ex2(m - top);
+        o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
+        l *= a;
+        m = top;
+#pragma unroll
+        for (int u = 1; u < PG; ++u) {
+            const float2 ml = s_ml[threadIdx.x + u * F];
+            const float4 v = s_o[threadIdx.x + u * F];
+            const float w = ex2(ml.x - top);
+            o.x = fmaf(v.x, w, o.x);
+            o.y = fmaf(v.y, w, o.y);
+            o.z = fmaf(v.z, w, o.z);
+            o.w = fmaf(v.w, w, o.w);
+            l = fmaf(ml.y, w, l);
+        }
+    }
+    const float f = l == 0.f ? 0.f : 1.f / l;
+    const int64_t at = paged_row(P, req, note.z, row0 + r);
+    if (d4 * 4 < P.cache.D)
+        paged_store4<T>(P.out, at * P.cache.D + d4 * 4,
+                        make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
+    if (P.lse && d4 == 0) P.lse[at] = paged_lse(m, l);
+}
+
+// How a call is run.
+struct Plan {
+    int mt, rows, grid;     // groups of 16 rows of an item; rows; CTAs
+};
+Plan plan(int64_t T, int max_new, int G, int D, int kind, int sms) {
+    (void)T;
+    Plan p;
+    const int DP = paged_padded(D);
+    p.mt = (int64_t)max_new * G > 16 && DP <= 128 ? 2 : 1;
+    p.rows = 16 * p.mt;
+    p.grid = sms * paged_few_ctas(kind != SPEC_CACHE_SAME, DP);
+    return p;
+}
+
+template <int T, int DP>
+cudaError_t launch_join(const PagedAttnParams &p, const Plan &n, cudaStream_t st) {
+    constexpr int F = DP / 4, PG = DP == 256 ? 4 : 8;
+    const int64_t R = (int64_t)p.max_new * p.G;
+    const int rows = (int)(R < n.rows ? R : n.rows), per = kJoinThreads / F;
+    const int64_t items = (int64_t)p.B * p.cache.H;
+    if (n.grid > 8 * items && rows <= 32)
+        return launch_dependent(paged_join_kernel<T, DP, PG>,
+                                dim3((rows * PG + per - 1) / per, n.grid), dim3(kJoinThreads), 0, st,
+                                p, n.rows);
+    return launch_dependent(paged_join_kernel<T, DP, 1>, dim3((rows + per - 1) / per, n.grid),
+                            dim3(kJoinThreads), 0, st, p, n.rows);
+}
+
+int64_t notes_bytes(const Plan &n) { return ((int64_t)n.grid * sizeof(int4) + 255) / 256 * 256; }
+int64_t plan_bytes(const Plan &n, int D) {
+    const int64_t bytes = (int64_t)n.grid * 2 * n.rows * (paged_padded(D) + 2) * (int64_t)sizeof(float);
+    return notes_bytes(n) + (bytes + 255) / 256 * 256;
+}
+
+}  // namespace
+
+int64_t paged_attn_workspace(int64_t T, int max_new, int G, int D, int sms) {
+    int64_t most = 256;       // whatever the cache's type
+    for (int kind = 0; kind < 2; ++kind) {
+        const int64_t b = plan_bytes(plan(T, max_new, G, D, kind, sms), D);
+        most = b > most ? b : most;
+    }
+    return most;
+}
+
+cudaError_t launch_paged_attn(const PagedAttnParams &given, cudaStream_t st) {
+    if (given.B <= 0) return cudaSuccess;
+    PagedAttnParams p = given;
+    const int DP = paged_padded(p.cache.D);
+    const Plan n = plan(p.T, p.max_new, p.G, p.cache.D, p.cache.kind, p.sms);
+    p.notes = static_cast<int4 *>(p.workspace);
+    p.ws = reinterpret_cast<float *>(static_cast<char *>(p.workspace) + notes_bytes(n));
+    const cudaError_t e = p.dtype == 1 ? launch_paged_few_bf16(p, n.mt, n.grid, st)
+                                       : launch_paged_few_f16(p, n.mt, n.grid, st);
+    if (e != cudaSuccess) return e;
+    if (p.dtype == 1)
+        return DP == 64    ? launch_join<1, 64>(p, n, st)
+               : DP == 128 ? launch_join<1, 128>(p, n, st)
+                           : launch_join<1, 256>(p, n, st);
+    return DP == 64    ? launch_join<2, 64>(p, n, st)
+           : DP == 128 ? launch_join<2, 128>(p, n, st)
+                       : launch_join<2, 256>(p, n, st);
+}
+
+}  // namespace specv

@@ -257,6 +257,67 @@ struct QkRopeParams {
 
 cudaError_t launch_qk_rope(const QkRopeParams &p, cudaStream_t st);
 
+// New tokens into the paged cache (see spec_kv_append).
+struct KvAppendParams {
+    spec_kv_cache cache;
+    const void *x[3];             // q, k, v rows
+    int64_t stride[3];            // elements between rows
+    void *q_out;
+    int64_t q_out_stride;
+    const void *w[2];             // norm weights of q and k, or null
+    int dtype;                    // of the rows: 0 f32, 1 bf16, 2 f16
+    int B, Hq, N;                 // N: rows of each request, without row_start
+    int64_t T;
+    const int32_t *row_start, *seq_pos;
+    int rot, pairs;
+    float eps;
+    const float *inv_freq;
+    int32_t *status;
+    int sms;
+};
+
+cudaError_t launch_kv_append(const KvAppendParams &p, cudaStream_t st);
+
+// Scores of tokens (see spec_token_logprobs).
+struct LogprobsParams {
+    const void *logits;
+    int B, P, C, top;
+    int64_t N, V;
+    const int32_t *node, *tokens;
+    float k, inv_t;               // log2(e) / temperature, 1 / temperature
+    float *logprob, *entropy, *top_logprobs;
+    int32_t *top_ids, *flags;
+    int sms;
+};
+
+cudaError_t launch_logprobs(const LogprobsParams &p, int dtype, cudaStream_t st);
+
+// Attention of new tokens over the paged cache (see spec_paged_attention).
+struct PagedAttnParams {
+    spec_kv_cache cache;
+    const void *q;
+    int64_t q_stride;
+    int dtype;                    // 1 bf16, 2 f16
+    int B, Hq, G, N;              // G = Hq / cache.H; N: rows of each request, without row_start
+    int64_t T;
+    int max_new;                  // most rows of a request
+    const int32_t *row_start, *seq_pos;
+    float scale;
+    int window, sinks;            // window 0: none
+    void *out;
+    float *lse;
+    int32_t *status;
+    void *workspace;
+    int4 *notes;                  // in the workspace: cut items [CTAs] (see paged_attn.cuh)
+    float *ws;                    // ... and their parts
+    int lose;                     // debug builds: every wait of the tcgen05 kernel gives up at once
+    int sms;
+};
+
+// Bytes of notes and parts that a launch may write.
+int64_t paged_attn_workspace(int64_t T, int max_new, int G, int D, int sms);
+cudaError_t launch_paged_attn(const PagedAttnParams &p, cudaStream_t st);
+
 // Division of n < 2^31 by a number known on the host: a multiplication and a shift (the round-up
 // method of Granlund and Montgomery, "Division by invariant integers using multiplication").
 struct FastDiv {
