@@ -24,7 +24,7 @@ SOURCES = ["api.cu", "row_stats.cu", "tree_mask.cu", "walk_greedy.cu", "walk_sam
            "lazy_greedy.cu", "kv_commit.cu", "noalloc.cu", "budget.cu", "qk_rope.cu", "kv_fp4.cu",
            "tree_attn.cu", "tree_attn_tc.cu", "kv_append.cu", "kv_append_f16.cu",
            "kv_append_f32.cu", "paged_attn.cu", "paged_few_bf16.cu", "paged_few_f16.cu",
-           "logprobs.cu"]
+           "paged_tc_bf16.cu", "paged_tc_f16.cu", "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr"]

@@ -932,7 +932,8 @@ int check_paged(const spec_kv_cache *c, int dtype, int B) {
     if ((int64_t)c->max_blocks * c->block_size > INT32_MAX - 1024)    // tiles past the end count too
         return SPEC_ERR_ARG;
     const int64_t block = (int64_t)c->block_size * c->H;
-    if (block > INT32_MAX) return SPEC_ERR_ARG;
+    // the kernels count a block's 16-byte units in 32 bits
+    if (block > INT32_MAX || block * c->D * e / 16 > INT32_MAX) return SPEC_ERR_ARG;
     for (int64_t s : {c->k_block_stride, c->v_block_stride})
         if (s < block * c->D || s > (int64_t(1) << 40) || s * e % 16 != 0) return SPEC_ERR_ARG;
     if (!c->k || !c->v || (B > 0 && !c->block_table)) return SPEC_ERR_ARG;
@@ -1038,7 +1039,7 @@ int spec_paged_attention_workspace(spec_handle h, int B, int64_t T, int max_new,
     const int rc = check_paged_attention(h, B, T, max_new, Hq, H, D);
     if (rc != SPEC_OK) return rc;
     if (!bytes) return SPEC_ERR_ARG;
-    *bytes = paged_attn_workspace(T, max_new, Hq / H, D, h->sms);
+    *bytes = paged_attn_workspace(max_new, Hq / H, D, h->sms);
     return SPEC_OK;
 }
 
@@ -1061,7 +1062,7 @@ int spec_paged_attention(spec_handle h, const void *q, int64_t q_stride, int dty
     if (T > 0 && (!rows_ok(q, q_stride, Hq, D, dtype) || !out || !aligned(out, 2)))
         return SPEC_ERR_ARG;
     if (!workspace || !aligned(workspace, 256) ||
-        workspace_bytes < paged_attn_workspace(T, max_new, Hq / H, D, h->sms))
+        workspace_bytes < paged_attn_workspace(max_new, Hq / H, D, h->sms))
         return SPEC_ERR_ARG;
     DeviceScope ds(h->device);
     if (!ds.ok()) return SPEC_ERR_CUDA;

@@ -90,17 +90,18 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (P.lse && d4 == 0) P.lse[at] = paged_lse(m, l);
 }
 
-// How a call is run.
+// How a call is run: by the warps' matrix unit up to 32 rows an item, beyond on the tcgen05 tensor
+// cores, which have no form for D above 128 (Q, K and V tiles do not fit in shared memory together).
 struct Plan {
-    int mt, rows, grid;     // groups of 16 rows of an item; rows; CTAs
+    int mt, rows, grid;     // groups of 16 rows of an item, 0: tcgen05; rows; CTAs
 };
-Plan plan(int64_t T, int max_new, int G, int D, int kind, int sms) {
-    (void)T;
+Plan plan(int max_new, int G, int D, int kind, int sms) {
     Plan p;
     const int DP = paged_padded(D);
-    p.mt = (int64_t)max_new * G > 16 && DP <= 128 ? 2 : 1;
-    p.rows = 16 * p.mt;
-    p.grid = sms * paged_few_ctas(kind != SPEC_CACHE_SAME, DP);
+    const int64_t R = (int64_t)max_new * G;
+    p.mt = DP == 256 ? 1 : R > 32 ? 0 : R > 16 ? 2 : 1;
+    p.rows = p.mt ? 16 * p.mt : kPagedTcRows;
+    p.grid = sms * (p.mt ? paged_few_ctas(kind != SPEC_CACHE_SAME, DP) : 1);
     return p;
 }
 
@@ -126,10 +127,10 @@ int64_t plan_bytes(const Plan &n, int D) {
 
 }  // namespace
 
-int64_t paged_attn_workspace(int64_t T, int max_new, int G, int D, int sms) {
+int64_t paged_attn_workspace(int max_new, int G, int D, int sms) {
     int64_t most = 256;       // whatever the cache's type
     for (int kind = 0; kind < 2; ++kind) {
-        const int64_t b = plan_bytes(plan(T, max_new, G, D, kind, sms), D);
+        const int64_t b = plan_bytes(plan(max_new, G, D, kind, sms), D);
         most = b > most ? b : most;
     }
     return most;
@@ -139,11 +140,14 @@ cudaError_t launch_paged_attn(const PagedAttnParams &given, cudaStream_t st) {
     if (given.B <= 0) return cudaSuccess;
     PagedAttnParams p = given;
     const int DP = paged_padded(p.cache.D);
-    const Plan n = plan(p.T, p.max_new, p.G, p.cache.D, p.cache.kind, p.sms);
+    const Plan n = plan(p.max_new, p.G, p.cache.D, p.cache.kind, p.sms);
     p.notes = static_cast<int4 *>(p.workspace);
     p.ws = reinterpret_cast<float *>(static_cast<char *>(p.workspace) + notes_bytes(n));
-    const cudaError_t e = p.dtype == 1 ? launch_paged_few_bf16(p, n.mt, n.grid, st)
-                                       : launch_paged_few_f16(p, n.mt, n.grid, st);
+    const bool bf16 = p.dtype == SPEC_BF16;
+    const cudaError_t e = n.mt == 0 ? bf16 ? launch_paged_tc_bf16(p, n.grid, st)
+                                           : launch_paged_tc_f16(p, n.grid, st)
+                          : bf16 ? launch_paged_few_bf16(p, n.mt, n.grid, st)
+                                 : launch_paged_few_f16(p, n.mt, n.grid, st);
     if (e != cudaSuccess) return e;
     if (p.dtype == 1)
         return DP == 64    ? launch_join<1, 64>(p, n, st)

@@ -316,6 +316,49 @@ __device__ __forceinline__ unsigned paged_bits(int j0, int p, int hi, int window
     return seen;
 }
 
+// A 16-byte copy to shared memory; zeros when !ok.
+__device__ __forceinline__ void copy16(uint32_t smem, const void *gmem, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem),
+                 "r"(ok ? 16 : 0)
+                 : "memory");
+}
+
+template <int I>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (I == 1) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+template <int I>
+__device__ __forceinline__ float value16(uint32_t x) {
+    return I == 1 ? __uint_as_float(x << 16) : __half2float(__ushort_as_half((unsigned short)x));
+}
+// Two 8-bit codes (the low 16 bits) as halves, exactly.
+template <int KIND>
+__device__ __forceinline__ uint32_t halves2(uint32_t two) {
+    if constexpr (KIND == 1) {
+        uint32_t r;
+        asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
+            : "=r"(r)
+            : "r"(two));
+        return r;
+    } else {       // e5m2 is a half's upper byte
+        return __byte_perm(two, 0u, 0x1404);
+    }
+}
+// Whether one of the elements in a word is NaN or infinite.
+template <int I, int KIND>
+__device__ __forceinline__ bool odd_word(uint32_t w) {
+    if constexpr (KIND == 1) return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+    if constexpr (KIND == 2) return __vcmpeq4(w & 0x7c7c7c7cu, 0x7c7c7c7cu) != 0;
+    constexpr uint32_t ex = I == 1 ? 0x7f807f80u : 0x7c007c00u;
+    return __vcmpeq2(w & ex, ex) != 0;
+}
+
 // D up to the next size that the kernels are built for.
 inline int paged_padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
@@ -327,8 +370,9 @@ constexpr int paged_few_ctas(bool fp8, int DP) {
 cudaError_t launch_paged_few_bf16(const PagedAttnParams &p, int mt, int grid, cudaStream_t st);
 cudaError_t launch_paged_few_f16(const PagedAttnParams &p, int mt, int grid, cudaStream_t st);
 
-// Launches on the tcgen05 tensor cores (paged_attn_tc.cu).
-int paged_attn_tc_rows();
-cudaError_t launch_paged_attn_tc(const PagedAttnParams &p, int grid, cudaStream_t st);
+// Launches on the tcgen05 tensor cores (paged_tc.cuh).
+constexpr int kPagedTcRows = 256;   // of an item
+cudaError_t launch_paged_tc_bf16(const PagedAttnParams &p, int grid, cudaStream_t st);
+cudaError_t launch_paged_tc_f16(const PagedAttnParams &p, int grid, cudaStream_t st);
 
 }  // namespace specv

@@ -315,7 +315,7 @@ struct PagedAttnParams {
 };
 
 // Bytes of notes and parts that a launch may write.
-int64_t paged_attn_workspace(int64_t T, int max_new, int G, int D, int sms);
+int64_t paged_attn_workspace(int max_new, int G, int D, int sms);
 cudaError_t launch_paged_attn(const PagedAttnParams &p, cudaStream_t st);
 
 // Division of n < 2^31 by a number known on the host: a multiplication and a shift (the round-up
