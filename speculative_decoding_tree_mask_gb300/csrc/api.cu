@@ -1027,6 +1027,7 @@ int check_paged_attention(spec_handle h, int B, int64_t T, int &max_new, int Hq,
     if (B < 0 || B > h->max_B || T < 0 || T > INT32_MAX || max_new < 0) return SPEC_ERR_ARG;
     if (H < 1 || Hq < H || Hq % H != 0 || Hq > (1 << 16)) return SPEC_ERR_ARG;
     if (D < 16 || D % 16 != 0 || D > 256) return SPEC_ERR_UNSUPPORTED;
+    if (T * (Hq / H) > INT32_MAX - 1024) return SPEC_ERR_UNSUPPORTED;   // rows of a head, in 32 bits
     if (max_new == 0 || max_new > T) max_new = (int)T;
     return SPEC_OK;
 }
@@ -1089,6 +1090,8 @@ int spec_paged_attention(spec_handle h, const void *q, int64_t q_stride, int dty
     p.status = status;
     p.workspace = workspace;
     p.sms = h->sms;
+    p.by_page = FastDiv((uint32_t)cache->block_size);
+    p.by_group = FastDiv((uint32_t)p.G);
     p.lose = h->inject_lost;
     h->inject_lost = 0;
     if (status && cudaMemsetAsync(status, 0, sizeof(int32_t) * (size_t)B, st) != cudaSuccess)

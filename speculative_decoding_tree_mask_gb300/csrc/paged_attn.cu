@@ -21,8 +21,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     const int c1 = note.w;
     PagedReq req;
     paged_req(P, note.x, req);
-    const int64_t row0 = (int64_t)note.y * rows_tile, all = (int64_t)req.n * P.G;
-    const int rows = (int)min((int64_t)rows_tile, all - row0);
+    const int row0 = note.y * rows_tile, rows = min(rows_tile, req.n * P.G - row0);
     const int d4 = threadIdx.x % F, group = threadIdx.x / F % PG;
     const int r = blockIdx.x * kPer + threadIdx.x / (F * PG);
     if (PG == 1 && r >= rows) return;
@@ -83,7 +82,7 @@ __global__ void __launch_bounds__(kJoinThreads)
         }
     }
     const float f = l == 0.f ? 0.f : 1.f / l;
-    const int64_t at = paged_row(P, req, note.z, row0 + r);
+    const int64_t at = paged_row(P, req.first, note.z, row0 + r);
     if (d4 * 4 < P.cache.D)
         paged_store4<T>(P.out, at * P.cache.D + d4 * 4,
                         make_float4(o.x * f, o.y * f, o.z * f, o.w * f));

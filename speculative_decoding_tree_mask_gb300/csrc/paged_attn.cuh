@@ -101,12 +101,11 @@ template <int RT>
 struct PagedWalk {
     PagedRange range;
     int64_t at;                     // where the item at hand begins
-    int b, head, fixed;
-    int64_t r;                      // row tile at hand
+    int b, r, head, fixed;          // request, row tile, K/V head at hand
     PagedReq req;
 
-    __device__ __forceinline__ int64_t tiles(const PagedAttnParams &P, const PagedReq &q) const {
-        return ((int64_t)q.n * P.G + RT - 1) / RT;
+    __device__ __forceinline__ int tiles(const PagedAttnParams &P, const PagedReq &q) const {
+        return (q.n * P.G + RT - 1) / RT;           // fits: checked on the host
     }
 
     // `least`: the least weight that is a CTA's.
@@ -153,9 +152,9 @@ struct PagedWalk {
             paged_req(P, i, req);
             const PagedWeights<RT> W(P, req.pos, fixed);
             // the last row tile that begins at or before `left`
-            int64_t lo = 0, hi = tiles(P, req) - 1;
+            int lo = 0, hi = tiles(P, req) - 1;
             while (lo < hi) {
-                const int64_t mid = (lo + hi + 1) / 2;
+                const int mid = lo + (hi - lo + 1) / 2;
                 if (W.before(mid) * P.cache.H <= left) lo = mid;
                 else hi = mid - 1;
             }
@@ -185,16 +184,17 @@ struct PagedWalk {
         }
         const int64_t w = PagedWeights<RT>(P, req.pos, fixed).of(r);
         p.b = b;
-        p.r = (int)r;
+        p.r = r;
         p.head = head;
         p.req = req;
         p.at = at;
         p.w = w;
-        const int64_t row0 = r * RT, all = (int64_t)req.n * P.G;
-        p.rows = (int)min((int64_t)RT, all - row0);
+        const int row0 = r * RT;
+        p.rows = min(RT, req.n * P.G - row0);
         // positions in 64 bits first: seq_pos may be anything
         const int64_t most = (int64_t)P.cache.max_blocks * P.cache.block_size;
-        const int64_t p0 = req.pos + row0 / P.G, p1 = req.pos + (row0 + p.rows - 1) / P.G;
+        const int64_t p0 = (int64_t)req.pos + P.by_group((uint32_t)row0),
+                      p1 = (int64_t)req.pos + P.by_group((uint32_t)(row0 + p.rows - 1));
         p.p0 = (int)min(max(p0, (int64_t)-1), most);
         p.p1 = (int)min(max(p1, (int64_t)-1), most);
         const int64_t hi = min(p1 + 1, most);
@@ -229,13 +229,9 @@ __device__ __forceinline__ void paged_status(const PagedAttnParams &P, int threa
     }
 }
 
-// Position p of a request in the cache: its block (-1: none) and 16-byte unit in the block.
-struct PagedSlot {
-    int block, unit;
-};
-__device__ __forceinline__ int paged_page(const PagedAttnParams &P, const FastDiv &by_page, int b,
-                                          int p) {
-    return __ldg(P.cache.block_table + (int64_t)b * P.cache.max_blocks + by_page((uint32_t)p));
+// The block that the table has for position p of request b.
+__device__ __forceinline__ int paged_page(const PagedAttnParams &P, int b, int p) {
+    return __ldg(P.cache.block_table + (int64_t)b * P.cache.max_blocks + P.by_page((uint32_t)p));
 }
 
 // Where CTA `cta` leaves a part of an item: slot 0 if it came into the item from the middle,
@@ -255,11 +251,22 @@ __device__ __forceinline__ void paged_note(const PagedAttnParams &P, const Paged
     P.notes[blockIdx.x] = note;
 }
 
-// Row (token, query head) of row i of a row tile that begins at row0, as an index of lse.
-__device__ __forceinline__ int64_t paged_row(const PagedAttnParams &P, const PagedReq &q, int head,
-                                             int64_t i) {
-    const int64_t t = i / P.G;
-    return (q.first + t) * P.Hq + (int64_t)head * P.G + (i - t * P.G);
+// Row i of a request (whose first is `first` of the batch) and K/V head as an index of lse [T, Hq].
+__device__ __forceinline__ int64_t paged_row(const PagedAttnParams &P, int first, int head, int i) {
+    const int t = (int)P.by_group((uint32_t)i);
+    return (int64_t)(first + t) * P.Hq + head * P.G + (i - t * P.G);
+}
+// Where it begins among the queries.
+__device__ __forceinline__ const unsigned short *paged_query(const PagedAttnParams &P, int first,
+                                                             int head, int i) {
+    const int t = (int)P.by_group((uint32_t)i);
+    return static_cast<const unsigned short *>(P.q) + (first + t) * P.q_stride +
+           (int64_t)(head * P.G + (i - t * P.G)) * P.cache.D;
+}
+// The position of its token in a request that begins at pos, within -1 and the table's end.
+__device__ __forceinline__ int paged_position(const PagedAttnParams &P, int pos, int i) {
+    const int64_t p = (int64_t)pos + P.by_group((uint32_t)i);
+    return (int)min(max(p, (int64_t)-1), (int64_t)P.cache.max_blocks * P.cache.block_size);
 }
 
 // Four values of an output row.

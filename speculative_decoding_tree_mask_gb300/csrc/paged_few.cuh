@@ -96,7 +96,7 @@ __device__ __forceinline__ uint4 ldmatrix_t(uint32_t at) {
 // and 256; MT: groups of 16 query rows of an item.
 template <int T, int KIND, int DP, int MT>
 __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
-    paged_few_kernel(PagedAttnParams P, FastDiv by_page) {
+    paged_few_kernel(PagedAttnParams P) {
     using S = Few<KIND, DP, MT>;
     constexpr int I = KIND ? 2 : T;                 // the operands' type
     constexpr int RT = S::kRows, KS = DP / 16, NT = DP / 8, kStages = S::kStages;
@@ -113,7 +113,6 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
     const float v_scale = C.v_scale ? __ldg(C.v_scale) : 1.f;
     const float unit = P.scale * kLog2e * (C.k_scale ? __ldg(C.k_scale) : 1.f);
     const int units = C.D * S::kEsz / 16;           // of a position in the cache
-    const int64_t most = (int64_t)C.max_blocks * C.block_size;
 
     paged_status(P, kThreads);
     // a tile of positions is the least work worth a CTA
@@ -128,14 +127,14 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
         auto page = [&](int s) -> int {
             const int p = s < steps ? first(s) + (lane & 15) : A.hi;
             if (p >= A.hi || (p < A.lo && p >= P.sinks)) return -1;
-            const int block = paged_page(P, by_page, A.b, p);
+            const int block = paged_page(P, A.b, p);
             return block >= 0 && block < C.num_blocks ? block : -2;
         };
         // Starts the copies of step s into its place.
         auto issue = [&](int s, int block) {
             if (s < steps) {
                 const int p = first(s) + (lane & 15);
-                const uint32_t off = p - by_page((uint32_t)p) * C.block_size;
+                const uint32_t off = p - P.by_page((uint32_t)p) * C.block_size;
                 const uint32_t in = (C.layout == SPEC_KV_NHD ? off * C.H + A.head
                                                              : A.head * C.block_size + off) * units;
                 if (block == -2 && P.status) atomicMax(P.status + A.b, SPEC_REQ_BAD_SLOT);
@@ -166,14 +165,11 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
         }
 
         // Q in the order of the products' operands, a 16-byte word of a lane for each step.
-        const int64_t row0 = (int64_t)A.r * RT;
+        const int row0 = A.r * RT;
         for (int r = warp; r < RT; r += kWarps) {
             constexpr int E = DP / 64;                   // pairs of elements of a lane
             const bool live = r < A.rows;
-            const int64_t i = row0 + (live ? r : 0), t = i / P.G;
-            const unsigned short *q = reinterpret_cast<const unsigned short *>(P.q) +
-                                      (A.req.first + t) * P.q_stride +
-                                      ((int64_t)A.head * P.G + (i - t * P.G)) * C.D;
+            const unsigned short *q = paged_query(P, A.req.first, A.head, row0 + (live ? r : 0));
             float x[E][2], big = 0.f, down = 1.f, up = 1.f;
             uint32_t raw[E];
 #pragma unroll
@@ -229,8 +225,7 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
                 fac[i][e] = s_fac[r];
                 m[i][e] = kPagedNoMax;
                 l[i][e] = 0.f;
-                at[i][e] = r < A.rows
-                               ? (int)min(max(A.req.pos + (row0 + r) / P.G, (int64_t)-1), most) : -1;
+                at[i][e] = r < A.rows ? paged_position(P, A.req.pos, row0 + r) : -1;
             }
 #pragma unroll
         for (int i = 0; i < MT; ++i)
@@ -512,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
             for (int w = 0; w < kWarps; ++w) sum += s_l[w * RT + r] * exp2f(s_m[w * RT + r] - top);
             if (whole) {
                 const float n1 = sum == 0.f ? 0.f : 1.f / sum;
-                const int64_t to = paged_row(P, A.req, A.head, row0 + r);
+                const int64_t to = paged_row(P, A.req.first, A.head, row0 + r);
                 paged_store4<T>(P.out, to * C.D + d4 * 4,
                                 make_float4(v.x * n1, v.y * n1, v.z * n1, v.w * n1));
                 if (P.lse && d4 == 0) P.lse[to] = paged_lse(top, sum);
@@ -536,8 +531,7 @@ cudaError_t launch(const PagedAttnParams &p, int grid, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(paged_few_kernel<T, KIND, DP, MT>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    paged_few_kernel<T, KIND, DP, MT><<<grid, kThreads, smem, st>>>(
-        p, FastDiv((uint32_t)p.cache.block_size));
+    paged_few_kernel<T, KIND, DP, MT><<<grid, kThreads, smem, st>>>(p);
     return cudaGetLastError();
 }
 template <int T, int KIND>

@@ -5,21 +5,27 @@
 // operations a row and position. One CTA an SM; its warps have one part each and meet at mbarriers
 // only:
 //
-//   load     (4 warps for K, 4 for V) tiles of 128 positions by asynchronous copies to a ring of
-//            five places that K and V share, laid out for the tensor core (128-byte swizzle; K
-//            contiguous along D, and V as it is, read transposed). Any page size, stride and layout
-//            is a matter of their addresses. 8-bit codes pass through registers and become halves;
-//   queries  (2 warps) an item's rows, when the last products of the item before are done;
+//   load     (4 warps for K, 4 for V) tiles of 128 positions to a ring of five places that K and V
+//            share, laid out for the tensor core (128-byte swizzle; K contiguous along D, and V as it
+//            is, read transposed): by TMA, a box of a page's rows at a time, where the warp's 32
+//            positions are all wanted, else by asynchronous copies, whose addresses take any page
+//            size. 8-bit codes pass through registers and become halves. An item's queries come
+//            after its first tile, as soon as the scores of the item before are done;
 //   multiply (2 warps, a thread of each issues for one softmax group) S = Q K^T for 128 rows and a
-//            whole tile, then O += P V in two halves of 64 positions, the first of which runs while
-//            softmax works on the second half. Sums are in tensor memory: S and O twice, all 512
-//            columns at D = 128; P overwrites the S it came from;
+//            whole tile, then O += P V. Sums are in tensor memory: S and O twice, all 512 columns at
+//            D = 128; P overwrites the S it came from;
 //   softmax  (2 groups of 4 warps) S to P, a row a thread, no exchange between threads, reference
-//            and sum in registers. O is rescaled in place when a reference rises, which is rare.
+//            and sum in registers. The row's largest score is not looked for: a tile's sum tells
+//            when one has passed the reference by too much. Then, which is rare, and for an item's
+//            first tile, the scores are read again, the reference raised and O rescaled in place;
+//   deal     (1 warp) the CTA's parts, one after another, as words in shared memory: up to four
+//            ahead, so that the others neither compute them nor hold them in registers.
 //
 // With S of 64 columns a product reads 6 KB of shared memory for 32 clocks of work and gets 48 clocks
 // of its bandwidth; with 128 columns 8 KB for 64 clocks, which is even. One group's softmax runs
-// beside the other's products.
+// beside the other's products. What is left is issue slots: a tile's products take 2048 clocks, and
+// a form with the rows' maxima, copies by address and the dealing in every warp issued 2470
+// instructions a scheduler meanwhile.
 //
 // Items of up to 128 rows (a decoding request in a mixed batch) leave the second group idle, and
 // warps without a live row touch nothing: a tile then takes less time than its bytes do.
@@ -30,6 +36,10 @@
 // see them.
 #pragma once
 
+#include <climits>
+
+#include <cuda.h>
+
 #include "paged_attn.cuh"
 #include "tc_device.cuh"
 
@@ -38,9 +48,8 @@ namespace {
 
 constexpr int kLoad = 256;        // loading threads: K's, then V's
 constexpr int kSoftmax = 256;     // threads of the two softmax groups
-constexpr int kThreads = kSoftmax + kLoad + 128;   // the last: two warps multiply, two fetch queries
+constexpr int kThreads = kSoftmax + kLoad + 128;   // the last warpgroup: two warps multiply
 constexpr int kMmaWarp = (kSoftmax + kLoad) / 32;
-constexpr int kQuery = 64;        // threads that fetch queries
 constexpr int kRing = 5;
 // What an item costs besides its keys, in positions.
 constexpr int kTcFixed = 256;
@@ -55,13 +64,26 @@ struct Tc {
     static constexpr int kColumns = 512;                         // 2 (128 + DP), a power of two
 };
 
+// A part as the warps read it (see PagedPart); b -1: there are no more.
+struct PartWords {
+    int b, r, head, first, pos, rows, p0, p1, lo, hi, skip, base, tile, stop, begins, ends;
+
+    __device__ __forceinline__ int position(int i) const {
+        return (i < skip ? i : base + i) * kPosTile;
+    }
+};
+constexpr int kDealt = 4;
+constexpr int kReaders = 18;      // warps that read a part: softmax, load, multiply
+
 struct Words {
+    PartWords part[kDealt];
+    uint64_t part_full[kDealt], part_free[kDealt];
     uint64_t q_full, q_free, full[kRing], free[kRing], drain[2];
-    uint64_t s_full[2], p_full[2][2], o_full[2];                 // of a softmax group; halves
+    uint64_t s_full[2], p_full[2];                               // of a softmax group
     uint64_t o_last[2];                                          // once a part
     // Positions of a tile that are there. K's loader writes a tile's words again for the fourth
     // after it, whose place was that of a V whose products are done.
-    unsigned seen[4][4];
+    alignas(16) unsigned seen[4][4];
     // A part's V has NaN or infinities that not every row sees. Of eight parts: V's loader clears
     // the word of the fourth part to come, where its own other warps are three tiles ahead at most
     // and softmax three behind.
@@ -79,9 +101,13 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int j) {
     return (uint32_t)(j >> 3) * (128 * 128) + r * 128 + (((j & 7) ^ (r & 7)) << 4);
 }
 
-// A wait of a whole warp: all of it goes on or none.
+// A wait of a whole warp: all of it goes on or none. And an arrival for what all its lanes have done.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *gave_up) {
     return __all_sync(0xffffffffu, bar_wait(bar, parity, gave_up));
+}
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) bar_arrive(bar);
 }
 
 // 32 bytes to a 32-byte boundary.
@@ -91,86 +117,67 @@ __device__ __forceinline__ void store32(void *to, const uint32_t (&w)[8]) {
                  : "memory");
 }
 
-// Whether every row of the item sees all of positions j0 .. j0 + n - 1, as far as they are there.
-__device__ __forceinline__ bool all_see(const PagedAttnParams &P, const PagedPart &A, int j0, int n) {
-    return j0 + n - 1 <= A.p0 &&
-           (P.window == 0 || j0 > A.p1 - P.window || j0 + n - 1 < P.sinks);
+// Whether every row of the item sees all of tile j0, as far as it is there.
+__device__ __forceinline__ bool all_see(const PagedAttnParams &P, int p0, int p1, int j0) {
+    return j0 + kPosTile - 1 <= p0 &&
+           (P.window == 0 || j0 > p1 - P.window || j0 + kPosTile - 1 < P.sinks);
 }
 
 // The reference of a row comes from a rounded product f s, within 2^-24 of it, which f s - top in
 // one rounding brings to light: as 2^-4 at most up to scores of 2^20, beyond as more than a half
-// holds. There the products are rounded alike first (Scores::apart).
+// holds. There the products are rounded alike first.
 constexpr float kApart = 1048576.f;
 
-// S to P of 64 positions, the thread's row.
-template <int I>
-struct Scores {
-    uint32_t s[2][32];
+// What the sum of a tile's probabilities may come to without its largest being looked for.
+constexpr float kMost = 32768.f;
 
-    // The scores, -inf where `see` has no bit; returns their largest.
-    __device__ __forceinline__ float load(uint32_t s_tm, const unsigned (&see)[2]) {
-        tmem_ld32(s_tm, s[0]);
-        tmem_ld32(s_tm + 32, s[1]);
-        tmem_wait_ld(s[0]);
-        tmem_loaded(s[1]);
-        if ((see[0] & see[1]) != 0xffffffffu) {
+// 32 scores of a row to probabilities 2^(f s - top), or 2^(RN(f s) - top) (apart), packed; returns
+// their sum. -inf where `see` has no bit (MASK).
+template <int I, bool MASK>
+__device__ __forceinline__ uint64_t probabilities(uint32_t (&s)[32], unsigned see, float f, float top,
+                                                  uint64_t sum) {
+    const uint64_t f2 = pack_f32x2(f, f), t2 = pack_f32x2(-top, -top);
+    if (MASK) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (!((see[q] >> e) & 1)) s[q][e] = 0xff800000u;
-        }
-        float big[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int e = 0; e < 32; e += 2)
-                big[e / 2 & 3] = fmaxf(fmaxf(big[e / 2 & 3], __uint_as_float(s[q][e])),
-                                       __uint_as_float(s[q][e + 1]));
-        return fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
+        for (int e = 0; e < 32; ++e)
+            if (!((see >> e) & 1)) s[e] = 0xff800000u;
     }
-    // The scores times f, which becomes 1.
-    __device__ __forceinline__ void apart(float &f) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-                s[q][e] = __float_as_uint(__fmul_rn(__uint_as_float(s[q][e]), f));
-        f = 1.f;
-    }
-    // P = 2^(f s - top) over the scores in tensor memory; returns the row's sum.
-    __device__ __forceinline__ float store(uint32_t s_tm, float f, float top) {
-        const uint64_t f2 = pack_f32x2(f, f), t2 = pack_f32x2(-top, -top);
-        uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                float a, b;
-                unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[q][e]),
-                                                  __uint_as_float(s[q][e + 1])), f2, t2), a, b);
-                a = ex2(a);
-                b = ex2(b);
-                sum[e / 2 & 1] = add_f32x2(sum[e / 2 & 1], pack_f32x2(a, b));
-                s[q][e / 2] = pack2<I>(a, b);
-            }
-            tmem_st16(s_tm + q * 16, s[q]);
-        }
+    for (int e = 0; e < 32; e += 2) {
         float a, b;
-        unpack_f32x2(add_f32x2(sum[0], sum[1]), a, b);
-        return a + b;
+        unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), f2, t2), a,
+                     b);
+        a = ex2(a);
+        b = ex2(b);
+        sum = add_f32x2(sum, pack_f32x2(a, b));
+        s[e / 2] = pack2<I>(a, b);
     }
-};
+    return sum;
+}
 
-// A loading warp's 32 positions of a tile: where they are in the cache.
-struct Place {
-    int block;                    // -1: no row sees it, -2: it is not there
-    uint32_t unit;                // 16-byte units from the block's begin
+// TMA: a box of a tensor map's cache to shared memory; `bar` counts its bytes.
+__device__ __forceinline__ void tma_box(uint32_t to, const CUtensorMap *map, int x, int c1, int c2,
+                                        int block, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3, %4, %5}], [%6];" ::"r"(to),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(c1), "r"(c2), "r"(block), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t *bar, int bytes) {      // and arrives
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)),
+                 "r"(bytes)
+                 : "memory");
+}
+
+// The cache's tensor maps (16-bit caches).
+struct Maps {
+    CUtensorMap k, v;
 };
 
 template <int T, int KIND, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_tc_kernel(PagedAttnParams P, FastDiv by_page, int vec) {
+    paged_tc_kernel(PagedAttnParams P, int vec, int box, const __grid_constant__ Maps maps) {
     using C_ = Tc<DP>;
     constexpr int I = KIND ? 2 : T;                              // the operands' type
     constexpr int kType = I == 1 ? 1 : 0;                        // of the descriptors
@@ -183,18 +190,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const spec_kv_cache &C = P.cache;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
-        bar_init(&W.q_full, kQuery);
+        bar_init(&W.q_full, kLoad / 32);
         bar_init(&W.q_free, 2);
         for (int i = 0; i < kRing; ++i) {
-            bar_init(&W.full[i], kLoad / 2);
+            bar_init(&W.full[i], kLoad / 64);
             bar_init(&W.free[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(&W.drain[i], 1);
             bar_init(&W.s_full[i], 1);
-            bar_init(&W.o_full[i], 1);
             bar_init(&W.o_last[i], 1);
-            for (int j = 0; j < 2; ++j) bar_init(&W.p_full[i][j], 128);
+            bar_init(&W.p_full[i], 4);
+        }
+        for (int i = 0; i < kDealt; ++i) {
+            bar_init(&W.part_full[i], 1);
+            bar_init(&W.part_free[i], kReaders);
         }
         for (int i = 0; i < 8; ++i) W.odd[i] = 0;
 #ifdef SPEC_DEBUG
@@ -218,26 +228,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto slot = [](uint32_t x) { return x % kRing; };
     auto phase = [](uint32_t x) { return (x / kRing) & 1; };
     uint32_t done = 0, parts = 0;     // tiles before this part; parts with any: the phases count them
-    PagedPart A;
+    // the words of the x-th part dealt, once they are there, and when this warp has read them
+    auto dealt = [&](uint32_t x) { return warp_wait(&W.part_full[x % kDealt], x / kDealt & 1, gave_up); };
+    auto read = [&](uint32_t x) { warp_arrive(&W.part_free[x % kDealt]); };
 
-    // Launched with 96 registers a thread, 20 warps: 8 x 136 + 8 x 72 + 4 x 64 = 20 x 96.
+    // Launched with 96 registers a thread, 20 warps: 8 x 168 + 8 x 48 + 4 x 48 = 20 x 96, and
+    // 8 x 152 + 8 x 64 + 4 x 48 where a loading thread holds codes.
     if (tid >= kSoftmax + kLoad) {
-        fewer_registers<64>();
-        PagedWalk<RT> walk(P, kTcFixed, (int64_t)P.G * kPosTile);
+        fewer_registers<48>();
         const int m = warp - kMmaWarp;
-        if (m < 2) {
+        if (m == 2) {
+            // ---- deal ----
+            PagedWalk<RT> walk(P, kTcFixed, (int64_t)P.G * kPosTile);
+            PagedPart A;
+            bool any = false, go = true;
+            for (uint32_t x = 0;; ++x) {
+                const bool more = walk.next(P, A);
+                go = go && warp_wait(&W.part_free[x % kDealt], (x / kDealt & 1) ^ 1, gave_up);
+                if (go && lane == 0) {
+                    PartWords &w = W.part[x % kDealt];
+                    w = PartWords{more ? A.b : -1, A.r, A.head, A.req.first, A.req.pos, A.rows, A.p0,
+                                  A.p1, A.lo, A.hi, A.skip, A.base, A.tile, A.stop, A.begins, A.ends};
+                    bar_arrive(&W.part_full[x % kDealt]);
+                }
+                __syncwarp();
+                if (!more) break;
+                any = true;
+            }
+            if (lane == 0) paged_note(P, walk.range, A, any);
+        } else if (m < 2) {
             // ---- multiply, for softmax group m. The whole warp runs the loop and waits, one
             // thread of it issues: what the products are given is then the same in all of the warp.
             const bool lead = elect_one();
             const uint32_t o = o_at(m), s = s_at(m);
             uint32_t mine = 0;           // tiles of this group before this one
             bool ok = true;
-            while (ok && walk.next(P, A)) {
-                const int n = A.stop - A.tile;
+            for (uint32_t part = 0;; ++part) {
+                ok = ok && dealt(part);
+                if (!ok) break;
+                const PartWords &A = W.part[part % kDealt];
+                const int n = A.stop - A.tile, rows = A.rows, b = A.b;
+                read(part);
+                if (b < 0) break;
                 if (n == 0) continue;
                 ok = warp_wait(&W.q_full, parts & 1, gave_up);
                 tc_fence_after();
-                if (m == 1 && A.rows <= 128) {
+                if (m == 1 && rows <= 128) {
                     // no rows for this group. The tiles are there, so their places' earlier phases
                     // are over, and these arrivals count for the right ones.
                     for (int i = 0; ok && i < 2 * n; ++i) {
@@ -277,24 +313,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = warp_wait(&W.full[slot(x)], phase(x), gave_up);
                     const uint64_t v = smem_desc(base + C_::kTiles + slot(x) * C_::kOperand,
                                                  128 * 128, 1024);
+                    ok = ok && warp_wait(&W.p_full[m], mine & 1, gave_up);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lead) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        ok = ok && warp_wait(&W.p_full[m][h], mine & 1, gave_up);
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (lead) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_ts(o, s + h * 64 + k * 8, desc_plus(v, (h * 4 + k) * 2048),
-                                       mma_desc(kType, DP, true), i > 0 || h > 0 || k > 0);
-                            mma_commit(&W.o_full[m]);
-                            if (h == 1) {
-                                if (i == n - 1) mma_commit(&W.o_last[m]);
-                                mma_commit(&W.free[slot(x)]);
-                            }
-                        }
-                        __syncwarp();
+                        for (int k = 0; k < 8; ++k)
+                            mma_ts(o, s + k * 8, desc_plus(v, k * 2048), mma_desc(kType, DP, true),
+                                   i > 0 || k > 0);
+                        if (i == n - 1) mma_commit(&W.o_last[m]);
+                        mma_commit(&W.free[slot(x)]);
                     }
+                    __syncwarp();
                     ++mine;
                     if (ok && i + 1 < n) scores(i + 1);
                 }
@@ -308,78 +338,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             __syncwarp();
-        } else {
-            // ---- queries: the D / 8 chunks of a row side by side, rows past the item's zeros ----
-            const int t = tid - (kSoftmax + kLoad + 64);
-            bool go = true;
-            while (walk.next(P, A)) {
-                if (A.stop == A.tile) continue;
-                go = go && warp_wait(&W.q_free, (parts & 1) ^ 1, gave_up);
-                if (go) {
-                    const int64_t row0 = (int64_t)A.r * RT;
-                    const int chunks = C.D / 8;
-                    constexpr int J = DP / 8;
-                    for (int i = t; i < RT * J; i += kQuery) {
-                        const int r = i / J, j = i - r * J;
-                        const uint32_t to = (r >> 7) * C_::kOperand + chunk_at(r & 127, j);
-                        const bool in = r < A.rows && j < chunks;
-                        const int64_t k = row0 + (in ? r : 0), n = k / P.G;
-                        const unsigned short *from =
-                            reinterpret_cast<const unsigned short *>(P.q) +
-                            (A.req.first + n) * P.q_stride +
-                            ((int64_t)A.head * P.G + (k - n * P.G)) * C.D + (in ? j * 8 : 0);
-                        if (vec) {
-                            copy16(base + to, from, in);
-                        } else {
-                            uint32_t w[4] = {0, 0, 0, 0};
-                            if (in) {
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    w[e] = (uint32_t)__ldg(from + 2 * e) |
-                                           (uint32_t)__ldg(from + 2 * e + 1) << 16;
-                            }
-                            *reinterpret_cast<uint4 *>(smem + to) = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                    }
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                    if (kScaleQ) {
-                        // each thread the chunks it brought, a row's beside each other in its warp
-                        for (int i = t; i < RT * J; i += kQuery) {
-                            const int r = i / J, j = i - r * J;
-                            uint4 *at = reinterpret_cast<uint4 *>(
-                                smem + (r >> 7) * C_::kOperand + chunk_at(r & 127, j));
-                            uint32_t w[4] = {at->x, at->y, at->z, at->w};
-                            float big = 0.f;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float a = fabsf(value16<T>((w[e / 2] >> (e % 2 * 16)) & 0xffffu));
-                                if (a < INFINITY) big = fmaxf(big, a);
-                            }
-#pragma unroll
-                            for (int o = J / 2; o > 0; o >>= 1)
-                                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-                            // into [2^14, 2^15), by 2^126 at most
-                            const uint32_t ex = max(__float_as_uint(big) >> 23, 15u);
-                            const float up = __uint_as_float((268u - ex) << 23);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                w[e] = pack2<2>(value16<T>(w[e] & 0xffffu) * up,
-                                                value16<T>(w[e] >> 16) * up);
-                            *at = make_uint4(w[0], w[1], w[2], w[3]);
-                            if (j == 0)
-                                W.q_down[parts & 1][r] = (unsigned short)((ex - 14u) << 7);
-                        }
-                    }
-                    fence_async_smem();
-                    bar_arrive(&W.q_full);
-                }
-                ++parts;
-            }
         }
     } else if (tid >= kSoftmax) {
-        fewer_registers<72>();
+        fewer_registers<KIND ? 64 : 48>();
         // ---- load: K or V, 32 positions a warp ----
-        PagedWalk<RT> walk(P, kTcFixed, (int64_t)P.G * kPosTile);
         const bool of_v = tid >= kSoftmax + kLoad / 2;
         const int w4 = (tid - kSoftmax) % (kLoad / 2) / 32;
         const char *cache = static_cast<const char *>(of_v ? C.v : C.k);
@@ -387,18 +349,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int units = C.D * kEsz / 16;                       // of a position in the cache
         constexpr int U = DP * kEsz / 16;                        // ... in the operand's width
         bool go = true;               // no wait has given up
-        while (walk.next(P, A)) {
+        for (uint32_t part = 0;; ++part) {
+            go = go && dealt(part);
+            if (!go) break;
+            const PartWords &A = W.part[part % kDealt];      // until read(part)
             const int n = A.stop - A.tile;
-            if (n == 0) continue;
+            if (A.b < 0) break;
+            if (n == 0) {
+                read(part);
+                continue;
+            }
             auto page = [&](int i) -> int {
                 const int p = i < n ? A.position(A.tile + i) + w4 * 32 + lane : A.hi;
                 if (p >= A.hi || (p < A.lo && p >= P.sinks)) return -1;
-                const int block = paged_page(P, by_page, A.b, p);
+                const int block = paged_page(P, A.b, p);
                 return block >= 0 && block < C.num_blocks ? block : -2;
             };
             auto unit = [&](int i) -> uint32_t {
                 const int p = A.position(A.tile + i) + w4 * 32 + lane;
-                const uint32_t off = p - by_page((uint32_t)p) * C.block_size;
+                const uint32_t off = p - P.by_page((uint32_t)p) * C.block_size;
                 return (C.layout == SPEC_KV_NHD ? off * C.H + A.head : A.head * C.block_size + off) *
                        units;
             };
@@ -412,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Tile i has come to its place: what the rows see in part is looked through.
             auto arrived = [&](int i) {
                 const uint32_t x = 2 * (done + i) + of_v;
-                if (of_v && !all_see(P, A, A.position(A.tile + i), kPosTile)) {
+                if (of_v && !all_see(P, A.p0, A.p1, A.position(A.tile + i))) {
                     char *to = smem + C_::kTiles + slot(x) * C_::kOperand;
                     bool odd = false;
                     constexpr int J = DP / 8;
@@ -436,41 +405,113 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (odd) W.odd[parts & 7] = 1;
                 }
                 fence_async_smem();
-                bar_arrive(&W.full[slot(x)]);
+                warp_arrive(&W.full[slot(x)]);
             };
             auto note = [&](int i, int block) {      // K's warps: which positions are there
                 if (block == -2 && P.status) atomicMax(P.status + A.b, SPEC_REQ_BAD_SLOT);
                 const unsigned seen = __ballot_sync(0xffffffffu, block >= 0);
                 if (!of_v && lane == 0) W.seen[(done + i) & 3][w4] = seen;
             };
+            // The item's rows, the D / 8 chunks of a row side by side, rows past the item's zeros:
+            // issued by all loading threads, and (with the first tile) waited for.
+            auto queries = [&] {
+                constexpr int J = DP / 8;
+                const int row0 = A.r * RT, chunks = C.D / 8, t = tid - kSoftmax;
+                go = go && warp_wait(&W.q_free, (parts & 1) ^ 1, gave_up);
+                if (go) {
+#pragma unroll 2
+                    for (int i = t; i < RT * J; i += kLoad) {
+                        const int r = i / J, j = i - r * J;
+                        const uint32_t to = (r >> 7) * C_::kOperand + chunk_at(r & 127, j);
+                        const bool in = r < A.rows && j < chunks;
+                        const unsigned short *from =
+                            paged_query(P, A.first, A.head, row0 + (in ? r : 0)) + (in ? j * 8 : 0);
+                        if (vec) {
+                            copy16(base + to, from, in);
+                        } else {
+                            uint32_t w[4] = {0, 0, 0, 0};
+                            if (in) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    w[e] = (uint32_t)__ldg(from + 2 * e) |
+                                           (uint32_t)__ldg(from + 2 * e + 1) << 16;
+                            }
+                            *reinterpret_cast<uint4 *>(smem + to) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                if (kScaleQ && go) {
+                    // each thread the chunks it brought, a row's beside each other in its warp
+#pragma unroll 1
+                    for (int i = t; i < RT * J; i += kLoad) {
+                        const int r = i / J, j = i - r * J;
+                        uint4 *at = reinterpret_cast<uint4 *>(smem + (r >> 7) * C_::kOperand +
+                                                              chunk_at(r & 127, j));
+                        uint32_t w[4] = {at->x, at->y, at->z, at->w};
+                        float big = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float a = fabsf(value16<T>((w[e / 2] >> (e % 2 * 16)) & 0xffffu));
+                            if (a < INFINITY) big = fmaxf(big, a);
+                        }
+#pragma unroll
+                        for (int o = J / 2; o > 0; o >>= 1)
+                            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                        // into [2^14, 2^15), by 2^126 at most
+                        const uint32_t ex = max(__float_as_uint(big) >> 23, 15u);
+                        const float up = __uint_as_float((268u - ex) << 23);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack2<2>(value16<T>(w[e] & 0xffffu) * up, value16<T>(w[e] >> 16) * up);
+                        *at = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (j == 0) W.q_down[parts & 1][r] = (unsigned short)((ex - 14u) << 7);
+                    }
+                }
+                fence_async_smem();
+                if (go) warp_arrive(&W.q_full);
+            };
             if (of_v && lane == 0 && w4 == 0) W.odd[(parts + 4) & 7] = 0;
             if constexpr (KIND == 0) {
                 int next = page(0);
-                for (int i = 0; i <= n; ++i) {
+                for (int i = 0; i < n; ++i) {
                     const int block = next;
                     next = page(i + 1);
-                    if (i < n) {
-                        const uint32_t x = 2 * (done + i) + of_v;
-                        go = go && warp_wait(&W.free[slot(x)], phase(x) ^ 1, gave_up);
-                        if (go) {
-                            note(i, block);
-                            const uint32_t to = base + C_::kTiles + slot(x) * C_::kOperand;
-                            const uint32_t in = unit(i);
-#pragma unroll
-                            for (int q = 0; q < U; ++q) {
-                                const int t = (q * 32 + lane) / U, u = lane % U;
-                                bool ok;
-                                const char *from = source(block, in, t, u, ok);
-                                copy16(to + chunk_at(w4 * 32 + t, u), from, ok);
-                            }
+                    const uint32_t x = 2 * (done + i) + of_v;
+                    go = go && warp_wait(&W.free[slot(x)], phase(x) ^ 1, gave_up);
+                    const int j0 = A.position(A.tile + i);
+                    const uint32_t place = C_::kTiles + slot(x) * C_::kOperand + w4 * (32 * 128);
+                    if (go && box > 0 && __all_sync(0xffffffffu, block >= 0) &&
+                        !(of_v && !all_see(P, A.p0, A.p1, j0))) {
+                        // `box` rows of a page a time (they divide 32 and the page), 64 columns
+                        note(i, block);
+                        if (lane == 0) bar_expect(&W.full[slot(x)], 32 * DP * 2);
+                        __syncwarp();
+                        const int g = lane / (DP / 64), q = lane % (DP / 64), t = g * box;
+                        const int blk = __shfl_sync(0xffffffffu, block, t & 31);
+                        if (t < 32) {
+                            const uint32_t p = (uint32_t)(j0 + w4 * 32 + t);
+                            const int off = (int)(p - P.by_page(p) * C.block_size);
+                            const bool nhd = C.layout == SPEC_KV_NHD;
+                            tma_box(base + place + q * (128 * 128) + t * 128, of_v ? &maps.v : &maps.k,
+                                    q * 64, nhd ? A.head : off, nhd ? off : A.head, blk,
+                                    &W.full[slot(x)]);
                         }
-                    }
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    if (i > 0) {
-                        asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    } else if (go) {
+                        note(i, block);
+                        const uint32_t in = unit(i);
+#pragma unroll 4
+                        for (int q = 0; q < U; ++q) {
+                            const int t = (q * 32 + lane) / U, u = lane % U;
+                            bool ok;
+                            const char *from = source(block, in, t, u, ok);
+                            copy16(base + place + chunk_at(t, u), from, ok);
+                        }
+                        asm volatile("cp.async.wait_all;" ::: "memory");
                         __syncwarp();     // the warp's copies, all lanes'
-                        if (go) arrived(i - 1);
+                        arrived(i);
                     }
+                    if (i == 0) queries();
                 }
             } else {
                 // a tile's codes wait in registers for its place
@@ -510,15 +551,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     block = next;
                     next = page(i + 2);
                     if (i + 1 < n) fetch(i + 1, block);
+                    if (i == 0) queries();
                 }
             }
+            read(part);
             done += n;
             ++parts;
         }
+        if (!go) {      // copies in flight come to shared memory before it is given back
+            const uint64_t t0 = now_ns();
+            for (int i = 0; i < (1 << 20) && now_ns() - t0 < 1000000ull; ++i) {
+            }
+        }
     } else {
-        more_registers<136>();
+        more_registers<KIND ? 152 : 168>();
         // ---- softmax: this thread's row. A wait that gives up is followed by none.
-        PagedWalk<RT> walk(P, kTcFixed, (int64_t)P.G * kPosTile);
         const int m = warp >> 2;
         const int r = m * 128 + (warp & 3) * 32 + lane;          // of the item
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -526,18 +573,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float v_scale = C.v_scale ? __ldg(C.v_scale) : 1.f;
         const float unit = P.scale * kLog2e * (C.k_scale ? __ldg(C.k_scale) : 1.f);
         uint32_t mine = 0, results = 0;   // tiles of this group so far; parts
-        bool go = true, any = false;
-        while (walk.next(P, A)) {
-            any = true;
-            const int n = A.stop - A.tile;
-            const int64_t row0 = (int64_t)A.r * RT;
+        bool go = true;
+        uint32_t part_at = 0;
+        for (;; ++part_at) {
+            go = go && dealt(part_at);
+            if (!go) break;
+            const PartWords &A = W.part[part_at % kDealt];   // until read(part_at)
+            const int n = A.stop - A.tile, tile0 = A.tile, skip = A.skip, base_tile = A.base;
+            if (A.b < 0) break;
+            const int row0 = A.r * RT;
             const bool live = r < A.rows, work = n > 0 && m * 128 < A.rows;
             const bool warp_live = m * 128 + (warp & 3) * 32 < A.rows;
-            const int64_t token = (row0 + min(r, A.rows - 1)) / P.G;
-            const int64_t most = (int64_t)C.max_blocks * C.block_size;
-            const int at = (int)min(max(A.req.pos + token, (int64_t)-1), most);
-            // top: the row's reference; limit: what raises it, or calls for apart()
-            float top = kPagedNoMax, limit = -INFINITY, sum = 0.f, factor = 0.f;
+            const int at = paged_position(P, A.pos, row0 + min(r, A.rows - 1));
+            float top = kPagedNoMax, sum = 0.f, factor = 0.f;    // top: the row's reference
+            bool apart = false;       // a row of the warp has scores beyond kApart
+            // every row sees all of a tile that ends at p0 at most and begins past the edge of the
+            // last row's window, or is the sinks'
+            const int p0 = A.p0, edge = P.window > 0 ? A.p1 - P.window : INT_MIN, hi = A.hi;
             for (int i = 0; work && i < n; ++i, ++mine) {
                 go = go && warp_wait(&W.s_full[m], mine & 1, gave_up);
                 if (!go) break;
@@ -545,52 +597,110 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (i == 0)
                     factor = paged_factor(
                         kScaleQ ? unit * __uint_as_float((uint32_t)W.q_down[parts & 1][r] << 16) : unit);
-                const int j0 = A.position(A.tile + i);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (warp_live) {
-                        unsigned see[2] = {W.seen[(done + i) & 3][2 * h],
-                                           W.seen[(done + i) & 3][2 * h + 1]};
-                        if (!all_see(P, A, j0 + 64 * h, 64)) {
-#pragma unroll
-                            for (int q = 0; q < 2; ++q)
-                                see[q] &= paged_bits(j0 + 64 * h + 32 * q, at, A.hi, P.window, P.sinks);
-                        }
-                        Scores<I> tile;
-                        float f = factor;
-                        const float x = fmaxf(kPagedNoMax, tile.load(s_tm + 64 * h, see) * f);
-                        if (__any_sync(0xffffffffu, x > limit)) {
-                            const float to = paged_reference(top, x), a = ex2(top - to);
-                            top = to;
-                            sum *= a;
-                            limit = paged_limit(top);
-                            if (fabsf(top) > kApart) {
-                                limit = -INFINITY;      // and so for each tile to come
-                                tile.apart(f);
-                            }
-                            // O so far: the product of the first half may be under way; the
-                            // scores at hand were made after those before
-                            if (i > 0 || h > 0) {
-                                if (h > 0) go = go && warp_wait(&W.o_full[m], 0, gave_up);
-                                tc_fence_after();
-#pragma unroll 1
-                                for (int q = 0; q < DP / 16; ++q) {   // S stays in registers meanwhile
-                                    uint32_t o[16];
-                                    tmem_ld16(o_tm + q * 16, o);
-                                    tmem_wait_ld16(o);
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e)
-                                        o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-                                    tmem_st16(o_tm + q * 16, o);
-                                }
-                            }
-                        }
-                        sum += tile.store(s_tm + 64 * h, f, top);
-                        tmem_wait_st();
-                    }
+                if (!warp_live) {
                     tc_fence_before();
-                    bar_arrive(&W.p_full[m][h]);
+                    warp_arrive(&W.p_full[m]);
+                    continue;
                 }
+                const int ti = tile0 + i, j0 = (ti < skip ? ti : base_tile + ti) * kPosTile;
+                const uint4 there = *reinterpret_cast<const uint4 *>(W.seen[(done + i) & 3]);
+                const bool plain =
+                    (there.x & there.y & there.z & there.w) == 0xffffffffu &&
+                    j0 + kPosTile - 1 <= p0 && (j0 > edge || j0 + kPosTile - 1 < P.sinks);
+                float tile_sum = INFINITY;
+                // A later tile: P by the reference at hand, and kept if no score was too far above it.
+                if (i > 0 && !apart) {
+                    uint32_t x[4][32];
+                    tmem_ld32(s_tm, x[0]);
+                    tmem_ld32(s_tm + 32, x[1]);
+                    tmem_ld32(s_tm + 64, x[2]);
+                    tmem_ld32(s_tm + 96, x[3]);
+                    tmem_wait_ld(x[0]);
+                    tmem_loaded(x[1]);
+                    tmem_loaded(x[2]);
+                    tmem_loaded(x[3]);
+                    uint64_t sums[2] = {0ull, 0ull};
+                    if (plain) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            sums[q & 1] = probabilities<I, false>(x[q], 0u, factor, top, sums[q & 1]);
+                    } else {
+                        const unsigned w[4] = {there.x, there.y, there.z, there.w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            sums[q & 1] = probabilities<I, true>(
+                                x[q], w[q] & paged_bits(j0 + 32 * q, at, hi, P.window, P.sinks), factor,
+                                top, sums[q & 1]);
+                    }
+                    float a, b;
+                    unpack_f32x2(add_f32x2(sums[0], sums[1]), a, b);
+                    tile_sum = a + b;
+                    if (__all_sync(0xffffffffu, tile_sum <= kMost)) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) tmem_st16(s_tm + q * 16, x[q]);
+                    }
+                }
+                if (__any_sync(0xffffffffu, !(tile_sum <= kMost))) {
+                    // The scores again: their largest raises the reference; P of 32 positions takes
+                    // the place of 16 that have been read.
+                    const unsigned w[4] = {there.x, there.y, there.z, there.w};
+                    float x = kPagedNoMax;
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        const unsigned see = (q == 0 ? w[0] : q == 1 ? w[1] : q == 2 ? w[2] : w[3]) &
+                                             paged_bits(j0 + 32 * q, at, hi, P.window, P.sinks);
+                        uint32_t y[32];
+                        tmem_ld32(s_tm + q * 32, y);
+                        tmem_wait_ld(y);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if ((see >> e) & 1)
+                                x = fmaxf(x, __fmul_rn(__uint_as_float(y[e]), factor));
+                    }
+                    // (kept where it is high enough: a row's own need, not its warp's)
+                    const float to = x > paged_limit(top) || i == 0 || tile_sum > kMost
+                                         ? paged_reference(top, x) : top;
+                    const float a = ex2(top - to);
+                    top = to;
+                    sum *= a;
+                    apart = apart || __any_sync(0xffffffffu, fabsf(top) > kApart && top != kPagedNoMax);
+                    // O so far: the scores at hand were made after all its products
+                    if (i > 0) {
+#pragma unroll 1
+                        for (int q = 0; q < DP / 16; ++q) {
+                            uint32_t o[16];
+                            tmem_ld16(o_tm + q * 16, o);
+                            tmem_wait_ld16(o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                            tmem_st16(o_tm + q * 16, o);
+                        }
+                    }
+                    uint64_t sums = 0ull;
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        const unsigned see = (q == 0 ? w[0] : q == 1 ? w[1] : q == 2 ? w[2] : w[3]) &
+                                             paged_bits(j0 + 32 * q, at, hi, P.window, P.sinks);
+                        uint32_t y[32];
+                        tmem_ld32(s_tm + q * 32, y);
+                        tmem_wait_ld(y);
+                        if (apart) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                y[e] = __float_as_uint(__fmul_rn(__uint_as_float(y[e]), factor));
+                        }
+                        sums = probabilities<I, true>(y, see, apart ? 1.f : factor, top, sums);
+                        tmem_st16(s_tm + q * 16, y);
+                    }
+                    float b;
+                    unpack_f32x2(sums, tile_sum, b);
+                    tile_sum += b;
+                }
+                sum += tile_sum;
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(&W.p_full[m]);
             }
             // The result: O is done after the group's last product.
             if (work) go = go && warp_wait(&W.o_last[m], results++ & 1, gave_up);
@@ -599,9 +709,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sum = NAN;
                 if (P.status && lane == 0) atomicMax(P.status + A.b, SPEC_REQ_INTERNAL);
             }
-            const bool whole = A.whole();
+            const bool whole = A.begins && A.ends;
             const float norm = (whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f) * v_scale;
-            const int64_t to = live ? paged_row(P, A.req, A.head, row0 + r) : 0;
+            const int64_t to = live ? paged_row(P, A.first, A.head, row0 + r) : 0;
             float *part = paged_slot(P, blockIdx.x, A.begins, RT, DP);
             const bool out32 = (reinterpret_cast<uintptr_t>(P.out) & 31) == 0;
             const bool odd = n > 0 && *(volatile int *)&W.odd[parts & 7] != 0;
@@ -622,13 +732,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (odd) {      // NaN and infinities of positions that this row sees
                     for (int i = A.tile; i < A.stop; ++i) {
                         const int j0 = A.position(i);
-                        if (all_see(P, A, j0, kPosTile)) continue;
+                        if (all_see(P, A.p0, A.p1, j0)) continue;
 #pragma unroll 1
                         for (int j = j0; j < j0 + kPosTile; ++j) {
                             if (!(paged_bits(j, at, A.hi, P.window, P.sinks) & 1)) continue;
-                            const int block = paged_page(P, by_page, A.b, j);
+                            const int block = paged_page(P, A.b, j);
                             if (block < 0 || block >= C.num_blocks) continue;
-                            const uint32_t off = j - by_page((uint32_t)j) * C.block_size;
+                            const uint32_t off = j - P.by_page((uint32_t)j) * C.block_size;
                             const int64_t e0 =
                                 block * C.v_block_stride +
                                 (int64_t)(C.layout == SPEC_KV_NHD ? off * C.H + A.head
@@ -682,14 +792,64 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             tc_fence_before();
+            read(part_at);
             done += n;
             parts += n > 0;
         }
-        if (tid == 0) paged_note(P, walk.range, A, any);
+        if (!go) {      // the parts that did not come are lost, too
+            PagedWalk<RT> walk(P, kTcFixed, (int64_t)P.G * kPosTile);
+            PagedPart A;
+            for (uint32_t x = 0; walk.next(P, A); ++x) {
+                if (x < part_at) continue;
+                if (P.status && lane == 0) atomicMax(P.status + A.b, SPEC_REQ_INTERNAL);
+                if (r >= A.rows) continue;
+                const int64_t to = paged_row(P, A.req.first, A.head, A.r * RT + r);
+                float *part = paged_slot(P, blockIdx.x, A.begins, RT, DP);
+                for (int e = 0; e < C.D; e += 4) {
+                    const float4 v = make_float4(NAN, NAN, NAN, NAN);
+                    if (A.whole()) paged_store4<T>(P.out, to * C.D + e, v);
+                    else *reinterpret_cast<float4 *>(part + (int64_t)r * DP + e) = v;
+                }
+                if (A.whole()) {
+                    if (P.lse) P.lse[to] = NAN;
+                } else {
+                    part[RT * DP + r] = kPagedNoMax;
+                    part[RT * (DP + 1) + r] = NAN;
+                }
+            }
+        }
     }
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) tmem_free(tmem, C_::kColumns);
+}
+
+// A tensor map of a 16-bit cache: boxes of 64 columns and `box` positions of one head and block.
+bool make_map(CUtensorMap &map, const spec_kv_cache &c, void *at, int64_t block_stride, int dtype,
+              int box) {
+    using Encode = decltype(&cuTensorMapEncodeTiled);
+    static const Encode encode = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                                               cudaEnableDefault, &found);
+        if (e != cudaSuccess) cudaGetLastError();
+        return e == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<Encode>(f)
+                                                                         : nullptr;
+    }();
+    if (!encode) return false;
+    const bool nhd = c.layout == SPEC_KV_NHD;
+    const cuuint64_t d = (cuuint64_t)c.D, h = (cuuint64_t)c.H, n = (cuuint64_t)c.block_size;
+    const cuuint64_t dims[4] = {d, nhd ? h : n, nhd ? n : h, (cuuint64_t)c.num_blocks};
+    const cuuint64_t strides[3] = {d * 2, (nhd ? h : n) * d * 2, (cuuint64_t)block_stride * 2};
+    const cuuint32_t boxes[4] = {64, nhd ? 1u : (cuuint32_t)box, nhd ? (cuuint32_t)box : 1u, 1};
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    if (strides[2] >= cuuint64_t(1) << 40 || strides[1] >= cuuint64_t(1) << 40) return false;
+    return encode(&map, dtype == SPEC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  4, at, dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int T, int KIND, int DP>
@@ -699,9 +859,19 @@ cudaError_t launch(const PagedAttnParams &p, int grid, cudaStream_t st) {
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                C_::kBytes);
     if (e != cudaSuccess) return e;
+    const spec_kv_cache &c = p.cache;
     const int vec = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.q_stride % 8 == 0;
-    paged_tc_kernel<T, KIND, DP><<<grid, kThreads, C_::kBytes, st>>>(
-        p, FastDiv((uint32_t)p.cache.block_size), vec);
+    // Pages of a multiple of eight positions: boxes of the largest power of two that divides both
+    // them and 32 (their places in shared memory begin where the swizzle's pattern does).
+    Maps maps = {};
+    int box = 0;
+    if (KIND == 0 && c.block_size % 8 == 0 && c.D >= 64) {
+        box = c.block_size % 32 == 0 ? 32 : c.block_size % 16 == 0 ? 16 : 8;
+        if (!make_map(maps.k, c, c.k, c.k_block_stride, p.dtype, box) ||
+            !make_map(maps.v, c, c.v, c.v_block_stride, p.dtype, box))
+            box = 0;
+    }
+    paged_tc_kernel<T, KIND, DP><<<grid, kThreads, C_::kBytes, st>>>(p, vec, box, maps);
     return cudaGetLastError();
 }
 

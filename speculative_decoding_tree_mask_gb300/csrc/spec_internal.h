@@ -292,6 +292,22 @@ struct LogprobsParams {
 
 cudaError_t launch_logprobs(const LogprobsParams &p, int dtype, cudaStream_t st);
 
+// Division of n < 2^31 by a number known on the host: a multiplication and a shift (the round-up
+// method of Granlund and Montgomery, "Division by invariant integers using multiplication").
+struct FastDiv {
+    uint32_t d = 1, mul = 1, shift = 0;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t divisor) : d(divisor) {
+        while (shift < 32 && (uint64_t(1) << shift) < d) ++shift;
+        mul = (uint32_t)((((uint64_t(1) << shift) - d) << 32) / d + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+        return (__umulhi(n, mul) + n) >> shift;
+    }
+#endif
+};
+
 // Attention of new tokens over the paged cache (see spec_paged_attention).
 struct PagedAttnParams {
     spec_kv_cache cache;
@@ -312,27 +328,12 @@ struct PagedAttnParams {
     float *ws;                    // ... and their parts
     int lose;                     // debug builds: every wait of the tcgen05 kernel gives up at once
     int sms;
+    FastDiv by_page, by_group;    // block_size; G
 };
 
 // Bytes of notes and parts that a launch may write.
 int64_t paged_attn_workspace(int max_new, int G, int D, int sms);
 cudaError_t launch_paged_attn(const PagedAttnParams &p, cudaStream_t st);
-
-// Division of n < 2^31 by a number known on the host: a multiplication and a shift (the round-up
-// method of Granlund and Montgomery, "Division by invariant integers using multiplication").
-struct FastDiv {
-    uint32_t d = 1, mul = 1, shift = 0;
-    FastDiv() = default;
-    explicit FastDiv(uint32_t divisor) : d(divisor) {
-        while (shift < 32 && (uint64_t(1) << shift) < d) ++shift;
-        mul = (uint32_t)((((uint64_t(1) << shift) - d) << 32) / d + 1);
-    }
-#ifdef __CUDACC__
-    __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
-        return (__umulhi(n, mul) + n) >> shift;
-    }
-#endif
-};
 
 // K/V rows into the 4-bit cache, and back (see spec_kv_commit_fp4, spec_kv_load_fp4).
 struct KvFp4Params {
