@@ -131,17 +131,10 @@ constexpr float kApart = 1048576.f;
 // What the sum of a tile's probabilities may come to without its largest being looked for.
 constexpr float kMost = 32768.f;
 
-// 32 scores of a row to probabilities 2^(f s - top), or 2^(RN(f s) - top) (apart), packed; returns
-// their sum. -inf where `see` has no bit (MASK).
-template <int I, bool MASK>
-__device__ __forceinline__ uint64_t probabilities(uint32_t (&s)[32], unsigned see, float f, float top,
-                                                  uint64_t sum) {
+// 32 scores of a row to probabilities 2^(f s - top), packed; returns their sum.
+template <int I>
+__device__ __forceinline__ uint64_t probabilities(uint32_t (&s)[32], float f, float top, uint64_t sum) {
     const uint64_t f2 = pack_f32x2(f, f), t2 = pack_f32x2(-top, -top);
-    if (MASK) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-            if (!((see >> e) & 1)) s[e] = 0xff800000u;
-    }
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
         float a, b;
@@ -154,8 +147,30 @@ __device__ __forceinline__ uint64_t probabilities(uint32_t (&s)[32], unsigned se
     }
     return sum;
 }
+// -inf where `see` has no bit.
+__device__ __forceinline__ void mask32(uint32_t (&s)[32], unsigned see) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        if (!((see >> e) & 1)) s[e] = 0xff800000u;
+}
+__device__ __forceinline__ float largest32(const uint32_t (&s)[32]) {
+    float big[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int e = 0; e < 32; e += 2)
+        big[e / 2 & 1] =
+            fmaxf(fmaxf(big[e / 2 & 1], __uint_as_float(s[e])), __uint_as_float(s[e + 1]));
+    return fmaxf(big[0], big[1]);
+}
 
-// TMA: a box of a tensor map's cache to shared memory; `bar` counts its bytes.
+// TMA: a box of a tensor to shared memory; `bar` counts its bytes.
+__device__ __forceinline__ void tma_box3(uint32_t to, const CUtensorMap *map, int x, int c1, int c2,
+                                         uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3, %4}], [%5];" ::"r"(to),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(c1), "r"(c2), "r"(smem_addr(bar))
+        : "memory");
+}
 __device__ __forceinline__ void tma_box(uint32_t to, const CUtensorMap *map, int x, int c1, int c2,
                                         int block, uint64_t *bar) {
     asm volatile(
@@ -170,19 +185,22 @@ __device__ __forceinline__ void bar_expect(uint64_t *bar, int bytes) {      // a
                  : "memory");
 }
 
-// The cache's tensor maps (16-bit caches).
+// Tensor maps of the cache and the queries (16-bit caches), and their boxes' rows: positions of a
+// page, tokens (0: no map).
 struct Maps {
-    CUtensorMap k, v;
+    CUtensorMap k, v, q;
+    int page_rows, tokens;
 };
 
 template <int T, int KIND, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_tc_kernel(PagedAttnParams P, int vec, int box, const __grid_constant__ Maps maps) {
+    paged_tc_kernel(PagedAttnParams P, int vec, const __grid_constant__ Maps maps) {
     using C_ = Tc<DP>;
     constexpr int I = KIND ? 2 : T;                              // the operands' type
     constexpr int kType = I == 1 ? 1 : 0;                        // of the descriptors
     constexpr int RT = kPagedTcRows, KS = DP / 16, kEsz = KIND ? 1 : 2;
     constexpr bool kScaleQ = T == 1 && I == 2;
+    const int box = KIND ? 0 : maps.page_rows;
     extern __shared__ char raw[];
     char *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     Words &W = *reinterpret_cast<Words *>(smem + C_::kSmall);
@@ -190,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const spec_kv_cache &C = P.cache;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
-        bar_init(&W.q_full, kLoad / 32);
+        bar_init(&W.q_full, KIND == 0 && maps.tokens > 0 ? 1 : kLoad / 32);
         bar_init(&W.q_free, 2);
         for (int i = 0; i < kRing; ++i) {
             bar_init(&W.full[i], kLoad / 64);
@@ -417,6 +435,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto queries = [&] {
                 constexpr int J = DP / 8;
                 const int row0 = A.r * RT, chunks = C.D / 8, t = tid - kSoftmax;
+                if (KIND == 0 && maps.tokens > 0) {
+                    // by TMA: boxes of 128 rows and 64 columns. Rows past the item's may be another
+                    // request's: their results go nowhere.
+                    if (of_v || w4 != 0) return;
+                    go = go && warp_wait(&W.q_free, (parts & 1) ^ 1, gave_up);
+                    const int halves = A.rows > 128 ? 2 : 1, token = A.first + (int)P.by_group((uint32_t)row0);
+                    if (go && lane == 0) bar_expect(&W.q_full, halves * C_::kOperand);
+                    __syncwarp();
+                    const int m = lane / (DP / 64), q = lane % (DP / 64);
+                    if (go && m < halves)
+                        tma_box3(base + m * C_::kOperand + q * (128 * 128), &maps.q, q * 64,
+                                 A.head * P.G, token + m * maps.tokens, &W.q_full);
+                    return;
+                }
                 go = go && warp_wait(&W.q_free, (parts & 1) ^ 1, gave_up);
                 if (go) {
 #pragma unroll 2
@@ -607,34 +639,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool plain =
                     (there.x & there.y & there.z & there.w) == 0xffffffffu &&
                     j0 + kPosTile - 1 <= p0 && (j0 > edge || j0 + kPosTile - 1 < P.sinks);
+                const unsigned w[4] = {there.x, there.y, there.z, there.w};
                 float tile_sum = INFINITY;
-                // A later tile: P by the reference at hand, and kept if no score was too far above it.
-                if (i > 0 && !apart) {
+                // P by the reference at hand, kept if no score was too far above it.
+                if (!apart) {
                     uint32_t x[4][32];
-                    tmem_ld32(s_tm, x[0]);
-                    tmem_ld32(s_tm + 32, x[1]);
-                    tmem_ld32(s_tm + 64, x[2]);
-                    tmem_ld32(s_tm + 96, x[3]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld32(s_tm + q * 32, x[q]);
                     tmem_wait_ld(x[0]);
-                    tmem_loaded(x[1]);
-                    tmem_loaded(x[2]);
-                    tmem_loaded(x[3]);
-                    uint64_t sums[2] = {0ull, 0ull};
-                    if (plain) {
+#pragma unroll
+                    for (int q = 1; q < 4; ++q) tmem_loaded(x[q]);
+                    if (!plain) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            sums[q & 1] = probabilities<I, false>(x[q], 0u, factor, top, sums[q & 1]);
-                    } else {
-                        const unsigned w[4] = {there.x, there.y, there.z, there.w};
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            sums[q & 1] = probabilities<I, true>(
-                                x[q], w[q] & paged_bits(j0 + 32 * q, at, hi, P.window, P.sinks), factor,
-                                top, sums[q & 1]);
+                            mask32(x[q], w[q] & paged_bits(j0 + 32 * q, at, hi, P.window, P.sinks));
                     }
+                    if (i == 0) {
+                        const float big = fmaxf(fmaxf(largest32(x[0]), largest32(x[1])),
+                                                fmaxf(largest32(x[2]), largest32(x[3])));
+                        top = paged_reference(kPagedNoMax, fmaxf(kPagedNoMax, big * factor));
+                        apart = __any_sync(0xffffffffu, fabsf(top) > kApart && top != kPagedNoMax);
+                    }
+                    uint64_t sums[2] = {0ull, 0ull};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        sums[q & 1] = probabilities<I>(x[q], factor, top, sums[q & 1]);
                     float a, b;
                     unpack_f32x2(add_f32x2(sums[0], sums[1]), a, b);
-                    tile_sum = a + b;
+                    tile_sum = apart ? INFINITY : a + b;
                     if (__all_sync(0xffffffffu, tile_sum <= kMost)) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) tmem_st16(s_tm + q * 16, x[q]);
@@ -643,23 +675,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (__any_sync(0xffffffffu, !(tile_sum <= kMost))) {
                     // The scores again: their largest raises the reference; P of 32 positions takes
                     // the place of 16 that have been read.
-                    const unsigned w[4] = {there.x, there.y, there.z, there.w};
                     float x = kPagedNoMax;
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        const unsigned see = (q == 0 ? w[0] : q == 1 ? w[1] : q == 2 ? w[2] : w[3]) &
-                                             paged_bits(j0 + 32 * q, at, hi, P.window, P.sinks);
-                        uint32_t y[32];
+                    auto scores = [&](int q, uint32_t (&y)[32]) {
                         tmem_ld32(s_tm + q * 32, y);
                         tmem_wait_ld(y);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if ((see >> e) & 1)
-                                x = fmaxf(x, __fmul_rn(__uint_as_float(y[e]), factor));
+                        mask32(y, (q == 0 ? w[0] : q == 1 ? w[1] : q == 2 ? w[2] : w[3]) &
+                                      paged_bits(j0 + 32 * q, at, hi, P.window, P.sinks));
+                    };
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t y[32];
+                        scores(q, y);
+                        x = fmaxf(x, largest32(y) * factor);
                     }
-                    // (kept where it is high enough: a row's own need, not its warp's)
-                    const float to = x > paged_limit(top) || i == 0 || tile_sum > kMost
-                                         ? paged_reference(top, x) : top;
+                    // (a row whose scores are near its reference keeps it)
+                    const float to = x > paged_limit(top) || tile_sum > kMost ? paged_reference(top, x)
+                                                                              : top;
                     const float a = ex2(top - to);
                     top = to;
                     sum *= a;
@@ -680,17 +711,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint64_t sums = 0ull;
 #pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
-                        const unsigned see = (q == 0 ? w[0] : q == 1 ? w[1] : q == 2 ? w[2] : w[3]) &
-                                             paged_bits(j0 + 32 * q, at, hi, P.window, P.sinks);
                         uint32_t y[32];
-                        tmem_ld32(s_tm + q * 32, y);
-                        tmem_wait_ld(y);
+                        scores(q, y);
                         if (apart) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
                                 y[e] = __float_as_uint(__fmul_rn(__uint_as_float(y[e]), factor));
                         }
-                        sums = probabilities<I, true>(y, see, apart ? 1.f : factor, top, sums);
+                        sums = probabilities<I>(y, apart ? 1.f : factor, top, sums);
                         tmem_st16(s_tm + q * 16, y);
                     }
                     float b;
@@ -729,34 +757,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 32; ++e) v[e] = sum == sum ? 0.f : NAN;
                 }
                 if (!live) continue;
-                if (odd) {      // NaN and infinities of positions that this row sees
-                    for (int i = A.tile; i < A.stop; ++i) {
-                        const int j0 = A.position(i);
-                        if (all_see(P, A.p0, A.p1, j0)) continue;
-#pragma unroll 1
-                        for (int j = j0; j < j0 + kPosTile; ++j) {
-                            if (!(paged_bits(j, at, A.hi, P.window, P.sinks) & 1)) continue;
-                            const int block = paged_page(P, A.b, j);
-                            if (block < 0 || block >= C.num_blocks) continue;
-                            const uint32_t off = j - P.by_page((uint32_t)j) * C.block_size;
-                            const int64_t e0 =
-                                block * C.v_block_stride +
-                                (int64_t)(C.layout == SPEC_KV_NHD ? off * C.H + A.head
-                                                                  : A.head * C.block_size + off) * C.D;
-#pragma unroll 1
-                            for (int d = q * 32; d < min(q * 32 + 32, C.D); ++d) {
-                                const float y =
-                                    KIND ? value16<2>(halves2<KIND>(__ldg(static_cast<const uint8_t *>(C.v) +
-                                                                         e0 + d)) & 0xffffu)
-                                         : value16<I>(__ldg(static_cast<const unsigned short *>(C.v) + e0 + d));
-                                if (fabsf(y) < INFINITY) continue;
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (e == d - q * 32) v[e] += y;
-                            }
-                        }
-                    }
-                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (q * 32 + h * 16 >= C.D) break;
@@ -789,6 +789,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     part[RT * DP + r] = top;
                     part[RT * (DP + 1) + r] = sum;
+                }
+            }
+            if (odd && live) {      // NaN and infinities of positions that this row sees
+                for (int i = tile0; i < A.stop; ++i) {
+                    const int j0 = A.position(i);
+                    if (all_see(P, A.p0, A.p1, j0)) continue;
+#pragma unroll 1
+                    for (int j = j0; j < j0 + kPosTile; ++j) {
+                        if (!(paged_bits(j, at, hi, P.window, P.sinks) & 1)) continue;
+                        const int block = paged_page(P, A.b, j);
+                        if (block < 0 || block >= C.num_blocks) continue;
+                        const uint32_t off = j - P.by_page((uint32_t)j) * C.block_size;
+                        const int64_t e0 = block * C.v_block_stride +
+                                           (int64_t)(C.layout == SPEC_KV_NHD ? off * C.H + A.head
+                                                                             : A.head * C.block_size + off) *
+                                               C.D;
+#pragma unroll 1
+                        for (int d = 0; d < C.D; ++d) {
+                            const float y =
+                                KIND ? value16<2>(halves2<KIND>(__ldg(static_cast<const uint8_t *>(C.v) +
+                                                                     e0 + d)) & 0xffffu)
+                                     : value16<I>(__ldg(static_cast<const unsigned short *>(C.v) + e0 + d));
+                            if (fabsf(y) < INFINITY) continue;
+                            if (whole) {
+                                unsigned short *o = static_cast<unsigned short *>(P.out) + to * C.D + d;
+                                *o = (unsigned short)pack2<T>(value16<T>(*o) + y, 0.f);
+                            } else {
+                                part[(int64_t)r * DP + d] += y;
+                            }
+                        }
+                    }
                 }
             }
             tc_fence_before();
@@ -824,9 +855,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) tmem_free(tmem, C_::kColumns);
 }
 
-// A tensor map of a 16-bit cache: boxes of 64 columns and `box` positions of one head and block.
-bool make_map(CUtensorMap &map, const spec_kv_cache &c, void *at, int64_t block_stride, int dtype,
-              int box) {
+// A tensor map of 16-bit elements with 128-byte swizzle: boxes of 64 x box[1] x ...; false if it
+// cannot be had.
+bool make_map(CUtensorMap &map, int dtype, const void *at, int rank, const cuuint64_t *dims,
+              const cuuint64_t *strides, const cuuint32_t *box) {
     using Encode = decltype(&cuTensorMapEncodeTiled);
     static const Encode encode = [] {
         void *f = nullptr;
@@ -838,18 +870,43 @@ bool make_map(CUtensorMap &map, const spec_kv_cache &c, void *at, int64_t block_
                                                                          : nullptr;
     }();
     if (!encode) return false;
-    const bool nhd = c.layout == SPEC_KV_NHD;
-    const cuuint64_t d = (cuuint64_t)c.D, h = (cuuint64_t)c.H, n = (cuuint64_t)c.block_size;
-    const cuuint64_t dims[4] = {d, nhd ? h : n, nhd ? n : h, (cuuint64_t)c.num_blocks};
-    const cuuint64_t strides[3] = {d * 2, (nhd ? h : n) * d * 2, (cuuint64_t)block_stride * 2};
-    const cuuint32_t boxes[4] = {64, nhd ? 1u : (cuuint32_t)box, nhd ? (cuuint32_t)box : 1u, 1};
+    for (int i = 0; i + 1 < rank; ++i)
+        if (strides[i] >= cuuint64_t(1) << 40) return false;
     const cuuint32_t ones[4] = {1, 1, 1, 1};
-    if (strides[2] >= cuuint64_t(1) << 40 || strides[1] >= cuuint64_t(1) << 40) return false;
     return encode(&map, dtype == SPEC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                  4, at, dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  (cuuint32_t)rank, const_cast<void *>(at), dims, strides, box, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+Maps make_maps(const PagedAttnParams &p) {
+    Maps m = {};
+    const spec_kv_cache &c = p.cache;
+    if (c.D < 64) return m;
+    const cuuint64_t d = (cuuint64_t)c.D, h = (cuuint64_t)c.H, n = (cuuint64_t)c.block_size;
+    // Pages of a multiple of eight positions: boxes of the largest power of two that divides both
+    // them and 32 (their places in shared memory begin where the swizzle's pattern does).
+    if (n % 8 == 0) {
+        const bool nhd = c.layout == SPEC_KV_NHD;
+        const cuuint32_t rows = n % 32 == 0 ? 32 : n % 16 == 0 ? 16 : 8;
+        const cuuint64_t dims[4] = {d, nhd ? h : n, nhd ? n : h, (cuuint64_t)c.num_blocks};
+        const cuuint32_t box[4] = {64, nhd ? 1 : rows, nhd ? rows : 1, 1};
+        cuuint64_t strides[3] = {d * 2, (nhd ? h : n) * d * 2, (cuuint64_t)c.k_block_stride * 2};
+        bool ok = make_map(m.k, p.dtype, c.k, 4, dims, strides, box);
+        strides[2] = (cuuint64_t)c.v_block_stride * 2;
+        ok = ok && make_map(m.v, p.dtype, c.v, 4, dims, strides, box);
+        if (ok) m.page_rows = (int)rows;
+    }
+    // Queries whose groups of heads divide 128 rows: boxes of whole tokens.
+    if (128 % p.G == 0 && reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.q_stride % 8 == 0) {
+        const cuuint64_t dims[3] = {d, (cuuint64_t)p.Hq, (cuuint64_t)p.T};
+        const cuuint64_t strides[2] = {d * 2, (cuuint64_t)p.q_stride * 2};
+        const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)(128 / p.G)};
+        if (make_map(m.q, p.dtype, p.q, 3, dims, strides, box)) m.tokens = 128 / p.G;
+    }
+    return m;
 }
 
 template <int T, int KIND, int DP>
@@ -859,19 +916,9 @@ cudaError_t launch(const PagedAttnParams &p, int grid, cudaStream_t st) {
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                C_::kBytes);
     if (e != cudaSuccess) return e;
-    const spec_kv_cache &c = p.cache;
     const int vec = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.q_stride % 8 == 0;
-    // Pages of a multiple of eight positions: boxes of the largest power of two that divides both
-    // them and 32 (their places in shared memory begin where the swizzle's pattern does).
-    Maps maps = {};
-    int box = 0;
-    if (KIND == 0 && c.block_size % 8 == 0 && c.D >= 64) {
-        box = c.block_size % 32 == 0 ? 32 : c.block_size % 16 == 0 ? 16 : 8;
-        if (!make_map(maps.k, c, c.k, c.k_block_stride, p.dtype, box) ||
-            !make_map(maps.v, c, c.v, c.v_block_stride, p.dtype, box))
-            box = 0;
-    }
-    paged_tc_kernel<T, KIND, DP><<<grid, kThreads, C_::kBytes, st>>>(p, vec, box, maps);
+    paged_tc_kernel<T, KIND, DP><<<grid, kThreads, C_::kBytes, st>>>(p, vec,
+                                                                   KIND ? Maps{} : make_maps(p));
     return cudaGetLastError();
 }
 
