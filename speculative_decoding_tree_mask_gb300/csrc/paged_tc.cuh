@@ -11,9 +11,9 @@
 //            positions are all wanted, else by asynchronous copies, whose addresses take any page
 //            size. 8-bit codes pass through registers and become halves. An item's queries come
 //            after its first tile, as soon as the scores of the item before are done;
-//   multiply (2 warps, a thread of each issues for one softmax group) S = Q K^T for 128 rows and a
-//            whole tile, then O += P V. Sums are in tensor memory: S and O twice, all 512 columns at
-//            D = 128; P overwrites the S it came from;
+//   multiply (2 warps, a thread of each issues for one softmax group) S = Q K^T for 128 rows and 64
+//            positions, two of them in turn, and O += P V. Sums are in tensor memory: two S and an O
+//            a group, all 512 columns at D = 128; P overwrites the S it came from;
 //   softmax  (2 groups of 4 warps) S to P, a row a thread, no exchange between threads, reference
 //            and sum in registers. The row's largest score is not looked for: a tile's sum tells
 //            when one has passed the reference by too much. Then, which is rare, and for an item's
@@ -21,11 +21,11 @@
 //   deal     (1 warp) the CTA's parts, one after another, as words in shared memory: up to four
 //            ahead, so that the others neither compute them nor hold them in registers.
 //
-// With S of 64 columns a product reads 6 KB of shared memory for 32 clocks of work and gets 48 clocks
-// of its bandwidth; with 128 columns 8 KB for 64 clocks, which is even. One group's softmax runs
-// beside the other's products. What is left is issue slots: a tile's products take 2048 clocks, and
-// a form with the rows' maxima, copies by address and the dealing in every warp issued 2470
-// instructions a scheduler meanwhile.
+// While softmax works on one S, the tensor core multiplies with the P before and makes the next
+// scores: with one S of 128 columns a group it had to wait for softmax, and softmax for it (2.2 us a
+// tile where products and shared memory need 1.1). The price is that a product of 64 columns reads
+// 6 KB of shared memory for 32 clocks of work and gets 48: a tile's reads and writes take 2560
+// clocks, its products 2048.
 //
 // Items of up to 128 rows (a decoding request in a mixed batch) leave the second group idle, and
 // warps without a live row touch nothing: a tile then takes less time than its bytes do.
@@ -79,7 +79,7 @@ struct Words {
     PartWords part[kDealt];
     uint64_t part_full[kDealt], part_free[kDealt];
     uint64_t q_full, q_free, full[kRing], free[kRing], drain[2];
-    uint64_t s_full[2], p_full[2];                               // of a softmax group
+    uint64_t s_full[2][2], p_full[2][2], o_full[2];              // of a softmax group; its two S
     uint64_t o_last[2];                                          // once a part
     // Positions of a tile that are there. K's loader writes a tile's words again for the fourth
     // after it, whose place was that of a V whose products are done.
@@ -128,7 +128,9 @@ __device__ __forceinline__ bool all_see(const PagedAttnParams &P, int p0, int p1
 // holds. There the products are rounded alike first.
 constexpr float kApart = 1048576.f;
 
-// What the sum of a tile's probabilities may come to without its largest being looked for.
+constexpr int kHalf = 64 * 128;   // bytes from the first 64 rows of an operand to the others
+
+// What the sum of 64 probabilities may come to without its largest being looked for.
 constexpr float kMost = 32768.f;
 
 // 32 scores of a row to probabilities 2^(f s - top), packed; returns their sum.
@@ -146,12 +148,6 @@ __device__ __forceinline__ uint64_t probabilities(uint32_t (&s)[32], float f, fl
         s[e / 2] = pack2<I>(a, b);
     }
     return sum;
-}
-// -inf where `see` has no bit.
-__device__ __forceinline__ void mask32(uint32_t (&s)[32], unsigned see) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e)
-        if (!((see >> e) & 1)) s[e] = 0xff800000u;
 }
 __device__ __forceinline__ float largest32(const uint32_t (&s)[32]) {
     float big[2] = {-INFINITY, -INFINITY};
@@ -216,9 +212,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(&W.drain[i], 1);
-            bar_init(&W.s_full[i], 1);
+            bar_init(&W.o_full[i], 1);
             bar_init(&W.o_last[i], 1);
-            bar_init(&W.p_full[i], 4);
+            for (int j = 0; j < 2; ++j) {
+                bar_init(&W.s_full[i][j], 1);
+                bar_init(&W.p_full[i][j], 4);
+            }
         }
         for (int i = 0; i < kDealt; ++i) {
             bar_init(&W.part_full[i], 1);
@@ -239,7 +238,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = W.tmem;
     volatile int *gave_up = &W.gave_up;
-    // tensor memory of softmax group m: S (and P over it) at 128 m, O behind both groups'
+    // tensor memory of softmax group m: two S of 64 columns (and P over each) at 128 m, O behind both
+    // groups'
     auto s_at = [&](int m) { return tmem + 128 * m; };
     auto o_at = [&](int m) { return tmem + 256 + DP * m; };
     // tiles of K and V take the ring's places in turn: K of tile c is the 2c-th, V the next
@@ -250,8 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto dealt = [&](uint32_t x) { return warp_wait(&W.part_full[x % kDealt], x / kDealt & 1, gave_up); };
     auto read = [&](uint32_t x) { warp_arrive(&W.part_free[x % kDealt]); };
 
-    // Launched with 96 registers a thread, 20 warps: 8 x 168 + 8 x 48 + 4 x 48 = 20 x 96, and
-    // 8 x 152 + 8 x 64 + 4 x 48 where a loading thread holds codes.
+    // Launched with 96 registers a thread, 20 warps: 8 x 128 + 8 x 88 + 4 x 48 = 20 x 96.
     if (tid >= kSoftmax + kLoad) {
         fewer_registers<48>();
         const int m = warp - kMmaWarp;
@@ -279,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // thread of it issues: what the products are given is then the same in all of the warp.
             const bool lead = elect_one();
             const uint32_t o = o_at(m), s = s_at(m);
-            uint32_t mine = 0;           // tiles of this group before this one
+            uint32_t jobs = 0;           // of this group before this part; a job is 64 positions
             bool ok = true;
             for (uint32_t part = 0;; ++part) {
                 ok = ok && dealt(part);
@@ -306,46 +305,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++parts;
                     continue;
                 }
-                auto scores = [&](int i) {
-                    const uint32_t x = 2 * (done + i);
-                    ok = ok && warp_wait(&W.full[slot(x)], phase(x), gave_up);
+                const int count = 2 * n;
+                auto scores = [&](int j) {
+                    const uint32_t x = 2 * (done + (j >> 1)), buf = (jobs + j) & 1;
+                    if ((j & 1) == 0)             // a tile's second half came with its first
+                        ok = ok && warp_wait(&W.full[slot(x)], phase(x), gave_up);
                     if (!ok) return;              // no products of what did not come
                     const uint64_t a = smem_desc(base + m * C_::kOperand, 16, 1024);
-                    const uint64_t k = smem_desc(base + C_::kTiles + slot(x) * C_::kOperand, 16, 1024);
+                    const uint64_t k = smem_desc(
+                        base + C_::kTiles + slot(x) * C_::kOperand + (j & 1) * kHalf, 16, 1024);
                     if (lead) {
 #pragma unroll
                         for (int d = 0; d < KS; ++d) {
                             const int off = (d >> 2) * (128 * 128) + (d & 3) * 32;
-                            mma_ss(s, desc_plus(a, off), desc_plus(k, off),
-                                   mma_desc(kType, 128, false), d > 0);
+                            mma_ss(s + buf * 64, desc_plus(a, off), desc_plus(k, off),
+                                   mma_desc(kType, 64, false), d > 0);
                         }
-                        mma_commit(&W.s_full[m]);
-                        mma_commit(&W.free[slot(x)]);
-                        if (i == n - 1) mma_commit(&W.q_free);
+                        mma_commit(&W.s_full[m][buf]);
+                        if (j & 1) mma_commit(&W.free[slot(x)]);
+                        if (j == count - 1) mma_commit(&W.q_free);
                     }
                     __syncwarp();
                 };
                 scores(0);
-                for (int i = 0; ok && i < n; ++i) {
-                    const uint32_t x = 2 * (done + i) + 1;
-                    ok = warp_wait(&W.full[slot(x)], phase(x), gave_up);
-                    const uint64_t v = smem_desc(base + C_::kTiles + slot(x) * C_::kOperand,
-                                                 128 * 128, 1024);
-                    ok = ok && warp_wait(&W.p_full[m], mine & 1, gave_up);
+                scores(1);
+                for (int j = 0; ok && j < count; ++j) {
+                    const uint32_t x = 2 * (done + (j >> 1)) + 1, buf = (jobs + j) & 1;
+                    if ((j & 1) == 0) ok = warp_wait(&W.full[slot(x)], phase(x), gave_up);
+                    ok = ok && warp_wait(&W.p_full[m][buf], (jobs + j) >> 1 & 1, gave_up);
                     if (!ok) break;
                     tc_fence_after();
+                    const uint64_t v = smem_desc(
+                        base + C_::kTiles + slot(x) * C_::kOperand + (j & 1) * kHalf, 128 * 128, 1024);
                     if (lead) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mma_ts(o, s + k * 8, desc_plus(v, k * 2048), mma_desc(kType, DP, true),
-                                   i > 0 || k > 0);
-                        if (i == n - 1) mma_commit(&W.o_last[m]);
-                        mma_commit(&W.free[slot(x)]);
+                        for (int k = 0; k < 4; ++k)
+                            mma_ts(o, s + buf * 64 + k * 8, desc_plus(v, k * 2048),
+                                   mma_desc(kType, DP, true), j > 0 || k > 0);
+                        mma_commit(&W.o_full[m]);
+                        if (j == count - 1) mma_commit(&W.o_last[m]);
+                        if (j & 1) mma_commit(&W.free[slot(x)]);
                     }
                     __syncwarp();
-                    ++mine;
-                    if (ok && i + 1 < n) scores(i + 1);
+                    if (j + 2 < count) scores(j + 2);
                 }
+                jobs += count;
                 done += n;
                 ++parts;
             }
@@ -358,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         }
     } else if (tid >= kSoftmax) {
-        fewer_registers<KIND ? 64 : 48>();
+        fewer_registers<88>();
         // ---- load: K or V, 32 positions a warp ----
         const bool of_v = tid >= kSoftmax + kLoad / 2;
         const int w4 = (tid - kSoftmax) % (kLoad / 2) / 32;
@@ -505,7 +509,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             if (of_v && lane == 0 && w4 == 0) W.odd[(parts + 4) & 7] = 0;
             if constexpr (KIND == 0) {
-                int next = page(0);
+                int next = page(0), pending = -1;     // a tile whose copies are waited for later
+                auto settle = [&](bool behind) {
+                    if (pending < 0) return;
+                    if (behind) asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    __syncwarp();     // the warp's copies, all lanes'
+                    if (go) arrived(pending);
+                    pending = -1;
+                };
                 for (int i = 0; i < n; ++i) {
                     const int block = next;
                     next = page(i + 1);
@@ -513,15 +525,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     go = go && warp_wait(&W.free[slot(x)], phase(x) ^ 1, gave_up);
                     const int j0 = A.position(A.tile + i);
                     const uint32_t place = C_::kTiles + slot(x) * C_::kOperand + w4 * (32 * 128);
-                    if (go && box > 0 && __all_sync(0xffffffffu, block >= 0) &&
-                        !(of_v && !all_see(P, A.p0, A.p1, j0))) {
+                    const unsigned wanted = __ballot_sync(0xffffffffu, block >= 0);
+                    // Of K what is not wanted may be anything; of V it has to be zeros, and what some
+                    // rows alone see is looked through.
+                    if (go && box > 0 &&
+                        (!of_v || (wanted == 0xffffffffu && all_see(P, A.p0, A.p1, j0)))) {
                         // `box` rows of a page a time (they divide 32 and the page), 64 columns
                         note(i, block);
-                        if (lane == 0) bar_expect(&W.full[slot(x)], 32 * DP * 2);
-                        __syncwarp();
                         const int g = lane / (DP / 64), q = lane % (DP / 64), t = g * box;
-                        const int blk = __shfl_sync(0xffffffffu, block, t & 31);
-                        if (t < 32) {
+                        const unsigned some = t < 32 ? wanted >> t & (0xffffffffu >> (32 - box)) : 0u;
+                        const int blk = __shfl_sync(0xffffffffu, block,
+                                                    some ? t + __ffs(some) - 1 : 0);
+                        const unsigned mine = __ballot_sync(0xffffffffu, some != 0u);
+                        if (lane == 0) {
+                            if (mine) bar_expect(&W.full[slot(x)], __popc(mine) * box * 128);
+                            else bar_arrive(&W.full[slot(x)]);
+                        }
+                        __syncwarp();
+                        if (some) {
                             const uint32_t p = (uint32_t)(j0 + w4 * 32 + t);
                             const int off = (int)(p - P.by_page(p) * C.block_size);
                             const bool nhd = C.layout == SPEC_KV_NHD;
@@ -529,22 +550,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     q * 64, nhd ? A.head : off, nhd ? off : A.head, blk,
                                     &W.full[slot(x)]);
                         }
-                    } else if (go) {
-                        note(i, block);
-                        const uint32_t in = unit(i);
+                        settle(false);
+                    } else {
+                        if (go) {
+                            note(i, block);
+                            const uint32_t in = unit(i);
 #pragma unroll 4
-                        for (int q = 0; q < U; ++q) {
-                            const int t = (q * 32 + lane) / U, u = lane % U;
-                            bool ok;
-                            const char *from = source(block, in, t, u, ok);
-                            copy16(base + place + chunk_at(t, u), from, ok);
+                            for (int q = 0; q < U; ++q) {
+                                const int t = (q * 32 + lane) / U, u = lane % U;
+                                bool ok;
+                                const char *from = source(block, in, t, u, ok);
+                                copy16(base + place + chunk_at(t, u), from, ok);
+                            }
                         }
-                        asm volatile("cp.async.wait_all;" ::: "memory");
-                        __syncwarp();     // the warp's copies, all lanes'
-                        arrived(i);
+                        asm volatile("cp.async.commit_group;" ::: "memory");
+                        settle(true);
+                        pending = i;
                     }
-                    if (i == 0) queries();
+                    if (i == 0) {
+                        queries();
+                        settle(false);
+                    }
                 }
+                settle(false);
             } else {
                 // a tile's codes wait in registers for its place
                 constexpr int Q = U;                          // chunks of a thread
@@ -596,15 +624,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else {
-        more_registers<KIND ? 152 : 168>();
+        more_registers<128>();
         // ---- softmax: this thread's row. A wait that gives up is followed by none.
         const int m = warp >> 2;
         const int r = m * 128 + (warp & 3) * 32 + lane;          // of the item
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t o_tm = o_at(m) + lanes, s_tm = s_at(m) + lanes;
+        const uint32_t o_tm = o_at(m) + lanes;
         const float v_scale = C.v_scale ? __ldg(C.v_scale) : 1.f;
         const float unit = P.scale * kLog2e * (C.k_scale ? __ldg(C.k_scale) : 1.f);
-        uint32_t mine = 0, results = 0;   // tiles of this group so far; parts
+        uint32_t jobs = 0, results = 0;   // of this group so far (64 positions each); parts
         bool go = true;
         uint32_t part_at = 0;
         for (;; ++part_at) {
@@ -619,84 +647,86 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int at = paged_position(P, A.pos, row0 + min(r, A.rows - 1));
             float top = kPagedNoMax, sum = 0.f, factor = 0.f;    // top: the row's reference
             bool apart = false;       // a row of the warp has scores beyond kApart
-            // every row sees all of a tile that ends at p0 at most and begins past the edge of the
+            // every row sees all of a job that ends at p0 at most and begins past the edge of the
             // last row's window, or is the sinks'
             const int p0 = A.p0, edge = P.window > 0 ? A.p1 - P.window : INT_MIN, hi = A.hi;
-            for (int i = 0; work && i < n; ++i, ++mine) {
-                go = go && warp_wait(&W.s_full[m], mine & 1, gave_up);
+            for (int j = 0; work && j < 2 * n; ++j, ++jobs) {
+                const int i = j >> 1, h = j & 1;
+                const uint32_t buf = jobs & 1, s_tm = s_at(m) + lanes + buf * 64;
+                go = go && warp_wait(&W.s_full[m][buf], jobs >> 1 & 1, gave_up);
                 if (!go) break;
                 tc_fence_after();
-                if (i == 0)
+                if (j == 0)
                     factor = paged_factor(
                         kScaleQ ? unit * __uint_as_float((uint32_t)W.q_down[parts & 1][r] << 16) : unit);
                 if (!warp_live) {
                     tc_fence_before();
-                    warp_arrive(&W.p_full[m]);
+                    warp_arrive(&W.p_full[m][buf]);
                     continue;
                 }
-                const int ti = tile0 + i, j0 = (ti < skip ? ti : base_tile + ti) * kPosTile;
-                const uint4 there = *reinterpret_cast<const uint4 *>(W.seen[(done + i) & 3]);
-                const bool plain =
-                    (there.x & there.y & there.z & there.w) == 0xffffffffu &&
-                    j0 + kPosTile - 1 <= p0 && (j0 > edge || j0 + kPosTile - 1 < P.sinks);
-                const unsigned w[4] = {there.x, there.y, there.z, there.w};
-                float tile_sum = INFINITY;
+                const int ti = tile0 + i, j0 = (ti < skip ? ti : base_tile + ti) * kPosTile + 64 * h;
+                const uint2 there = *reinterpret_cast<const uint2 *>(&W.seen[(done + i) & 3][2 * h]);
+                const bool plain = (there.x & there.y) == 0xffffffffu && j0 + 63 <= p0 &&
+                                   (j0 > edge || j0 + 63 < P.sinks);
+                auto mask = [&](int q, uint32_t (&y)[32]) {
+                    const unsigned see = (q ? there.y : there.x) &
+                                         paged_bits(j0 + 32 * q, at, hi, P.window, P.sinks);
+                    if (__all_sync(0xffffffffu, see == 0xffffffffu)) return;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (!((see >> e) & 1)) y[e] = 0xff800000u;
+                };
+                float job_sum = INFINITY;
                 // P by the reference at hand, kept if no score was too far above it.
                 if (!apart) {
-                    uint32_t x[4][32];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld32(s_tm + q * 32, x[q]);
+                    uint32_t x[2][32];
+                    tmem_ld32(s_tm, x[0]);
+                    tmem_ld32(s_tm + 32, x[1]);
                     tmem_wait_ld(x[0]);
-#pragma unroll
-                    for (int q = 1; q < 4; ++q) tmem_loaded(x[q]);
+                    tmem_loaded(x[1]);
                     if (!plain) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            mask32(x[q], w[q] & paged_bits(j0 + 32 * q, at, hi, P.window, P.sinks));
+                        mask(0, x[0]);
+                        mask(1, x[1]);
                     }
-                    if (i == 0) {
-                        const float big = fmaxf(fmaxf(largest32(x[0]), largest32(x[1])),
-                                                fmaxf(largest32(x[2]), largest32(x[3])));
+                    if (j == 0) {
+                        const float big = fmaxf(largest32(x[0]), largest32(x[1]));
                         top = paged_reference(kPagedNoMax, fmaxf(kPagedNoMax, big * factor));
                         apart = __any_sync(0xffffffffu, fabsf(top) > kApart && top != kPagedNoMax);
                     }
-                    uint64_t sums[2] = {0ull, 0ull};
+                    uint64_t sums[2];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        sums[q & 1] = probabilities<I>(x[q], factor, top, sums[q & 1]);
+                    for (int q = 0; q < 2; ++q) sums[q] = probabilities<I>(x[q], factor, top, 0ull);
                     float a, b;
                     unpack_f32x2(add_f32x2(sums[0], sums[1]), a, b);
-                    tile_sum = apart ? INFINITY : a + b;
-                    if (__all_sync(0xffffffffu, tile_sum <= kMost)) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) tmem_st16(s_tm + q * 16, x[q]);
+                    job_sum = apart ? INFINITY : a + b;
+                    if (__all_sync(0xffffffffu, job_sum <= kMost)) {
+                        tmem_st16(s_tm, x[0]);
+                        tmem_st16(s_tm + 16, x[1]);
                     }
                 }
-                if (__any_sync(0xffffffffu, !(tile_sum <= kMost))) {
-                    // The scores again: their largest raises the reference; P of 32 positions takes
-                    // the place of 16 that have been read.
+                if (__any_sync(0xffffffffu, !(job_sum <= kMost))) {
+                    // The scores again: their largest raises the references of all the warp's rows; P
+                    // of 32 positions takes the place of 16 that have been read.
                     float x = kPagedNoMax;
                     auto scores = [&](int q, uint32_t (&y)[32]) {
                         tmem_ld32(s_tm + q * 32, y);
                         tmem_wait_ld(y);
-                        mask32(y, (q == 0 ? w[0] : q == 1 ? w[1] : q == 2 ? w[2] : w[3]) &
-                                      paged_bits(j0 + 32 * q, at, hi, P.window, P.sinks));
+                        mask(q, y);
                     };
 #pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < 2; ++q) {
                         uint32_t y[32];
                         scores(q, y);
                         x = fmaxf(x, largest32(y) * factor);
                     }
-                    // (a row whose scores are near its reference keeps it)
-                    const float to = x > paged_limit(top) || tile_sum > kMost ? paged_reference(top, x)
-                                                                              : top;
-                    const float a = ex2(top - to);
+                    const float to = paged_reference(top, x), a = ex2(top - to);
                     top = to;
                     sum *= a;
                     apart = apart || __any_sync(0xffffffffu, fabsf(top) > kApart && top != kPagedNoMax);
-                    // O so far: the scores at hand were made after all its products
-                    if (i > 0) {
+                    if (j > 0) {
+                        // the scores at hand were made after the product two before this one's
+                        go = go && warp_wait(&W.o_full[m], (jobs - 1) & 1, gave_up);
+                        tc_fence_after();
 #pragma unroll 1
                         for (int q = 0; q < DP / 16; ++q) {
                             uint32_t o[16];
@@ -710,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     uint64_t sums = 0ull;
 #pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < 2; ++q) {
                         uint32_t y[32];
                         scores(q, y);
                         if (apart) {
@@ -722,13 +752,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_st16(s_tm + q * 16, y);
                     }
                     float b;
-                    unpack_f32x2(sums, tile_sum, b);
-                    tile_sum += b;
+                    unpack_f32x2(sums, job_sum, b);
+                    job_sum += b;
                 }
-                sum += tile_sum;
+                sum += job_sum;
                 tmem_wait_st();
                 tc_fence_before();
-                warp_arrive(&W.p_full[m]);
+                warp_arrive(&W.p_full[m][buf]);
             }
             // The result: O is done after the group's last product.
             if (work) go = go && warp_wait(&W.o_last[m], results++ & 1, gave_up);
