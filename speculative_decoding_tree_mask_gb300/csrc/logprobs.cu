@@ -8,12 +8,16 @@
 //
 // The likeliest K tokens need no second pass and no sorting of the row. Every thread keeps its own
 // maximum and, for each group of vectors it reads, the group's maximum (shared memory). The K-th
-// largest of the threads' maxima is a bound: K tokens at least are not below it, about K in all.
-// Only groups that reach it are read again (a few KB, from L2), and what passes the bound is sorted,
+// largest of the threads' maxima is a bound: K tokens at least are not below it, hardly more in all.
+// (Maxima of eight threads each are sorted sooner, but let more pass: K = 32 took 278 us for 248.)
+// Only groups that reach it are read again, a few KB from L2, a vector a thread and all at once (by
+// the threads they belong to, one after another, 4096 rows took 291 us for 236); what passes is sorted,
 // 64-bit keys of the value and the lower index, so that no arrival order changes the result. Where
 // too many tokens pass (equal logits), the K-th key of those at hand is the next bound.
 //
-// DRAM bounds it. A row has a CTA, or with few rows a cluster of up to eight CTAs, whose parts meet
+// DRAM bounds it: 4096 rows of 152064 bfloat16 logits, 8 tokens each, 236 us, 5.3 TB/s (78% of the
+// measured copy), without tokens 207 us. What is left is each row's end, during which its CTA loads
+// nothing: six CTAs an SM are what registers allow (four 256 us). A row has a CTA, or with few rows a cluster of up to eight CTAs, whose parts meet
 // in distributed shared memory (no workspace, no atomics on memory).
 
 #include "spec_device.cuh"
@@ -27,10 +31,11 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;          // vectors of a thread in flight
 constexpr int kGroups = 32;         // groups of a thread whose maxima are kept
 constexpr int kCandidates = 1024;
+constexpr int kHits = 512;          // groups read again together
 constexpr float kFar = -200.f;
 constexpr float kLn2 = 0.6931471805599453f;
-// CTAs of an SM: four with 64 registers a thread keep 64 KB of loads in flight.
-constexpr int kCtas = 4;
+// CTAs of an SM: while one orders its likeliest tokens the others have to keep the loads in flight.
+constexpr int kCtas = 6;
 
 __device__ __forceinline__ uint32_t order_of(float x) {     // increasing in x; -0 counts as 0
     const uint32_t u = __float_as_uint(x + 0.f);
@@ -171,7 +176,8 @@ struct Shared {
     uint32_t maxima[kWarps][32];
     unsigned long long best[32];              // the CTA's likeliest, sorted; 0: none
     unsigned long long bound;
-    int count;
+    int count, hits;
+    unsigned short hit[kHits];                // a thread's group: group << 8 | thread
     unsigned long long key[kCandidates];
 };
 
@@ -261,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(LogprobsParam
     if (lane == 0) S.part[warp] = p;
     if (TOP) {
         S.maxima[warp][lane] = sort_down(order_of(a.m));
-        if (tid == 0) S.count = 0;
+        if (tid == 0) S.count = S.hits = 0;
     }
     __syncthreads();
     if (warp == 0) {
@@ -297,29 +303,42 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(LogprobsParam
                     if (n < kCandidates) S.key[n] = key;
                 }
             };
+            auto offer_vector = [&](int i) {
+                const uint4 w = __ldg(vec + i);
+                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                const int e0 = head + i * E;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (DT == 1) {
+                        offer(bf_lo(ws[q]), e0 + 2 * q);
+                        offer(bf_hi(ws[q]), e0 + 2 * q + 1);
+                    } else {
+                        offer(__uint_as_float(ws[q]), e0 + q);
+                    }
+                }
+            };
+            const int of_group = per * kUnroll;      // vectors of a group
             if (order_of(a.m) >= low) {
                 if (at >= 0) offer(lone, at);
                 const int groups = (rounds + per - 1) / max(per, 1);
                 for (int g = 0; g < groups; ++g) {
                     if (order_of(group_max[g * kThreads + tid]) < low) continue;
-                    const int n0 = g * per * kUnroll;
-                    for (int n = n0; n < n0 + per * kUnroll; ++n) {
-                        const int i = v0 + n * kThreads + tid;
-                        if (i >= v1) break;
-                        const uint4 w = __ldg(vec + i);
-                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-                        const int e0 = head + i * E;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if (DT == 1) {
-                                offer(bf_lo(ws[q]), e0 + 2 * q);
-                                offer(bf_hi(ws[q]), e0 + 2 * q + 1);
-                            } else {
-                                offer(__uint_as_float(ws[q]), e0 + q);
-                            }
-                        }
+                    const int k = atomicAdd(&S.hits, 1);
+                    if (k < kHits) {
+                        S.hit[k] = (unsigned short)(g << 8 | tid);
+                        continue;
                     }
+                    for (int n = g * of_group; n < (g + 1) * of_group; ++n)
+                        if (v0 + n * kThreads + tid < v1) offer_vector(v0 + n * kThreads + tid);
                 }
+            }
+            __syncthreads();
+            // a vector a thread: all that are read again are under way at once
+            const int hits = min(S.hits, kHits) * of_group;
+            for (int k = tid; k < hits; k += kThreads) {
+                const int hit = S.hit[k / of_group], n = (hit >> 8) * of_group + k % of_group;
+                const int i = v0 + n * kThreads + (hit & (kThreads - 1));
+                if (i < v1) offer_vector(i);
             }
             __syncthreads();
             const int count = S.count;
@@ -331,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(LogprobsParam
                     v = merge_down(v, sort_down(i + lane < n ? S.key[i + lane] : 0ull));
                 S.best[lane] = v;
                 if (lane == P.top - 1) S.bound = v;
-                if (lane == 0) S.count = 0;
+                if (lane == 0) S.count = S.hits = 0;
             }
             __syncthreads();
             // more than fit: those at or above the K-th of the ones at hand are fewer

@@ -4,6 +4,10 @@
 namespace specv {
 namespace {
 
+constexpr int kFewRows = 32;
+// ... and beside a launch on the tensor cores (16: one token of up to 16 heads a group)
+int few_beside(int G) { return G <= 16 ? 16 : kFewRows; }
+
 // The parts of cut items into the result. A thread has a float4 of a row and, of the parts,
 // every PG-th, eight of them in flight together; the PG threads of a float4 meet in shared
 // memory. PG is 1 for items of few parts and many rows.
@@ -89,16 +93,15 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (P.lse && d4 == 0) P.lse[at] = paged_lse(m, l);
 }
 
-// How a call is run: by the warps' matrix unit up to 32 rows an item, beyond on the tcgen05 tensor
+// How requests are run: by the warps' matrix unit up to 32 rows an item, beyond on the tcgen05 tensor
 // cores, which have no form for D above 128 (Q, K and V tiles do not fit in shared memory together).
 struct Plan {
     int mt, rows, grid;     // groups of 16 rows of an item, 0: tcgen05; rows; CTAs
 };
-Plan plan(int max_new, int G, int D, int kind, int sms) {
+Plan plan(int64_t R, int D, int kind, int sms) {      // R: most rows a head
     Plan p;
     const int DP = paged_padded(D);
-    const int64_t R = (int64_t)max_new * G;
-    p.mt = DP == 256 ? 1 : R > 32 ? 0 : R > 16 ? 2 : 1;
+    p.mt = DP == 256 ? 1 : R > kFewRows ? 0 : R > 16 ? 2 : 1;
     p.rows = p.mt ? 16 * p.mt : kPagedTcRows;
     p.grid = sms * (p.mt ? paged_few_ctas(kind != SPEC_CACHE_SAME, DP) : 1);
     return p;
@@ -107,7 +110,7 @@ Plan plan(int max_new, int G, int D, int kind, int sms) {
 template <int T, int DP>
 cudaError_t launch_join(const PagedAttnParams &p, const Plan &n, cudaStream_t st) {
     constexpr int F = DP / 4, PG = DP == 256 ? 4 : 8;
-    const int64_t R = (int64_t)p.max_new * p.G;
+    const int64_t R = (int64_t)p.max_new * p.G < p.rows_most ? (int64_t)p.max_new * p.G : p.rows_most;
     const int rows = (int)(R < n.rows ? R : n.rows), per = kJoinThreads / F;
     const int64_t items = (int64_t)p.B * p.cache.H;
     if (n.grid > 8 * items && rows <= 32)
@@ -124,22 +127,11 @@ int64_t plan_bytes(const Plan &n, int D) {
     return notes_bytes(n) + (bytes + 255) / 256 * 256;
 }
 
-}  // namespace
-
-int64_t paged_attn_workspace(int max_new, int G, int D, int sms) {
-    int64_t most = 256;       // whatever the cache's type
-    for (int kind = 0; kind < 2; ++kind) {
-        const int64_t b = plan_bytes(plan(max_new, G, D, kind, sms), D);
-        most = b > most ? b : most;
-    }
-    return most;
-}
-
-cudaError_t launch_paged_attn(const PagedAttnParams &given, cudaStream_t st) {
-    if (given.B <= 0) return cudaSuccess;
-    PagedAttnParams p = given;
+// One launch and its joining, over requests of more than rows_over and at most rows_most rows.
+cudaError_t run(PagedAttnParams p, const Plan &n, int rows_over, int rows_most, cudaStream_t st) {
     const int DP = paged_padded(p.cache.D);
-    const Plan n = plan(p.max_new, p.G, p.cache.D, p.cache.kind, p.sms);
+    p.rows_over = rows_over;
+    p.rows_most = rows_most;
     p.notes = static_cast<int4 *>(p.workspace);
     p.ws = reinterpret_cast<float *>(static_cast<char *>(p.workspace) + notes_bytes(n));
     const bool bf16 = p.dtype == SPEC_BF16;
@@ -148,13 +140,45 @@ cudaError_t launch_paged_attn(const PagedAttnParams &given, cudaStream_t st) {
                           : bf16 ? launch_paged_few_bf16(p, n.mt, n.grid, st)
                                  : launch_paged_few_f16(p, n.mt, n.grid, st);
     if (e != cudaSuccess) return e;
-    if (p.dtype == 1)
+    if (bf16)
         return DP == 64    ? launch_join<1, 64>(p, n, st)
                : DP == 128 ? launch_join<1, 128>(p, n, st)
                            : launch_join<1, 256>(p, n, st);
     return DP == 64    ? launch_join<2, 64>(p, n, st)
            : DP == 128 ? launch_join<2, 128>(p, n, st)
                        : launch_join<2, 256>(p, n, st);
+}
+
+}  // namespace
+
+// A batch may hold requests of few rows and of many; which, the device knows alone. Where it may
+// hold both, both kernels are launched and take their own: 22 decoding requests over up to 12000
+// positions beside two chunks of 512 tokens (D = 64, 8 K/V heads) took 218 us when the tensor cores
+// had a tile of 256 rows for four.
+int64_t paged_attn_workspace(int max_new, int G, int D, int sms) {
+    const int64_t R = (int64_t)max_new * G;
+    int64_t most = 256;       // whatever the cache's type and the batch
+    for (int kind = 0; kind < 2; ++kind) {
+        int64_t bytes = plan_bytes(plan(R, D, kind, sms), D);
+        if (R > kFewRows && paged_padded(D) <= 128)
+            bytes += plan_bytes(plan(few_beside(G), D, kind, sms), D);
+        most = bytes > most ? bytes : most;
+    }
+    return most;
+}
+
+cudaError_t launch_paged_attn(const PagedAttnParams &given, cudaStream_t st) {
+    if (given.B <= 0 || given.T <= 0) return cudaSuccess;
+    PagedAttnParams p = given;
+    const int64_t R = (int64_t)p.max_new * p.G;
+    const Plan n = plan(R, p.cache.D, p.cache.kind, p.sms);
+    // (a batch as large as its largest requests has those alone)
+    const bool both = n.mt == 0 && p.T < (int64_t)p.B * p.max_new;
+    const int few = few_beside(p.G);
+    const cudaError_t e = run(p, n, both ? few : 0, INT32_MAX, st);
+    if (!both || e != cudaSuccess) return e;
+    p.workspace = static_cast<char *>(p.workspace) + plan_bytes(n, p.cache.D);
+    return run(p, plan(few, p.cache.D, p.cache.kind, p.sms), 0, few, st);
 }
 
 }  // namespace specv

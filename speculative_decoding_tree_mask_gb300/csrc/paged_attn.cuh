@@ -9,7 +9,8 @@
 //   w(r) = G fixed + min(G seq_pos + (r + 1) rows, what a window can span),
 // and the total weight, in the items' order, is cut into equal ranges, one for each CTA of a single
 // wave, whatever the requests' sizes (which only the device knows). A cut inside an item falls
-// between two of its tiles, the same one for both CTAs. Whole items are finished in place; the parts
+// between two of its tiles, the same one for both CTAs. (Short items left whole cost more than their
+// joining: 256 of up to 8 tiles took 50 us in one CTA each, 37 cut.) Whole items are finished in place; the parts
 // of a cut item go to the workspace (row sums and references and the unnormalised rows, float32),
 // and a second kernel joins them in their order.
 #pragma once
@@ -41,6 +42,10 @@ __device__ __forceinline__ int paged_req(const PagedAttnParams &P, int b, PagedR
         return SPEC_REQ_BAD_RANGE;
     }
     q.n = end - first;
+    if (q.n * P.G <= P.rows_over || q.n * P.G > P.rows_most) {      // another launch's
+        q.n = 0;
+        return 0;
+    }
     const int most = P.cache.max_blocks * P.cache.block_size;   // fits: checked on the host
     return q.n > 0 && (q.pos < 0 || (int64_t)q.pos + q.n > most) ? SPEC_REQ_BAD_SLOT : 0;
 }
@@ -372,7 +377,7 @@ inline int paged_padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 // Few rows (paged_few.cuh): CTAs an SM holds, by shared memory and registers; the launches, mt
 // groups of 16 rows an item.
 constexpr int paged_few_ctas(bool fp8, int DP) {
-    return DP == 64 ? 3 : DP == 128 ? 2 : fp8 ? 2 : 1;
+    return DP * (fp8 ? 1 : 2) <= 64 ? 3 : DP * (fp8 ? 1 : 2) <= 256 ? 2 : 1;
 }
 cudaError_t launch_paged_few_bf16(const PagedAttnParams &p, int mt, int grid, cudaStream_t st);
 cudaError_t launch_paged_few_f16(const PagedAttnParams &p, int mt, int grid, cudaStream_t st);

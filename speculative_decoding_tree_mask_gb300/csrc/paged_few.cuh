@@ -6,10 +6,10 @@
 // rows, and DRAM bounds it: 4 D bytes a position (2 D over an 8-bit cache) against 4 D operations a
 // row.
 //
-// A CTA is four warps; each takes 32 of a tile's 128 positions, 16 at a time, and keeps its own
-// references, sums and output in registers: the main loop has no barrier. Each warp has a ring of
-// its own in shared memory that asynchronous copies fill, 16 positions of K and V a place (8 KB at
-// D = 128), so that an SM keeps about 128 KB in flight. Products are m16n8k16 with the queries as
+// A CTA is four warps; each takes 32 of a tile's 128 positions, 16 or all 32 at a time, and keeps its
+// own references, sums and output in registers: the main loop has no barrier. Each warp has a ring of
+// its own in shared memory that asynchronous copies fill, 8 KB of K and V a place (16 positions at
+// D = 128, 32 of half that size), so that an SM keeps about 128 KB in flight. Products are m16n8k16 with the queries as
 // the 16 rows: with 8 rows an item half of that work is lost, but it is a tenth of what the time of
 // the bytes allows. Block-table entries are fetched a step before their copies.
 //
@@ -40,9 +40,10 @@ struct Few {
     static constexpr int kRows = 16 * MT;
     static constexpr int kEsz = KIND ? 1 : 2;
     static constexpr int kRow = DP * kEsz;                    // bytes of a position in its place
-    static constexpr int kStage = 2 * 16 * kRow;              // K, then V
+    static constexpr int kStep = kRow <= 128 ? 32 : 16;       // positions of a place
+    static constexpr int kStage = 2 * kStep * kRow;           // K, then V
     static constexpr int kCtas = paged_few_ctas(KIND != 0, DP);
-    static constexpr int kStages = KIND ? (DP == 64 ? 8 : DP == 128 ? 6 : 3) : (DP == 64 ? 4 : 3);
+    static constexpr int kStages = kRow == 64 ? 4 : 3;
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kPitch = DP + 8;                     // floats of a row being joined
     static constexpr int kJoin = kRows * kPitch * 4;          // in the ring's place
@@ -100,6 +101,8 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
     using S = Few<KIND, DP, MT>;
     constexpr int I = KIND ? 2 : T;                 // the operands' type
     constexpr int RT = S::kRows, KS = DP / 16, NT = DP / 8, kStages = S::kStages;
+    constexpr int NP = S::kStep, HT = NP / 8;       // positions of a step, eights of them
+    constexpr unsigned kAll = 0xffffffffu >> (32 - NP);
     constexpr int U = S::kRow / 16;                 // 16-byte units of a position
     extern __shared__ __align__(128) char smem[];
     const spec_kv_cache &C = P.cache;
@@ -121,11 +124,13 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
     bool any = false;
 
     while (walk.next(P, A)) {
-        const int steps = 2 * (A.stop - A.tile);
-        auto first = [&](int s) { return A.position(A.tile + (s >> 1)) + warp * 32 + (s & 1) * 16; };
+        const int steps = 32 / NP * (A.stop - A.tile);
+        auto first = [&](int s) {
+            return A.position(A.tile + s * NP / 32) + warp * 32 + s % (32 / NP) * NP;
+        };
         // The block of this lane's position in step s: -1 if no row sees it, -2 if it is not there.
         auto page = [&](int s) -> int {
-            const int p = s < steps ? first(s) + (lane & 15) : A.hi;
+            const int p = s < steps ? first(s) + lane % NP : A.hi;
             if (p >= A.hi || (p < A.lo && p >= P.sinks)) return -1;
             const int block = paged_page(P, A.b, p);
             return block >= 0 && block < C.num_blocks ? block : -2;
@@ -133,16 +138,16 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
         // Starts the copies of step s into its place.
         auto issue = [&](int s, int block) {
             if (s < steps) {
-                const int p = first(s) + (lane & 15);
+                const int p = first(s) + lane % NP;
                 const uint32_t off = p - P.by_page((uint32_t)p) * C.block_size;
                 const uint32_t in = (C.layout == SPEC_KV_NHD ? off * C.H + A.head
                                                              : A.head * C.block_size + off) * units;
                 if (block == -2 && P.status) atomicMax(P.status + A.b, SPEC_REQ_BAD_SLOT);
-                const unsigned seen = __ballot_sync(0xffffffffu, block >= 0) & 0xffffu;
+                const unsigned seen = __ballot_sync(0xffffffffu, block >= 0) & kAll;
                 if (lane == 0) s_seen[s % kStages] = seen;
                 const uint32_t to = ring_s + (uint32_t)(s % kStages) * S::kStage;
 #pragma unroll
-                for (int q = 0; q < U / 2; ++q) {
+                for (int q = 0; q < U * NP / 32; ++q) {
                     const int t = (q * 32 + lane) / U, u = lane % U;
                     const int blk = __shfl_sync(0xffffffffu, block, t);
                     const uint32_t from = __shfl_sync(0xffffffffu, in, t) + u;
@@ -151,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
                     const int64_t v = ok ? blk * C.v_block_stride * S::kEsz + (int64_t)from * 16 : 0;
                     const uint32_t dst = to + t * S::kRow + swizzle<KIND, DP>(t, u) * 16;
                     copy16(dst, static_cast<const char *>(C.k) + k, ok);
-                    copy16(dst + 16 * S::kRow, static_cast<const char *>(C.v) + v, ok);
+                    copy16(dst + NP * S::kRow, static_cast<const char *>(C.v) + v, ok);
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -245,14 +250,14 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
             const unsigned seen = s_seen[s % kStages];
             const int j0 = first(s);
             if (seen == 0u) continue;
-            // all 16 positions are there and every row sees them
-            const bool plain = seen == 0xffffu && j0 + 15 <= A.p0 &&
-                               (P.window == 0 || j0 > A.p1 - P.window || j0 + 15 < P.sinks);
-            float x[MT][2][4];
+            // all positions are there and every row sees them
+            const bool plain = seen == kAll && j0 + NP - 1 <= A.p0 &&
+                               (P.window == 0 || j0 > A.p1 - P.window || j0 + NP - 1 < P.sinks);
+            float x[MT][HT][4];
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < HT; ++h)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[i][h][e] = 0.f;
             const uint4 *qf = reinterpret_cast<const uint4 *>(smem + S::kQ) + lane;
@@ -260,21 +265,27 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
                 const int t = (lane & 7) + ((lane >> 4) << 3), u0 = (lane >> 3) & 1;
 #pragma unroll
                 for (int kk = 0; kk < KS; ++kk) {
-                    const uint4 k = ldmatrix(st_s + t * S::kRow +
-                                             swizzle<KIND, DP>(t, 2 * kk + u0) * 16);
+                    uint4 k[HT / 2];
+#pragma unroll
+                    for (int h = 0; h < HT / 2; ++h)
+                        k[h] = ldmatrix(st_s + (t + 16 * h) * S::kRow +
+                                        swizzle<KIND, DP>(t, 2 * kk + u0) * 16);
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
                         const uint4 a = qf[(i * KS + kk) * 32];
-                        mma<I>(x[i][0], a, k.x, k.y);
-                        mma<I>(x[i][1], a, k.z, k.w);
+#pragma unroll
+                        for (int h = 0; h < HT / 2; ++h) {
+                            mma<I>(x[i][2 * h], a, k[h].x, k[h].y);
+                            mma<I>(x[i][2 * h + 1], a, k[h].z, k[h].w);
+                        }
                     }
                 }
             } else {
 #pragma unroll
                 for (int q = 0; q < DP / 64; ++q) {          // 16 bytes of a position: four steps
-                    uint32_t w[2][4];
+                    uint32_t w[HT][4];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    for (int h = 0; h < HT; ++h) {
                         const int t = g + 8 * h;
                         const uint4 v = *reinterpret_cast<const uint4 *>(
                             st + t * S::kRow + swizzle<KIND, DP>(t, c * (DP / 64) + q) * 16);
@@ -289,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
                         for (int i = 0; i < MT; ++i) {
                             const uint4 a = qf[(i * KS + q * 4 + k) * 32];
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)
+                            for (int h = 0; h < HT; ++h)
                                 mma<I>(x[i][h], a, halves2<KIND>(w[h][k]), halves2<KIND>(w[h][k] >> 16));
                         }
                 }
@@ -300,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    bits[i][e] = plain ? 0xffffu
+                    bits[i][e] = plain ? kAll
                                        : seen & paged_bits(j0, at[i][e], A.hi, P.window, P.sinks);
             bool up = false;
             float top[MT][2];
@@ -310,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
                 for (int e2 = 0; e2 < 2; ++e2) {
                     top[i][e2] = kPagedNoMax;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                    for (int h = 0; h < HT; ++h)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             float &y = x[i][h][2 * e2 + e];
@@ -341,24 +352,28 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
                         for (int e = 0; e < 4; ++e) o[i][j][e] *= a[e >> 1];
                 }
             }
-            uint4 p[MT];
+            uint4 p[MT][HT / 2];
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < HT; ++h)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         x[i][h][e] = ex2(x[i][h][e] - m[i][e >> 1]);
                         l[i][e >> 1] += x[i][h][e];
                     }
-                p[i] = make_uint4(pack2<I>(x[i][0][0], x[i][0][1]), pack2<I>(x[i][0][2], x[i][0][3]),
-                                  pack2<I>(x[i][1][0], x[i][1][1]), pack2<I>(x[i][1][2], x[i][1][3]));
+#pragma unroll
+                for (int h = 0; h < HT / 2; ++h) {
+                    const float (&y)[4] = x[i][2 * h], (&z)[4] = x[i][2 * h + 1];
+                    p[i][h] = make_uint4(pack2<I>(y[0], y[1]), pack2<I>(y[2], y[3]),
+                                         pack2<I>(z[0], z[1]), pack2<I>(z[2], z[3]));
+                }
             }
-            const char *vs = st + 16 * S::kRow;
+            const char *vs = st + NP * S::kRow;
             bool odd = false;
             if (!plain) {
                 const uint4 *w = reinterpret_cast<const uint4 *>(vs);
-                for (int i = lane; i < 16 * U; i += 32) {
+                for (int i = lane; i < NP * U; i += 32) {
                     const uint4 v = w[i];
                     odd |= odd_word<I, KIND>(v.x) | odd_word<I, KIND>(v.y) | odd_word<I, KIND>(v.z) |
                            odd_word<I, KIND>(v.w);
@@ -369,16 +384,16 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
                 // Element by element, and only for the rows that see the position; p is rounded as
                 // for the products.
 #pragma unroll 1
-                for (int t = 0; t < 16; ++t)
+                for (int t = 0; t < NP; ++t)
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
 #pragma unroll
                         for (int e2 = 0; e2 < 2; ++e2) {
                             const int from = (lane & ~3) | ((t & 7) >> 1);
-                            const uint32_t w[2] = {e2 ? p[i].y : p[i].x, e2 ? p[i].w : p[i].z};
-                            const uint32_t w0 = __shfl_sync(0xffffffffu, w[0], from);
-                            const uint32_t w1 = __shfl_sync(0xffffffffu, w[1], from);
-                            const float pt = value16<I>(((t >> 3 ? w1 : w0) >> ((t & 1) * 16)) & 0xffffu);
+                            const uint4 &pp = p[i][HT == 4 && t >= 16 ? HT / 2 - 1 : 0];
+                            const uint32_t w0 = __shfl_sync(0xffffffffu, e2 ? pp.y : pp.x, from);
+                            const uint32_t w1 = __shfl_sync(0xffffffffu, e2 ? pp.w : pp.z, from);
+                            const float pt = value16<I>(((t >> 3 & 1 ? w1 : w0) >> ((t & 1) * 16)) & 0xffffu);
                             if (!((bits[i][e2] >> t) & 1)) continue;
 #pragma unroll
                             for (int j = 0; j < NT; ++j)
@@ -399,38 +414,42 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
             } else if constexpr (KIND == 0) {
                 const int t = lane & 15, u0 = lane >> 4;
 #pragma unroll
-                for (int j = 0; j < NT; j += 2) {
-                    const uint4 v = ldmatrix_t(st_s + 16 * S::kRow + t * S::kRow +
-                                               swizzle<KIND, DP>(t, j + u0) * 16);
+                for (int h = 0; h < HT / 2; ++h)
 #pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        mma<I>(o[i][j], p[i], v.x, v.y);
-                        mma<I>(o[i][j + 1], p[i], v.z, v.w);
-                    }
-                }
-            } else {
-                // columns g D/8 + j of positions 2c, 2c + 1 and 2c + 8, 2c + 9
-                const int ts[4] = {2 * c, 2 * c + 1, 2 * c + 8, 2 * c + 9};
-                uint32_t w[4][DP / 32];
+                    for (int j = 0; j < NT; j += 2) {
+                        const uint4 v = ldmatrix_t(st_s + (NP + 16 * h + t) * S::kRow +
+                                                   swizzle<KIND, DP>(t, j + u0) * 16);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const char *row = vs + ts[q] * S::kRow;
-                    if constexpr (DP == 64) {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(
-                            row + swizzle<KIND, DP>(ts[q], g >> 1) * 16 + (g & 1) * 8);
-                        w[q][0] = v.x;
-                        w[q][1] = v.y;
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < DP / 128; ++k) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(
-                                row + swizzle<KIND, DP>(ts[q], g * (DP / 128) + k) * 16);
-                            w[q][4 * k] = v.x;
-                            w[q][4 * k + 1] = v.y;
-                            w[q][4 * k + 2] = v.z;
-                            w[q][4 * k + 3] = v.w;
+                        for (int i = 0; i < MT; ++i) {
+                            mma<I>(o[i][j], p[i][h], v.x, v.y);
+                            mma<I>(o[i][j + 1], p[i][h], v.z, v.w);
                         }
                     }
+            } else {
+                // columns g D/8 + j of positions 2c, 2c + 1 and 2c + 8, 2c + 9
+#pragma unroll
+                for (int h = 0; h < HT / 2; ++h) {
+                    const int t0 = 16 * h + 2 * c, ts[4] = {t0, t0 + 1, t0 + 8, t0 + 9};
+                    uint32_t w[4][DP / 32];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const char *row = vs + ts[q] * S::kRow;
+                        if constexpr (DP == 64) {
+                            const uint2 v = *reinterpret_cast<const uint2 *>(
+                                row + swizzle<KIND, DP>(ts[q], g >> 1) * 16 + (g & 1) * 8);
+                            w[q][0] = v.x;
+                            w[q][1] = v.y;
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < DP / 128; ++k) {
+                                const uint4 v = *reinterpret_cast<const uint4 *>(
+                                    row + swizzle<KIND, DP>(ts[q], g * (DP / 128) + k) * 16);
+                                w[q][4 * k] = v.x;
+                                w[q][4 * k + 1] = v.y;
+                                w[q][4 * k + 2] = v.z;
+                                w[q][4 * k + 3] = v.w;
+                            }
+                        }
                 }
 #pragma unroll
                 for (int k = 0; k < DP / 32; ++k)
@@ -442,11 +461,12 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
                         const uint32_t b = __byte_perm(w[2][k], w[3][k], sel);
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
-                            mma<I>(o[i][4 * k + 2 * y], p[i], halves2<KIND>(a), halves2<KIND>(b));
-                            mma<I>(o[i][4 * k + 2 * y + 1], p[i], halves2<KIND>(a >> 16),
+                            mma<I>(o[i][4 * k + 2 * y], p[i][h], halves2<KIND>(a), halves2<KIND>(b));
+                            mma<I>(o[i][4 * k + 2 * y + 1], p[i][h], halves2<KIND>(a >> 16),
                                    halves2<KIND>(b >> 16));
                         }
                     }
+                }
             }
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");

@@ -317,6 +317,7 @@ struct PagedAttnParams {
     int B, Hq, G, N;              // G = Hq / cache.H; N: rows of each request, without row_start
     int64_t T;
     int max_new;                  // most rows of a request
+    int rows_over, rows_most;     // a launch takes requests of more and of at most so many rows a head
     const int32_t *row_start, *seq_pos;
     float scale;
     int window, sinks;            // window 0: none
