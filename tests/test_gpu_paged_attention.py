@@ -116,9 +116,11 @@ class Case:
             assert np.all(err <= tol[fine]), (b, (err / tol[fine]).max())
             none = r["lse"] == -np.inf
             assert np.array_equal(lse[rows] == -np.inf, none)
-            ref = r["lse"][~none]
-            ltol = soft[~none] + 2.0 ** -24 * L + 2.0 ** -22 * np.abs(ref)
-            assert np.all(np.abs(lse[rows][~none] - ref) <= ltol)
+            assert np.array_equal(np.isnan(lse[rows]), np.isnan(r["lse"]))
+            some = np.isfinite(r["lse"])
+            ref = r["lse"][some]
+            ltol = soft[some] + 2.0 ** -24 * L + 2.0 ** -22 * np.abs(ref)
+            assert np.all(np.abs(lse[rows][some] - ref) <= ltol)
 
 
 SIZES = [
@@ -164,3 +166,236 @@ def test_many_rows(h, dt, cache, size, layout, bs, window, sinks):
     out, lse = c.run(h, st)
     assert st.tolist() == [0] * len(counts)
     c.check(out, lse)
+
+
+def place(c, b, p):
+    """The block and offset of position p of request b."""
+    return int(c.table[b, p // c.bs]), p % c.bs
+
+
+def put(c, which, b, p, head, d, value):
+    """Sets an element of the cache and of the oracle's copy."""
+    blk, off = place(c, b, p)
+    t = (c.k, c.v)[which]
+    at = (blk, off, head, d) if c.layout == S.NHD else (blk, head, off, d)
+    if t.element_size() == 1:       # the code of a NaN or an infinity
+        code = 0x7F if c.kind == "e4m3" else 0x7C if value == np.inf else 0x7E
+        t.view(torch.uint8)[at] = code
+        value = np.nan if c.kind == "e4m3" else value
+    else:
+        t[at] = value
+    (c.k64, c.v64)[which][b][p, head, d] = value
+
+
+@pytest.mark.parametrize("dt,cache", [("bf16", "same"), ("f16", "same"), ("bf16", "e4m3"),
+                                      ("f16", "e5m2")])
+@pytest.mark.parametrize("counts,pos,Gq,D,window,sinks", [
+    ([5, 3], [100, 0], 2, 64, 0, 0), ([6, 1], [400, 30], 2, 128, 37, 5), ([3], [200], 1, 256, 50, 2),
+    ([130, 40], [60, 0], 2, 64, 0, 0), ([70, 100], [700, 300], 2, 128, 260, 3)])
+def test_values_that_are_no_numbers(h, dt, cache, counts, pos, Gq, D, window, sinks):
+    """NaN and infinities in K and V reach the rows that see them, and no others."""
+    rng = np.random.default_rng(D + len(counts))
+    c = Case(rng, counts, pos, 2, Gq, D, dt, cache, S.HND, 16, window, sinks)
+    for b, n in enumerate(counts):
+        last = pos[b] + n - 1
+        put(c, 1, b, last, 0, 3, np.inf)                  # the last row alone sees it
+        put(c, 1, b, pos[b] + n // 2, 1, D - 1, np.nan)   # about half of the rows
+        put(c, 0, b, last, 1, 5, np.nan)                  # a key: the whole last row
+        if window and pos[b] > window + n:
+            put(c, 1, b, pos[b] - window + n // 2, 0, 7, np.inf)     # leaves the window on the way
+    out, lse = c.run(h)
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("n,Gq", [(3, 2), (90, 2)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (200, 4)])
+def test_blocks_outside_the_cache(h, n, Gq, window, sinks):
+    rng = np.random.default_rng(5)
+    c = Case(rng, [n, n, 1], [300, 0, 600], 2, Gq, 64, "bf16", "same", S.NHD, 16, window, sinks)
+    c.table[0, 18] = -1
+    c.table[1, 0] = c.k.shape[0]
+    c.table[2, 3] = 2 ** 31 - 1        # outside the window if there is one
+    st = torch.full((3,), 9, dtype=torch.int32, device=DEV)
+    out, lse = c.run(h, st)
+    assert st.tolist() == [S.BAD_SLOT, S.BAD_SLOT, 0 if window else S.BAD_SLOT]
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("n,Gq", [(2, 2), (70, 4)])
+def test_rows_of_no_request_stay(h, n, Gq):
+    """Rows behind the last request, of requests out of range and of those over max_new are left."""
+    rng = np.random.default_rng(7)
+    c = Case(rng, [n, n, n], [10, 20, 30], 1, Gq, 64, "f16", spare=5)
+    T = 3 * n + 5
+    work = torch.empty(G.spec_paged_attention_workspace(h, 3, T, n, Gq, 1, 64), dtype=torch.uint8,
+                       device=DEV)
+
+    def call(start, max_new=n, pos=(10, 20, 30)):
+        out = torch.full((T, Gq, 64), 7.0, dtype=torch.float16, device=DEV)
+        lse = torch.full((T, Gq), 7.0, device=DEV)
+        st = torch.full((3,), 9, dtype=torch.int32, device=DEV)
+        G.spec_paged_attention(h, c.q, c.cache(), gpu(c.table), gpu(np.array(pos, np.int32)),
+                               c.scale, out, work, gpu(np.array(start, np.int32)),
+                               max_new=max_new, lse=lse, status=st)
+        return out, lse, st.tolist()
+
+    out, lse, st = call([0, n, 2 * n, 3 * n])
+    assert st == [0, 0, 0] and (out[3 * n:] == 7).all() and (lse[3 * n:] == 7).all()
+    assert not (lse[:3 * n] == 7).any()
+    out, lse, st = call([-1, n, 2 * n, T + 1])
+    assert st == [S.BAD_RANGE, 0, S.BAD_RANGE]
+    assert (out[:n] == 7).all() and (out[2 * n:] == 7).all() and not (lse[n:2 * n] == 7).any()
+    out, lse, st = call([0, n, n - 1, 2 * n - 1])
+    assert st == [0, S.BAD_RANGE, 0]
+    out, lse, st = call([0, n + 1, n + 1, 2 * n + 1])
+    assert st == [S.BAD_RANGE, 0, 0] and (lse[:n + 1] == 7).all()
+
+
+@pytest.mark.parametrize("n", [4, 80])
+def test_positions_outside_the_table(h, n):
+    """Rows before position 0 see nothing; rows past the table see what is in it."""
+    rng = np.random.default_rng(8)
+    c = Case(rng, [n, n], [-3, 40], 2, 2, 64, "bf16")
+    pages = c.table.shape[1]
+    st = torch.full((2,), 9, dtype=torch.int32, device=DEV)
+    out, lse = c.run(h, st)
+    assert st.tolist() == [S.BAD_SLOT, 0]
+    c.check(out, lse)
+    assert (out[:3] == 0).all() and (lse[:3] == -np.inf).all()
+    c.pos = [-(2 ** 31), 2 ** 31 - 1]
+    out, lse = c.run(h, st)
+    assert st.tolist() == [S.BAD_SLOT, S.BAD_SLOT]
+    assert (out[:n] == 0).all() and (lse[:n] == -np.inf).all()
+    assert torch.isfinite(lse[n:]).all() or pages * 16 > 40 + n     # unused pages hold NaN
+
+
+@pytest.mark.parametrize("B,n,Gq,D", [(3, 1, 4, 64), (2, 50, 2, 128), (64, 1, 1, 128)])
+def test_equal_rows_without_row_start(h, B, n, Gq, D):
+    rng = np.random.default_rng(B + n)
+    c = Case(rng, [n] * B, list(rng.integers(0, 400, B)), 2, Gq, D, "bf16", "same", S.HND, 32)
+    a = c.run(h, start=None, max_new=n)
+    b = c.run(h, max_new=n)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    c.check(*a)
+
+
+@pytest.mark.parametrize("dt,cache", [("bf16", "same"), ("f16", "e4m3")])
+def test_few_and_many_rows_of_one_batch(h, dt, cache):
+    """Requests of one token beside chunks, K and V of a block side by side: each kernel takes its
+    own."""
+    rng = np.random.default_rng(11)
+    counts = [1, 40, 0, 1, 9, 130, 1, 16, 17, 2]
+    pos = [900, 0, 5, 0, 250, 20, 131, 64, 3000, 1]
+    c = Case(rng, counts, pos, 2, 2, 128, dt, cache, S.NHD, 16, apart=True)
+    st = torch.full((10,), 9, dtype=torch.int32, device=DEV)
+    out, lse = c.run(h, st, max_new=130)
+    assert st.tolist() == [0] * 10
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("counts,Gq", [([1, 1, 1], 8), ([200, 1, 30], 4)])
+def test_repeated_and_captured(h, counts, Gq):
+    """The same bits every time, on a stream of the caller's, and from two graphs that share a
+    workspace; a replay follows new lengths."""
+    rng = np.random.default_rng(13)
+    pos = [2000, 700, 90]
+    c = Case(rng, counts, pos, 2, Gq, 128, "bf16")
+    T, B = sum(counts), 3
+    first = c.run(h)
+    for _ in range(5):
+        assert all(torch.equal(x, y) for x, y in zip(first, c.run(h)))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    again = c.run(h, stream=side)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(first, again))
+    work = torch.empty(G.spec_paged_attention_workspace(h, B, T, 0, 2 * Gq, 2, 128),
+                       dtype=torch.uint8, device=DEV)
+    table, at, start = gpu(c.table), gpu(np.array(pos, np.int32)), gpu(c.start)
+    outs = [(torch.zeros_like(first[0]), torch.zeros_like(first[1])) for _ in range(2)]
+    graphs = []
+    for out, lse in outs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            G.spec_paged_attention(h, c.q, c.cache(), table, at, c.scale, out, work, start, lse=lse)
+        graphs.append(g)
+    for _ in range(2):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for o in outs:
+        assert all(torch.equal(x, y) for x, y in zip(first, o))
+    c.pos = [1500, 3, 90]
+    at.copy_(gpu(np.array(c.pos, np.int32)))
+    graphs[0].replay()
+    assert all(torch.equal(x, y) for x, y in zip(c.run(h), outs[0]))
+
+
+@pytest.mark.parametrize("n,Gq", [(1, 4), (60, 2)])
+def test_blocks_beyond_four_gigabytes(h, n, Gq):
+    """A cache of more than 2^32 bytes, its last blocks in use."""
+    rng = np.random.default_rng(17)
+    c = Case(rng, [n], [300], 1, Gq, 128, "bf16")
+    nb = (2 ** 32 + 2 ** 28) // (16 * 128 * 2)
+    small_k, small_v, table, m = c.k, c.v, c.table, c.k.shape[0]
+    c.k = torch.empty((nb, 16, 1, 128), dtype=torch.bfloat16, device=DEV)
+    c.v = torch.empty((nb, 16, 1, 128), dtype=torch.bfloat16, device=DEV)
+    c.k[nb - m:], c.v[nb - m:] = small_k, small_v
+    c.table = table + (nb - m)
+    out, lse = c.run(h)
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("std", [1e-30, 30.0, 3e3])
+@pytest.mark.parametrize("n,Gq", [(3, 4), (80, 2)])
+def test_scores_of_any_size(h, n, Gq, std):
+    """Tiny scores weigh all keys alike; huge ones leave one key: numbers, and lse near its score."""
+    rng = np.random.default_rng(19)
+    c = Case(rng, [n], [500], 2, Gq, 64, "bf16", std=std)
+    out, lse = c.run(h)
+    r = S.attention(c.q64, c.k64[0], c.v64[0], 500 + np.arange(n), np.ones(500 + n, bool), c.scale, 0,
+                    0)
+    assert torch.isfinite(out).all()
+    got = lse.double().cpu().numpy()
+    tol = 2 * 2.0 ** -20 * (2 + r["X"]) + 2.0 ** -24 * 600 + 2.0 ** -22 * np.abs(r["lse"])
+    assert np.all(np.abs(got - r["lse"]) <= tol)
+    if std < 1:
+        c.check(out, lse)
+
+
+def test_an_empty_batch(h):
+    c = Case(np.random.default_rng(1), [1], [3], 1, 1, 64, "bf16")
+    none = torch.zeros((0, 1, 64), dtype=torch.bfloat16, device=DEV)
+    out, lse = G.paged_attention(h, none, c.cache(), gpu(c.table), gpu(np.zeros(1, np.int32)), 1.0,
+                                 gpu(np.zeros(2, np.int32)))
+    assert out.shape == (0, 1, 64) and lse.shape == (0, 1)
+    out, lse = G.paged_attention(h, none, c.cache(), gpu(c.table[:0]), gpu(np.zeros(0, np.int32)), 1.0)
+    assert out.shape == (0, 1, 64)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
+    dict(window=-1), dict(sinks=-1), dict(max_new=-1), dict(D=24), dict(D=272), dict(Hq=3),
+    dict(B=65), dict(work=0), dict(work="off"), dict(dtype="f32")])
+def test_library_refusals(h, kw):
+    dt = torch.float32 if kw.get("dtype") else torch.bfloat16
+    D, Hq, B = kw.get("D", 64), kw.get("Hq", 4), kw.get("B", 2)
+    q = torch.zeros((B, Hq, D), dtype=dt, device=DEV)
+    cache = G.KvCache.empty(4, 16, 2, D, dt, DEV)
+    work = torch.empty(32 << 20, dtype=torch.uint8, device=DEV)
+    work = {"off": work[16:], 0: work[:0]}.get(kw.get("work"), work)
+    one = torch.zeros(B, dtype=torch.int32, device=DEV)
+    with pytest.raises(G.SpecError):
+        G.spec_paged_attention(h, q, cache, torch.zeros((B, 4), dtype=torch.int32, device=DEV), one,
+                               kw.get("scale", 0.1), torch.empty_like(q), work,
+                               max_new=kw.get("max_new", 0), window=kw.get("window", 0),
+                               sinks=kw.get("sinks", 0))
+    torch.cuda.synchronize()
+
+
+def test_rows_that_do_not_divide(h):
+    q = torch.zeros((5, 2, 64), dtype=torch.bfloat16, device=DEV)
+    cache = G.KvCache.empty(4, 16, 2, 64, torch.bfloat16, DEV)
+    with pytest.raises(G.SpecError):
+        G.paged_attention(h, q, cache, torch.zeros((2, 4), dtype=torch.int32, device=DEV),
+                          torch.zeros(2, dtype=torch.int32, device=DEV), 0.1)
