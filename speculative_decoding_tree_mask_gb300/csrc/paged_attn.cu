@@ -4,9 +4,10 @@
 namespace specv {
 namespace {
 
-constexpr int kFewRows = 32;
-// ... and beside a launch on the tensor cores (16: one token of up to 16 heads a group)
-int few_beside(int G) { return G <= 16 ? 16 : kFewRows; }
+// The most rows of the kernel for few; and beside a launch on the tensor cores (16: one token of up to
+// 16 heads a group).
+int few_rows(int D) { return paged_padded(D) == 256 ? 16 : 32; }
+int few_beside(int G, int D) { return G <= 16 ? 16 : few_rows(D); }
 
 // The parts of cut items into the result. A thread has a float4 of a row and, of the parts,
 // every PG-th, eight of them in flight together; the PG threads of a float4 meet in shared
@@ -93,16 +94,16 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (P.lse && d4 == 0) P.lse[at] = paged_lse(m, l);
 }
 
-// How requests are run: by the warps' matrix unit up to 32 rows an item, beyond on the tcgen05 tensor
-// cores, which have no form for D above 128 (Q, K and V tiles do not fit in shared memory together).
+// How requests are run: by the warps' matrix unit up to 32 rows an item (16 where D is above 128: its
+// registers hold no more), beyond on the tcgen05 tensor cores.
 struct Plan {
     int mt, rows, grid;     // groups of 16 rows of an item, 0: tcgen05; rows; CTAs
 };
 Plan plan(int64_t R, int D, int kind, int sms) {      // R: most rows a head
     Plan p;
     const int DP = paged_padded(D);
-    p.mt = DP == 256 ? 1 : R > kFewRows ? 0 : R > 16 ? 2 : 1;
-    p.rows = p.mt ? 16 * p.mt : kPagedTcRows;
+    p.mt = R > few_rows(D) ? 0 : R > 16 ? 2 : 1;
+    p.rows = p.mt ? 16 * p.mt : paged_tc_rows(DP);
     p.grid = sms * (p.mt ? paged_few_ctas(kind != SPEC_CACHE_SAME, DP) : 1);
     return p;
 }
@@ -160,8 +161,7 @@ int64_t paged_attn_workspace(int max_new, int G, int D, int sms) {
     int64_t most = 256;       // whatever the cache's type and the batch
     for (int kind = 0; kind < 2; ++kind) {
         int64_t bytes = plan_bytes(plan(R, D, kind, sms), D);
-        if (R > kFewRows && paged_padded(D) <= 128)
-            bytes += plan_bytes(plan(few_beside(G), D, kind, sms), D);
+        if (R > few_rows(D)) bytes += plan_bytes(plan(few_beside(G, D), D, kind, sms), D);
         most = bytes > most ? bytes : most;
     }
     return most;
@@ -174,7 +174,7 @@ cudaError_t launch_paged_attn(const PagedAttnParams &given, cudaStream_t st) {
     const Plan n = plan(R, p.cache.D, p.cache.kind, p.sms);
     // (a batch as large as its largest requests has those alone)
     const bool both = n.mt == 0 && p.T < (int64_t)p.B * p.max_new;
-    const int few = few_beside(p.G);
+    const int few = few_beside(p.G, p.cache.D);
     const cudaError_t e = run(p, n, both ? few : 0, INT32_MAX, st);
     if (!both || e != cudaSuccess) return e;
     p.workspace = static_cast<char *>(p.workspace) + plan_bytes(n, p.cache.D);

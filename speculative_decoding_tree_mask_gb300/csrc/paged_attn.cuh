@@ -21,7 +21,7 @@
 
 namespace specv {
 
-constexpr int kPosTile = 128;       // positions of a tile
+constexpr int kPosTile = 128;       // positions of a tile, where a kernel has no other
 
 // A request as the kernels use it.
 struct PagedReq {
@@ -86,14 +86,11 @@ struct PagedPart {
     int rows;                       // of the tile
     int p0, p1;                     // positions of its first and last row's token
     int lo, hi;                     // positions that any row sees: [lo, hi), and those below sinks
-    int skip, base;                 // tile i stands at position kPosTile * (i < skip ? i : base + i)
+    int skip, base;                 // tile i stands at position PT * (i < skip ? i : base + i)
     int tile, stop, nt;             // tiles of this part, of the item
     bool begins, ends;              // the part has the item's begin, its end
     int64_t at, w;                  // where the item begins, its weight
 
-    __device__ __forceinline__ int position(int i) const {
-        return (i < skip ? i : base + i) * kPosTile;
-    }
     __device__ __forceinline__ bool whole() const { return begins && ends; }
 };
 
@@ -102,7 +99,7 @@ __device__ __forceinline__ int paged_owner(const PagedRange &r, int64_t x) {   /
 }
 
 // Steps through a CTA's parts, in order. Every warp runs it for itself (all 32 lanes).
-template <int RT>
+template <int RT, int PT = kPosTile>
 struct PagedWalk {
     PagedRange range;
     int64_t at;                     // where the item at hand begins
@@ -206,8 +203,8 @@ struct PagedWalk {
         p.hi = (int)max(hi, (int64_t)0);
         const int64_t lo = P.window > 0 ? max(p0 - P.window + 1, (int64_t)0) : 0;
         p.lo = (int)min(lo, (int64_t)p.hi);
-        const int t0 = p.lo / kPosTile, t1 = (p.hi + kPosTile - 1) / kPosTile;
-        p.skip = min((min(P.sinks, p.hi) + kPosTile - 1) / kPosTile, t0);
+        const int t0 = p.lo / PT, t1 = (p.hi + PT - 1) / PT;
+        p.skip = min((min(P.sinks, p.hi) + PT - 1) / PT, t0);
         p.base = t0 - p.skip;
         p.nt = p.skip + max(t1 - t0, 0);
         const int64_t xa = max(range.begin - at, (int64_t)0), xb = min(range.end - at, w);
@@ -383,7 +380,7 @@ cudaError_t launch_paged_few_bf16(const PagedAttnParams &p, int mt, int grid, cu
 cudaError_t launch_paged_few_f16(const PagedAttnParams &p, int mt, int grid, cudaStream_t st);
 
 // Launches on the tcgen05 tensor cores (paged_tc.cuh).
-constexpr int kPagedTcRows = 256;   // of an item
+constexpr int paged_tc_rows(int DP) { return DP == 256 ? 128 : 256; }   // of an item
 cudaError_t launch_paged_tc_bf16(const PagedAttnParams &p, int grid, cudaStream_t st);
 cudaError_t launch_paged_tc_f16(const PagedAttnParams &p, int grid, cudaStream_t st);
 

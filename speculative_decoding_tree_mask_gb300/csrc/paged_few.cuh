@@ -126,7 +126,8 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
     while (walk.next(P, A)) {
         const int steps = 32 / NP * (A.stop - A.tile);
         auto first = [&](int s) {
-            return A.position(A.tile + s * NP / 32) + warp * 32 + s % (32 / NP) * NP;
+            const int i = A.tile + s * NP / 32;
+            return (i < A.skip ? i : A.base + i) * kPosTile + warp * 32 + s % (32 / NP) * NP;
         };
         // The block of this lane's position in step s: -1 if no row sees it, -2 if it is not there.
         auto page = [&](int s) -> int {

@@ -54,26 +54,32 @@ constexpr int kRing = 5;
 // What an item costs besides its keys, in positions.
 constexpr int kTcFixed = 256;
 
+// D above 128: one softmax group and tiles of 64 positions, so that queries, ring and sums take the
+// same room.
 template <int DP>
 struct Tc {
-    static constexpr int kOperand = 128 * DP * 2;                // a 128 x DP operand of 16 bits
-    static constexpr int kTiles = 2 * kOperand;                  // Q first, then the ring
+    static constexpr int kGroups = DP == 256 ? 1 : 2;            // of 128 rows
+    static constexpr int kPos = DP == 256 ? 64 : 128;            // positions of a tile
+    static constexpr int kQuery = 128 * DP * 2;                  // a group's queries, 16-bit elements
+    static constexpr int kOperand = kPos * DP * 2;               // a tile of K or V
+    static constexpr int kTiles = kGroups * kQuery;              // Q first, then the ring
     static constexpr int kSmall = kTiles + kRing * kOperand;     // barriers and words
     static constexpr int kBytes = kSmall + 2048 + 1024;          // and room to align by 1024
     static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
-    static constexpr int kColumns = 512;                         // 2 (128 + DP), a power of two
+    static constexpr int kColumns = 512;                         // groups x (128 + DP), a power of two
+    static constexpr int kReaders = 8 + 5 * kGroups;             // warps that read a part
 };
 
 // A part as the warps read it (see PagedPart); b -1: there are no more.
 struct PartWords {
     int b, r, head, first, pos, rows, p0, p1, lo, hi, skip, base, tile, stop, begins, ends;
 
+    template <int PT>
     __device__ __forceinline__ int position(int i) const {
-        return (i < skip ? i : base + i) * kPosTile;
+        return (i < skip ? i : base + i) * PT;
     }
 };
 constexpr int kDealt = 4;
-constexpr int kReaders = 18;      // warps that read a part: softmax, load, multiply
 
 struct Words {
     PartWords part[kDealt];
@@ -96,9 +102,10 @@ struct Words {
 };
 static_assert(sizeof(Words) <= 2048, "room for the words");
 
-// Byte of 16-byte chunk `j` of row r of an operand of D elements a row.
+// Byte of 16-byte chunk `j` of row r of an operand of R rows.
+template <int R>
 __device__ __forceinline__ uint32_t chunk_at(int r, int j) {
-    return (uint32_t)(j >> 3) * (128 * 128) + r * 128 + (((j & 7) ^ (r & 7)) << 4);
+    return (uint32_t)(j >> 3) * (R * 128) + r * 128 + (((j & 7) ^ (r & 7)) << 4);
 }
 
 // A wait of a whole warp: all of it goes on or none. And an arrival for what all its lanes have done.
@@ -117,10 +124,9 @@ __device__ __forceinline__ void store32(void *to, const uint32_t (&w)[8]) {
                  : "memory");
 }
 
-// Whether every row of the item sees all of tile j0, as far as it is there.
-__device__ __forceinline__ bool all_see(const PagedAttnParams &P, int p0, int p1, int j0) {
-    return j0 + kPosTile - 1 <= p0 &&
-           (P.window == 0 || j0 > p1 - P.window || j0 + kPosTile - 1 < P.sinks);
+// Whether every row of the item sees all of the n positions from j0 on, as far as they are there.
+__device__ __forceinline__ bool all_see(const PagedAttnParams &P, int p0, int p1, int j0, int n) {
+    return j0 + n - 1 <= p0 && (P.window == 0 || j0 > p1 - P.window || j0 + n - 1 < P.sinks);
 }
 
 // The reference of a row comes from a rounded product f s, within 2^-24 of it, which f s - top in
@@ -194,7 +200,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     using C_ = Tc<DP>;
     constexpr int I = KIND ? 2 : T;                              // the operands' type
     constexpr int kType = I == 1 ? 1 : 0;                        // of the descriptors
-    constexpr int RT = kPagedTcRows, KS = DP / 16, kEsz = KIND ? 1 : 2;
+    constexpr int NG = C_::kGroups, RT = 128 * NG, PT = C_::kPos, KS = DP / 16, kEsz = KIND ? 1 : 2;
+    constexpr int HALVES = PT / 64;                              // jobs of a tile
+    static_assert(RT == paged_tc_rows(DP), "rows of an item");
     constexpr bool kScaleQ = T == 1 && I == 2;
     const int box = KIND ? 0 : maps.page_rows;
     extern __shared__ char raw[];
@@ -205,10 +213,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
         bar_init(&W.q_full, KIND == 0 && maps.tokens > 0 ? 1 : kLoad / 32);
-        bar_init(&W.q_free, 2);
+        bar_init(&W.q_free, NG);
         for (int i = 0; i < kRing; ++i) {
             bar_init(&W.full[i], kLoad / 64);
-            bar_init(&W.free[i], 2);
+            bar_init(&W.free[i], NG);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(&W.drain[i], 1);
@@ -221,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kDealt; ++i) {
             bar_init(&W.part_full[i], 1);
-            bar_init(&W.part_free[i], kReaders);
+            bar_init(&W.part_free[i], C_::kReaders);
         }
         for (int i = 0; i < 8; ++i) W.odd[i] = 0;
 #ifdef SPEC_DEBUG
@@ -241,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // tensor memory of softmax group m: two S of 64 columns (and P over each) at 128 m, O behind both
     // groups'
     auto s_at = [&](int m) { return tmem + 128 * m; };
-    auto o_at = [&](int m) { return tmem + 256 + DP * m; };
+    auto o_at = [&](int m) { return tmem + 128 * NG + DP * m; };
     // tiles of K and V take the ring's places in turn: K of tile c is the 2c-th, V the next
     auto slot = [](uint32_t x) { return x % kRing; };
     auto phase = [](uint32_t x) { return (x / kRing) & 1; };
@@ -256,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int m = warp - kMmaWarp;
         if (m == 2) {
             // ---- deal ----
-            PagedWalk<RT> walk(P, kTcFixed, (int64_t)P.G * kPosTile);
+            PagedWalk<RT, PT> walk(P, kTcFixed, (int64_t)P.G * kPosTile);
             PagedPart A;
             bool any = false, go = true;
             for (uint32_t x = 0;; ++x) {
@@ -273,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 any = true;
             }
             if (lane == 0) paged_note(P, walk.range, A, any);
-        } else if (m < 2) {
+        } else if (m < NG) {
             // ---- multiply, for softmax group m. The whole warp runs the loop and waits, one
             // thread of it issues: what the products are given is then the same in all of the warp.
             const bool lead = elect_one();
@@ -305,38 +313,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++parts;
                     continue;
                 }
-                const int count = 2 * n;
+                const int count = HALVES * n;
                 auto scores = [&](int j) {
-                    const uint32_t x = 2 * (done + (j >> 1)), buf = (jobs + j) & 1;
-                    if ((j & 1) == 0)             // a tile's second half came with its first
+                    const int half = j % HALVES;
+                    const uint32_t x = 2 * (done + j / HALVES), buf = (jobs + j) & 1;
+                    if (half == 0)                // a tile's second half came with its first
                         ok = ok && warp_wait(&W.full[slot(x)], phase(x), gave_up);
                     if (!ok) return;              // no products of what did not come
-                    const uint64_t a = smem_desc(base + m * C_::kOperand, 16, 1024);
+                    const uint64_t a = smem_desc(base + m * C_::kQuery, 16, 1024);
                     const uint64_t k = smem_desc(
-                        base + C_::kTiles + slot(x) * C_::kOperand + (j & 1) * kHalf, 16, 1024);
+                        base + C_::kTiles + slot(x) * C_::kOperand + half * kHalf, 16, 1024);
                     if (lead) {
 #pragma unroll
                         for (int d = 0; d < KS; ++d) {
-                            const int off = (d >> 2) * (128 * 128) + (d & 3) * 32;
-                            mma_ss(s + buf * 64, desc_plus(a, off), desc_plus(k, off),
+                            const int in = (d & 3) * 32;
+                            mma_ss(s + buf * 64, desc_plus(a, (d >> 2) * (128 * 128) + in),
+                                   desc_plus(k, (d >> 2) * (PT * 128) + in),
                                    mma_desc(kType, 64, false), d > 0);
                         }
                         mma_commit(&W.s_full[m][buf]);
-                        if (j & 1) mma_commit(&W.free[slot(x)]);
+                        if (half == HALVES - 1) mma_commit(&W.free[slot(x)]);
                         if (j == count - 1) mma_commit(&W.q_free);
                     }
                     __syncwarp();
                 };
                 scores(0);
-                scores(1);
+                if (count > 1) scores(1);
                 for (int j = 0; ok && j < count; ++j) {
-                    const uint32_t x = 2 * (done + (j >> 1)) + 1, buf = (jobs + j) & 1;
-                    if ((j & 1) == 0) ok = warp_wait(&W.full[slot(x)], phase(x), gave_up);
+                    const int half = j % HALVES;
+                    const uint32_t x = 2 * (done + j / HALVES) + 1, buf = (jobs + j) & 1;
+                    if (half == 0) ok = warp_wait(&W.full[slot(x)], phase(x), gave_up);
                     ok = ok && warp_wait(&W.p_full[m][buf], (jobs + j) >> 1 & 1, gave_up);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t v = smem_desc(
-                        base + C_::kTiles + slot(x) * C_::kOperand + (j & 1) * kHalf, 128 * 128, 1024);
+                        base + C_::kTiles + slot(x) * C_::kOperand + half * kHalf, PT * 128, 1024);
                     if (lead) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -344,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    mma_desc(kType, DP, true), j > 0 || k > 0);
                         mma_commit(&W.o_full[m]);
                         if (j == count - 1) mma_commit(&W.o_last[m]);
-                        if (j & 1) mma_commit(&W.free[slot(x)]);
+                        if (half == HALVES - 1) mma_commit(&W.free[slot(x)]);
                     }
                     __syncwarp();
                     if (j + 2 < count) scores(j + 2);
@@ -363,7 +374,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (tid >= kSoftmax) {
         fewer_registers<88>();
-        // ---- load: K or V, 32 positions a warp ----
+        // ---- load: K or V, PW positions a warp ----
+        constexpr int PW = PT / 4;
+        constexpr unsigned kMine = 0xffffffffu >> (32 - PW);
         const bool of_v = tid >= kSoftmax + kLoad / 2;
         const int w4 = (tid - kSoftmax) % (kLoad / 2) / 32;
         const char *cache = static_cast<const char *>(of_v ? C.v : C.k);
@@ -382,13 +395,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             auto page = [&](int i) -> int {
-                const int p = i < n ? A.position(A.tile + i) + w4 * 32 + lane : A.hi;
+                const int p = i < n && lane < PW ? A.position<PT>(A.tile + i) + w4 * PW + lane : A.hi;
                 if (p >= A.hi || (p < A.lo && p >= P.sinks)) return -1;
                 const int block = paged_page(P, A.b, p);
                 return block >= 0 && block < C.num_blocks ? block : -2;
             };
             auto unit = [&](int i) -> uint32_t {
-                const int p = A.position(A.tile + i) + w4 * 32 + lane;
+                const int p = A.position<PT>(A.tile + i) + w4 * PW + lane;
                 const uint32_t off = p - P.by_page((uint32_t)p) * C.block_size;
                 return (C.layout == SPEC_KV_NHD ? off * C.H + A.head : A.head * C.block_size + off) *
                        units;
@@ -403,13 +416,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Tile i has come to its place: what the rows see in part is looked through.
             auto arrived = [&](int i) {
                 const uint32_t x = 2 * (done + i) + of_v;
-                if (of_v && !all_see(P, A.p0, A.p1, A.position(A.tile + i))) {
+                if (of_v && !all_see(P, A.p0, A.p1, A.position<PT>(A.tile + i), PT)) {
                     char *to = smem + C_::kTiles + slot(x) * C_::kOperand;
                     bool odd = false;
                     constexpr int J = DP / 8;
 #pragma unroll 4
-                    for (int q = lane; q < 32 * J; q += 32) {
-                        uint4 *at = reinterpret_cast<uint4 *>(to + chunk_at(w4 * 32 + q / J, q % J));
+                    for (int q = lane; q < PW * J; q += 32) {
+                        uint4 *at = reinterpret_cast<uint4 *>(to + chunk_at<PT>(w4 * PW + q / J, q % J));
                         const uint4 y = *at;
                         if (!(odd_word<I, 0>(y.x) | odd_word<I, 0>(y.y) | odd_word<I, 0>(y.z) |
                               odd_word<I, 0>(y.w)))
@@ -432,7 +445,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto note = [&](int i, int block) {      // K's warps: which positions are there
                 if (block == -2 && P.status) atomicMax(P.status + A.b, SPEC_REQ_BAD_SLOT);
                 const unsigned seen = __ballot_sync(0xffffffffu, block >= 0);
-                if (!of_v && lane == 0) W.seen[(done + i) & 3][w4] = seen;
+                if (!of_v && lane == 0) {
+                    if (PW == 32) W.seen[(done + i) & 3][w4] = seen;
+                    else reinterpret_cast<unsigned short *>(W.seen[(done + i) & 3])[w4] = (unsigned short)seen;
+                }
             };
             // The item's rows, the D / 8 chunks of a row side by side, rows past the item's zeros:
             // issued by all loading threads, and (with the first tile) waited for.
@@ -444,12 +460,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // request's: their results go nowhere.
                     if (of_v || w4 != 0) return;
                     go = go && warp_wait(&W.q_free, (parts & 1) ^ 1, gave_up);
-                    const int halves = A.rows > 128 ? 2 : 1, token = A.first + (int)P.by_group((uint32_t)row0);
-                    if (go && lane == 0) bar_expect(&W.q_full, halves * C_::kOperand);
+                    const int halves = NG > 1 && A.rows > 128 ? 2 : 1, token = A.first + (int)P.by_group((uint32_t)row0);
+                    if (go && lane == 0) bar_expect(&W.q_full, halves * C_::kQuery);
                     __syncwarp();
                     const int m = lane / (DP / 64), q = lane % (DP / 64);
                     if (go && m < halves)
-                        tma_box3(base + m * C_::kOperand + q * (128 * 128), &maps.q, q * 64,
+                        tma_box3(base + m * C_::kQuery + q * (128 * 128), &maps.q, q * 64,
                                  A.head * P.G, token + m * maps.tokens, &W.q_full);
                     return;
                 }
@@ -458,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 2
                     for (int i = t; i < RT * J; i += kLoad) {
                         const int r = i / J, j = i - r * J;
-                        const uint32_t to = (r >> 7) * C_::kOperand + chunk_at(r & 127, j);
+                        const uint32_t to = (r >> 7) * C_::kQuery + chunk_at<128>(r & 127, j);
                         const bool in = r < A.rows && j < chunks;
                         const unsigned short *from =
                             paged_query(P, A.first, A.head, row0 + (in ? r : 0)) + (in ? j * 8 : 0);
@@ -482,8 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int i = t; i < RT * J; i += kLoad) {
                         const int r = i / J, j = i - r * J;
-                        uint4 *at = reinterpret_cast<uint4 *>(smem + (r >> 7) * C_::kOperand +
-                                                              chunk_at(r & 127, j));
+                        uint4 *at = reinterpret_cast<uint4 *>(smem + (r >> 7) * C_::kQuery +
+                                                              chunk_at<128>(r & 127, j));
                         uint32_t w[4] = {at->x, at->y, at->z, at->w};
                         float big = 0.f;
 #pragma unroll
@@ -523,17 +539,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     next = page(i + 1);
                     const uint32_t x = 2 * (done + i) + of_v;
                     go = go && warp_wait(&W.free[slot(x)], phase(x) ^ 1, gave_up);
-                    const int j0 = A.position(A.tile + i);
-                    const uint32_t place = C_::kTiles + slot(x) * C_::kOperand + w4 * (32 * 128);
+                    const int j0 = A.position<PT>(A.tile + i);
+                    const uint32_t place = C_::kTiles + slot(x) * C_::kOperand + w4 * (PW * 128);
                     const unsigned wanted = __ballot_sync(0xffffffffu, block >= 0);
                     // Of K what is not wanted may be anything; of V it has to be zeros, and what some
                     // rows alone see is looked through.
                     if (go && box > 0 &&
-                        (!of_v || (wanted == 0xffffffffu && all_see(P, A.p0, A.p1, j0)))) {
-                        // `box` rows of a page a time (they divide 32 and the page), 64 columns
+                        (!of_v || (wanted == kMine && all_see(P, A.p0, A.p1, j0, PT)))) {
+                        // `box` rows of a page a time (they divide PW and the page), 64 columns
                         note(i, block);
                         const int g = lane / (DP / 64), q = lane % (DP / 64), t = g * box;
-                        const unsigned some = t < 32 ? wanted >> t & (0xffffffffu >> (32 - box)) : 0u;
+                        const unsigned some = t < PW ? wanted >> t & (0xffffffffu >> (32 - box)) : 0u;
                         const int blk = __shfl_sync(0xffffffffu, block,
                                                     some ? t + __ffs(some) - 1 : 0);
                         const unsigned mine = __ballot_sync(0xffffffffu, some != 0u);
@@ -543,10 +559,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         __syncwarp();
                         if (some) {
-                            const uint32_t p = (uint32_t)(j0 + w4 * 32 + t);
+                            const uint32_t p = (uint32_t)(j0 + w4 * PW + t);
                             const int off = (int)(p - P.by_page(p) * C.block_size);
                             const bool nhd = C.layout == SPEC_KV_NHD;
-                            tma_box(base + place + q * (128 * 128) + t * 128, of_v ? &maps.v : &maps.k,
+                            tma_box(base + place + q * (PT * 128) + t * 128, of_v ? &maps.v : &maps.k,
                                     q * 64, nhd ? A.head : off, nhd ? off : A.head, blk,
                                     &W.full[slot(x)]);
                         }
@@ -556,11 +572,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             note(i, block);
                             const uint32_t in = unit(i);
 #pragma unroll 4
-                            for (int q = 0; q < U; ++q) {
+                            for (int q = 0; q < U * PW / 32; ++q) {
                                 const int t = (q * 32 + lane) / U, u = lane % U;
                                 bool ok;
                                 const char *from = source(block, in, t, u, ok);
-                                copy16(base + place + chunk_at(t, u), from, ok);
+                                copy16(base + place + chunk_at<PT>(t, u), from, ok);
                             }
                         }
                         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -575,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 settle(false);
             } else {
                 // a tile's codes wait in registers for its place
-                constexpr int Q = U;                          // chunks of a thread
+                constexpr int Q = U * PW / 32;                // chunks of a thread
                 uint4 y[Q];
                 int block = page(0), next = page(1);
                 auto fetch = [&](int i, int blk) {
@@ -600,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const uint32_t w[4] = {y[q].x, y[q].y, y[q].z, y[q].w};
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
-                                *reinterpret_cast<uint4 *>(to + chunk_at(w4 * 32 + t, 2 * u + h)) =
+                                *reinterpret_cast<uint4 *>(to + chunk_at<PT>(w4 * PW + t, 2 * u + h)) =
                                     make_uint4(halves2<KIND>(w[2 * h]), halves2<KIND>(w[2 * h] >> 16),
                                                halves2<KIND>(w[2 * h + 1]),
                                                halves2<KIND>(w[2 * h + 1] >> 16));
@@ -635,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t jobs = 0, results = 0;   // of this group so far (64 positions each); parts
         bool go = true;
         uint32_t part_at = 0;
-        for (;; ++part_at) {
+        for (; m < NG; ++part_at) {
             go = go && dealt(part_at);
             if (!go) break;
             const PartWords &A = W.part[part_at % kDealt];   // until read(part_at)
@@ -650,8 +666,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // every row sees all of a job that ends at p0 at most and begins past the edge of the
             // last row's window, or is the sinks'
             const int p0 = A.p0, edge = P.window > 0 ? A.p1 - P.window : INT_MIN, hi = A.hi;
-            for (int j = 0; work && j < 2 * n; ++j, ++jobs) {
-                const int i = j >> 1, h = j & 1;
+            for (int j = 0; work && j < HALVES * n; ++j, ++jobs) {
+                const int i = j / HALVES, h = j % HALVES;
                 const uint32_t buf = jobs & 1, s_tm = s_at(m) + lanes + buf * 64;
                 go = go && warp_wait(&W.s_full[m][buf], jobs >> 1 & 1, gave_up);
                 if (!go) break;
@@ -664,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     warp_arrive(&W.p_full[m][buf]);
                     continue;
                 }
-                const int ti = tile0 + i, j0 = (ti < skip ? ti : base_tile + ti) * kPosTile + 64 * h;
+                const int ti = tile0 + i, j0 = (ti < skip ? ti : base_tile + ti) * PT + 64 * h;
                 const uint2 there = *reinterpret_cast<const uint2 *>(&W.seen[(done + i) & 3][2 * h]);
                 const bool plain = (there.x & there.y) == 0xffffffffu && j0 + 63 <= p0 &&
                                    (j0 > edge || j0 + 63 < P.sinks);
@@ -823,10 +839,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (odd && live) {      // NaN and infinities of positions that this row sees
                 for (int i = tile0; i < A.stop; ++i) {
-                    const int j0 = A.position(i);
-                    if (all_see(P, A.p0, A.p1, j0)) continue;
+                    const int j0 = A.position<PT>(i);
+                    if (all_see(P, A.p0, A.p1, j0, PT)) continue;
 #pragma unroll 1
-                    for (int j = j0; j < j0 + kPosTile; ++j) {
+                    for (int j = j0; j < j0 + PT; ++j) {
                         if (!(paged_bits(j, at, hi, P.window, P.sinks) & 1)) continue;
                         const int block = paged_page(P, A.b, j);
                         if (block < 0 || block >= C.num_blocks) continue;
@@ -857,8 +873,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             done += n;
             parts += n > 0;
         }
-        if (!go) {      // the parts that did not come are lost, too
-            PagedWalk<RT> walk(P, kTcFixed, (int64_t)P.G * kPosTile);
+        if (m < NG && !go) {      // the parts that did not come are lost, too
+            PagedWalk<RT, PT> walk(P, kTcFixed, (int64_t)P.G * kPosTile);
             PagedPart A;
             for (uint32_t x = 0; walk.next(P, A); ++x) {
                 if (x < part_at) continue;
@@ -911,16 +927,16 @@ bool make_map(CUtensorMap &map, int dtype, const void *at, int rank, const cuuin
            CUDA_SUCCESS;
 }
 
-Maps make_maps(const PagedAttnParams &p) {
+Maps make_maps(const PagedAttnParams &p, int most) {      // most: positions of a loading warp
     Maps m = {};
     const spec_kv_cache &c = p.cache;
     if (c.D < 64) return m;
     const cuuint64_t d = (cuuint64_t)c.D, h = (cuuint64_t)c.H, n = (cuuint64_t)c.block_size;
     // Pages of a multiple of eight positions: boxes of the largest power of two that divides both
-    // them and 32 (their places in shared memory begin where the swizzle's pattern does).
+    // them and a loading warp's (their places in shared memory begin where the swizzle's pattern does).
     if (n % 8 == 0) {
         const bool nhd = c.layout == SPEC_KV_NHD;
-        const cuuint32_t rows = n % 32 == 0 ? 32 : n % 16 == 0 ? 16 : 8;
+        const cuuint32_t rows = n % 32 == 0 && most == 32 ? 32 : n % 16 == 0 ? 16 : 8;
         const cuuint64_t dims[4] = {d, nhd ? h : n, nhd ? n : h, (cuuint64_t)c.num_blocks};
         const cuuint32_t box[4] = {64, nhd ? 1 : rows, nhd ? rows : 1, 1};
         cuuint64_t strides[3] = {d * 2, (nhd ? h : n) * d * 2, (cuuint64_t)c.k_block_stride * 2};
@@ -948,20 +964,25 @@ cudaError_t launch(const PagedAttnParams &p, int grid, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int vec = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.q_stride % 8 == 0;
     paged_tc_kernel<T, KIND, DP><<<grid, kThreads, C_::kBytes, st>>>(p, vec,
-                                                                   KIND ? Maps{} : make_maps(p));
+                                                                   KIND ? Maps{} : make_maps(p, C_::kPos / 4));
     return cudaGetLastError();
+}
+
+template <int T, int KIND>
+cudaError_t launch_size(const PagedAttnParams &p, int grid, cudaStream_t st) {
+    const int DP = paged_padded(p.cache.D);
+    return DP == 64    ? launch<T, KIND, 64>(p, grid, st)
+           : DP == 128 ? launch<T, KIND, 128>(p, grid, st)
+                       : launch<T, KIND, 256>(p, grid, st);
 }
 
 }  // namespace
 
 template <int T>
 cudaError_t launch_paged_tc_type(const PagedAttnParams &p, int grid, cudaStream_t st) {
-    const bool narrow = p.cache.D <= 64;
-    if (p.cache.kind == SPEC_CACHE_SAME)
-        return narrow ? launch<T, 0, 64>(p, grid, st) : launch<T, 0, 128>(p, grid, st);
-    if (p.cache.kind == SPEC_CACHE_FP8_E4M3)
-        return narrow ? launch<T, 1, 64>(p, grid, st) : launch<T, 1, 128>(p, grid, st);
-    return narrow ? launch<T, 2, 64>(p, grid, st) : launch<T, 2, 128>(p, grid, st);
+    if (p.cache.kind == SPEC_CACHE_SAME) return launch_size<T, 0>(p, grid, st);
+    if (p.cache.kind == SPEC_CACHE_FP8_E4M3) return launch_size<T, 1>(p, grid, st);
+    return launch_size<T, 2>(p, grid, st);
 }
 
 }  // namespace specv

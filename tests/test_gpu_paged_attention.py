@@ -149,7 +149,8 @@ def test_few_rows(h, dt, cache, size, layout, bs, window, sinks):
 MANY = [
     ([33], [0], 1, 1, 64), ([70], [0], 1, 4, 128), ([300], [0], 1, 1, 128), ([65], [190], 2, 4, 64),
     ([1, 140, 0, 2], [700, 100, 3, 0], 2, 2, 128), ([257], [1], 1, 3, 96), ([90], [600], 1, 5, 80),
-    ([129, 64], [0, 64], 1, 2, 48),
+    ([129, 64], [0, 64], 1, 2, 48), ([100], [50], 1, 2, 256), ([130, 20], [300, 0], 2, 4, 192),
+    ([17], [900], 1, 2, 256), ([5, 0, 70], [40, 7, 0], 1, 8, 256),
 ]
 
 
@@ -191,7 +192,8 @@ def put(c, which, b, p, head, d, value):
                                       ("f16", "e5m2")])
 @pytest.mark.parametrize("counts,pos,Gq,D,window,sinks", [
     ([5, 3], [100, 0], 2, 64, 0, 0), ([6, 1], [400, 30], 2, 128, 37, 5), ([3], [200], 1, 256, 50, 2),
-    ([130, 40], [60, 0], 2, 64, 0, 0), ([70, 100], [700, 300], 2, 128, 260, 3)])
+    ([130, 40], [60, 0], 2, 64, 0, 0), ([70, 100], [700, 300], 2, 128, 260, 3),
+    ([70, 33], [300, 0], 2, 256, 90, 3)])
 def test_values_that_are_no_numbers(h, dt, cache, counts, pos, Gq, D, window, sinks):
     """NaN and infinities in K and V reach the rows that see them, and no others."""
     rng = np.random.default_rng(D + len(counts))

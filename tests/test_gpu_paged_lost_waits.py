@@ -20,7 +20,7 @@ def h():
 
 
 @pytest.mark.parametrize("dt,cache", [("bf16", "same"), ("f16", "e4m3")])
-@pytest.mark.parametrize("Gq,D", [(2, 64), (4, 128)])
+@pytest.mark.parametrize("Gq,D", [(2, 64), (4, 128), (2, 256)])
 def test_lost_results_are_not_numbers(h, dt, cache, Gq, D):
     """Whole items and cut ones: every row is NaN and every request has its status; the next call is
     as ever."""
