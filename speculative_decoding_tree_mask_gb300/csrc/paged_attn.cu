@@ -23,75 +23,75 @@ __global__ void __launch_bounds__(kJoinThreads)
     const int c0 = blockIdx.y;
     const int4 note = P.notes[c0];
     if (note.x < 0) return;
-    const int c1 = note.w;
-    PagedReq req;
-    paged_req(P, note.x, req);
-    const int row0 = note.y * rows_tile, rows = min(rows_tile, req.n * P.G - row0);
+    const int c1 = note.w & ((1 << kNoteCtas) - 1), rows = note.z;
     const int d4 = threadIdx.x % F, group = threadIdx.x / F % PG;
-    const int r = blockIdx.x * kPer + threadIdx.x / (F * PG);
-    if (PG == 1 && r >= rows) return;
-    float m = kPagedNoMax, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0 + group; c <= c1 && r < rows; c += 8 * PG) {
-        float4 v[8];
-        float pm[8], pl[8], top = m;
+    const int first = blockIdx.x * kPer + threadIdx.x / (F * PG);
+    // PG 1: more rows than the CTA holds, one after another, two under way
+#pragma unroll 2
+    for (int r = first; r < (PG == 1 ? rows : first + 1); r += gridDim.x * kPer) {
+        float m = kPagedNoMax, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = c0 + group; c <= c1 && r < rows; c += 8 * PG) {
+            float4 v[8];
+            float pm[8], pl[8], top = m;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            pm[u] = kPagedNoMax;
-            const int k = c + u * PG;
-            if (k > c1) continue;
-            const float *part = paged_slot(P, k, k == c0, rows_tile, DP);
-            v[u] = __ldcg(reinterpret_cast<const float4 *>(part + r * DP) + d4);
-            pm[u] = __ldcg(part + rows_tile * DP + r);
-            pl[u] = __ldcg(part + rows_tile * (DP + 1) + r);
+            for (int u = 0; u < 8; ++u) {
+                pm[u] = kPagedNoMax;
+                const int k = c + u * PG;
+                if (k > c1) continue;
+                const float *part = paged_slot(P, k, k == c0, rows_tile, DP);
+                v[u] = __ldcg(reinterpret_cast<const float4 *>(part + r * DP) + d4);
+                pm[u] = __ldcg(part + rows_tile * DP + r);
+                pl[u] = __ldcg(part + rows_tile * (DP + 1) + r);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) top = fmaxf(top, pm[u]);
+            const float a = ex2(m - top);
+            m = top;
+            l *= a;
+            o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (c + u * PG > c1) continue;
+                const float w = ex2(pm[u] - top);
+                o.x = fmaf(v[u].x, w, o.x);
+                o.y = fmaf(v[u].y, w, o.y);
+                o.z = fmaf(v[u].z, w, o.z);
+                o.w = fmaf(v[u].w, w, o.w);
+                l = fmaf(pl[u], w, l);
+            }
         }
+        if (PG > 1) {
+            s_o[threadIdx.x] = o;
+            s_ml[threadIdx.x] = make_float2(m, l);
+            __syncthreads();
+            if (group != 0 || r >= rows) return;
+            float top = m;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) top = fmaxf(top, pm[u]);
-        const float a = ex2(m - top);
-        m = top;
-        l *= a;
-        o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
+            for (int u = 1; u < PG; ++u) top = fmaxf(top, s_ml[threadIdx.x + u * F].x);
+            const float a = ex2(m - top);
+            o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
+            l *= a;
+            m = top;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            if (c + u * PG > c1) continue;
-            const float w = ex2(pm[u] - top);
-            o.x = fmaf(v[u].x, w, o.x);
-            o.y = fmaf(v[u].y, w, o.y);
-            o.z = fmaf(v[u].z, w, o.z);
-            o.w = fmaf(v[u].w, w, o.w);
-            l = fmaf(pl[u], w, l);
+            for (int u = 1; u < PG; ++u) {
+                const float2 ml = s_ml[threadIdx.x + u * F];
+                const float4 v = s_o[threadIdx.x + u * F];
+                const float w = ex2(ml.x - top);
+                o.x = fmaf(v.x, w, o.x);
+                o.y = fmaf(v.y, w, o.y);
+                o.z = fmaf(v.z, w, o.z);
+                o.w = fmaf(v.w, w, o.w);
+                l = fmaf(ml.y, w, l);
+            }
         }
+        const float f = l == 0.f ? 0.f : 1.f / l;
+        const int64_t at = paged_row(P, note.x, note.w >> kNoteCtas, note.y + r);
+        if (d4 * 4 < P.cache.D)
+            paged_store4<T>(P.out, at * P.cache.D + d4 * 4,
+                            make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
+        if (P.lse && d4 == 0) P.lse[at] = paged_lse(m, l);
     }
-    if (PG > 1) {
-        s_o[threadIdx.x] = o;
-        s_ml[threadIdx.x] = make_float2(m, l);
-        __syncthreads();
-        if (group != 0 || r >= rows) return;
-        float top = m;
-#pragma unroll
-        for (int u = 1; u < PG; ++u) top = fmaxf(top, s_ml[threadIdx.x + u * F].x);
-        const float a = ex2(m - top);
-        o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
-        l *= a;
-        m = top;
-#pragma unroll
-        for (int u = 1; u < PG; ++u) {
-            const float2 ml = s_ml[threadIdx.x + u * F];
-            const float4 v = s_o[threadIdx.x + u * F];
-            const float w = ex2(ml.x - top);
-            o.x = fmaf(v.x, w, o.x);
-            o.y = fmaf(v.y, w, o.y);
-            o.z = fmaf(v.z, w, o.z);
-            o.w = fmaf(v.w, w, o.w);
-            l = fmaf(ml.y, w, l);
-        }
-    }
-    const float f = l == 0.f ? 0.f : 1.f / l;
-    const int64_t at = paged_row(P, req.first, note.z, row0 + r);
-    if (d4 * 4 < P.cache.D)
-        paged_store4<T>(P.out, at * P.cache.D + d4 * 4,
-                        make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
-    if (P.lse && d4 == 0) P.lse[at] = paged_lse(m, l);
 }
 
 // How requests are run: by the warps' matrix unit up to 32 rows an item (16 where D is above 128: its
@@ -118,7 +118,9 @@ cudaError_t launch_join(const PagedAttnParams &p, const Plan &n, cudaStream_t st
         return launch_dependent(paged_join_kernel<T, DP, PG>,
                                 dim3((rows * PG + per - 1) / per, n.grid), dim3(kJoinThreads), 0, st,
                                 p, n.rows);
-    return launch_dependent(paged_join_kernel<T, DP, 1>, dim3((rows + per - 1) / per, n.grid),
+    // (one wave of CTAs that have eight SM's worth of them at most)
+    const int wide = (rows + per - 1) / per, most = 8 * p.sms / n.grid > 1 ? 8 * p.sms / n.grid : 1;
+    return launch_dependent(paged_join_kernel<T, DP, 1>, dim3(wide < most ? wide : most, n.grid),
                             dim3(kJoinThreads), 0, st, p, n.rows);
 }
 

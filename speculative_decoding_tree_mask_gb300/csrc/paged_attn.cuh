@@ -243,13 +243,16 @@ __device__ __forceinline__ float *paged_slot(const PagedAttnParams &P, int cta, 
     return P.ws + ((int64_t)cta * 2 + slot) * rows * (d + 2);
 }
 
-// A CTA's note for the joining kernel: the item it began and did not finish (its last), if any,
-// and the CTA that has the item's end. One thread calls it, at the CTA's end.
+// A CTA's note for the joining kernel: of the item it began and did not finish (its last), if any, the
+// request's first row (else -1), the item's first row in the request, its rows, and its K/V head with
+// the CTA that has its end. One thread calls it, at the CTA's end.
+constexpr int kNoteCtas = 12;       // bits
 __device__ __forceinline__ void paged_note(const PagedAttnParams &P, const PagedRange &r,
-                                           const PagedPart &last, bool any) {
+                                           const PagedPart &last, int rows_tile, bool any) {
     int4 note = make_int4(-1, 0, 0, 0);
     if (any && last.begins && !last.ends)
-        note = make_int4(last.b, last.r, last.head, paged_owner(r, last.at + last.w - 1));
+        note = make_int4(last.req.first, last.r * rows_tile, last.rows,
+                         last.head << kNoteCtas | paged_owner(r, last.at + last.w - 1));
     P.notes[blockIdx.x] = note;
 }
 

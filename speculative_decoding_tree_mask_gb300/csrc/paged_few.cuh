@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
         __syncthreads();      // shared memory is free for the next item
         any = true;
     }
-    if (tid == 0) paged_note(P, walk.range, A, any);
+    if (tid == 0) paged_note(P, walk.range, A, RT, any);
 }
 
 template <int T, int KIND, int DP, int MT>

@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!more) break;
                 any = true;
             }
-            if (lane == 0) paged_note(P, walk.range, A, any);
+            if (lane == 0) paged_note(P, walk.range, A, RT, any);
         } else if (m < NG) {
             // ---- multiply, for softmax group m. The whole warp runs the loop and waits, one
             // thread of it issues: what the products are given is then the same in all of the warp.
@@ -313,52 +313,76 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++parts;
                     continue;
                 }
-                const int count = HALVES * n;
-                auto scores = [&](int j) {
-                    const int half = j % HALVES;
-                    const uint32_t x = 2 * (done + j / HALVES), buf = (jobs + j) & 1;
+                // Places of K of tile i and V of tile i, and the words that follow from them: this warp's
+                // own instructions are what a job waits for longest, so they are kept few.
+                uint32_t kx = 2 * done, vx = kx + 1;
+                const uint64_t q_desc = smem_desc(base + m * C_::kQuery, 16, 1024);
+                const uint64_t k0 = smem_desc(base + C_::kTiles, 16, 1024);
+                const uint64_t v0 = smem_desc(base + C_::kTiles, PT * 128, 1024);
+                uint32_t ks = slot(kx), vs = slot(vx);
+                // S of half `half` of the next tile of K
+                auto scores = [&](int half, uint32_t buf, bool last) {
                     if (half == 0)                // a tile's second half came with its first
-                        ok = ok && warp_wait(&W.full[slot(x)], phase(x), gave_up);
+                        ok = ok && warp_wait(&W.full[ks], phase(kx), gave_up);
                     if (!ok) return;              // no products of what did not come
-                    const uint64_t a = smem_desc(base + m * C_::kQuery, 16, 1024);
-                    const uint64_t k = smem_desc(
-                        base + C_::kTiles + slot(x) * C_::kOperand + half * kHalf, 16, 1024);
                     if (lead) {
+                        const uint64_t k = desc_plus(k0 + ks * (C_::kOperand >> 4), half * kHalf);
 #pragma unroll
                         for (int d = 0; d < KS; ++d) {
                             const int in = (d & 3) * 32;
-                            mma_ss(s + buf * 64, desc_plus(a, (d >> 2) * (128 * 128) + in),
+                            mma_ss(s + buf * 64, desc_plus(q_desc, (d >> 2) * (128 * 128) + in),
                                    desc_plus(k, (d >> 2) * (PT * 128) + in),
                                    mma_desc(kType, 64, false), d > 0);
                         }
                         mma_commit(&W.s_full[m][buf]);
-                        if (half == HALVES - 1) mma_commit(&W.free[slot(x)]);
-                        if (j == count - 1) mma_commit(&W.q_free);
+                        if (half == HALVES - 1) mma_commit(&W.free[ks]);
+                        if (last && half == HALVES - 1) mma_commit(&W.q_free);
                     }
                     __syncwarp();
+                    if (half == HALVES - 1) {
+                        kx += 2;
+                        ks = ks + 2 >= kRing ? ks + 2 - kRing : ks + 2;
+                    }
                 };
-                scores(0);
-                if (count > 1) scores(1);
-                for (int j = 0; ok && j < count; ++j) {
-                    const int half = j % HALVES;
-                    const uint32_t x = 2 * (done + j / HALVES) + 1, buf = (jobs + j) & 1;
-                    if (half == 0) ok = warp_wait(&W.full[slot(x)], phase(x), gave_up);
-                    ok = ok && warp_wait(&W.p_full[m][buf], (jobs + j) >> 1 & 1, gave_up);
-                    if (!ok) break;
+                // O of half `half` of the next tile of V; job: of the part
+                auto values = [&](int half, uint32_t buf, int job) {
+                    if (half == 0) ok = warp_wait(&W.full[vs], phase(vx), gave_up);
+                    ok = ok && warp_wait(&W.p_full[m][buf], (jobs + job) >> 1 & 1, gave_up);
+                    if (!ok) return;
                     tc_fence_after();
-                    const uint64_t v = smem_desc(
-                        base + C_::kTiles + slot(x) * C_::kOperand + half * kHalf, PT * 128, 1024);
                     if (lead) {
+                        const uint64_t v = desc_plus(v0 + vs * (C_::kOperand >> 4), half * kHalf);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             mma_ts(o, s + buf * 64 + k * 8, desc_plus(v, k * 2048),
-                                   mma_desc(kType, DP, true), j > 0 || k > 0);
+                                   mma_desc(kType, DP, true), job > 0 || k > 0);
                         mma_commit(&W.o_full[m]);
-                        if (j == count - 1) mma_commit(&W.o_last[m]);
-                        if (half == HALVES - 1) mma_commit(&W.free[slot(x)]);
+                        if (job == HALVES * n - 1) mma_commit(&W.o_last[m]);
+                        if (half == HALVES - 1) mma_commit(&W.free[vs]);
                     }
                     __syncwarp();
-                    if (j + 2 < count) scores(j + 2);
+                    if (half == HALVES - 1) {
+                        vx += 2;
+                        vs = vs + 2 >= kRing ? vs + 2 - kRing : vs + 2;
+                    }
+                };
+                const int count = HALVES * n;
+                if constexpr (HALVES == 2) {      // jobs are even here: a half has its S
+                    scores(0, 0, n == 1);
+                    scores(1, 1, n == 1);
+                    for (int i = 0; ok && i < n; ++i) {
+                        values(0, 0, 2 * i);
+                        if (ok && i + 1 < n) scores(0, 0, i + 2 == n);
+                        if (ok) values(1, 1, 2 * i + 1);
+                        if (ok && i + 1 < n) scores(1, 1, i + 2 == n);
+                    }
+                } else {
+                    scores(0, jobs & 1, n == 1);
+                    if (n > 1) scores(0, (jobs + 1) & 1, n == 2);
+                    for (int i = 0; ok && i < n; ++i) {
+                        values(0, (jobs + i) & 1, i);
+                        if (ok && i + 2 < n) scores(0, (jobs + i) & 1, i + 3 == n);
+                    }
                 }
                 jobs += count;
                 done += n;
