@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 go = go && warp_wait(&W.q_free, (parts & 1) ^ 1, gave_up);
                 if (go) {
-#pragma unroll 2
+#pragma unroll 4
                     for (int i = t; i < RT * J; i += kLoad) {
                         const int r = i / J, j = i - r * J;
                         const uint32_t to = (r >> 7) * C_::kQuery + chunk_at<128>(r & 127, j);
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 if (kScaleQ && go) {
                     // each thread the chunks it brought, a row's beside each other in its warp
-#pragma unroll 1
+#pragma unroll 4
                     for (int i = t; i < RT * J; i += kLoad) {
                         const int r = i / J, j = i - r * J;
                         uint4 *at = reinterpret_cast<uint4 *>(smem + (r >> 7) * C_::kQuery +
@@ -693,6 +693,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; work && j < HALVES * n; ++j, ++jobs) {
                 const int i = j / HALVES, h = j % HALVES;
                 const uint32_t buf = jobs & 1, s_tm = s_at(m) + lanes + buf * 64;
+                const int ti = tile0 + i, j0 = (ti < skip ? ti : base_tile + ti) * PT + 64 * h;
+                const bool inside = j0 + 63 <= p0 && (j0 > edge || j0 + 63 < P.sinks);
                 go = go && warp_wait(&W.s_full[m][buf], jobs >> 1 & 1, gave_up);
                 if (!go) break;
                 tc_fence_after();
@@ -704,10 +706,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     warp_arrive(&W.p_full[m][buf]);
                     continue;
                 }
-                const int ti = tile0 + i, j0 = (ti < skip ? ti : base_tile + ti) * PT + 64 * h;
                 const uint2 there = *reinterpret_cast<const uint2 *>(&W.seen[(done + i) & 3][2 * h]);
-                const bool plain = (there.x & there.y) == 0xffffffffu && j0 + 63 <= p0 &&
-                                   (j0 > edge || j0 + 63 < P.sinks);
+                const bool plain = inside && (there.x & there.y) == 0xffffffffu;
                 auto mask = [&](int q, uint32_t (&y)[32]) {
                     const unsigned see = (q ? there.y : there.x) &
                                          paged_bits(j0 + 32 * q, at, hi, P.window, P.sinks);
@@ -716,7 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 32; ++e)
                         if (!((see >> e) & 1)) y[e] = 0xff800000u;
                 };
-                float job_sum = INFINITY;
+                float job_sum = 0.f;
+                bool fine = false;
                 // P by the reference at hand, kept if no score was too far above it.
                 if (!apart) {
                     uint32_t x[2][32];
@@ -738,13 +739,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int q = 0; q < 2; ++q) sums[q] = probabilities<I>(x[q], factor, top, 0ull);
                     float a, b;
                     unpack_f32x2(add_f32x2(sums[0], sums[1]), a, b);
-                    job_sum = apart ? INFINITY : a + b;
-                    if (__all_sync(0xffffffffu, job_sum <= kMost)) {
+                    job_sum = a + b;
+                    fine = __all_sync(0xffffffffu, job_sum <= kMost) && !apart;
+                    if (fine) {
                         tmem_st16(s_tm, x[0]);
                         tmem_st16(s_tm + 16, x[1]);
                     }
                 }
-                if (__any_sync(0xffffffffu, !(job_sum <= kMost))) {
+                if (!fine) {
                     // The scores again: their largest raises the references of all the warp's rows; P
                     // of 32 positions takes the place of 16 that have been read.
                     float x = kPagedNoMax;
