@@ -174,9 +174,10 @@ cudaError_t launch_paged_attn(const PagedAttnParams &given, cudaStream_t st) {
     PagedAttnParams p = given;
     const int64_t R = (int64_t)p.max_new * p.G;
     const Plan n = plan(R, p.cache.D, p.cache.kind, p.sms);
-    // (a batch as large as its largest requests has those alone)
-    const bool both = n.mt == 0 && p.T < (int64_t)p.B * p.max_new;
     const int few = few_beside(p.G, p.cache.D);
+    // the fewest rows that a request may have, the others having the most
+    const int64_t least = p.T - (int64_t)(p.B - 1) * p.max_new;
+    const bool both = n.mt == 0 && least * p.G <= few;
     const cudaError_t e = run(p, n, both ? few : 0, INT32_MAX, st);
     if (!both || e != cudaSuccess) return e;
     p.workspace = static_cast<char *>(p.workspace) + plan_bytes(n, p.cache.D);

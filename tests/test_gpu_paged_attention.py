@@ -295,6 +295,14 @@ def test_few_and_many_rows_of_one_batch(h, dt, cache):
     c.check(out, lse)
 
 
+@pytest.mark.parametrize("counts", [[40, 40, 1], [40, 40, 2], [40, 0, 40], [40, 39], [33, 1], [1, 33]])
+@pytest.mark.parametrize("Gq", [1, 8])
+def test_the_fewest_rows_that_a_batch_may_hold(h, counts, Gq):
+    """Where the sizes given leave room for a request of few rows, and where they do not."""
+    c = Case(np.random.default_rng(len(counts)), counts, [70] * len(counts), 1, Gq, 64, "f16")
+    c.check(*c.run(h, max_new=max(counts)))
+
+
 @pytest.mark.parametrize("counts,Gq", [([1, 1, 1], 8), ([200, 1, 30], 4)])
 def test_repeated_and_captured(h, counts, Gq):
     """The same bits every time, on a stream of the caller's, and from two graphs that share a
