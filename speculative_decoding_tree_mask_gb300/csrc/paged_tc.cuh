@@ -51,8 +51,14 @@ constexpr int kSoftmax = 256;     // threads of the two softmax groups
 constexpr int kThreads = kSoftmax + kLoad + 128;   // the last warpgroup: two warps multiply
 constexpr int kMmaWarp = (kSoftmax + kLoad) / 32;
 constexpr int kRing = 5;
-// What an item costs besides its keys, in positions.
-constexpr int kTcFixed = 256;
+// What an item costs besides its keys, in positions, so that CTAs of many short items and of few long
+// ones end together. Two prompts of 8192 and 5844 tokens took, with 256, 384, 448, 512:
+//   D = 128, 16 bits    671, 637, 642, 646 us   (five of 3300 after 1000: 398, 384, 383, 385)
+//   D = 128, 8 bits    1126, 987, 935, 918 us   (eight of 2000: 332, 309, 295, 300)
+//   D = 64, 16 bits     598, 609, 607, 611 us   (192: 608)
+//   D = 256, two of 4096, 16 bits 230, 234, 237, 240 us; 8 bits 428, 441, 445 us.
+template <int KIND, int DP>
+constexpr int kTcFixed = DP == 256 ? 256 : KIND ? 448 : DP == 128 ? 384 : 256;
 
 // D above 128: one softmax group and tiles of 64 positions, so that queries, ring and sums take the
 // same room.
@@ -264,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int m = warp - kMmaWarp;
         if (m == 2) {
             // ---- deal ----
-            PagedWalk<RT, PT> walk(P, kTcFixed, (int64_t)P.G * kPosTile);
+            PagedWalk<RT, PT> walk(P, kTcFixed<KIND, DP>, (int64_t)P.G * kPosTile);
             PagedPart A;
             bool any = false, go = true;
             for (uint32_t x = 0;; ++x) {
@@ -900,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             parts += n > 0;
         }
         if (m < NG && !go) {      // the parts that did not come are lost, too
-            PagedWalk<RT, PT> walk(P, kTcFixed, (int64_t)P.G * kPosTile);
+            PagedWalk<RT, PT> walk(P, kTcFixed<KIND, DP>, (int64_t)P.G * kPosTile);
             PagedPart A;
             for (uint32_t x = 0; walk.next(P, A); ++x) {
                 if (x < part_at) continue;
