@@ -370,7 +370,8 @@ int spec_tree_attention_fp4(spec_handle h, const void *q, int64_t q_stride, cons
  * seq_pos[b] + i of its sequence; seq_pos int32 [B] is the number of positions before. A request
  * whose rows are not within 0 .. T - 1 (or with row_start[b] > row_start[b + 1]) takes no part
  * (SPEC_REQ_BAD_RANGE). Rows of no request are not read, and their results are left as they were.
- * Requests do not share rows: row_start does not fall. B is limited by the handle, T by 2^31 - 1.
+ * Requests do not share rows: row_start does not fall. B is limited by the handle, T by 2^31 - 1;
+ * with T 0 nothing is launched and the statuses are 0.
  *
  * The paged cache (host struct, copied at the call; the pointers are device memory):
  *   k, v         SPEC_KV_NHD [num_blocks, block_size, H, D] or SPEC_KV_HND [num_blocks, H,
@@ -584,9 +585,10 @@ const char *spec_error_string(int code);
  *   into the arrival counter of row `row` (b * N + node) after zeroing the counters, so its
  *   check must catch it. Returns SPEC_ERR_UNSUPPORTED in release builds.
  * spec_debug_inject_lost_wait: arms a one-shot injection for tests: if the next
- *   spec_tree_attention_fp4 call on the handle runs on the tcgen05 tensor cores (more than 32
- *   query rows a K/V head, D 64 or 128), every wait between the kernel's warps gives up at once,
- *   before any product is issued. SPEC_ERR_UNSUPPORTED in release builds.
+ *   spec_tree_attention_fp4 or spec_paged_attention call on the handle runs on the tcgen05 tensor
+ *   cores (more than 32 query rows a K/V head; the former with D 64 or 128), every wait between the
+ *   kernel's warps gives up at once, before any product is issued. SPEC_ERR_UNSUPPORTED in release
+ *   builds.
  * spec_debug_words: copies the debug words of requests 0..B-1 of the handle's last call into
  *   the device int32 array `words` (asynchronously on `stream`). SPEC_ERR_UNSUPPORTED in
  *   release builds.

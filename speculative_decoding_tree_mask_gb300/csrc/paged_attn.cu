@@ -4,8 +4,11 @@
 namespace specv {
 namespace {
 
-// The most rows of the kernel for few; and beside a launch on the tensor cores (16: one token of up to
-// 16 heads a group).
+// The most rows of the kernel for few. With 24 rows (chains of six, 32 and 8 heads x 128) it takes 259 us
+// for 64 chains over up to 8192 positions where the tensor cores take 255, but 246 against 306 over an
+// 8-bit cache, 39 against 54 for 16 chains over 1000, and with 32 rows at D = 64 164 against 212. Beside a
+// launch on the tensor cores 16, one token of up to 16 heads a group: a mixed batch (below) takes 177 us,
+// 183 with 32.
 int few_rows(int D) { return paged_padded(D) == 256 ? 16 : 32; }
 int few_beside(int G, int D) { return G <= 16 ? 16 : few_rows(D); }
 
@@ -156,7 +159,7 @@ cudaError_t run(PagedAttnParams p, const Plan &n, int rows_over, int rows_most, 
 
 // A batch may hold requests of few rows and of many; which, the device knows alone. Where it may
 // hold both, both kernels are launched and take their own: 22 decoding requests over up to 12000
-// positions beside two chunks of 512 tokens (D = 64, 8 K/V heads) took 218 us when the tensor cores
+// positions beside a chunk of 512 tokens (D = 64, 8 K/V heads) take 181 us, 218 when the tensor cores
 // had a tile of 256 rows for four.
 int64_t paged_attn_workspace(int max_new, int G, int D, int sms) {
     const int64_t R = (int64_t)max_new * G;

@@ -10,9 +10,9 @@
 // and the total weight, in the items' order, is cut into equal ranges, one for each CTA of a single
 // wave, whatever the requests' sizes (which only the device knows). A cut inside an item falls
 // between two of its tiles, the same one for both CTAs. (Short items left whole cost more than their
-// joining: 256 of up to 8 tiles took 50 us in one CTA each, 37 cut.) Whole items are finished in place; the parts
-// of a cut item go to the workspace (row sums and references and the unnormalised rows, float32),
-// and a second kernel joins them in their order.
+// joining: 256 of up to 8 tiles took 50 us in one CTA each, 37 cut.) Whole items are finished in place;
+// the parts of a cut item go to the workspace (row sums and references and the unnormalised rows,
+// float32), and a second kernel joins them in their order.
 #pragma once
 
 #include "rope_device.cuh"

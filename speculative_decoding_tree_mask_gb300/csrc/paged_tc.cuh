@@ -22,10 +22,18 @@
 //            ahead, so that the others neither compute them nor hold them in registers.
 //
 // While softmax works on one S, the tensor core multiplies with the P before and makes the next
-// scores: with one S of 128 columns a group it had to wait for softmax, and softmax for it (2.2 us a
-// tile where products and shared memory need 1.1). The price is that a product of 64 columns reads
-// 6 KB of shared memory for 32 clocks of work and gets 48: a tile's reads and writes take 2560
-// clocks, its products 2048.
+// scores: with one S of 128 columns a group it had to wait for softmax, and softmax for it (2048 tokens
+// after 60000: 1.96 ms against 1.54 at the time, and no less when the two groups took turns). The price
+// is that a product of 64 columns reads 6 KB of shared memory for 32 clocks of work and gets 48: a
+// tile's reads and writes take 2560 clocks, its products 2048. What is left is latency, that of a job of
+// 64 positions from S to P and the meetings at its ends: issue slots are taken in 49% of the cycles, the
+// tensor pipe is active in 51%, and no other pipe in more than 33%.
+//
+// 32 query and 8 K/V heads x 128: two prompts of 8192 and 5845 tokens 634 us, 1.31 PFLOP/s (66% of the
+// measured cuBLAS rate), over an e4m3 cache 969 us (the codes' way through registers); 2048 tokens after
+// 60000 1.43 ms, 1.43 PFLOP/s; a window of 4096 with sinks 238 us, 0.97 PFLOP/s (items of 35 tiles, two
+// of them seen in part); D = 64 600 us, 0.69 PFLOP/s (softmax costs as much as at 128); D = 256, two of
+// 4096 with 16 and 4 heads, 230 us, 0.90 PFLOP/s.
 //
 // Items of up to 128 rows (a decoding request in a mixed batch) leave the second group idle, and
 // warps without a live row touch nothing: a tile then takes less time than its bytes do.
@@ -52,7 +60,7 @@ constexpr int kThreads = kSoftmax + kLoad + 128;   // the last warpgroup: two wa
 constexpr int kMmaWarp = (kSoftmax + kLoad) / 32;
 constexpr int kRing = 5;
 // What an item costs besides its keys, in positions, so that CTAs of many short items and of few long
-// ones end together. Two prompts of 8192 and 5844 tokens took, with 256, 384, 448, 512:
+// ones end together. Two prompts of 8192 and 5845 tokens took, with 256, 384, 448, 512:
 //   D = 128, 16 bits    671, 637, 642, 646 us   (five of 3300 after 1000: 398, 384, 383, 385)
 //   D = 128, 8 bits    1126, 987, 935, 918 us   (eight of 2000: 332, 309, 295, 300)
 //   D = 64, 16 bits     598, 609, 607, 611 us   (192: 608)
