@@ -16,9 +16,10 @@
 // too many tokens pass (equal logits), the K-th key of those at hand is the next bound.
 //
 // DRAM bounds it: 4096 rows of 152064 bfloat16 logits, 8 tokens each, 236 us, 5.3 TB/s (78% of the
-// measured copy), without tokens 207 us. What is left is each row's end, during which its CTA loads
-// nothing: six CTAs an SM are what registers allow (four 256 us). A row has a CTA, or with few rows a
-// cluster of up to eight CTAs (20 rows of 50257: 17 us, 25 with a CTA each), whose parts meet in
+// measured copy), without tokens 207 us; 2048 rows of float32 224 us, 5.6 TB/s. What is left is each
+// row's end, during which its CTA loads nothing: six CTAs an SM are what registers allow (four 256 us).
+// (The next row's first 8 to 64 KB brought to L2 meanwhile: no difference.) A row has a CTA, or with few
+// rows a cluster of up to eight CTAs (20 rows of 50257: 17 us, 25 with a CTA each), whose parts meet in
 // distributed shared memory (no workspace, no atomics on memory).
 
 #include "spec_device.cuh"
@@ -38,6 +39,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 // CTAs of an SM: while one orders its likeliest tokens the others have to keep the loads in flight.
 constexpr int kCtas = 6;
 
+// `bytes` (a multiple of 16) from p (16-byte aligned) on to L2.
+__device__ __forceinline__ void prefetch_l2(const void *p, int bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ uint32_t order_of(float x) {     // increasing in x; -0 counts as 0
     const uint32_t u = __float_as_uint(x + 0.f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
@@ -238,6 +243,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(LogprobsParam
         int left = per;
         float *to = group_max + tid;
         for (int i = v0 + tid; i - tid < v1; i += kUnroll * kThreads) {
+            // float32: the next round to L2 meanwhile (2048 rows of 152064, 8 tokens: 247 us -> 224;
+            // bfloat16, twice the instructions a byte, loses by it: 4096 rows 234 -> 240; so do rows
+            // of several CTAs, with few rounds each: 192 of 50257 25 -> 27)
+            if (DT == 0 && cluster == 1 && tid == 0) {
+                const int next = i + kUnroll * kThreads;
+                if (next < v1) prefetch_l2(vec + next, min(kUnroll * kThreads, v1 - next) * 16);
+            }
             uint4 w[kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u)
