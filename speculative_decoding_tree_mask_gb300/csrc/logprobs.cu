@@ -19,7 +19,7 @@
 // measured copy), without tokens 207 us; 2048 rows of float32 224 us, 5.6 TB/s. What is left is each
 // row's end, during which its CTA loads nothing: six CTAs an SM are what registers allow (four 256 us).
 // (The next row's first 8 to 64 KB brought to L2 meanwhile: no difference.) A row has a CTA, or with few
-// rows a cluster of up to eight CTAs (20 rows of 50257: 17 us, 25 with a CTA each), whose parts meet in
+// rows a cluster of up to eight CTAs (20 rows of 50257: 11 us, 19 with a CTA each), whose parts meet in
 // distributed shared memory (no workspace, no atomics on memory).
 
 #include "spec_device.cuh"
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(LogprobsParam
         for (int i = v0 + tid; i - tid < v1; i += kUnroll * kThreads) {
             // float32: the next round to L2 meanwhile (2048 rows of 152064, 8 tokens: 247 us -> 224;
             // bfloat16, twice the instructions a byte, loses by it: 4096 rows 234 -> 240; so do rows
-            // of several CTAs, with few rounds each: 192 of 50257 25 -> 27)
+            // of several CTAs, with few rounds each: 192 of 50257 19 -> 21)
             if (DT == 0 && cluster == 1 && tid == 0) {
                 const int next = i + kUnroll * kThreads;
                 if (next < v1) prefetch_l2(vec + next, min(kUnroll * kThreads, v1 - next) * 16);
