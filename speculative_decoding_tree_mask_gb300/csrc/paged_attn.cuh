@@ -50,6 +50,14 @@ __device__ __forceinline__ int paged_req(const PagedAttnParams &P, int b, PagedR
     return q.n > 0 && (q.pos < 0 || (int64_t)q.pos + q.n > most) ? SPEC_REQ_BAD_SLOT : 0;
 }
 
+// Where row i of a request that begins at `pos` ends: the positions up to its token's, that included,
+// 0 if it stands before them all. pos may be any int32, so this goes past 2^31 (and not past 2^32),
+// and past the table: a window ends with its row's own position, whether the table has that or not.
+__device__ __forceinline__ uint32_t paged_end(const PagedAttnParams &P, int pos, int i) {
+    const int64_t p = (int64_t)pos + P.by_group((uint32_t)i);
+    return (uint32_t)max(p + 1, (int64_t)0);
+}
+
 // Weights (see above). RT: rows of a tile, a power of two.
 template <int RT>
 struct PagedWeights {
@@ -84,7 +92,7 @@ struct PagedPart {
     int b, r, head;                 // request, row tile, K/V head
     PagedReq req;
     int rows;                       // of the tile
-    int p0, p1;                     // positions of its first and last row's token
+    uint32_t e0, e1;                // ends (see paged_end) of its first and last row
     int lo, hi;                     // positions that any row sees: [lo, hi), and those below sinks
     int skip, base;                 // tile i stands at position PT * (i < skip ? i : base + i)
     int tile, stop, nt;             // tiles of this part, of the item
@@ -193,16 +201,11 @@ struct PagedWalk {
         p.w = w;
         const int row0 = r * RT;
         p.rows = min(RT, req.n * P.G - row0);
-        // positions in 64 bits first: seq_pos may be anything
-        const int64_t most = (int64_t)P.cache.max_blocks * P.cache.block_size;
-        const int64_t p0 = (int64_t)req.pos + P.by_group((uint32_t)row0),
-                      p1 = (int64_t)req.pos + P.by_group((uint32_t)(row0 + p.rows - 1));
-        p.p0 = (int)min(max(p0, (int64_t)-1), most);
-        p.p1 = (int)min(max(p1, (int64_t)-1), most);
-        const int64_t hi = min(p1 + 1, most);
-        p.hi = (int)max(hi, (int64_t)0);
-        const int64_t lo = P.window > 0 ? max(p0 - P.window + 1, (int64_t)0) : 0;
-        p.lo = (int)min(lo, (int64_t)p.hi);
+        const int most = P.cache.max_blocks * P.cache.block_size;       // fits: checked on the host
+        p.e0 = paged_end(P, req.pos, row0);
+        p.e1 = paged_end(P, req.pos, row0 + p.rows - 1);
+        p.hi = (int)min(p.e1, (uint32_t)most);
+        p.lo = P.window > 0 ? (int)min(p.e0 - min(p.e0, (uint32_t)P.window), (uint32_t)p.hi) : 0;
         const int t0 = p.lo / PT, t1 = (p.hi + PT - 1) / PT;
         p.skip = min((min(P.sinks, p.hi) + PT - 1) / PT, t0);
         p.base = t0 - p.skip;
@@ -268,12 +271,6 @@ __device__ __forceinline__ const unsigned short *paged_query(const PagedAttnPara
     return static_cast<const unsigned short *>(P.q) + (first + t) * P.q_stride +
            (int64_t)(head * P.G + (i - t * P.G)) * P.cache.D;
 }
-// The position of its token in a request that begins at pos, within -1 and the table's end.
-__device__ __forceinline__ int paged_position(const PagedAttnParams &P, int pos, int i) {
-    const int64_t p = (int64_t)pos + P.by_group((uint32_t)i);
-    return (int)min(max(p, (int64_t)-1), (int64_t)P.cache.max_blocks * P.cache.block_size);
-}
-
 // Four values of an output row.
 template <int T>
 __device__ __forceinline__ void paged_store4(void *out, int64_t e, float4 v) {
@@ -318,14 +315,22 @@ __device__ __forceinline__ float paged_lse(float m, float l) {
     return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// Bits of the 32 positions from j0 on that a row at position p sees, among those below `hi`.
-__device__ __forceinline__ unsigned paged_bits(int j0, int p, int hi, int window, int sinks) {
-    auto below = [&](int n) -> unsigned {      // positions j0 .. n - 1
+// Bits of the 32 positions from j0 on that a row of this end sees, among those below `hi`.
+__device__ __forceinline__ unsigned paged_bits(uint32_t j0, uint32_t end, int hi, int window,
+                                               int sinks) {
+    auto below = [&](uint32_t n) -> unsigned {      // positions j0 .. n - 1
         return n <= j0 ? 0u : n - j0 >= 32 ? 0xffffffffu : (1u << (n - j0)) - 1u;
     };
-    unsigned seen = below(min(p + 1, hi));
-    if (window > 0) seen &= ~below(p - window + 1) | below(sinks);
+    unsigned seen = below(min(end, (uint32_t)hi));
+    if (window > 0) seen &= ~below(end - min(end, (uint32_t)window)) | below((uint32_t)sinks);
     return seen;
+}
+// Whether rows of ends e0 (the first's) to e1 all see all of the n positions from j0 on, as far as
+// those are there.
+__device__ __forceinline__ bool all_see(const PagedAttnParams &P, uint32_t e0, uint32_t e1, int j0,
+                                        int n) {
+    return (uint32_t)(j0 + n) <= e0 &&
+           (P.window == 0 || (uint32_t)j0 + (uint32_t)P.window >= e1 || j0 + n <= P.sinks);
 }
 
 // A 16-byte copy to shared memory; zeros when !ok.

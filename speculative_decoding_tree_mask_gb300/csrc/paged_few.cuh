@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
         __syncthreads();
 
         float fac[MT][2], m[MT][2], l[MT][2], o[MT][NT][4];
-        int at[MT][2];                             // positions of this lane's rows g and g + 8
+        uint32_t at[MT][2];                        // ends of this lane's rows g and g + 8
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
                 fac[i][e] = s_fac[r];
                 m[i][e] = kPagedNoMax;
                 l[i][e] = 0.f;
-                at[i][e] = r < A.rows ? paged_position(P, A.req.pos, row0 + r) : -1;
+                at[i][e] = r < A.rows ? paged_end(P, A.req.pos, row0 + r) : 0u;
             }
 #pragma unroll
         for (int i = 0; i < MT; ++i)
@@ -260,8 +260,7 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, DP, MT>::kCtas)
             const int j0 = first(s);
             if (seen == 0u) continue;
             // all positions are there and every row sees them
-            const bool plain = seen == kAll && j0 + NP - 1 <= A.p0 &&
-                               (P.window == 0 || j0 > A.p1 - P.window || j0 + NP - 1 < P.sinks);
+            const bool plain = seen == kAll && all_see(P, A.e0, A.e1, j0, NP);
             float x[MT][HT][4];
 #pragma unroll
             for (int i = 0; i < MT; ++i)

@@ -44,8 +44,6 @@
 // see them.
 #pragma once
 
-#include <climits>
-
 #include <cuda.h>
 
 #include "paged_attn.cuh"
@@ -86,7 +84,9 @@ struct Tc {
 
 // A part as the warps read it (see PagedPart); b -1: there are no more.
 struct PartWords {
-    int b, r, head, first, pos, rows, p0, p1, lo, hi, skip, base, tile, stop, begins, ends;
+    int b, r, head, first, pos, rows;
+    uint32_t e0, e1;
+    int lo, hi, skip, base, tile, stop, begins, ends;
 
     template <int PT>
     __device__ __forceinline__ int position(int i) const {
@@ -136,11 +136,6 @@ __device__ __forceinline__ void store32(void *to, const uint32_t (&w)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]),
                  "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
-}
-
-// Whether every row of the item sees all of the n positions from j0 on, as far as they are there.
-__device__ __forceinline__ bool all_see(const PagedAttnParams &P, int p0, int p1, int j0, int n) {
-    return j0 + n - 1 <= p0 && (P.window == 0 || j0 > p1 - P.window || j0 + n - 1 < P.sinks);
 }
 
 // The reference of a row comes from a rounded product f s, within 2^-24 of it, which f s - top in
@@ -286,8 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 go = go && warp_wait(&W.part_free[x % kDealt], (x / kDealt & 1) ^ 1, gave_up);
                 if (go && lane == 0) {
                     PartWords &w = W.part[x % kDealt];
-                    w = PartWords{more ? A.b : -1, A.r, A.head, A.req.first, A.req.pos, A.rows, A.p0,
-                                  A.p1, A.lo, A.hi, A.skip, A.base, A.tile, A.stop, A.begins, A.ends};
+                    w = PartWords{more ? A.b : -1, A.r, A.head, A.req.first, A.req.pos, A.rows, A.e0,
+                                  A.e1, A.lo, A.hi, A.skip, A.base, A.tile, A.stop, A.begins, A.ends};
                     bar_arrive(&W.part_full[x % kDealt]);
                 }
                 __syncwarp();
@@ -454,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Tile i has come to its place: what the rows see in part is looked through.
             auto arrived = [&](int i) {
                 const uint32_t x = 2 * (done + i) + of_v;
-                if (of_v && !all_see(P, A.p0, A.p1, A.position<PT>(A.tile + i), PT)) {
+                if (of_v && !all_see(P, A.e0, A.e1, A.position<PT>(A.tile + i), PT)) {
                     char *to = smem + C_::kTiles + slot(x) * C_::kOperand;
                     bool odd = false;
                     constexpr int J = DP / 8;
@@ -583,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // Of K what is not wanted may be anything; of V it has to be zeros, and what some
                     // rows alone see is looked through.
                     if (go && box > 0 &&
-                        (!of_v || (wanted == kMine && all_see(P, A.p0, A.p1, j0, PT)))) {
+                        (!of_v || (wanted == kMine && all_see(P, A.e0, A.e1, j0, PT)))) {
                         // `box` rows of a page a time (they divide PW and the page), 64 columns
                         note(i, block);
                         const int g = lane / (DP / 64), q = lane % (DP / 64), t = g * box;
@@ -698,17 +693,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row0 = A.r * RT;
             const bool live = r < A.rows, work = n > 0 && m * 128 < A.rows;
             const bool warp_live = m * 128 + (warp & 3) * 32 < A.rows;
-            const int at = paged_position(P, A.pos, row0 + min(r, A.rows - 1));
+            const uint32_t at = paged_end(P, A.pos, row0 + min(r, A.rows - 1));
             float top = kPagedNoMax, sum = 0.f, factor = 0.f;    // top: the row's reference
             bool apart = false;       // a row of the warp has scores beyond kApart
-            // every row sees all of a job that ends at p0 at most and begins past the edge of the
-            // last row's window, or is the sinks'
-            const int p0 = A.p0, edge = P.window > 0 ? A.p1 - P.window : INT_MIN, hi = A.hi;
+            // every row sees all of a job that is not past the first row's end and begins in the last
+            // row's window, or is the sinks'
+            const uint32_t e0 = A.e0, from = P.window > 0 ? A.e1 - min(A.e1, (uint32_t)P.window) : 0u;
+            const int hi = A.hi;
             for (int j = 0; work && j < HALVES * n; ++j, ++jobs) {
                 const int i = j / HALVES, h = j % HALVES;
                 const uint32_t buf = jobs & 1, s_tm = s_at(m) + lanes + buf * 64;
                 const int ti = tile0 + i, j0 = (ti < skip ? ti : base_tile + ti) * PT + 64 * h;
-                const bool inside = j0 + 63 <= p0 && (j0 > edge || j0 + 63 < P.sinks);
+                const bool inside =
+                    (uint32_t)(j0 + 64) <= e0 && ((uint32_t)j0 >= from || j0 + 64 <= P.sinks);
                 go = go && warp_wait(&W.s_full[m][buf], jobs >> 1 & 1, gave_up);
                 if (!go) break;
                 tc_fence_after();
@@ -880,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (odd && live) {      // NaN and infinities of positions that this row sees
                 for (int i = tile0; i < A.stop; ++i) {
                     const int j0 = A.position<PT>(i);
-                    if (all_see(P, A.p0, A.p1, j0, PT)) continue;
+                    if (all_see(P, A.e0, A.e1, j0, PT)) continue;
 #pragma unroll 1
                     for (int j = j0; j < j0 + PT; ++j) {
                         if (!(paged_bits(j, at, hi, P.window, P.sinks) & 1)) continue;

@@ -1,0 +1,60 @@
+"""Paged attention at the edges of what a call may say (needs a GB300). Tolerances are those of
+test_gpu_paged_attention, whose cases these are built from."""
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_paged_attention as T
+from oracle import paged_step as S
+from speculative_decoding_tree_mask_gb300 import binding as G
+
+pytestmark = pytest.mark.gpu
+DEV = T.DEV
+
+
+@pytest.fixture(scope="module")
+def h():
+    G.load()
+    with G.Handle(4096, 64, 1 << 10, 0) as handle:
+        yield handle
+
+
+def cut_table(c, pages):
+    """The first `pages` of each request's table, and of what the oracle knows."""
+    c.table = np.ascontiguousarray(c.table[:, :pages])
+    for all_ in (c.k64, c.v64):
+        all_[:] = [x[:pages * c.bs] for x in all_]
+
+
+# ---- positions past the table -------------------------------------------------------------------
+
+@pytest.mark.parametrize("dt,cache", [("bf16", "same"), ("f16", "e4m3")])
+@pytest.mark.parametrize("n,Gq,D", [(8, 2, 64), (8, 2, 128), (8, 1, 256), (80, 2, 64), (150, 2, 128),
+                                    (80, 2, 256)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (4, 0), (4, 3), (40, 1), (100, 0), (3, 500)])
+def test_windows_of_rows_past_the_table(h, dt, cache, n, Gq, D, window, sinks):
+    """A row whose position the table does not have sees the window that ends with that position, as
+    far as the table goes, and the sinks; rows whose whole window is past it see nothing else."""
+    rng = np.random.default_rng(D + n)
+    pos = [254, 250 - n, 300]             # the table ends at 256: all but two rows, some, all
+    c = T.Case(rng, [n] * 3, pos, 2, Gq, D, dt, cache, S.HND, 16, window, sinks)
+    cut_table(c, 16)
+    st = torch.full((3,), 9, dtype=torch.int32, device=DEV)
+    out, lse = c.run(h, st)
+    assert st.tolist() == [S.BAD_SLOT, 0, S.BAD_SLOT]
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("n,Gq", [(8, 2), (80, 2)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (2 ** 31 - 1, 0), (2 ** 31 - 1, 5), (2 ** 31 - 100, 0),
+                                          (2 ** 31 - 1, 2 ** 31 - 1), (7, 2)])
+def test_positions_near_two_to_the_31(h, n, Gq, window, sinks):
+    """Positions up to and beyond 2^31 and windows as large: sums of the two stay exact."""
+    rng = np.random.default_rng(n)
+    c = T.Case(rng, [n, n], [100, 200], 2, Gq, 64, "bf16", "same", S.NHD, 16, window, sinks)
+    cut_table(c, 6)
+    c.pos = [2 ** 31 - 1, 2 ** 31 - 4]
+    st = torch.full((2,), 9, dtype=torch.int32, device=DEV)
+    out, lse = c.run(h, st)
+    assert st.tolist() == [S.BAD_SLOT, S.BAD_SLOT]
+    c.check(out, lse)
