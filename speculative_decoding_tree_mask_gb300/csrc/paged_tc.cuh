@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int row0 = A.r * RT, chunks = C.D / 8, t = tid - kSoftmax;
                 if (KIND == 0 && maps.tokens > 0) {
                     // by TMA: boxes of 128 rows and 64 columns. Rows past the item's may be another
-                    // request's: their results go nowhere.
+                    // request's or no request's: their results go nowhere, and nothing depends on them.
                     if (of_v || w4 != 0) return;
                     go = go && warp_wait(&W.q_free, (parts & 1) ^ 1, gave_up);
                     const int halves = NG > 1 && A.rows > 128 ? 2 : 1, token = A.first + (int)P.by_group((uint32_t)row0);
@@ -696,6 +696,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t at = paged_end(P, A.pos, row0 + min(r, A.rows - 1));
             float top = kPagedNoMax, sum = 0.f, factor = 0.f;    // top: the row's reference
             bool apart = false;       // a row of the warp has scores beyond kApart
+            // Lanes past the item's rows hold queries of the rows behind it (see queries()), which may
+            // be anything: they have no vote in what the warp does.
+            auto far_apart = [&] {
+                return __any_sync(0xffffffffu, live && fabsf(top) > kApart && top != kPagedNoMax) != 0;
+            };
             // every row sees all of a job that is not past the first row's end and begins in the last
             // row's window, or is the sinks'
             const uint32_t e0 = A.e0, from = P.window > 0 ? A.e1 - min(A.e1, (uint32_t)P.window) : 0u;
@@ -743,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j == 0) {
                         const float big = fmaxf(largest32(x[0]), largest32(x[1]));
                         top = paged_reference(kPagedNoMax, fmaxf(kPagedNoMax, big * factor));
-                        apart = __any_sync(0xffffffffu, fabsf(top) > kApart && top != kPagedNoMax);
+                        apart = far_apart();
                     }
                     uint64_t sums[2];
 #pragma unroll
@@ -751,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float a, b;
                     unpack_f32x2(add_f32x2(sums[0], sums[1]), a, b);
                     job_sum = a + b;
-                    fine = __all_sync(0xffffffffu, job_sum <= kMost) && !apart;
+                    fine = __all_sync(0xffffffffu, !live || job_sum <= kMost) && !apart;
                     if (fine) {
                         tmem_st16(s_tm, x[0]);
                         tmem_st16(s_tm + 16, x[1]);
@@ -775,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float to = paged_reference(top, x), a = ex2(top - to);
                     top = to;
                     sum *= a;
-                    apart = apart || __any_sync(0xffffffffu, fabsf(top) > kApart && top != kPagedNoMax);
+                    apart = apart || far_apart();
                     if (j > 0) {
                         // the scores at hand were made after the product two before this one's
                         go = go && warp_wait(&W.o_full[m], (jobs - 1) & 1, gave_up);

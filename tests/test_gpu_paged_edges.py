@@ -58,3 +58,24 @@ def test_positions_near_two_to_the_31(h, n, Gq, window, sinks):
     out, lse = c.run(h, st)
     assert st.tolist() == [S.BAD_SLOT, S.BAD_SLOT]
     c.check(out, lse)
+
+
+# ---- rows that are not a request's ---------------------------------------------------------------
+
+@pytest.mark.parametrize("dt,cache", [("bf16", "same"), ("f16", "same"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,Gq", [(21, 2), (67, 4)])
+@pytest.mark.parametrize("value", [float("nan"), 1e30, float("inf")])
+def test_queries_of_others_change_nothing(h, dt, cache, D, n, Gq, value):
+    """A request's results are the same bits whatever stands in the rows behind it, those of no
+    request and those of the next."""
+    c = T.Case(np.random.default_rng(D), [n, n], [400, 30], 2, Gq, D, dt, cache, spare=70)
+    c.q[2 * n:] = 0
+    first = c.run(h)
+    c.q[2 * n:] = value
+    again = c.run(h)
+    assert all(torch.equal(x[:2 * n], y[:2 * n]) for x, y in zip(first, again))
+    c.check(*again)
+    c.q[n:2 * n] = value
+    again = c.run(h)
+    assert all(torch.equal(x[:n], y[:n]) for x, y in zip(first, again))
