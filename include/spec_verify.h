@@ -369,10 +369,9 @@ int spec_tree_attention_fp4(spec_handle h, const void *q, int64_t q_stride, cons
  * elements from one row to the next, at least H * D. Row i of request b stands at position
  * seq_pos[b] + i of its sequence; seq_pos int32 [B] is the number of positions before. A request
  * whose rows are not within 0 .. T - 1 (or with row_start[b] > row_start[b + 1]) takes no part
- * (SPEC_REQ_BAD_RANGE). Nothing depends on rows of no request (padding behind the last one may hold
- * anything, but it has to be readable), and their results are left as they were. Requests do not share
- * rows: row_start does not fall. B is limited by the handle, T by 2^31 - 1;
- * with T 0 nothing is launched and the statuses are 0.
+ * (SPEC_REQ_BAD_RANGE); the others do, and share no rows. Nothing depends on rows of no request (padding
+ * behind the last one may hold anything, but it has to be readable), and their results are left as they
+ * were. B is limited by the handle, T by 2^31 - 1; with T 0 nothing is launched and the statuses are 0.
  *
  * The paged cache (host struct, copied at the call; the pointers are device memory):
  *   k, v         SPEC_KV_NHD [num_blocks, block_size, H, D] or SPEC_KV_HND [num_blocks, H,

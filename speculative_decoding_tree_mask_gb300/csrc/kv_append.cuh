@@ -19,19 +19,31 @@ namespace {
 
 using namespace rope;
 
-// The last request whose first row is not past r, or -1; all lanes of a warp, B >= 1.
-__device__ __forceinline__ int owner_of(const int32_t *start, int B, int r) {
+// Whether request b has row r among its rows, which are within those given.
+__device__ __forceinline__ bool has_row(const KvAppendParams &P, int b, int r) {
+    const int s = __ldg(P.row_start + b), e = __ldg(P.row_start + b + 1);
+    return s >= 0 && e <= P.T && s <= r && r < e;
+}
+
+// The request that has row r, or -1; all lanes of a warp, B >= 1. The search takes it that row_start
+// does not fall. What it finds is looked at: a request out of range beside others may lead it astray,
+// so that they are gone through one after another where it found none (rows of no request pay for that).
+__device__ __forceinline__ int owner_of(const KvAppendParams &P, int r) {
     const int lane = threadIdx.x & 31;
-    int lo = 0, n = B;
-    do {
+    int lo = 0, n = P.B;
+    do {      // the last of n requests from lo on whose first row is not past r
         const int step = (n + 31) / 32, at = lane * step;
-        const bool le = at < n && __ldg(start + lo + at) <= r;
-        const int c = __popc(__ballot_sync(0xffffffffu, le));
-        if (c == 0) return -1;
+        const bool le = at < n && __ldg(P.row_start + lo + at) <= r;
+        const int c = max(1, __popc(__ballot_sync(0xffffffffu, le)));
         lo += (c - 1) * step;
         n = min(step, n - (c - 1) * step);
     } while (n > 1);
-    return lo;
+    if (has_row(P, lo, r)) return lo;
+    for (int b = 0; b < P.B; b += 32) {
+        const unsigned has = __ballot_sync(0xffffffffu, b + lane < P.B && has_row(P, b + lane, r));
+        if (has) return b + __ffs(has) - 1;
+    }
+    return -1;
 }
 
 // KIND: 0 elements of type T, 1 e4m3, 2 e5m2.
@@ -136,12 +148,8 @@ __device__ __forceinline__ NewRows<T, KIND> warp_rows(const KvAppendParams &P, i
     int b = -1, first = 0;
     if (io.row < P.T) {
         if (P.row_start) {
-            b = owner_of(P.row_start, P.B, (int)io.row);
-            if (b >= 0) {
-                first = __ldg(P.row_start + b);
-                const int end = __ldg(P.row_start + b + 1);
-                if (first < 0 || end > P.T || first > io.row || io.row >= end) b = -1;
-            }
+            b = owner_of(P, (int)io.row);
+            if (b >= 0) first = __ldg(P.row_start + b);
         } else {
             b = (int)(io.row / P.N);
             first = b * P.N;
