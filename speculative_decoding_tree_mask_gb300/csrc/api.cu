@@ -964,8 +964,7 @@ int spec_kv_append(spec_handle h, const void *q, int64_t q_stride, const void *k
     const int rc = check_paged(cache, dtype, B);
     if (rc != SPEC_OK) return rc;
     const int H = cache->H, D = cache->D;
-    if (Hq < 0 || Hq > (1 << 20) || (Hq > 0) != (q != nullptr) || (Hq > 0) != (q_out != nullptr))
-        return SPEC_ERR_ARG;
+    if (Hq < 0 || Hq > (1 << 20) || (Hq == 0 && (q || q_out))) return SPEC_ERR_ARG;
     if (rot < 0 || rot > D || rot % 2 != 0) return SPEC_ERR_ARG;
     if (style != SPEC_ROPE_HALVES && style != SPEC_ROPE_PAIRS) return SPEC_ERR_ARG;
     if (!std::isfinite(eps) || eps < 0.f) return SPEC_ERR_ARG;

@@ -62,3 +62,21 @@ def test_valid_requests_beside_bad_ones(h, T, start):
     assert torch.equal(cache.k, want) and torch.equal(cache.v, want)
     mine = gpu(owner >= 0)
     assert torch.equal(qo[mine], q[mine]) and (qo[~mine] == 7).all()
+
+
+# ---- no rows --------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("B", [0, 1, 3])
+@pytest.mark.parametrize("queries", [True, False])
+@pytest.mark.parametrize("given", [True, False])
+def test_no_rows(h, B, queries, given):
+    """Nothing is launched and the statuses are 0, with and without queries."""
+    cache = G.KvCache.empty(4, 16, 2, 64, torch.bfloat16, DEV)
+    q = torch.zeros((0, 4, 64), dtype=torch.bfloat16, device=DEV) if queries else None
+    k = torch.zeros((0, 2, 64), dtype=torch.bfloat16, device=DEV)
+    st = torch.full((B,), 9, dtype=torch.int32, device=DEV)
+    zeros = torch.zeros(B + 1, dtype=torch.int32, device=DEV)
+    qo = G.kv_append(h, q, k, k, cache, torch.zeros((B, 4), dtype=torch.int32, device=DEV), zeros[:B],
+                     zeros if given else None, torch.ones(32, device=DEV), status=st)
+    assert (qo.shape == q.shape) if queries else qo is None
+    assert st.tolist() == [0] * B and not cache.k.any()
