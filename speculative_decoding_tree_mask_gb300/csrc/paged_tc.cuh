@@ -94,6 +94,7 @@ struct PartWords {
     }
 };
 constexpr int kDealt = 4;
+constexpr int kOdd = 16;
 
 struct Words {
     PartWords part[kDealt];
@@ -104,10 +105,11 @@ struct Words {
     // Positions of a tile that are there. K's loader writes a tile's words again for the fourth
     // after it, whose place was that of a V whose products are done.
     alignas(16) unsigned seen[4][4];
-    // A part's V has NaN or infinities that not every row sees. Of eight parts: V's loader clears
-    // the word of the fourth part to come, where its own other warps are three tiles ahead at most
-    // and softmax three behind.
-    int odd[8];
+    // A part's V has NaN or infinities that not every row sees. V's first loading warp clears the word
+    // of the eighth part to come. When it comes to part k, the place of part k - 1's V was given back by
+    // K of two tiles earlier, of part k - 3 at the earliest; those products follow part k - 4's, whose
+    // word softmax may be about to read. V's other warps are three tiles ahead at most.
+    int odd[kOdd];
     uint32_t tmem;
     int gave_up;
     // 1 / the power of two of each row of Q: a float's upper half. Of two parts: a part of one tile
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_init(&W.part_full[i], 1);
             bar_init(&W.part_free[i], C_::kReaders);
         }
-        for (int i = 0; i < 8; ++i) W.odd[i] = 0;
+        for (int i = 0; i < kOdd; ++i) W.odd[i] = 0;
 #ifdef SPEC_DEBUG
         W.gave_up = P.lose;
 #else
@@ -470,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         *at = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    if (odd) W.odd[parts & 7] = 1;
+                    if (odd) W.odd[parts % kOdd] = 1;
                 }
                 fence_async_smem();
                 warp_arrive(&W.full[slot(x)]);
@@ -556,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_async_smem();
                 if (go) warp_arrive(&W.q_full);
             };
-            if (of_v && lane == 0 && w4 == 0) W.odd[(parts + 4) & 7] = 0;
+            if (of_v && lane == 0 && w4 == 0) W.odd[(parts + kOdd / 2) % kOdd] = 0;
             if constexpr (KIND == 0) {
                 int next = page(0), pending = -1;     // a tile whose copies are waited for later
                 auto settle = [&](bool behind) {
@@ -830,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t to = live ? paged_row(P, A.first, A.head, row0 + r) : 0;
             float *part = paged_slot(P, blockIdx.x, A.begins, RT, DP);
             const bool out32 = (reinterpret_cast<uintptr_t>(P.out) & 31) == 0;
-            const bool odd = n > 0 && *(volatile int *)&W.odd[parts & 7] != 0;
+            const bool odd = n > 0 && *(volatile int *)&W.odd[parts % kOdd] != 0;
             for (int q = 0; warp_live && q < DP / 32; ++q) {
                 float v[32];
                 __syncwarp();

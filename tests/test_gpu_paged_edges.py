@@ -79,3 +79,27 @@ def test_queries_of_others_change_nothing(h, dt, cache, D, n, Gq, value):
     c.q[n:2 * n] = value
     again = c.run(h)
     assert all(torch.equal(x[:n], y[:n]) for x, y in zip(first, again))
+
+
+# ---- infinities in many short parts ---------------------------------------------------------------
+
+@pytest.mark.parametrize("D,n,Gq", [(64, 40, 1), (128, 40, 1), (128, 70, 2), (256, 40, 1)])
+def test_infinities_in_short_items(h, D, n, Gq):
+    """Thousands of items of a tile each, dealt several to a CTA, an infinity that the last row alone
+    sees in every third request: it is in that row's element and nowhere else."""
+    B, bs = 4000, 128
+    g = torch.Generator(device=DEV)
+    g.manual_seed(D)
+    k, v = (torch.randn((B, bs, 1, D), generator=g, device=DEV).half() for _ in range(2))
+    pos = torch.randint(0, bs - n + 1 - n, (B,), generator=g, device=DEV) if bs >= 2 * n else \
+        torch.zeros(B, dtype=torch.int64, device=DEV)
+    b = torch.arange(0, B, 3, device=DEV)
+    v[b, pos[b] + n - 1, 0, b % D] = float("inf")
+    q = torch.randn((B * n, Gq, D), generator=g, device=DEV).half()
+    table = torch.arange(B, dtype=torch.int32, device=DEV)[:, None]
+    want = torch.zeros((B, n, Gq, D), dtype=torch.bool, device=DEV)
+    want[b, n - 1, :, b % D] = True
+    for _ in range(5):
+        out, _ = G.paged_attention(h, q, G.KvCache(k, v), table, pos.int(), D ** -0.5, max_new=n)
+        assert torch.equal(torch.isposinf(out.view(B, n, Gq, D)), want)
+        assert torch.equal(torch.isfinite(out.view(B, n, Gq, D)), ~want)
