@@ -475,7 +475,8 @@ int spec_paged_attention(spec_handle h, const void *q, int64_t q_stride, int dty
  *                logprob, entropy and top_logprobs NaN, top_ids -1), SPEC_ROW_BAD_NODE for a node of
  *                N or more, or below -1 (likewise), SPEC_ROW_BAD_TOKEN for a token of V or more, or
  *                below -1 (its logprob is NaN).
- * Sums are float32 (of at most 2^11 terms a thread, then pairwise). Nothing is kept between calls.
+ * Sums are float32: a thread's terms in two chains (of 2^12 each at most: V 2^21, a row a CTA), then
+ * pairwise. Nothing is kept between calls.
  */
 int spec_token_logprobs(spec_handle h, const void *logits, int dtype, int B, int64_t N, int64_t V,
                         const int32_t *node, int P, const int32_t *tokens, int C,
