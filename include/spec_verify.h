@@ -379,8 +379,8 @@ int spec_tree_attention_fp4(spec_handle h, const void *q, int64_t q_stride, cons
  *                k_block_stride, v_block_stride elements apart (multiples of 16 bytes, so that K and V
  *                may be interleaved block by block);
  *   kind         SPEC_CACHE_SAME (elements of the rows' dtype) or SPEC_CACHE_FP8_E4M3 / _E5M2;
- *   k_scale, v_scale   device float32, one value each (NULL = 1), for fp8: an element's value is
- *                its code's times the scale; ignored otherwise;
+ *   k_scale, v_scale   device float32, one value each (NULL = 1), positive and finite, for fp8: an
+ *                element's value is its code's times the scale; ignored otherwise;
  *   block_table  int32 [B, max_blocks]: cache block of each block_size positions of request b.
  * H at most 65536, D at most 1024, a head's bytes a multiple of 16; a request has at most 2^31 - 1025
  * positions (max_blocks * block_size), the cache at most 2^31 - 1 blocks.

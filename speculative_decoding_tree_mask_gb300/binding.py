@@ -624,8 +624,8 @@ class KvCache:
     """A paged K/V cache (spec_kv_cache), the one that spec_kv_commit writes: k, v [num_blocks,
     block_size, H, D] (SPEC_KV_NHD) or [num_blocks, H, block_size, D] (SPEC_KV_HND) of float32,
     bfloat16, float16 or a float8 type, or uint8 with `kind` saying which float8. Blocks may stand
-    apart (kv[:, 0] and kv[:, 1] of one tensor). Tensor scales of fp8: float32 of one element
-    (None = 1). Holds the tensors; block tables come with each call."""
+    apart (kv[:, 0] and kv[:, 1] of one tensor). Tensor scales of fp8: float32 of one element,
+    positive (None = 1). Holds the tensors; block tables come with each call."""
 
     def __init__(self, k, v, layout: int = SPEC_KV_NHD, k_scale=None, v_scale=None,
                  kind: int | None = None):
