@@ -1,4 +1,6 @@
 """New tokens into the paged cache at the edges of what a call may say (needs a GB300)."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -80,3 +82,22 @@ def test_no_rows(h, B, queries, given):
                      zeros if given else None, torch.ones(32, device=DEV), status=st)
     assert (qo.shape == q.shape) if queries else qo is None
     assert st.tolist() == [0] * B and not cache.k.any()
+
+
+# ---- refusals at the C entry ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rot,want", [(63, G.SPEC_ERR_ARG), (65, G.SPEC_ERR_ARG), (-2, G.SPEC_ERR_ARG),
+                                      (66, G.SPEC_ERR_ARG), (64, 0)])
+def test_rotated_elements(h, rot, want):
+    """An odd, negative or too large number of rotated elements is refused."""
+    x = torch.zeros((2, 2, 64), dtype=torch.bfloat16, device=DEV)
+    cache = G.KvCache.empty(4, 16, 2, 64, torch.bfloat16, DEV)
+    table, pos = (torch.zeros(s, dtype=torch.int32, device=DEV) for s in ((2, 4), (2,)))
+    freq = torch.zeros(64, device=DEV)
+    view = cache.struct(table, 2, 0, torch.bfloat16)
+    rc = G.load().spec_kv_append(
+        h.ptr, x.data_ptr(), 128, x.data_ptr(), 128, x.data_ptr(), 128, G.SPEC_BF16, 2, 2, 2, None,
+        pos.data_ptr(), ctypes.byref(view), None, None, 1e-6, freq.data_ptr(), rot, 0, x.data_ptr(), 128,
+        None, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == want

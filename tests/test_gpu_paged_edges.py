@@ -103,3 +103,29 @@ def test_infinities_in_short_items(h, D, n, Gq):
         out, _ = G.paged_attention(h, q, G.KvCache(k, v), table, pos.int(), D ** -0.5, max_new=n)
         assert torch.equal(torch.isposinf(out.view(B, n, Gq, D)), want)
         assert torch.equal(torch.isfinite(out.view(B, n, Gq, D)), ~want)
+
+
+# ---- alignment ------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dt,cache", [("bf16", "same"), ("f16", "e5m2")])
+@pytest.mark.parametrize("counts,Gq,D", [([3, 1], 2, 64), ([1], 4, 96), ([2], 2, 256), ([70, 2], 2, 64),
+                                         ([200], 2, 128), ([50, 1], 3, 80), ([60], 1, 256)])
+@pytest.mark.parametrize("q_off,out_off", [(1, 1), (4, 4), (8, 8), (0, 3), (5, 0)])
+def test_queries_and_results_at_any_address(h, dt, cache, counts, Gq, D, q_off, out_off):
+    """Queries whose rows begin off 16-byte boundaries, and an output that begins anywhere; what is
+    beside it stays."""
+    rng = np.random.default_rng(q_off)
+    c = T.Case(rng, counts, [500, 40][:len(counts)], 2, Gq, D, dt, cache, pad=16)
+    wide = torch.zeros((len(c.q), c.Hq * D + 16 + q_off % 2), dtype=c.q.dtype, device=DEV)
+    wide[:, q_off:q_off + c.Hq * D] = c.q.flatten(1)
+    c.q = wide[:, q_off:q_off + c.Hq * D].unflatten(1, (c.Hq, D))
+    n = c.q.numel()
+    flat = torch.full((n + 32,), 7.0, dtype=c.q.dtype, device=DEV)
+    out = flat[out_off:out_off + n].view(c.q.shape)
+    lse = torch.empty(c.q.shape[:2], device=DEV)
+    size = G.spec_paged_attention_workspace(h, len(counts), len(c.q), 0, c.Hq, 2, D)
+    work = torch.empty(size, dtype=torch.uint8, device=DEV)
+    G.spec_paged_attention(h, c.q, c.cache(), T.gpu(c.table), T.gpu(np.array(c.pos, np.int32)), c.scale,
+                           out, work, T.gpu(c.start), lse=lse)
+    c.check(out, lse)
+    assert (flat[:out_off] == 7).all() and (flat[out_off + n:] == 7).all()
