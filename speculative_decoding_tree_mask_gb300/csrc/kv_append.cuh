@@ -84,49 +84,46 @@ struct NewRows {
     __device__ __forceinline__ const E_t *weight(int r) const {
         return reinterpret_cast<const E_t *>(P.w[r >= P.Hq]);
     }
-    __device__ __forceinline__ void put(int r, int v, const float (&x)[E]) const {
+    // A row's place: its address, null if it has none, and for a row of an 8-bit cache the scale.
+    struct Place {
+        char *at;
+        bool codes;
+        float scale;
+    };
+    __device__ __forceinline__ Place place(int r) const {
         const int i = kind(r);
-        if (i == 0) {
-            E_t *o = reinterpret_cast<E_t *>(P.q_out) + row * P.q_out_stride +
-                     (int64_t)r * P.cache.D + v * E;
-            *reinterpret_cast<uint4 *>(o) = pack<T>(x);
-            return;
-        }
-        char *to = slot[i - 1];
-        if (!to) return;
-        to += r * head;
-        if constexpr (KIND == 0) {
-            *reinterpret_cast<uint4 *>(to + v * 16) = pack<T>(x);
-        } else {
-            uint32_t w[E / 4];
-#pragma unroll
-            for (int e = 0; e < E; e += 4) {
-                float y[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = __fdiv_rn(x[e + k], scale[i - 1]);
-                w[e / 4] = fp8x2<KIND>(y[0], y[1]) | fp8x2<KIND>(y[2], y[3]) << 16;
-            }
-            if constexpr (E == 8)
-                *reinterpret_cast<uint2 *>(to + v * 8) = make_uint2(w[0], w[1]);
-            else
-                *reinterpret_cast<uint32_t *>(to + v * 4) = w[0];
-        }
+        if (i == 0)
+            return Place{reinterpret_cast<char *>(reinterpret_cast<E_t *>(P.q_out) +
+                                                  row * P.q_out_stride + (int64_t)r * P.cache.D),
+                         false, 1.f};
+        char *to = i == 1 ? slot[0] : slot[1];
+        return Place{to ? to + r * head : nullptr, KIND != 0, i == 1 ? scale[0] : scale[1]};
     }
-    __device__ __forceinline__ void put1(int r, int e, float x) const {
-        const int i = kind(r);
-        if (i == 0) {
-            reinterpret_cast<E_t *>(P.q_out)[row * P.q_out_stride + (int64_t)r * P.cache.D + e] =
-                from_f32<T>(x);
+    __device__ __forceinline__ void put(const Place &p, int v, const float (&x)[E]) const {
+        if (!p.at) return;
+        if (KIND == 0 || !p.codes) {
+            *reinterpret_cast<uint4 *>(p.at + v * 16) = pack<T>(x);
             return;
         }
-        char *to = slot[i - 1];
-        if (!to) return;
-        to += r * head;
-        if constexpr (KIND == 0)
-            reinterpret_cast<E_t *>(to)[e] = from_f32<T>(x);
+        uint32_t w[E / 4];
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+            float y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = __fdiv_rn(x[e + k], p.scale);
+            w[e / 4] = fp8x2<KIND>(y[0], y[1]) | fp8x2<KIND>(y[2], y[3]) << 16;
+        }
+        if constexpr (E == 8)
+            *reinterpret_cast<uint2 *>(p.at + v * 8) = make_uint2(w[0], w[1]);
         else
-            reinterpret_cast<uint8_t *>(to)[e] =
-                (uint8_t)fp8x2<KIND>(__fdiv_rn(x, scale[i - 1]), 0.f);
+            *reinterpret_cast<uint32_t *>(p.at + v * 4) = w[0];
+    }
+    __device__ __forceinline__ void put1(const Place &p, int e, float x) const {
+        if (!p.at) return;
+        if (KIND == 0 || !p.codes)
+            reinterpret_cast<E_t *>(p.at)[e] = from_f32<T>(x);
+        else
+            reinterpret_cast<uint8_t *>(p.at)[e] = (uint8_t)fp8x2<KIND>(__fdiv_rn(x, p.scale), 0.f);
     }
 };
 

@@ -61,7 +61,7 @@ struct TokenRows {
         return reinterpret_cast<const E_t *>(P.x[kind]) + token * P.stride[kind] +
                (int64_t)(r - (kind ? P.H[0] : 0)) * P.D;
     }
-    __device__ __forceinline__ E_t *dst(int r) const {
+    __device__ __forceinline__ E_t *place(int r) const {
         const int kind = r >= P.H[0];
         return reinterpret_cast<E_t *>(P.y[kind]) + token * P.ystride[kind] +
                (int64_t)(r - (kind ? P.H[0] : 0)) * P.D;
@@ -71,10 +71,10 @@ struct TokenRows {
     __device__ __forceinline__ const E_t *weight(int r) const {
         return reinterpret_cast<const E_t *>(P.w[r >= P.H[0]]);
     }
-    __device__ __forceinline__ void put(int r, int v, const float (&x)[E]) const {
-        *reinterpret_cast<uint4 *>(dst(r) + v * E) = pack<T>(x);
+    __device__ __forceinline__ void put(E_t *to, int v, const float (&x)[E]) const {
+        *reinterpret_cast<uint4 *>(to + v * E) = pack<T>(x);
     }
-    __device__ __forceinline__ void put1(int r, int e, float x) const { dst(r)[e] = from_f32<T>(x); }
+    __device__ __forceinline__ void put1(E_t *to, int e, float x) const { to[e] = from_f32<T>(x); }
 };
 
 // T: element type; LPR: lanes per head row.

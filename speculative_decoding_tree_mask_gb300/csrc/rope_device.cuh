@@ -5,8 +5,9 @@
 //   const E_t *src(int r)      row r of the token (its heads one after another);
 //   bool turns(int r)          whether the row is normalised and rotated (values are not);
 //   const E_t *weight(int r)   norm weights; norm(): whether there are any;
-//   void put(int r, int v, const float (&x)[E])   vector v of row r (E elements of 16 bytes);
-//   void put1(int r, int e, float x)              element e, for rows that 16-byte vectors do not fit.
+//   Place place(int r)         where row r goes, once for all of it;
+//   void put(Place p, int v, const float (&x)[E])   its vector v (E elements of 16 bytes);
+//   void put1(Place p, int e, float x)              element e, for rows that 16-byte vectors do not fit.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -182,7 +183,7 @@ __device__ __forceinline__ void share_vec(IO &io, int row0, int row1, int pos, i
     const float inv_d = 1.f / (float)D;
     for (int r0 = row0; r0 < row1; r0 += G) {
         const int r = r0 + g;
-        const bool live = r < row1, turns = live && io.turns(r);
+        const bool live = r < row1, turns = io.turns(r);
         float x[E], y[E];
         unpack<T>(a, x);
         unpack<T>(b, y);
@@ -254,8 +255,9 @@ __device__ __forceinline__ void share_vec(IO &io, int row0, int row1, int pos, i
             }
         }
         if (live) {
-            if (va >= 0) io.put(r, va, x);
-            if (vb >= 0) io.put(r, vb, y);
+            const auto to = io.place(r);
+            if (va >= 0) io.put(to, va, x);
+            if (vb >= 0) io.put(to, vb, y);
         }
     }
 }
@@ -270,6 +272,7 @@ __device__ __forceinline__ void share_any(IO &io, int row0, int row1, int pos, i
     for (int i = lane; i < half; i += 32) cs[i] = cos_sin(inv_freq, i, pos);
     for (int r = row0; r < row1; ++r) {
         const E_t *x = io.src(r);
+        const auto to = io.place(r);
         const bool turns = io.turns(r);
         const int turned = turns ? half : 0;
         float sum = 0.f;
@@ -290,10 +293,10 @@ __device__ __forceinline__ void share_any(IO &io, int row0, int row1, int pos, i
             const int ia = pairs ? 2 * i : i, ic = pairs ? 2 * i + 1 : i + half;
             const float2 t = cs[i];
             const float p = row[ia], q = row[ic];
-            io.put1(r, ia, p * t.x - q * t.y);
-            io.put1(r, ic, q * t.x + p * t.y);
+            io.put1(to, ia, p * t.x - q * t.y);
+            io.put1(to, ic, q * t.x + p * t.y);
         }
-        for (int e = 2 * turned + lane; e < D; e += 32) io.put1(r, e, row[e]);
+        for (int e = 2 * turned + lane; e < D; e += 32) io.put1(to, e, row[e]);
         __syncwarp();
     }
 }
