@@ -7,7 +7,7 @@
 // 32 at a time, so that 1024 requests take two dependent loads, then one block-table entry.
 // DRAM bounds it: each row once in and once out, and nothing between. Writing K and V where they
 // belong instead of in rows saves the copy's read and write of both. 32380 new tokens of 32 + 16 heads
-// x 128 in bfloat16 with head norms take 148 us, 5.4 TB/s (79% of the measured copy); 15 tokens 3.1 us,
+// x 128 in bfloat16 with head norms take 144 us, 5.5 TB/s (81% of the measured copy); 15 tokens 4 us,
 // dependent loads from a cold cache.
 
 #pragma once

@@ -15,9 +15,10 @@
 // 64-bit keys of the value and the lower index, so that no arrival order changes the result. Where
 // too many tokens pass (equal logits), the K-th key of those at hand is the next bound.
 //
-// DRAM bounds it: 4096 rows of 152064 bfloat16 logits, 8 tokens each, 236 us, 5.3 TB/s (78% of the
-// measured copy), without tokens 207 us; 2048 rows of float32 224 us, 5.6 TB/s. What is left is each
-// row's end, during which its CTA loads nothing: six CTAs an SM are what registers allow (four 256 us).
+// DRAM bounds it: 4096 rows of 152064 bfloat16 logits, 8 tokens each, 229 us, 5.4 TB/s (80% of the
+// measured copy), without tokens 200 us; 2048 rows of float32 216 us, 5.8 TB/s. What is left is each
+// row's end, during which its CTA loads nothing: six CTAs an SM are what registers allow (four took 20 us
+// more). Times that are compared here are of single replays, about 7 us above these.
 // (The next row's first 8 to 64 KB brought to L2 meanwhile: no difference.) A row has a CTA, or with few
 // rows a cluster of up to eight CTAs (20 rows of 50257: 11 us, 19 with a CTA each), whose parts meet in
 // distributed shared memory (no workspace, no atomics on memory).

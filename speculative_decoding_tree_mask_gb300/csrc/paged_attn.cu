@@ -7,8 +7,8 @@ namespace {
 // The most rows of the kernel for few. With 24 rows (chains of six, 32 and 8 heads x 128) it takes 259 us
 // for 64 chains over up to 8192 positions where the tensor cores take 255, but 246 against 306 over an
 // 8-bit cache, 39 against 54 for 16 chains over 1000, and with 32 rows at D = 64 164 against 212. Beside a
-// launch on the tensor cores 16, one token of up to 16 heads a group: a mixed batch (below) takes 177 us,
-// 183 with 32.
+// launch on the tensor cores 16, one token of up to 16 heads a group: a mixed batch (below) took 6 us more
+// with 32.
 int few_rows(int D) { return paged_padded(D) == 256 ? 16 : 32; }
 int few_beside(int G, int D) { return G <= 16 ? 16 : few_rows(D); }
 
@@ -159,8 +159,8 @@ cudaError_t run(PagedAttnParams p, const Plan &n, int rows_over, int rows_most, 
 
 // A batch may hold requests of few rows and of many; which, the device knows alone. Where it may
 // hold both, both kernels are launched and take their own: 22 decoding requests over up to 12000
-// positions beside a chunk of 512 tokens (D = 64, 8 K/V heads) take 181 us, 218 when the tensor cores
-// had a tile of 256 rows for four.
+// positions beside a chunk of 512 tokens (D = 64, 8 K/V heads) take 170 us, 37 less than when the tensor
+// cores had a tile of 256 rows for four.
 int64_t paged_attn_workspace(int max_new, int G, int D, int sms) {
     const int64_t R = (int64_t)max_new * G;
     int64_t most = 256;       // whatever the cache's type and the batch

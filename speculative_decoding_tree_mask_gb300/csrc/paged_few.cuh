@@ -15,9 +15,9 @@
 // work is lost, but it is a tenth of what the time of the bytes allows. Block-table entries are fetched
 // a step before their copies.
 //
-// One token of 128 requests over up to 8192 positions (32 query and 8 K/V heads x 128, bfloat16): 392 to
-// 400 us, 6.7 to 6.9 TB/s (the measured copy: 6.8). Over 500000 positions in e4m3, 64 query heads: 207 us,
-// 4.9 TB/s: there the conversions count, issued in 49% of the cycles by eight warps an SM with the
+// One token of 128 requests over up to 8192 positions (32 query and 8 K/V heads x 128, bfloat16): 384 to
+// 394 us, 6.8 to 7.0 TB/s (the measured copy: 6.8). Over 500000 positions in e4m3, 64 query heads: 200 us,
+// 5.1 TB/s: there the conversions count, issued in 49% of the cycles by eight warps an SM with the
 // integer pipe at 49% and DRAM at 66%.
 //
 // 8-bit caches: codes become halves on the way from shared memory to the products' operands. Both

@@ -29,11 +29,14 @@
 // 64 positions from S to P and the meetings at its ends: issue slots are taken in 49% of the cycles, the
 // tensor pipe is active in 51%, and no other pipe in more than 33%.
 //
-// 32 query and 8 K/V heads x 128: two prompts of 8192 and 5845 tokens 634 us, 1.31 PFLOP/s (66% of the
-// measured cuBLAS rate), over an e4m3 cache 969 us (the codes' way through registers); 2048 tokens after
-// 60000 1.43 ms, 1.43 PFLOP/s; a window of 4096 with sinks 238 us, 0.97 PFLOP/s (items of 35 tiles, two
-// of them seen in part); D = 64 600 us, 0.69 PFLOP/s (softmax costs as much as at 128); D = 256, two of
-// 4096 with 16 and 4 heads, 230 us, 0.90 PFLOP/s.
+// 32 query and 8 K/V heads x 128: two prompts of 8192 and 5845 tokens 666 us, 1.25 PFLOP/s (63% of the
+// measured cuBLAS rate) one call after another, where the power limit holds the SMs at 1.96 to 1.99 GHz;
+// 636 us at 2.07 GHz, calls that stand alone. Over an e4m3 cache 976 us (the codes' way through
+// registers); 2048 tokens after 60000 1.54 ms, 1.33 PFLOP/s; a window of 4096 with sinks 230 us, 1.0
+// PFLOP/s (items of 35 tiles, two of them seen in part); D = 64 592 us, 0.70 PFLOP/s (softmax costs as
+// much as at 128); D = 256, two of 4096 with 16 and 4 heads, 224 us, 0.93 PFLOP/s. Short prompts are far
+// from that, since an item's queries, first scores and result overlap with no other item's: 32 of up to
+// 512 tokens 125 us, 0.24 PFLOP/s, 128 of up to 100 103 us.
 //
 // Items of up to 128 rows (a decoding request in a mixed batch) leave the second group idle, and
 // warps without a live row touch nothing: a tile then takes less time than its bytes do.
@@ -62,6 +65,8 @@ constexpr int kRing = 5;
 //   D = 128, 16 bits    671, 637, 642, 646 us   (five of 3300 after 1000: 398, 384, 383, 385)
 //   D = 128, 8 bits    1126, 987, 935, 918 us   (eight of 2000: 332, 309, 295, 300)
 //   D = 64, 16 bits     598, 609, 607, 611 us   (192: 608)
+//   D = 64, 8 bits      685, 646, 648, 654 us   (320: 644; eight of 2000: 201, 181, 177, 177; 32 of 512:
+//                                                130, 124, 123, 121)
 //   D = 256, two of 4096, 16 bits 230, 234, 237, 240 us; 8 bits 428, 441, 445 us.
 template <int KIND, int DP>
 constexpr int kTcFixed = DP == 256 ? 256 : KIND ? 448 : DP == 128 ? 384 : 256;

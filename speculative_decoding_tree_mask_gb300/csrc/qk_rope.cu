@@ -11,8 +11,8 @@
 // heads of one token: it forms the token's rot/2 sines and cosines once, in shared memory, and
 // keeps its lanes' own in registers for all its rows. Heads are shared out over more warps
 // when there are few tokens, so that a small call still fills the GPU. 16384 tokens of 40 heads
-// x 128 in bfloat16 take 58 us, 5.8 TB/s in and out (86% of the measured copy), by pairs 59 us; 256
-// tokens 4.3 us.
+// x 128 in bfloat16 take 57 us, 5.8 TB/s in and out (86% of the measured copy), by pairs 58 us; 256
+// tokens 3.8 us, one call after another.
 // Sizes and alignments that 16-byte vectors do not fit take a warp per row.
 //
 // The angle: turns = position * inv_freq / (2 pi). inv_freq / (2 pi) becomes a 64-bit fixed
